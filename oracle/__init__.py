@@ -21,6 +21,8 @@ source documentation pages named in its docstring:
   per row, the last Q tokens of its range).
 * ``nsa_select_attention_backward`` -- gradients (dq, dk, dv) of the selection
   forward, the softmax backward over the same explicit key sets.
+* ``paged_kv_append``, ``paged_attention``, ``nsa_select_paged`` -- the decode operations
+  over a paged cache (bf16, or e4m3 with a scale for each page and head).
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 library routines (torch SDPA in float64), brute force on tiny inputs and the
@@ -33,6 +35,7 @@ from .blocksparse import blocksparse_attention
 from .ragged_decode import ragged_decode_attention
 from .ragged_attention import ragged_flash_attention
 from .nsa_backward import nsa_select_attention_backward
+from .paged import nsa_select_paged, paged_attention, paged_kv_append
 
 __all__ = [
     "nsa_select_attention",
@@ -42,4 +45,7 @@ __all__ = [
     "ragged_decode_attention",
     "ragged_flash_attention",
     "nsa_select_attention_backward",
+    "nsa_select_paged",
+    "paged_attention",
+    "paged_kv_append",
 ]

@@ -11,7 +11,8 @@ Entry points (same names as the C ABI without the ``sba_`` prefix):
   nsa_select_fwd, sparse_mask_bounds (forward and dK/dV bounds), blocksparse_attn_fwd,
   ragged_decode_fwd,
   ragged_decode_fwd_noalloc, ragged_decode_workspace_size, ragged_flash_attention_fwd,
-  ragged_flash_attention_workspace_size, check_error.
+  ragged_flash_attention_workspace_size, paged_kv_append, paged_attention_fwd,
+  paged_attention_workspace_size, nsa_select_paged_fwd, check_error.
 """
 
 from __future__ import annotations
@@ -30,7 +31,8 @@ __all__ = [
     "ragged_decode_workspace_size", "ragged_flash_attention_fwd",
     "ragged_flash_attention_workspace_size", "l2_read_probe", "check_error",
     "set_wait_timeout_cycles", "get_wait_timeout_cycles", "nsa_select_bwd",
-    "nsa_select_bwd_workspace_size", "EXPORTED_SYMBOLS",
+    "nsa_select_bwd_workspace_size", "paged_kv_append", "paged_attention_fwd",
+    "paged_attention_workspace_size", "nsa_select_paged_fwd", "EXPORTED_SYMBOLS",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -42,9 +44,11 @@ EXPORTED_SYMBOLS = (
     "sba_nsa_select_host_workspace_size", "sba_nsa_select_fwd_host",
     "sba_set_wait_timeout_cycles", "sba_get_wait_timeout_cycles",
     "sba_nsa_select_bwd", "sba_nsa_select_bwd_workspace_size",
+    "sba_paged_kv_append", "sba_paged_attention_workspace_size", "sba_paged_attention_fwd",
+    "sba_nsa_select_paged_fwd",
 )
 
-SBA_BF16, SBA_F32 = 0, 1
+SBA_BF16, SBA_F32, SBA_E4M3 = 0, 1, 2
 _ERRORS = {-1: "invalid argument", -2: "unsupported", -3: "CUDA error", -4: "timeout",
            -5: "malformed device input"}
 
@@ -116,6 +120,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sba_nsa_select_bwd.argtypes = [vp, vp, vp, vp, f32p, vp, i32p, i32p, ci, ci, i32p, ci, ci, ci,
                                        ci, ci, ci, ci, ci, cf, ci, vp, vp, vp, vp, csz, vp]
     lib.sba_nsa_select_bwd.restype = ci
+    cll = ctypes.c_longlong
+    lib.sba_paged_kv_append.argtypes = [vp, cll, vp, cll, vp, cll, vp, cll, f32p, f32p, ci, ci, ci, vp,
+                                        vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p, i32p, ci, ci, ci,
+                                        ci, ci, ci, ci, vp]
+    lib.sba_paged_kv_append.restype = ci
+    lib.sba_paged_attention_workspace_size.argtypes = [ci]
+    lib.sba_paged_attention_workspace_size.restype = csz
+    lib.sba_paged_attention_fwd.argtypes = [vp, cll, vp, vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p,
+                                            i32p, ci, ci, ci, ci, ci, ci, ci, cf, ci, ci, cf, f32p, ci,
+                                            ci, vp, f32p, vp, csz, vp]
+    lib.sba_paged_attention_fwd.restype = ci
+    lib.sba_nsa_select_paged_fwd.argtypes = [vp, cll, vp, vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p,
+                                             ci, ci, ci, ci, ci, ci, i32p, i32p, ci, ci, ci, ci, cf,
+                                             vp, vp, f32p, vp]
+    lib.sba_nsa_select_paged_fwd.restype = ci
     lib.sba_set_wait_timeout_cycles.argtypes = [ctypes.c_longlong]
     lib.sba_set_wait_timeout_cycles.restype = ci
     lib.sba_get_wait_timeout_cycles.argtypes = []
@@ -454,6 +473,200 @@ def ragged_flash_attention_fwd(q, k, v, sequence_start, sequence_end, *, softmax
         float(softmax_scale or 0.0), int(window_left), int(window_right),
         float(logits_soft_cap or 0.0), _ptr(sink_bias), num_sinks, per_head, _ptr(out), _ptr(lse),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev))
+    return out, lse
+
+
+# ---------------------------------------------------------------- paged caches
+def _call_on(index, fn, *args):
+    """_call with tensors' device index; most calls find their device current already."""
+    if torch.cuda.current_device() == index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args))
+
+
+def _at(t, name, index, dtype=None, shape=None):
+    """Address of a contiguous CUDA tensor on device ``index``; None passes through."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other tensors")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _pool_args(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens):
+    """(device index, the library's cache arguments, (num_pages, Hkv, P, D), cache dtype)."""
+    index = k_pages.get_device()
+    if index < 0:
+        raise ValueError("libsba works on CUDA tensors only (no CPU path)")
+    dtype = {torch.float8_e4m3fn: SBA_E4M3, torch.bfloat16: SBA_BF16}.get(k_pages.dtype)
+    if dtype is None or v_pages.dtype != k_pages.dtype:
+        raise TypeError("k_pages and v_pages must both be float8_e4m3fn or both bfloat16")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.get_device() != index:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D] on one device")
+    pages, hkv, size, d = k_pages.shape
+    stride = k_pages.stride(0) if pages > 1 else hkv * size * d
+    for t in (k_pages, v_pages):
+        st = t.stride()
+        if (st[3] != 1 or st[2] != d or (hkv > 1 and st[1] != size * d) or (pages > 1 and st[0] != stride)):
+            raise ValueError("k_pages, v_pages: pages must be dense and lie as far apart in both pools")
+    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
+        raise ValueError("page_table must be [B, width] and seq_lens [B]")
+    args = (k_pages.data_ptr(), v_pages.data_ptr(),
+            _at(k_scales, "k_scales", index, torch.float32, (pages, hkv)),
+            _at(v_scales, "v_scales", index, torch.float32, (pages, hkv)), stride, pages, size,
+            _at(page_table, "page_table", index, torch.int32), page_table.shape[1],
+            _at(seq_lens, "seq_lens", index, torch.int32))
+    return index, args, (pages, hkv, size, d), dtype
+
+
+def _token_rows(t, name, index, d, cu_seqlens, batch):
+    """(Q, N, heads, token stride) of bf16 token rows: [N, H, D] with cu_seqlens, else
+    [B, H, D] (one token per row) or [B, Q, H, D].  Heads are dense inside a token."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the cache's device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 and (t.dim() != 4 or cu_seqlens is not None):
+        raise ValueError(f"{name} must be [B, H, D] or [B, Q, H, D], or [N, H, D] with cu_seqlens")
+    if t.shape[-1] != d:
+        raise ValueError(f"{name} must have the cache's head dimension")
+    heads, st = t.shape[-2], t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if t.dim() == 3:
+        n, q, stride = t.shape[0], 1, st[0]
+    else:
+        b, q = t.shape[0], t.shape[1]
+        n, stride = b * q, st[1] if q > 1 else st[0]
+        if b > 1 and q > 1 and st[0] != q * st[1]:
+            raise ValueError(f"{name}: tokens must lie equally far apart")
+    if cu_seqlens is None and t.shape[0] != batch:
+        raise ValueError(f"{name} must have one entry per row of page_table")
+    return q, n, heads, stride if n > 1 else heads * d
+
+
+def _cu(cu_seqlens, index, batch):
+    return _at(cu_seqlens, "cu_seqlens", index, torch.int32, (batch + 1,))
+
+
+def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
+                    cu_seqlens=None, q=None, cos=None, sin=None, interleaved=False, q_out=None):
+    """Write the rows' last tokens into a paged cache.  k / v bf16 [B, Hkv, D] (one token
+    per row), [B, Q, Hkv, D], or [N, Hkv, D] with cu_seqlens int32 [B + 1]; token strides
+    may be those of a slice.  k_pages / v_pages [num_pages, Hkv, page_size, D]
+    float8_e4m3fn (with fp32 scales [num_pages, Hkv]) or bfloat16, page_table int32
+    [B, width], seq_lens int32 [B] with the new tokens counted.  cos / sin fp32
+    [max_pos, rot_dim / 2] turn keys (and q, [..., Hq, D]) by their positions.  Returns
+    q_out (new unless given; may be q), or None without q."""
+    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
+                                                    seq_lens)
+    batch = page_table.shape[0]
+    Q, N, heads, k_stride = _token_rows(k, "k", index, d, cu_seqlens, batch)
+    if v.shape != k.shape or heads != hkv:
+        raise ValueError("k and v must have the same shape and the cache's heads")
+    v_stride = _token_rows(v, "v", index, d, cu_seqlens, batch)[3]
+    hq = q_stride = o_stride = 0
+    if q is not None:
+        if q.shape[:-2] != k.shape[:-2]:
+            raise ValueError("q must have k's tokens")
+        _, _, hq, q_stride = _token_rows(q, "q", index, d, cu_seqlens, batch)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        o_stride = _token_rows(q_out, "q_out", index, d, cu_seqlens, batch)[3]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rot = max_pos = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2 or sin.shape != cos.shape:
+            raise ValueError("cos and sin go together, [max_pos, rot_dim / 2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    _call_on(index, load_library().sba_paged_kv_append, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+             None if q is None else q.data_ptr(), q_stride, None if q is None else q_out.data_ptr(),
+             o_stride, _at(cos, "cos", index, torch.float32), _at(sin, "sin", index, torch.float32), rot,
+             max_pos, int(bool(interleaved)), *pool, _cu(cu_seqlens, index, batch), batch, Q, N, hq, hkv,
+             d, dtype, torch.cuda.current_stream(index).cuda_stream)
+    return q_out
+
+
+def paged_attention_workspace_size(D) -> int:
+    return int(load_library().sba_paged_attention_workspace_size(D))
+
+
+def _results(q, index, out, lse, return_lse):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    return (out, lse, _at(out, "out", index, torch.bfloat16),
+            _at(lse, "lse", index, torch.float32, tuple(q.shape[:-1])))
+
+
+def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
+                        cu_seqlens=None, softmax_scale=None, window_left=-1, window_right=-1,
+                        logits_soft_cap=None, sink_bias=None, out=None, lse=None, workspace=None,
+                        return_lse=True):
+    """Attention of the rows' last tokens over a paged cache (as paged_kv_append fills it).
+    q bf16 [B, Hq, D], [B, Q, Hq, D], or [N, Hq, D] with cu_seqlens; windows, soft cap and
+    sink_bias as in ragged_flash_attention_fwd (window_right=0 is causal).  Returns
+    (out, lse) in q's shape and [..., Hq]."""
+    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
+                                                    seq_lens)
+    batch = page_table.shape[0]
+    Q, N, hq, q_stride = _token_rows(q, "q", index, d, cu_seqlens, batch)
+    lib = load_library()
+    num_sinks = per_head = 0
+    if sink_bias is not None:
+        if sink_bias.dim() not in (1, 2) or (sink_bias.dim() == 2 and sink_bias.shape[0] != hq):
+            raise ValueError("sink_bias must be [Hq, num_sinks] or [num_sinks]")
+        num_sinks, per_head = sink_bias.shape[-1], int(sink_bias.dim() == 2)
+    out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
+    if workspace is None:
+        workspace = torch.empty(max(16, lib.sba_paged_attention_workspace_size(d)), dtype=torch.uint8,
+                                device=q.device)
+    _call_on(index, lib.sba_paged_attention_fwd, q.data_ptr(), q_stride, *pool,
+             _cu(cu_seqlens, index, batch), batch, Q, N, hq, hkv, d, dtype, softmax_scale or 0.0,
+             window_left, window_right, logits_soft_cap or 0.0,
+             _at(sink_bias, "sink_bias", index, torch.float32) if num_sinks else None, num_sinks,
+             per_head, out_p, lse_p, _at(workspace, "workspace", index),
+             workspace.numel() * workspace.element_size(),
+             torch.cuda.current_stream(index).cuda_stream)
+    return out, lse
+
+
+def nsa_select_paged_fwd(q, k_pages, v_pages, page_table, seq_lens, block_indices, block_counts,
+                         block_size, *, k_scales=None, v_scales=None, causal=True, softmax_scale=None,
+                         g_slc=None, out=None, lse=None, return_lse=True):
+    """Selection-branch NSA of the rows' last tokens over a paged cache: the decode form of
+    nsa_select_fwd.  q bf16 [B, Hq, D] or [B, Q, Hq, D], block_indices int32 [B, (Q,) Hkv, S],
+    block_counts int or int32 [B, (Q,) Hkv], g_slc bf16 [B, (Q,) Hq] or None.  Returns
+    (out, lse)."""
+    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
+                                                    seq_lens)
+    batch = page_table.shape[0]
+    Q, _, hq, q_stride = _token_rows(q, "q", index, d, None, batch)
+    S = block_indices.shape[-1]
+    lead = tuple(q.shape[:-2])
+    idx_p = _at(block_indices, "block_indices", index, torch.int32, lead + (hkv, S))
+    counts = isinstance(block_counts, torch.Tensor)
+    cnt_p = _at(block_counts, "block_counts", index, torch.int32, lead + (hkv,)) if counts else None
+    gate_p = _at(g_slc, "g_slc", index, torch.bfloat16, lead + (hq,))
+    out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
+    _call_on(index, load_library().sba_nsa_select_paged_fwd, q.data_ptr(), q_stride, *pool, batch, Q, hq,
+             hkv, d, dtype, idx_p, cnt_p, 0 if counts else int(block_counts), S, int(block_size),
+             int(bool(causal)), softmax_scale or 0.0, gate_p, out_p, lse_p,
+             torch.cuda.current_stream(index).cuda_stream)
     return out, lse
 
 

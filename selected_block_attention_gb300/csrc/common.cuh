@@ -37,6 +37,9 @@ unsigned read_and_clear_error_mask(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_blocksparse(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_decode(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_nsa_bwd(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_append(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_paged(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_select(cudaStream_t s, std::string* where);
 
 // Launch entry points implemented by the kernel files (arguments already validated).
 int launch_nsa_select(const void* q, const void* k, const void* v, const void* g_slc,
@@ -84,6 +87,20 @@ int launch_nsa_select_bwd(const void* q, const void* k, const void* v, const voi
                           const int32_t* cu_seqlens, int num_seqs, int B, int T, int Hq, int Hkv,
                           int causal, float scale, void* dq, void* dk, void* dv, void* workspace,
                           cudaStream_t stream);
+struct PagedView;  // paged.cuh
+int launch_paged_append(const PagedView& c, int f8, int D, const void* k, long long k_tok,
+                        const void* v, long long v_tok, const void* q, long long q_tok, void* q_out,
+                        long long qo_tok, int Hq, const float* cosp, const float* sinp, int rot,
+                        int max_pos, int interleaved, cudaStream_t stream);
+size_t paged_attention_workspace_bytes(int D);
+int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq,
+                           float scale, int window_left, int window_right, float cap,
+                           const float* sink_bias, int num_sinks, int sink_per_head, void* out,
+                           float* lse, void* workspace, cudaStream_t stream);
+int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq,
+                        const int32_t* idx, const int32_t* cnt, int cnt_scalar, int S, int block_size,
+                        int causal, float scale, const void* gate, void* out, float* lse,
+                        cudaStream_t stream);
 int launch_l2_read_probe(const void* buf, size_t bytes, int reps, unsigned* sink,
                          cudaStream_t stream);
 

@@ -1,0 +1,554 @@
+// One warp's walk over key tiles of a paged cache: 16 query rows, an online softmax.
+//
+// Rows are (query, head) pairs of one KV head, the 16 rows of an m16n8k16 MMA.  A tile is
+// 32 keys (e4m3) or 16 keys (bf16), whole 16-key subtiles of one page each, brought into
+// shared memory with 16-byte cp.async through a ring of kStages tiles per warp.
+//
+// e4m3 operands.  The tensor instruction takes fp16 pairs.  Codes become fp16 exactly
+// (one conversion per pair); the query row is multiplied by a power of two that puts its
+// largest element near 2^14, so its conversion drops only what lies 2^-38 below it; the
+// page's key scale and the query's factor multiply the logit.  A page's value scale
+// s = a 2^e (1 <= a < 2) multiplies the probability: with p = 2^(x - m) the kernel sums
+// l += p in fp32 and feeds p s 2^(m - u + 8) to the MMA, where u is a running maximum of
+// x + e over the keys, so the product stays below 2^15 whatever the pages' scales are, and
+// what rounds to zero in fp16 lies 2^-33 below the largest contribution.  fp16 keeps 11
+// bits of each probability; a bf16 cache uses bf16 probabilities (8 bits) and u = m.
+//
+// Fragments.  The order of the contraction index is free, so the thread that holds
+// elements (2c, 2c+1, 2c+8, 2c+9) of a 16-step takes four neighbouring bytes instead: its
+// part of a key row is 16-byte chunks c and c + 4, its part of a value row is the run of
+// kD / 8 dimensions from (kD / 8) g on, for the four keys that its probabilities belong
+// to; two byte permutes per word put a pair of keys next to each other.  Output column n
+// of MMA j is dimension (kD / 8) n + j.  Chunks are stored at chunk ^ f(row), which
+// spreads both reads over all banks (f below).
+#pragma once
+
+#include <climits>
+
+#include "paged.cuh"
+
+namespace sba {
+
+constexpr float kPagedLog2e = 1.4426950408889634f;
+constexpr float kPagedLn2 = 0.6931471805599453f;
+constexpr int kPagedWarps = 4;
+constexpr int kPagedStages = 2;
+
+__device__ __forceinline__ void paged_cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void paged_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void paged_cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 paged_lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 paged_lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+template <bool kHalf>
+__device__ __forceinline__ void paged_mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What the 16 rows may see and how their logits are formed.
+struct PagedMask {
+  int len;         // keys < len exist
+  int wlo0, whi0;  // window of the thread's row g
+  int wlo1, whi1;  // window of row g + 8
+  int all_lo, all_hi;  // the part of the window that every row shares
+  int num_sinks;       // keys < num_sinks are always visible
+  const float* bias0;  // their biases, rows g and g + 8
+  const float* bias1;
+};
+
+template <bool kF8, int kD, bool kHi, bool kCap>
+struct PagedWarp {
+  static constexpr int kKeys = kF8 ? 32 : 16;
+  static constexpr int kSub = kKeys / 16;
+  static constexpr int kRowBytes = kD * (kF8 ? 1 : 2);
+  static constexpr int kTileBytes = kKeys * kRowBytes;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kWarpBytes = kPagedStages * kStageBytes;
+  static constexpr int kChunks = kRowBytes / 16;   // 16-byte chunks per row
+  static constexpr int kStep = 32 / kChunks;       // rows per warp-wide copy
+  static constexpr int kCopies = kKeys / kStep;
+  static constexpr int kNT = kD / 8;               // output columns / 8
+  static constexpr int kKS = kD / 16;              // contraction steps of Q K^T
+  static constexpr int kSmemRow = kD + 8;          // merge buffer row, floats
+  static constexpr float kRaise = 8.f;             // m moves when a tile exceeds it by 2^8
+
+  uint32_t qa[kKS][4];
+  float o[kNT][4];
+  float m0, m1, l0, l1;
+  float u0, u1;    // e4m3: reference of the values' probabilities
+  float r0, r1;    // logit factors of rows g, g + 8
+  float c1k, cap2; // cap: log2(e) cap, and 1 / cap
+  int lane, g, c;
+  uint32_t ring;
+  const uint8_t* kbase;
+  const uint8_t* vbase;
+  const float* ks;
+  const float* vs;
+  const int* table;
+  long long page_bytes;
+  int p_shift, Hkv, num_pages;
+  unsigned* err;
+
+  // Byte offset of 16-byte chunk `ch` of row `row` inside a tile.
+  static __device__ __forceinline__ uint32_t at(int row, int ch) {
+    if constexpr (!kF8) return row * kRowBytes + ((ch ^ (row & 7)) << 4);
+    if constexpr (kF8 && kD == 128) {
+      const int f = (((row >> 1) & 3) << 1) ^ ((row & 1) << 2);
+      return row * 128 + ((ch ^ f) << 4);
+    }
+    const int line = row >> 1;
+    return line * 128 + (((((row & 1) << 2) + ch) ^ ((line & 3) << 1)) << 4);
+  }
+
+  __device__ __forceinline__ void init(const PagedView& v, int b, int h, uint32_t smem_ring, float scale,
+                                       float cap, unsigned* e) {
+    lane = threadIdx.x & 31;
+    g = lane >> 2;
+    c = lane & 3;
+    ring = smem_ring;
+    p_shift = v.p_shift;
+    Hkv = v.Hkv;
+    num_pages = v.num_pages;
+    page_bytes = v.page_bytes;
+    const long long head = ((long long)h << p_shift) * kRowBytes;
+    kbase = v.k + head;
+    vbase = v.v + head;
+    ks = kF8 ? v.ks + h : nullptr;
+    vs = kF8 ? v.vs + h : nullptr;
+    table = v.table + (long long)b * v.width;
+    err = e;
+#pragma unroll
+    for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = u0 = u1 = -INFINITY;
+    l0 = l1 = 0.f;
+    r0 = r1 = kCap ? scale : scale * kPagedLog2e;
+    c1k = cap * kPagedLog2e;
+    cap2 = kCap ? 1.f / cap : 0.f;
+  }
+
+  // Query rows g and g + 8 (null: a row of zeros).
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* q0, const __nv_bfloat16* q1) {
+    if constexpr (!kF8) {
+#pragma unroll
+      for (int s = 0; s < kKS; ++s) {
+        const int d = s * 16 + 2 * c;
+        qa[s][0] = q0 ? __ldg(reinterpret_cast<const unsigned*>(q0 + d)) : 0u;
+        qa[s][2] = q0 ? __ldg(reinterpret_cast<const unsigned*>(q0 + d + 8)) : 0u;
+        qa[s][1] = kHi && q1 ? __ldg(reinterpret_cast<const unsigned*>(q1 + d)) : 0u;
+        qa[s][3] = kHi && q1 ? __ldg(reinterpret_cast<const unsigned*>(q1 + d + 8)) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int hi = 0; hi < (kHi ? 2 : 1); ++hi) {
+        const __nv_bfloat16* q = hi ? q1 : q0;
+        uint2 w[kKS];
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < kKS; ++s) {
+          const int d = 16 * (c + 4 * (s >> 2)) + 4 * (s & 3);
+          w[s] = q ? __ldg(reinterpret_cast<const uint2*>(q + d)) : make_uint2(0u, 0u);
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(w[s].x)), fabsf(bf16_hi(w[s].x))),
+                                 fmaxf(fabsf(bf16_lo(w[s].y)), fabsf(bf16_hi(w[s].y)))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // power of two f with top f in [2^14, 2^15); 1 for zero and non-finite rows.  Both
+        // f and 1 / f stay normal numbers.
+        const int ex = (int)((__float_as_uint(top) >> 23) & 255);
+        const int fe = (ex == 0 || ex == 255) ? 127 : min(127 + 14 - (ex - 127), 253);
+        const float f = __uint_as_float((uint32_t)fe << 23);
+        const float inv = __uint_as_float((uint32_t)(254 - fe) << 23);
+        if (hi) r1 *= inv; else r0 *= inv;
+#pragma unroll
+        for (int s = 0; s < kKS; ++s) {
+          qa[s][hi] = pack_f16x2(bf16_lo(w[s].x) * f, bf16_hi(w[s].x) * f);
+          qa[s][hi + 2] = pack_f16x2(bf16_lo(w[s].y) * f, bf16_hi(w[s].y) * f);
+        }
+      }
+      if constexpr (!kHi) {
+#pragma unroll
+        for (int s = 0; s < kKS; ++s) qa[s][1] = qa[s][3] = 0u;
+      }
+    }
+  }
+
+  struct Pages { int page[kSub]; };
+  struct Scales { float k[kSub], v[kSub]; };
+
+  // Page numbers of the tile's subtiles; keys are clamped into [cl, ch].
+  __device__ __forceinline__ Pages fetch(int key0, int cl, int ch) const {
+    Pages p;
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      const int key = min(max(key0 + 16 * s, cl), ch);
+      p.page[s] = __ldg(table + (key >> p_shift));
+    }
+    return p;
+  }
+  __device__ __forceinline__ void check(Pages& p) const {
+#pragma unroll
+    for (int s = 0; s < kSub; ++s)
+      if ((unsigned)p.page[s] >= (unsigned)num_pages) {
+        if (lane == 0) atomicOr(err, (unsigned)kDevErrInput);
+        p.page[s] = 0;  // any page that exists: the row's result is undefined, the read is not
+      }
+  }
+  __device__ __forceinline__ Scales scales(const Pages& p) const {
+    Scales s;
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      s.k[i] = kF8 ? __ldg(ks + (long long)p.page[i] * Hkv) : 1.f;
+      s.v[i] = kF8 ? __ldg(vs + (long long)p.page[i] * Hkv) : 1.f;
+    }
+    return s;
+  }
+  // Starts the copies of the tile at key0.  Keys outside [cl, ch] repeat its ends: slots
+  // that the row does not own may hold anything, and 0 * NaN would reach the output.
+  __device__ __forceinline__ void issue(int key0, int cl, int ch, const Pages& p, int stage) const {
+    const uint32_t kd = ring + stage * kStageBytes, vd = kd + kTileBytes;
+    const int chunk = lane % kChunks, row0 = lane / kChunks;
+    const int pmask = (1 << p_shift) - 1;
+    const bool inside = key0 >= cl && key0 + kKeys - 1 <= ch;
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      const long long page_off = p.page[s] * page_bytes + chunk * 16;
+      const uint8_t* kp = kbase + page_off;
+      const uint8_t* vp = vbase + page_off;
+#pragma unroll
+      for (int i = 0; i < kCopies / kSub; ++i) {
+        const int row = 16 * s + row0 + i * kStep;
+        int key = key0 + row;
+        if (!inside) key = min(max(key, cl), ch);
+        const int src = (key & pmask) * kRowBytes;
+        paged_cp16(kd + at(row, chunk), kp + src);
+        paged_cp16(vd + at(row, chunk), vp + src);
+      }
+    }
+  }
+
+  __device__ __forceinline__ float logit(float x, float f) const {
+    if constexpr (!kCap) {
+      return x * f;
+    } else {
+      // log2(e) cap tanh(y), y = x f / cap.  Near zero the odd series (its next term is
+      // below 2^-28 of the sum at |y| = 0.25), elsewhere 1 - 2 / (1 + e^(2y)).
+      const float y = x * f * cap2;
+      const float e = ptx::ex2(y * (2.f * kPagedLog2e));
+      float rc;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
+      const float far = fmaf(-2.f, rc, 1.f);
+      const float y2 = y * y;
+      float pl = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
+      pl = fmaf(y2, pl, 2.f / 15.f);
+      pl = fmaf(y2, pl, -1.f / 3.f);
+      const float near = fmaf(y * y2, pl, y);
+      return c1k * (fabsf(y) < 0.25f ? near : far);
+    }
+  }
+
+  // Scores of the tile in `stage` into the softmax, its values into o.
+  __device__ __forceinline__ void consume(int key0, const Scales& sl, int stage, const PagedMask& mk) {
+    const uint32_t kt = ring + stage * kStageBytes, vt = kt + kTileBytes;
+    float sc[kSub][2][4];
+#pragma unroll
+    for (int s = 0; s < kSub; ++s)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) sc[s][n][0] = sc[s][n][1] = sc[s][n][2] = sc[s][n][3] = 0.f;
+    if constexpr (kF8) {
+#pragma unroll
+      for (int s = 0; s < kSub; ++s)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int row = 16 * s + 8 * n + g;
+#pragma unroll
+          for (int i = 0; i < kKS / 4; ++i) {
+            const uint4 w = paged_lds16(kt + at(row, c + 4 * i));
+            uint32_t b0, b1;
+            e4m3x4_to_f16x2(w.x, b0, b1);
+            paged_mma<true>(sc[s][n], qa[4 * i], b0, b1);
+            e4m3x4_to_f16x2(w.y, b0, b1);
+            paged_mma<true>(sc[s][n], qa[4 * i + 1], b0, b1);
+            e4m3x4_to_f16x2(w.z, b0, b1);
+            paged_mma<true>(sc[s][n], qa[4 * i + 2], b0, b1);
+            e4m3x4_to_f16x2(w.w, b0, b1);
+            paged_mma<true>(sc[s][n], qa[4 * i + 3], b0, b1);
+          }
+        }
+    } else {
+      const int mi = lane >> 3, ri = lane & 7;
+      const int row = (mi >> 1) * 8 + ri;
+#pragma unroll
+      for (int s = 0; s < kKS; ++s) {
+        uint32_t b00, b01, b10, b11;
+        ptx::ldsm_x4(kt + at(row, 2 * s + (mi & 1)), b00, b01, b10, b11);
+        paged_mma<false>(sc[0][0], qa[s], b00, b01);
+        paged_mma<false>(sc[0][1], qa[s], b10, b11);
+      }
+    }
+
+    // ---- logits (log2 units), masks, maxima
+    float t0 = -INFINITY, t1 = -INFINITY;  // tile maxima of rows g, g + 8
+    float d0 = -INFINITY, d1 = -INFINITY;  // e4m3: maxima of logit + value exponent
+    float mant[kSub], expo[kSub];
+    const bool plain = key0 >= mk.num_sinks && key0 >= mk.all_lo && key0 + kKeys - 1 <= mk.all_hi &&
+                       key0 + kKeys <= mk.len;
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      const float f0 = kF8 ? r0 * sl.k[s] : r0, f1 = kF8 ? r1 * sl.k[s] : r1;
+      float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x0 = logit(sc[s][n][e], f0);
+          float x1 = kHi ? logit(sc[s][n][2 + e], f1) : -INFINITY;
+          if (!plain) {
+            const int key = key0 + 16 * s + 8 * n + 2 * c + e;
+            const bool sink = key < mk.num_sinks;
+            if (sink) {
+              x0 = fmaf(mk.bias0[key], kPagedLog2e, x0);
+              if constexpr (kHi) x1 = fmaf(mk.bias1[key], kPagedLog2e, x1);
+            }
+            const bool here = key < mk.len;
+            x0 = here && ((key >= mk.wlo0 && key <= mk.whi0) || sink) ? x0 : -INFINITY;
+            if constexpr (kHi) x1 = here && ((key >= mk.wlo1 && key <= mk.whi1) || sink) ? x1 : -INFINITY;
+          }
+          sc[s][n][e] = x0;
+          a0 = fmaxf(a0, x0);
+          if constexpr (kHi) {
+            sc[s][n][2 + e] = x1;
+            a1 = fmaxf(a1, x1);
+          }
+        }
+      t0 = fmaxf(t0, a0);
+      t1 = fmaxf(t1, a1);
+      if constexpr (kF8) {
+        // value scale = mant 2^expo (0 for a zero or subnormal one)
+        const uint32_t bits = __float_as_uint(sl.v[s]);
+        const uint32_t field = (bits >> 23) & 255u;
+        expo[s] = (float)((int)field - 127);
+        mant[s] = field == 0 ? 0.f : __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
+        d0 = fmaxf(d0, a0 + expo[s]);
+        d1 = fmaxf(d1, a1 + expo[s]);
+      }
+    }
+    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+    if constexpr (kHi) {
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+    }
+    if constexpr (kF8) {
+      d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, 1));
+      d0 = fmaxf(d0, __shfl_xor_sync(0xffffffffu, d0, 2));
+      if constexpr (kHi) {
+        d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, 1));
+        d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, 2));
+      }
+    }
+    // ---- references: moved only when a tile passes them clearly
+    auto raise = [](float& ref, float top, float slack) -> float {
+      const bool move = top > ref + slack || (ref == -INFINITY && top != -INFINITY);
+      const float now = move ? top : ref;
+      const float alpha = (move && ref != -INFINITY) ? ptx::ex2(ref - now) : 1.f;
+      ref = now;
+      return alpha;
+    };
+    const float am0 = raise(m0, t0, kRaise), am1 = kHi ? raise(m1, t1, kRaise) : 1.f;
+    l0 *= am0;
+    l1 *= am1;
+    float ao0, ao1;
+    if constexpr (kF8) {
+      ao0 = raise(u0, d0, 6.f);
+      ao1 = kHi ? raise(u1, d1, 6.f) : 1.f;
+    } else {
+      ao0 = am0;
+      ao1 = am1;
+    }
+    if (__any_sync(0xffffffffu, ao0 != 1.f || ao1 != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < kNT; ++i) {
+        o[i][0] *= ao0; o[i][1] *= ao0;
+        if constexpr (kHi) { o[i][2] *= ao1; o[i][3] *= ao1; }
+      }
+    }
+    const float mm0 = m0 == -INFINITY ? 0.f : m0, mm1 = m1 == -INFINITY ? 0.f : m1;
+    uint32_t pa[kSub][4];
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+      float w0 = 1.f, w1 = 1.f;
+      if constexpr (kF8) {
+        // The exponent's limit only bites for keys whose weight is below 2^-110.
+        w0 = m0 == -INFINITY ? 0.f : mant[s] * ptx::ex2(fminf(expo[s] + m0 - u0 + 8.f, 126.f));
+        w1 = m1 == -INFINITY ? 0.f : mant[s] * ptx::ex2(fminf(expo[s] + m1 - u1 + 8.f, 126.f));
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float p00 = ptx::ex2(sc[s][n][0] - mm0), p01 = ptx::ex2(sc[s][n][1] - mm0);
+        l0 += p00 + p01;
+        pa[s][2 * n] = kF8 ? pack_f16x2(p00 * w0, p01 * w0) : pack_bf16x2(p00, p01);
+        if constexpr (kHi) {
+          const float p10 = ptx::ex2(sc[s][n][2] - mm1), p11 = ptx::ex2(sc[s][n][3] - mm1);
+          l1 += p10 + p11;
+          pa[s][2 * n + 1] = kF8 ? pack_f16x2(p10 * w1, p11 * w1) : pack_bf16x2(p10, p11);
+        } else {
+          pa[s][2 * n + 1] = 0u;
+        }
+      }
+    }
+    // ---- values
+    if constexpr (kF8) {
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) {
+        const int k0 = 16 * s + 2 * c;
+        constexpr int kWords = kD / 32;  // words of a thread's run of kD / 8 bytes
+        uint32_t w[4][kWords];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = k0 + (i & 1) + (i >> 1) * 8;
+          if constexpr (kD == 128) {
+            const uint4 v = paged_lds16(vt + at(row, g));
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+          } else {
+            const uint2 v = paged_lds8(vt + at(row, g >> 1) + (g & 1) * 8);
+            w[i][0] = v.x; w[i][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          uint32_t b0, b1, b2, b3;
+          e4m3x4_to_f16x2(__byte_perm(w[0][j], w[1][j], 0x5140), b0, b2);
+          e4m3x4_to_f16x2(__byte_perm(w[2][j], w[3][j], 0x5140), b1, b3);
+          paged_mma<true>(o[4 * j], pa[s], b0, b1);
+          paged_mma<true>(o[4 * j + 1], pa[s], b2, b3);
+          e4m3x4_to_f16x2(__byte_perm(w[0][j], w[1][j], 0x7362), b0, b2);
+          e4m3x4_to_f16x2(__byte_perm(w[2][j], w[3][j], 0x7362), b1, b3);
+          paged_mma<true>(o[4 * j + 2], pa[s], b0, b1);
+          paged_mma<true>(o[4 * j + 3], pa[s], b2, b3);
+        }
+      }
+    } else {
+      const int mi = lane >> 3, ri = lane & 7;
+      const int row = (mi & 1) * 8 + ri;
+#pragma unroll
+      for (int dn = 0; dn < kNT; dn += 2) {
+        uint32_t b00, b01, b10, b11;
+        ptx::ldsm_x4_t(vt + at(row, dn + (mi >> 1)), b00, b01, b10, b11);
+        paged_mma<false>(o[dn], pa[0], b00, b01);
+        paged_mma<false>(o[dn + 1], pa[0], b10, b11);
+      }
+    }
+  }
+
+  // Tiles first, first + step, ... below count; key_of(t) is tile t's first key and
+  // lim_of(t, cl, ch) the keys that may be read for it.
+  template <class KeyOf, class LimOf>
+  __device__ __forceinline__ void walk(int first, int step, int count, KeyOf key_of, LimOf lim_of,
+                                       const PagedMask& mk) {
+    if (first >= count) return;
+    int cl, ch;
+    int key = key_of(first);
+    lim_of(first, cl, ch);
+    Pages pg = fetch(key, cl, ch);
+    check(pg);
+    issue(key, cl, ch, pg, 0);
+    paged_cp_commit();
+    Scales sl = scales(pg);
+    int nkey = 0, ncl = 0, nch = 0;
+    if (first + step < count) {
+      nkey = key_of(first + step);
+      lim_of(first + step, ncl, nch);
+      pg = fetch(nkey, ncl, nch);
+    }
+    int stage = 0;
+    for (int t = first; t < count; t += step) {
+      Scales sn = sl;
+      const int this_key = key;
+      if (t + step < count) {
+        check(pg);
+        issue(nkey, ncl, nch, pg, stage ^ 1);
+        sn = scales(pg);
+        key = nkey;
+        if (t + 2 * step < count) {
+          nkey = key_of(t + 2 * step);
+          lim_of(t + 2 * step, ncl, nch);
+          pg = fetch(nkey, ncl, nch);
+        }
+      }
+      paged_cp_commit();
+      paged_cp_wait<1>();
+      __syncwarp();
+      consume(this_key, sl, stage, mk);
+      __syncwarp();
+      stage ^= 1;
+      sl = sn;
+    }
+    paged_cp_wait<0>();
+  }
+
+  // Dimension of merge-buffer position `pos`.
+  static __device__ __forceinline__ int dim_of(int pos) {
+    return kF8 ? kNT * (pos & 7) + (pos >> 3) : pos;
+  }
+
+  // The warp's state into the merge buffer: o rows at so[(warp * 16 + row) * kSmemRow +
+  // 8 j + n], (max, sum, exponent that multiplies o) at sm[(warp * 16 + row) * 3].
+  __device__ __forceinline__ void park(float* so, float* sm, int warp) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    float* a = so + (warp * 16 + g) * kSmemRow + 2 * c;
+#pragma unroll
+    for (int j = 0; j < kNT; ++j) {
+      *reinterpret_cast<float2*>(a + 8 * j) = make_float2(o[j][0], o[j][1]);
+      if constexpr (kHi)
+        *reinterpret_cast<float2*>(a + 8 * kSmemRow + 8 * j) = make_float2(o[j][2], o[j][3]);
+    }
+    if (c == 0) {
+      float* s = sm + (warp * 16 + g) * 3;
+      s[0] = m0; s[1] = l0; s[2] = kF8 ? u0 - 8.f : m0;
+      if constexpr (kHi) { s[24] = m1; s[25] = l1; s[26] = kF8 ? u1 - 8.f : m1; }
+    }
+  }
+};
+
+// Merge of the CTA's warps for row r: the common max, the sum, and each warp's weight.
+__device__ __forceinline__ void paged_merge_row(const float* sm, int r, float& M, float& L, float* w) {
+  M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPagedWarps; ++i) M = fmaxf(M, sm[(i * 16 + r) * 3]);
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPagedWarps; ++i) {
+    const float* s = sm + (i * 16 + r) * 3;
+    const bool some = s[1] != 0.f;  // a NaN sum has to reach the output
+    w[i] = some ? ptx::ex2(s[2] - M) : 0.f;
+    L += some ? ptx::ex2(s[0] - M) * s[1] : 0.f;
+  }
+}
+
+}  // namespace sba
