@@ -426,23 +426,10 @@ SBA_API int sba_ragged_flash_attention_fwd(const void* q, const void* k, const v
  * ---------------
  * A cache is a pool of pages for keys and one for values, and a table that names each
  * row's pages.  No counterpart on the pages that define the attention operations above:
- * these entry points give those operations' decode forms the storage a server keeps.
+ * these entry points give those operations' decode forms the storage a server keeps.  The
+ * cache and the call's rows are described by one struct, and each call's arguments by
+ * another that begins with it.
  *
- *  k_pages, v_pages  [num_pages, Hkv, page_size, D], SBA_BF16 or SBA_E4M3; a page is
- *                dense, pages lie page_stride elements apart (so both pools may be halves
- *                of one [num_pages, 2, Hkv, page_size, D] array); 16-byte aligned, page_stride
- *                a multiple of 16 bytes
- *  k_scales, v_scales  [num_pages, Hkv] float32, one positive normal number for each page
- *                and head of an SBA_E4M3 cache (value = code * scale); NULL for SBA_BF16
- *  page_table    [B, table_width] int32: page j of row b holds positions
- *                [j * page_size, (j + 1) * page_size).  Entries of pages that a call does
- *                not touch are not read.
- *  seq_lens      [B] int32: length of each row, the call's own tokens included.  0: no
- *                sequence.
- *  cu_seqlens    [B + 1] int32: row b has tokens [cu_seqlens[b], cu_seqlens[b + 1]) of the
- *                call's N token rows (0 <= ... <= N, not decreasing); token rows from
- *                cu_seqlens[B] on belong to nobody and are neither read nor written.  NULL:
- *                every row has Q tokens and N = B * Q.
  * The tokens of a row are its last ones: token i of n sits at position seq_len - n + i (a
  * row without a sequence, seq_len 0, has its tokens at negative positions).
  * A length outside [0, table_width * page_size], a page number outside [0, num_pages) or a
@@ -452,21 +439,37 @@ SBA_API int sba_ragged_flash_attention_fwd(const void* q, const void* k, const v
  * Limits: D in {64, 128}, page_size in {16, 32, 64, 128}, table_width * page_size <= 2^30,
  * B <= 2^24, N <= 2^28.
  */
+typedef struct sba_paged_cache {
+  /* [num_pages, Hkv, page_size, D], SBA_BF16 or SBA_E4M3; a page is dense, pages lie
+   * page_stride elements apart (so both pools may be halves of one [num_pages, 2, Hkv,
+   * page_size, D] array); 16-byte aligned, page_stride a multiple of 16 bytes */
+  void* k_pages;
+  void* v_pages;
+  /* [num_pages, Hkv], one positive normal number for each page and head of an SBA_E4M3
+   * cache (value = code * scale); NULL for SBA_BF16 */
+  float* k_scales;
+  float* v_scales;
+  /* [B, table_width]: page j of row b holds positions [j * page_size, (j + 1) * page_size).
+   * Entries of pages that a call does not touch are not read. */
+  const int32_t* page_table;
+  /* [B] length of each row, the call's own tokens included; 0: no sequence */
+  const int32_t* seq_lens;
+  /* [B + 1]: row b has tokens [cu_seqlens[b], cu_seqlens[b + 1]) of the call's N token rows
+   * (0 <= ... <= N, not decreasing); token rows from cu_seqlens[B] on belong to nobody and
+   * are neither read nor written.  NULL: every row has Q tokens and N = B * Q. */
+  const int32_t* cu_seqlens;
+  long long page_stride;
+  int num_pages, page_size, Hkv, D, dtype, table_width, B, Q, N;
+} sba_paged_cache;
 
 /*
  * sba_paged_kv_append -- write a call's keys and values into a paged cache, keys (and
  * queries) rotated by their positions.
  *
- *  k, v          [N, Hkv, D] bf16, tokens k_stride / v_stride elements apart (heads dense
- *                inside a token, strides multiples of 8), e.g. parts of one projection's
- *                output
- *  q, q_out      [N, Hq, D] bf16 with their own strides, or both NULL: rotated queries;
- *                q_out may be q
- *  cos, sin      [max_pos, rot_dim / 2] float32 tables, or both NULL for no rotation.  The
- *                first rot_dim dimensions (a multiple of 16) of each key and query head
- *                turn in pairs (x0, x1) -> (x0 c - x1 s, x1 c + x0 s), computed in fp32:
- *                pair i is dimensions (i, i + rot_dim / 2), or with `interleaved`
- *                (2 i, 2 i + 1).  Positions >= max_pos are reported as malformed input.
+ * With cos and sin the first rot_dim dimensions (a multiple of 16) of each key and query
+ * head turn in pairs (x0, x1) -> (x0 c - x1 s, x1 c + x0 s), computed in fp32: pair i is
+ * dimensions (i, i + rot_dim / 2), or with `interleaved` (2 i, 2 i + 1).  Positions >=
+ * max_pos are reported as malformed input.
  * An SBA_E4M3 cache gets power-of-two scales.  For each page and head that the call
  * writes: need = the least 2^e (e >= -126) with 448 * 2^e >= the call's largest finite
  * magnitude there; the scale becomes need if the call writes the page's first slot, else
@@ -477,16 +480,18 @@ SBA_API int sba_ragged_flash_attention_fwd(const void* q, const void* k, const v
  * Two rows that write the same page in one call race on it (rows may share pages that
  * they only read).  The call has no workspace and is one launch.
  */
-SBA_API int sba_paged_kv_append(const void* k, long long k_stride, const void* v,
-                                long long v_stride, const void* q, long long q_stride, void* q_out,
-                                long long q_out_stride, const float* cos, const float* sin,
-                                int rot_dim, int max_pos, int interleaved, void* k_pages,
-                                void* v_pages, float* k_scales, float* v_scales,
-                                long long page_stride, int num_pages, int page_size,
-                                const int32_t* page_table, int table_width,
-                                const int32_t* seq_lens, const int32_t* cu_seqlens, int B, int Q,
-                                int N, int Hq, int Hkv, int D, int cache_dtype,
-                                sba_stream_t stream);
+typedef struct sba_paged_append_args {
+  sba_paged_cache cache;
+  const void* k; /* [N, Hkv, D] bf16, tokens k_stride elements apart (heads dense inside a */
+  const void* v; /* token, strides multiples of 8), e.g. parts of one projection's output  */
+  const void* q; /* [N, Hq, D] bf16, or NULL (with q_out): queries to rotate               */
+  void* q_out;   /* [N, Hq, D] bf16, may be q                                              */
+  const float* cos; /* [max_pos, rot_dim / 2], or both NULL for no rotation                */
+  const float* sin;
+  long long k_stride, v_stride, q_stride, q_out_stride;
+  int Hq, rot_dim, max_pos, interleaved;
+} sba_paged_append_args;
+SBA_API int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream);
 
 /*
  * sba_paged_attention_workspace_size -- bytes of device workspace sba_paged_attention_fwd
@@ -504,56 +509,59 @@ SBA_API size_t sba_paged_attention_workspace_size(int D);
  * is causal) or k < num_sinks.  Logit = scale * <q, k>, then cap * tanh(logit / cap) when
  * cap > 0, then + sink bias for sink keys.  A query with no visible key gets output 0 and
  * LSE -inf.
- *
- *  q             [N, Hq, D] bf16, tokens q_stride elements apart (heads dense, a multiple
- *                of 8); Hq % Hkv == 0, query head hq reads KV head hq / (Hq / Hkv)
- *  sink_bias     float32 [Hq, num_sinks] (sink_bias_per_head != 0) or [num_sinks]; NULL
- *                with num_sinks == 0 for none.  num_sinks <= 16.
- *  out           [N, Hq, D] bf16 (written); lse [N, Hq] float32 (written) or NULL
- *  workspace     device scratch of at least sba_paged_attention_workspace_size(D) bytes,
- *                16-byte aligned, caller-owned; needs no initialisation.  Calls that may
- *                overlap on the GPU need one each.
  * Pages wholly left of every query's window, but for the sinks', are not read, so a server
  * may give them back.  The grid does not depend on the lengths, which the kernel reads on
  * the device: a captured call serves whatever seq_lens holds when it is replayed.
- * Results do not depend on timing.  Internally, on `stream`: a small kernel that clears
- * counters in the workspace and the attention kernel.
+ * Results do not depend on timing.  Internally, on `stream`: the attention kernel and a
+ * kernel that merges the items it cut into runs.
  */
-SBA_API int sba_paged_attention_fwd(const void* q, long long q_stride, const void* k_pages,
-                                    const void* v_pages, const float* k_scales, const float* v_scales,
-                                    long long page_stride, int num_pages, int page_size,
-                                    const int32_t* page_table, int table_width,
-                                    const int32_t* seq_lens, const int32_t* cu_seqlens, int B,
-                                    int Q, int N, int Hq, int Hkv, int D, int cache_dtype,
-                                    float softmax_scale, int window_left, int window_right,
-                                    float logits_soft_cap, const float* sink_bias, int num_sinks,
-                                    int sink_bias_per_head, void* out, float* lse,
-                                    void* workspace, size_t workspace_bytes, sba_stream_t stream);
+typedef struct sba_paged_attention_args {
+  sba_paged_cache cache; /* read only */
+  const void* q;          /* [N, Hq, D] bf16, tokens q_stride elements apart (heads dense, a
+                             multiple of 8); Hq % Hkv == 0, query head hq reads KV head
+                             hq / (Hq / Hkv) */
+  const float* sink_bias; /* [Hq, num_sinks] (sink_bias_per_head != 0) or [num_sinks]; NULL
+                             with num_sinks == 0 for none.  num_sinks <= 16. */
+  void* out;              /* [N, Hq, D] bf16 (written) */
+  float* lse;             /* [N, Hq] (written) or NULL */
+  void* workspace;        /* device scratch, 16-byte aligned, caller-owned, of at least
+                             sba_paged_attention_workspace_size(D) bytes; needs no
+                             initialisation.  Calls that may overlap on the GPU need one
+                             each. */
+  size_t workspace_bytes;
+  long long q_stride;
+  int Hq;
+  float softmax_scale;
+  int window_left, window_right;
+  float logits_soft_cap;
+  int num_sinks, sink_bias_per_head;
+} sba_paged_attention_args;
+SBA_API int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_stream_t stream);
 
 /*
  * sba_nsa_select_paged_fwd -- the decode form of sba_nsa_select_fwd: selected-block
- * attention of each row's last Q tokens over a paged cache.
+ * attention of each row's last Q tokens over a paged cache (cu_seqlens must be NULL).
  *
- *  q             [B, Q, Hq, D] bf16, tokens q_stride elements apart; Hq / Hkv <= 16
- *  block_indices [B, Q, Hkv, S] int32, block_counts [B, Q, Hkv] int32 or NULL for
- *                block_count_scalar, g_slc [B, Q, Hq] bf16 or NULL: as in
- *                sba_nsa_select_fwd, block ids relative to the row's sequence
- *  block_size    32, 64 or 128, independent of page_size; S <= 32
- *  causal        nonzero: the token at position p sees keys <= p
- *  out           [B, Q, Hq, D] bf16 (written); lse [B, Q, Hq] float32 (written) or NULL
- * A token without a visible key (also one left of position 0, when seq_len < Q) gets output
- * 0 and LSE -inf.  One launch, no workspace.
+ * Block ids are relative to the row's sequence; causal: the token at position p sees keys
+ * <= p.  A token without a visible key (also one left of position 0, when seq_len < Q)
+ * gets output 0 and LSE -inf.  One launch, no workspace.
  */
-SBA_API int sba_nsa_select_paged_fwd(const void* q, long long q_stride, const void* k_pages,
-                                     const void* v_pages, const float* k_scales, const float* v_scales,
-                                     long long page_stride, int num_pages, int page_size,
-                                     const int32_t* page_table, int table_width,
-                                     const int32_t* seq_lens, int B, int Q, int Hq, int Hkv, int D,
-                                     int cache_dtype, const int32_t* block_indices,
-                                     const int32_t* block_counts, int block_count_scalar, int S,
-                                     int block_size, int causal, float softmax_scale,
-                                     const void* g_slc, void* out, float* lse,
-                                     sba_stream_t stream);
+typedef struct sba_nsa_select_paged_args {
+  sba_paged_cache cache;         /* read only */
+  const void* q;                 /* [B, Q, Hq, D] bf16, tokens q_stride elements apart */
+  const int32_t* block_indices;  /* [B, Q, Hkv, S]: as in sba_nsa_select_fwd */
+  const int32_t* block_counts;   /* [B, Q, Hkv], or NULL for block_count_scalar */
+  const void* g_slc;             /* [B, Q, Hq] bf16, or NULL */
+  void* out;                     /* [B, Q, Hq, D] bf16 (written) */
+  float* lse;                    /* [B, Q, Hq] (written) or NULL */
+  long long q_stride;
+  int Hq;                        /* Hq / Hkv <= 16 */
+  int block_count_scalar, S;     /* S <= 32 */
+  int block_size;                /* 32, 64 or 128, independent of page_size */
+  int causal;
+  float softmax_scale;
+} sba_nsa_select_paged_args;
+SBA_API int sba_nsa_select_paged_fwd(const sba_nsa_select_paged_args* args, sba_stream_t stream);
 
 /*
  * sba_l2_read_probe -- measurement helper for the roofline's L2 term; computes nothing

@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -120,21 +121,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sba_nsa_select_bwd.argtypes = [vp, vp, vp, vp, f32p, vp, i32p, i32p, ci, ci, i32p, ci, ci, ci,
                                        ci, ci, ci, ci, ci, cf, ci, vp, vp, vp, vp, csz, vp]
     lib.sba_nsa_select_bwd.restype = ci
-    cll = ctypes.c_longlong
-    lib.sba_paged_kv_append.argtypes = [vp, cll, vp, cll, vp, cll, vp, cll, f32p, f32p, ci, ci, ci, vp,
-                                        vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p, i32p, ci, ci, ci,
-                                        ci, ci, ci, ci, vp]
-    lib.sba_paged_kv_append.restype = ci
     lib.sba_paged_attention_workspace_size.argtypes = [ci]
     lib.sba_paged_attention_workspace_size.restype = csz
-    lib.sba_paged_attention_fwd.argtypes = [vp, cll, vp, vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p,
-                                            i32p, ci, ci, ci, ci, ci, ci, ci, cf, ci, ci, cf, f32p, ci,
-                                            ci, vp, f32p, vp, csz, vp]
-    lib.sba_paged_attention_fwd.restype = ci
-    lib.sba_nsa_select_paged_fwd.argtypes = [vp, cll, vp, vp, f32p, f32p, cll, ci, ci, i32p, ci, i32p,
-                                             ci, ci, ci, ci, ci, ci, i32p, i32p, ci, ci, ci, ci, cf,
-                                             vp, vp, f32p, vp]
-    lib.sba_nsa_select_paged_fwd.restype = ci
+    for fn in (lib.sba_paged_kv_append, lib.sba_paged_attention_fwd, lib.sba_nsa_select_paged_fwd):
+        fn.argtypes = [ctypes.c_char_p, vp]  # the packed argument struct, the stream
+        fn.restype = ci
     lib.sba_set_wait_timeout_cycles.argtypes = [ctypes.c_longlong]
     lib.sba_set_wait_timeout_cycles.restype = ci
     lib.sba_get_wait_timeout_cycles.argtypes = []
@@ -477,84 +468,90 @@ def ragged_flash_attention_fwd(q, k, v, sequence_start, sequence_end, *, softmax
 
 
 # ---------------------------------------------------------------- paged caches
-def _call_on(index, fn, *args):
-    """_call with tensors' device index; most calls find their device current already."""
+# A decode step makes these calls once per layer on small batches, so their host time
+# counts: arguments travel as one packed struct (32 ctypes arguments take 5 us, packing
+# them 0.3 us), and every tensor attribute is read once.
+_CACHE = "7Pq9i"  # sba_paged_cache
+_APPEND_ARGS = struct.Struct("@" + _CACHE + "6P4q4i")
+_ATTENTION_ARGS = struct.Struct("@" + _CACHE + "5PNqif2if2i")
+_SELECT_ARGS = struct.Struct("@" + _CACHE + "6Pq5if")
+_CACHE_DTYPES = {torch.float8_e4m3fn: SBA_E4M3, torch.bfloat16: SBA_BF16}
+
+
+def _paged_call(index, fn, args):
+    """_call with a device index; most calls find their device current already."""
+    # the raw handle: torch.cuda.current_stream() builds a Stream object first
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
-        _check(fn(*args))
+        code = fn(args, stream)
     else:
         with torch.cuda.device(index):
-            _check(fn(*args))
+            code = fn(args, stream)
+    if code:
+        _check(code)
 
 
-def _at(t, name, index, dtype=None, shape=None):
-    """Address of a contiguous CUDA tensor on device ``index``; None passes through."""
+def _at(t, name, index, dtype, shape):
+    """Address of a contiguous CUDA tensor on device ``index``; 0 for None."""
     if t is None:
-        return None
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other tensors")
-    if dtype is not None and t.dtype != dtype:
+        return 0
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)} on the cache's device")
     return t.data_ptr()
 
 
-def _pool_args(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens):
-    """(device index, the library's cache arguments, (num_pages, Hkv, P, D), cache dtype)."""
+def _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens, cu_seqlens):
+    """(device index, Hkv, D, B, the fields of sba_paged_cache before Q)."""
     index = k_pages.get_device()
     if index < 0:
         raise ValueError("libsba works on CUDA tensors only (no CPU path)")
-    dtype = {torch.float8_e4m3fn: SBA_E4M3, torch.bfloat16: SBA_BF16}.get(k_pages.dtype)
+    dtype = _CACHE_DTYPES.get(k_pages.dtype)
     if dtype is None or v_pages.dtype != k_pages.dtype:
         raise TypeError("k_pages and v_pages must both be float8_e4m3fn or both bfloat16")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.get_device() != index:
+    shape, st = k_pages.shape, k_pages.stride()
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.get_device() != index:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D] on one device")
-    pages, hkv, size, d = k_pages.shape
-    stride = k_pages.stride(0) if pages > 1 else hkv * size * d
-    for t in (k_pages, v_pages):
-        st = t.stride()
-        if (st[3] != 1 or st[2] != d or (hkv > 1 and st[1] != size * d) or (pages > 1 and st[0] != stride)):
+    pages, hkv, size, d = shape
+    for s in (st, v_pages.stride()):
+        if s[3] != 1 or s[2] != d or (s[1] != size * d and hkv > 1) or (s[0] != st[0] and pages > 1):
             raise ValueError("k_pages, v_pages: pages must be dense and lie as far apart in both pools")
-    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != page_table.shape[0]:
-        raise ValueError("page_table must be [B, width] and seq_lens [B]")
-    args = (k_pages.data_ptr(), v_pages.data_ptr(),
-            _at(k_scales, "k_scales", index, torch.float32, (pages, hkv)),
-            _at(v_scales, "v_scales", index, torch.float32, (pages, hkv)), stride, pages, size,
-            _at(page_table, "page_table", index, torch.int32), page_table.shape[1],
-            _at(seq_lens, "seq_lens", index, torch.int32))
-    return index, args, (pages, hkv, size, d), dtype
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width]")
+    batch, width = table_shape = page_table.shape
+    scale_shape = (pages, hkv)
+    return index, hkv, d, batch, (
+        k_pages.data_ptr(), v_pages.data_ptr(),
+        _at(k_scales, "k_scales", index, torch.float32, scale_shape),
+        _at(v_scales, "v_scales", index, torch.float32, scale_shape),
+        _at(page_table, "page_table", index, torch.int32, table_shape),
+        _at(seq_lens, "seq_lens", index, torch.int32, (batch,)),
+        0 if cu_seqlens is None else _at(cu_seqlens, "cu_seqlens", index, torch.int32, (batch + 1,)),
+        st[0] if pages > 1 else hkv * size * d, pages, size, hkv, d, dtype, width, batch)
 
 
-def _token_rows(t, name, index, d, cu_seqlens, batch):
-    """(Q, N, heads, token stride) of bf16 token rows: [N, H, D] with cu_seqlens, else
-    [B, H, D] (one token per row) or [B, Q, H, D].  Heads are dense inside a token."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on the cache's device")
+def _token_rows(t, name, index, d, batch):
+    """(address, Q, N, heads, token stride) of bf16 token rows: [N, H, D] with cu_seqlens
+    (``batch`` None), else [batch, H, D] (one token per row) or [batch, Q, H, D].  Heads are
+    dense inside a token, tokens equally far apart."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 3 and (t.dim() != 4 or cu_seqlens is not None):
-        raise ValueError(f"{name} must be [B, H, D] or [B, Q, H, D], or [N, H, D] with cu_seqlens")
-    if t.shape[-1] != d:
-        raise ValueError(f"{name} must have the cache's head dimension")
-    heads, st = t.shape[-2], t.stride()
-    if st[-1] != 1 or (heads > 1 and st[-2] != d):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    if t.dim() == 3:
-        n, q, stride = t.shape[0], 1, st[0]
-    else:
-        b, q = t.shape[0], t.shape[1]
-        n, stride = b * q, st[1] if q > 1 else st[0]
-        if b > 1 and q > 1 and st[0] != q * st[1]:
+    shape, st = t.shape, t.stride()
+    if t.get_device() != index or shape[-1] != d or (st[-1] != 1 or (st[-2] != d and shape[-2] > 1)):
+        raise ValueError(f"{name} must be on the cache's device, with its head dimension and dense heads")
+    if len(shape) == 3:
+        n, q, stride = shape[0], 1, st[0]
+    elif len(shape) == 4 and batch is not None:
+        q = shape[1]
+        n, stride = shape[0] * q, st[1] if q > 1 else st[0]
+        if q > 1 and shape[0] > 1 and st[0] != q * stride:
             raise ValueError(f"{name}: tokens must lie equally far apart")
-    if cu_seqlens is None and t.shape[0] != batch:
+    else:
+        raise ValueError(f"{name} must be [B, H, D] or [B, Q, H, D], or [N, H, D] with cu_seqlens")
+    if batch is not None and shape[0] != batch:
         raise ValueError(f"{name} must have one entry per row of page_table")
-    return q, n, heads, stride if n > 1 else heads * d
-
-
-def _cu(cu_seqlens, index, batch):
-    return _at(cu_seqlens, "cu_seqlens", index, torch.int32, (batch + 1,))
+    return t.data_ptr(), q, n, shape[-2], stride if n > 1 else shape[-2] * d
 
 
 def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
@@ -566,35 +563,35 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=No
     [B, width], seq_lens int32 [B] with the new tokens counted.  cos / sin fp32
     [max_pos, rot_dim / 2] turn keys (and q, [..., Hq, D]) by their positions.  Returns
     q_out (new unless given; may be q), or None without q."""
-    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
-                                                    seq_lens)
-    batch = page_table.shape[0]
-    Q, N, heads, k_stride = _token_rows(k, "k", index, d, cu_seqlens, batch)
+    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
+                                               seq_lens, cu_seqlens)
+    rows = batch if cu_seqlens is None else None
+    kp, Q, N, heads, k_stride = _token_rows(k, "k", index, d, rows)
+    vp, _, _, _, v_stride = _token_rows(v, "v", index, d, rows)
     if v.shape != k.shape or heads != hkv:
         raise ValueError("k and v must have the same shape and the cache's heads")
-    v_stride = _token_rows(v, "v", index, d, cu_seqlens, batch)[3]
-    hq = q_stride = o_stride = 0
+    qp = op = hq = q_stride = o_stride = rot = max_pos = 0
     if q is not None:
-        if q.shape[:-2] != k.shape[:-2]:
+        qp, qq, qn, hq, q_stride = _token_rows(q, "q", index, d, rows)
+        if qq != Q or qn != N:
             raise ValueError("q must have k's tokens")
-        _, _, hq, q_stride = _token_rows(q, "q", index, d, cu_seqlens, batch)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-        o_stride = _token_rows(q_out, "q_out", index, d, cu_seqlens, batch)[3]
+        op, _, _, _, o_stride = _token_rows(q_out, "q_out", index, d, rows)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    rot = max_pos = 0
     if cos is not None or sin is not None:
-        if cos is None or sin is None or cos.dim() != 2 or sin.shape != cos.shape:
+        if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("cos and sin go together, [max_pos, rot_dim / 2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    _call_on(index, load_library().sba_paged_kv_append, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-             None if q is None else q.data_ptr(), q_stride, None if q is None else q_out.data_ptr(),
-             o_stride, _at(cos, "cos", index, torch.float32), _at(sin, "sin", index, torch.float32), rot,
-             max_pos, int(bool(interleaved)), *pool, _cu(cu_seqlens, index, batch), batch, Q, N, hq, hkv,
-             d, dtype, torch.cuda.current_stream(index).cuda_stream)
+        max_pos, rot = cos.shape
+        rot *= 2
+    _paged_call(index, load_library().sba_paged_kv_append, _APPEND_ARGS.pack(
+        *cache, Q, N, kp, vp, qp, op,
+        0 if cos is None else _at(cos, "cos", index, torch.float32, cos.shape),
+        0 if cos is None else _at(sin, "sin", index, torch.float32, cos.shape),
+        k_stride, v_stride, q_stride, o_stride, hq, rot, max_pos, 1 if interleaved else 0))
     return q_out
 
 
@@ -603,14 +600,17 @@ def paged_attention_workspace_size(D) -> int:
 
 
 def _results(q, index, out, lse, return_lse):
+    """(out, lse, their addresses) of a call on queries q."""
+    shape = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out_p = out.data_ptr()
+    else:
+        out_p = _at(out, "out", index, torch.bfloat16, shape)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    return (out, lse, _at(out, "out", index, torch.bfloat16),
-            _at(lse, "lse", index, torch.float32, tuple(q.shape[:-1])))
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        return out, lse, out_p, lse.data_ptr()
+    return out, lse, out_p, _at(lse, "lse", index, torch.float32, shape[:-1])
 
 
 def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
@@ -621,27 +621,25 @@ def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=N
     q bf16 [B, Hq, D], [B, Q, Hq, D], or [N, Hq, D] with cu_seqlens; windows, soft cap and
     sink_bias as in ragged_flash_attention_fwd (window_right=0 is causal).  Returns
     (out, lse) in q's shape and [..., Hq]."""
-    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
-                                                    seq_lens)
-    batch = page_table.shape[0]
-    Q, N, hq, q_stride = _token_rows(q, "q", index, d, cu_seqlens, batch)
+    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
+                                               seq_lens, cu_seqlens)
+    qp, Q, N, hq, q_stride = _token_rows(q, "q", index, d, batch if cu_seqlens is None else None)
     lib = load_library()
-    num_sinks = per_head = 0
+    bias_p = num_sinks = per_head = 0
     if sink_bias is not None:
-        if sink_bias.dim() not in (1, 2) or (sink_bias.dim() == 2 and sink_bias.shape[0] != hq):
-            raise ValueError("sink_bias must be [Hq, num_sinks] or [num_sinks]")
-        num_sinks, per_head = sink_bias.shape[-1], int(sink_bias.dim() == 2)
+        per_head = 1 if sink_bias.dim() == 2 else 0
+        num_sinks = sink_bias.shape[-1]
+        bias_p = _at(sink_bias, "sink_bias", index, torch.float32, (hq, num_sinks) if per_head else (num_sinks,))
     out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
     if workspace is None:
-        workspace = torch.empty(max(16, lib.sba_paged_attention_workspace_size(d)), dtype=torch.uint8,
+        workspace = torch.empty(lib.sba_paged_attention_workspace_size(d) or 16, dtype=torch.uint8,
                                 device=q.device)
-    _call_on(index, lib.sba_paged_attention_fwd, q.data_ptr(), q_stride, *pool,
-             _cu(cu_seqlens, index, batch), batch, Q, N, hq, hkv, d, dtype, softmax_scale or 0.0,
-             window_left, window_right, logits_soft_cap or 0.0,
-             _at(sink_bias, "sink_bias", index, torch.float32) if num_sinks else None, num_sinks,
-             per_head, out_p, lse_p, _at(workspace, "workspace", index),
-             workspace.numel() * workspace.element_size(),
-             torch.cuda.current_stream(index).cuda_stream)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _paged_call(index, lib.sba_paged_attention_fwd, _ATTENTION_ARGS.pack(
+        *cache, Q, N, qp, bias_p, out_p, lse_p, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), q_stride, hq, softmax_scale or 0.0, window_left,
+        window_right, logits_soft_cap or 0.0, num_sinks, per_head))
     return out, lse
 
 
@@ -652,21 +650,20 @@ def nsa_select_paged_fwd(q, k_pages, v_pages, page_table, seq_lens, block_indice
     nsa_select_fwd.  q bf16 [B, Hq, D] or [B, Q, Hq, D], block_indices int32 [B, (Q,) Hkv, S],
     block_counts int or int32 [B, (Q,) Hkv], g_slc bf16 [B, (Q,) Hq] or None.  Returns
     (out, lse)."""
-    index, pool, (_, hkv, _, d), dtype = _pool_args(k_pages, v_pages, k_scales, v_scales, page_table,
-                                                    seq_lens)
-    batch = page_table.shape[0]
-    Q, _, hq, q_stride = _token_rows(q, "q", index, d, None, batch)
+    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
+                                               seq_lens, None)
+    qp, Q, N, hq, q_stride = _token_rows(q, "q", index, d, batch)
+    lead = q.shape[:-2]
     S = block_indices.shape[-1]
-    lead = tuple(q.shape[:-2])
-    idx_p = _at(block_indices, "block_indices", index, torch.int32, lead + (hkv, S))
     counts = isinstance(block_counts, torch.Tensor)
-    cnt_p = _at(block_counts, "block_counts", index, torch.int32, lead + (hkv,)) if counts else None
-    gate_p = _at(g_slc, "g_slc", index, torch.bfloat16, lead + (hq,))
+    idx_p = _at(block_indices, "block_indices", index, torch.int32, (*lead, hkv, S))
+    cnt_p = _at(block_counts, "block_counts", index, torch.int32, (*lead, hkv)) if counts else 0
+    gate_p = 0 if g_slc is None else _at(g_slc, "g_slc", index, torch.bfloat16, q.shape[:-1])
     out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
-    _call_on(index, load_library().sba_nsa_select_paged_fwd, q.data_ptr(), q_stride, *pool, batch, Q, hq,
-             hkv, d, dtype, idx_p, cnt_p, 0 if counts else int(block_counts), S, int(block_size),
-             int(bool(causal)), softmax_scale or 0.0, gate_p, out_p, lse_p,
-             torch.cuda.current_stream(index).cuda_stream)
+    _paged_call(index, load_library().sba_nsa_select_paged_fwd, _SELECT_ARGS.pack(
+        *cache, Q, N, qp, idx_p, cnt_p, gate_p, out_p, lse_p, q_stride, hq,
+        0 if counts else int(block_counts), S, int(block_size), 1 if causal else 0,
+        softmax_scale or 0.0))
     return out, lse
 
 

@@ -542,48 +542,45 @@ int sba_ragged_flash_attention_fwd(const void* q, const void* k, const void* v,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
-// The arguments that describe a paged cache and a call's rows, checked the same way by
-// every entry point over one.
-static int paged_view(const char* who, const void* k_pages, const void* v_pages, const float* k_scales, const float* v_scales,
-                      long long page_stride, int num_pages, int page_size, const int32_t* page_table,
-                      int table_width, const int32_t* seq_lens, const int32_t* cu_seqlens, int B,
-                      int Q, int N, int Hkv, int D, int cache_dtype, PagedView* c) {
+// A paged cache and a call's rows, checked the same way by every entry point over one.
+static int paged_view(const char* who, const sba_paged_cache& a, PagedView* c) {
   auto bad = [&](const char* msg) { return set_error(SBA_ERR_INVALID_ARG, std::string(who) + ": " + msg); };
   auto no = [&](const char* msg) { return set_error(SBA_ERR_UNSUPPORTED, std::string(who) + ": " + msg); };
-  if (!k_pages || !v_pages || !page_table || !seq_lens) return bad("null pointer");
-  if (B < 1 || N < 1 || Hkv < 1 || num_pages < 1 || table_width < 1) return bad("sizes must be positive");
-  if (cu_seqlens == nullptr && (Q < 1 || (long long)B * Q != N))
+  if (!a.k_pages || !a.v_pages || !a.page_table || !a.seq_lens) return bad("null pointer");
+  if (a.B < 1 || a.N < 1 || a.Hkv < 1 || a.num_pages < 1 || a.table_width < 1)
+    return bad("sizes must be positive");
+  if (a.cu_seqlens == nullptr && (a.Q < 1 || (long long)a.B * a.Q != a.N))
     return bad("without cu_seqlens the call has N = B * Q tokens, Q >= 1");
-  if (cache_dtype != SBA_BF16 && cache_dtype != SBA_E4M3) return bad("cache dtype must be SBA_BF16 or SBA_E4M3");
-  const bool f8 = cache_dtype == SBA_E4M3;
-  if (f8 ? !(k_scales && v_scales) : (k_scales || v_scales))
+  if (a.dtype != SBA_BF16 && a.dtype != SBA_E4M3) return bad("cache dtype must be SBA_BF16 or SBA_E4M3");
+  const bool f8 = a.dtype == SBA_E4M3;
+  if (f8 ? !(a.k_scales && a.v_scales) : (a.k_scales || a.v_scales))
     return bad("an SBA_E4M3 cache needs k_scales and v_scales, an SBA_BF16 cache has none");
-  if (D != 64 && D != 128) return no("D must be 64 or 128");
+  if (a.D != 64 && a.D != 128) return no("D must be 64 or 128");
   int shift = -1;
   for (int i = 4; i <= 7; ++i)
-    if (page_size == 1 << i) shift = i;
+    if (a.page_size == 1 << i) shift = i;
   if (shift < 0) return no("page_size must be 16, 32, 64 or 128");
   const int item = f8 ? 1 : 2;
-  if (page_stride < (long long)Hkv * page_size * D || page_stride * item % 16 != 0)
+  if (a.page_stride < (long long)a.Hkv * a.page_size * a.D || a.page_stride * item % 16 != 0)
     return bad("page_stride must cover one page and keep pages 16-byte aligned");
-  if (!aligned16(k_pages) || !aligned16(v_pages)) return bad("pools must be 16-byte aligned");
-  if ((long long)table_width * page_size > (1LL << 30)) return no("table_width * page_size must be <= 2^30");
-  if (B > (1 << 24) || N > (1 << 28)) return no("B must be <= 2^24 and the tokens <= 2^28");
-  c->k = static_cast<uint8_t*>(const_cast<void*>(k_pages));
-  c->v = static_cast<uint8_t*>(const_cast<void*>(v_pages));
-  c->ks = const_cast<float*>(k_scales);
-  c->vs = const_cast<float*>(v_scales);
-  c->table = page_table;
-  c->lens = seq_lens;
-  c->cu = cu_seqlens;
-  c->page_bytes = page_stride * item;
-  c->B = B;
-  c->Qn = cu_seqlens ? 0 : Q;
-  c->N = N;
-  c->width = table_width;
-  c->num_pages = num_pages;
+  if (!aligned16(a.k_pages) || !aligned16(a.v_pages)) return bad("pools must be 16-byte aligned");
+  if ((long long)a.table_width * a.page_size > (1LL << 30)) return no("table_width * page_size must be <= 2^30");
+  if (a.B > (1 << 24) || a.N > (1 << 28)) return no("B must be <= 2^24 and the tokens <= 2^28");
+  c->k = static_cast<uint8_t*>(a.k_pages);
+  c->v = static_cast<uint8_t*>(a.v_pages);
+  c->ks = a.k_scales;
+  c->vs = a.v_scales;
+  c->table = a.page_table;
+  c->lens = a.seq_lens;
+  c->cu = a.cu_seqlens;
+  c->page_bytes = a.page_stride * item;
+  c->B = a.B;
+  c->Qn = a.cu_seqlens ? 0 : a.Q;
+  c->N = a.N;
+  c->width = a.table_width;
+  c->num_pages = a.num_pages;
   c->p_shift = shift;
-  c->Hkv = Hkv;
+  c->Hkv = a.Hkv;
   return SBA_OK;
 }
 // Token strides (elements): whole 16-byte chunks, heads dense inside a token.
@@ -591,115 +588,94 @@ static bool token_stride_ok(long long stride, int heads, int D, int N) {
   return N == 1 || (stride >= (long long)heads * D && stride % 8 == 0);
 }
 
-int sba_paged_kv_append(const void* k, long long k_stride, const void* v, long long v_stride,
-                        const void* q, long long q_stride, void* q_out, long long q_out_stride,
-                        const float* cos, const float* sin, int rot_dim, int max_pos, int interleaved,
-                        void* k_pages, void* v_pages, float* k_scales, float* v_scales,
-                        long long page_stride, int num_pages, int page_size,
-                        const int32_t* page_table, int table_width, const int32_t* seq_lens,
-                        const int32_t* cu_seqlens, int B, int Q, int N, int Hq, int Hkv, int D,
-                        int cache_dtype, sba_stream_t stream) {
+int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) {
   g_last_error.clear();
-  SBA_REQUIRE(k && v, "null pointer");
+  SBA_REQUIRE(args && args->k && args->v, "null pointer");
+  const sba_paged_append_args& a = *args;
   PagedView c{};
-  if (int rc = paged_view(__func__, k_pages, v_pages, k_scales, v_scales, page_stride, num_pages,
-                          page_size, page_table, table_width, seq_lens, cu_seqlens, B, Q, N, Hkv, D,
-                          cache_dtype, &c))
-    return rc;
-  SBA_REQUIRE(!q == !q_out, "q and q_out go together");
-  SBA_REQUIRE(q == nullptr || Hq >= 1, "sizes must be positive");
-  SBA_REQUIRE(aligned16(k) && aligned16(v) && aligned16(q) && aligned16(q_out),
+  if (int rc = paged_view(__func__, a.cache, &c)) return rc;
+  const int Hkv = c.Hkv, D = a.cache.D, N = c.N;
+  SBA_REQUIRE(!a.q == !a.q_out, "q and q_out go together");
+  SBA_REQUIRE(a.q == nullptr || a.Hq >= 1, "sizes must be positive");
+  SBA_REQUIRE(aligned16(a.k) && aligned16(a.v) && aligned16(a.q) && aligned16(a.q_out),
               "k, v, q and q_out must be 16-byte aligned");
-  SBA_REQUIRE(token_stride_ok(k_stride, Hkv, D, N) && token_stride_ok(v_stride, Hkv, D, N) &&
-                  (!q || (token_stride_ok(q_stride, Hq, D, N) && token_stride_ok(q_out_stride, Hq, D, N))),
+  SBA_REQUIRE(token_stride_ok(a.k_stride, Hkv, D, N) && token_stride_ok(a.v_stride, Hkv, D, N) &&
+                  (!a.q || (token_stride_ok(a.q_stride, a.Hq, D, N) && token_stride_ok(a.q_out_stride, a.Hq, D, N))),
               "token strides must cover the token's heads and be multiples of 8 elements");
-  SBA_REQUIRE(!cos == !sin, "cos and sin go together");
-  if (cos != nullptr) {
-    SBA_REQUIRE(rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0,
+  SBA_REQUIRE(!a.cos == !a.sin, "cos and sin go together");
+  if (a.cos != nullptr) {
+    SBA_REQUIRE(a.rot_dim >= 16 && a.rot_dim <= D && a.rot_dim % 16 == 0,
                 "rot_dim must be a multiple of 16 in [16, D]");
-    SBA_REQUIRE(max_pos >= 1 && aligned16(cos) && aligned16(sin),
+    SBA_REQUIRE(a.max_pos >= 1 && aligned16(a.cos) && aligned16(a.sin),
                 "cos and sin must be 16-byte aligned tables of at least one position");
   }
-  SBA_SUPPORT((long long)Hkv * 2 + (q ? Hq : 0) <= 65535 * 1LL, "Hq + 2 Hkv must be <= 65535");
-  SBA_SUPPORT(cu_seqlens != nullptr || (long long)B * ((Q >> c.p_shift) + 2) < (1LL << 31),
+  SBA_SUPPORT((long long)Hkv * 2 + (a.q ? a.Hq : 0) <= 65535, "Hq + 2 Hkv must be <= 65535");
+  SBA_SUPPORT(c.cu != nullptr || (long long)c.B * ((c.Qn >> c.p_shift) + 2) < (1LL << 31),
               "too many pages touched by one call");
-  return launch_paged_append(c, cache_dtype == SBA_E4M3, D, k, k_stride, v, v_stride, q, q_stride,
-                             q_out, q_out_stride, Hq, cos, sin, rot_dim, max_pos, interleaved ? 1 : 0,
-                             reinterpret_cast<cudaStream_t>(stream));
+  return launch_paged_append(c, a.cache.dtype == SBA_E4M3, D, a.k, a.k_stride, a.v, a.v_stride, a.q,
+                             a.q_stride, a.q_out, a.q_out_stride, a.Hq, a.cos, a.sin, a.rot_dim,
+                             a.max_pos, a.interleaved ? 1 : 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t sba_paged_attention_workspace_size(int D) {
   return D == 64 || D == 128 ? paged_attention_workspace_bytes(D) : 0;
 }
 
-int sba_paged_attention_fwd(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
-                            const float* k_scales, const float* v_scales, long long page_stride,
-                            int num_pages, int page_size, const int32_t* page_table, int table_width,
-                            const int32_t* seq_lens, const int32_t* cu_seqlens, int B, int Q, int N,
-                            int Hq, int Hkv, int D, int cache_dtype, float softmax_scale,
-                            int window_left, int window_right, float logits_soft_cap,
-                            const float* sink_bias, int num_sinks, int sink_bias_per_head, void* out,
-                            float* lse, void* workspace, size_t workspace_bytes,
-                            sba_stream_t stream) {
+int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_stream_t stream) {
   g_last_error.clear();
-  SBA_REQUIRE(q && out, "null pointer");
+  SBA_REQUIRE(args && args->q && args->out, "null pointer");
+  const sba_paged_attention_args& a = *args;
   PagedView c{};
-  if (int rc = paged_view(__func__, k_pages, v_pages, k_scales, v_scales, page_stride, num_pages,
-                          page_size, page_table, table_width, seq_lens, cu_seqlens, B, Q, N, Hkv, D, cache_dtype, &c))
-    return rc;
-  SBA_REQUIRE(Hq >= 1 && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
-  SBA_REQUIRE(window_left >= -1 && window_right >= -1, "windows must be >= -1");
-  SBA_REQUIRE(num_sinks >= 0 && (num_sinks == 0 || sink_bias != nullptr),
+  if (int rc = paged_view(__func__, a.cache, &c)) return rc;
+  const int D = a.cache.D;
+  SBA_REQUIRE(a.Hq >= 1 && a.Hq % c.Hkv == 0, "Hq must be a positive multiple of Hkv");
+  SBA_REQUIRE(a.window_left >= -1 && a.window_right >= -1, "windows must be >= -1");
+  SBA_REQUIRE(a.num_sinks >= 0 && (a.num_sinks == 0 || a.sink_bias != nullptr),
               "num_sinks > 0 needs sink_bias");
-  SBA_REQUIRE(aligned16(q) && aligned16(out), "q and out must be 16-byte aligned");
-  SBA_REQUIRE(token_stride_ok(q_stride, Hq, D, N),
+  SBA_REQUIRE(aligned16(a.q) && aligned16(a.out), "q and out must be 16-byte aligned");
+  SBA_REQUIRE(token_stride_ok(a.q_stride, a.Hq, D, c.N),
               "the token stride of q must cover its heads and be a multiple of 8 elements");
-  SBA_REQUIRE(std::isfinite(softmax_scale) && std::isfinite(logits_soft_cap),
+  SBA_REQUIRE(std::isfinite(a.softmax_scale) && std::isfinite(a.logits_soft_cap),
               "scale and cap must be finite");
-  SBA_SUPPORT(num_sinks <= 16, "num_sinks must be <= 16");
-  SBA_SUPPORT((long long)N * Hq < (1LL << 31), "tokens * Hq must be < 2^31");
-  SBA_REQUIRE(workspace != nullptr && aligned16(workspace) &&
-                  workspace_bytes >= paged_attention_workspace_bytes(D),
+  SBA_SUPPORT(a.num_sinks <= 16, "num_sinks must be <= 16");
+  SBA_SUPPORT((long long)c.N * a.Hq < (1LL << 31), "tokens * Hq must be < 2^31");
+  SBA_REQUIRE(a.workspace != nullptr && aligned16(a.workspace) &&
+                  a.workspace_bytes >= paged_attention_workspace_bytes(D),
               "workspace missing, misaligned or smaller than sba_paged_attention_workspace_size()");
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
-  return launch_paged_attention(c, cache_dtype == SBA_E4M3, D, q, q_stride, Hq, scale, window_left,
-                                window_right, logits_soft_cap, sink_bias, num_sinks,
-                                sink_bias_per_head ? 1 : 0, out, lse, workspace,
+  const float scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
+  return launch_paged_attention(c, a.cache.dtype == SBA_E4M3, D, a.q, a.q_stride, a.Hq, scale,
+                                a.window_left, a.window_right, a.logits_soft_cap, a.sink_bias,
+                                a.num_sinks, a.sink_bias_per_head ? 1 : 0, a.out, a.lse, a.workspace,
                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
-int sba_nsa_select_paged_fwd(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
-                             const float* k_scales, const float* v_scales, long long page_stride,
-                             int num_pages, int page_size, const int32_t* page_table, int table_width,
-                             const int32_t* seq_lens, int B, int Q, int Hq, int Hkv, int D,
-                             int cache_dtype, const int32_t* block_indices,
-                             const int32_t* block_counts, int block_count_scalar, int S,
-                             int block_size, int causal, float softmax_scale, const void* g_slc,
-                             void* out, float* lse, sba_stream_t stream) {
+int sba_nsa_select_paged_fwd(const sba_nsa_select_paged_args* args, sba_stream_t stream) {
   g_last_error.clear();
-  SBA_REQUIRE(q && out && block_indices, "null pointer");
-  SBA_REQUIRE(B >= 1 && Q >= 1 && (long long)B * Q < (1LL << 28), "B and Q must be positive, B * Q < 2^28");
+  SBA_REQUIRE(args && args->q && args->out && args->block_indices, "null pointer");
+  const sba_nsa_select_paged_args& a = *args;
+  SBA_REQUIRE(a.cache.cu_seqlens == nullptr, "cu_seqlens must be NULL: every row has Q tokens");
   PagedView c{};
-  if (int rc = paged_view(__func__, k_pages, v_pages, k_scales, v_scales, page_stride, num_pages,
-                          page_size, page_table, table_width, seq_lens, nullptr, B, Q, B * Q, Hkv, D, cache_dtype, &c))
-    return rc;
-  SBA_REQUIRE(Hq >= 1 && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
-  SBA_REQUIRE(S >= 1, "S (selected-block slots) must be >= 1");
-  SBA_REQUIRE(block_counts != nullptr || block_count_scalar >= 0, "block_count_scalar must be >= 0");
-  SBA_REQUIRE(aligned16(q) && aligned16(out), "q and out must be 16-byte aligned");
-  SBA_REQUIRE(token_stride_ok(q_stride, Hq, D, B * Q),
+  if (int rc = paged_view(__func__, a.cache, &c)) return rc;
+  const int D = a.cache.D;
+  SBA_REQUIRE(a.Hq >= 1 && a.Hq % c.Hkv == 0, "Hq must be a positive multiple of Hkv");
+  SBA_REQUIRE(a.S >= 1, "S (selected-block slots) must be >= 1");
+  SBA_REQUIRE(a.block_counts != nullptr || a.block_count_scalar >= 0,
+              "block_count_scalar must be >= 0");
+  SBA_REQUIRE(aligned16(a.q) && aligned16(a.out), "q and out must be 16-byte aligned");
+  SBA_REQUIRE(token_stride_ok(a.q_stride, a.Hq, D, c.N),
               "the token stride of q must cover its heads and be a multiple of 8 elements");
-  SBA_REQUIRE(std::isfinite(softmax_scale), "softmax_scale must be finite");
-  SBA_SUPPORT(block_size == 32 || block_size == 64 || block_size == 128,
+  SBA_REQUIRE(std::isfinite(a.softmax_scale), "softmax_scale must be finite");
+  SBA_SUPPORT(a.block_size == 32 || a.block_size == 64 || a.block_size == 128,
               "block_size must be 32, 64 or 128");
-  SBA_SUPPORT(Hq / Hkv <= 16, "Hq / Hkv must be <= 16");
-  SBA_SUPPORT(S <= 32, "S must be <= 32");
-  SBA_SUPPORT((long long)B * Q * Hq < (1LL << 31) && (long long)B * Q * Hkv < (1LL << 27),
+  SBA_SUPPORT(a.Hq / c.Hkv <= 16, "Hq / Hkv must be <= 16");
+  SBA_SUPPORT(a.S <= 32, "S must be <= 32");
+  SBA_SUPPORT((long long)c.N * a.Hq < (1LL << 31) && (long long)c.N * c.Hkv < (1LL << 27),
               "B * Q * Hq must be < 2^31 and B * Q * Hkv < 2^27");
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
-  return launch_paged_select(c, cache_dtype == SBA_E4M3, D, q, q_stride, Hq, block_indices,
-                             block_counts, block_count_scalar, S, block_size, causal ? 1 : 0, scale,
-                             g_slc, out, lse, reinterpret_cast<cudaStream_t>(stream));
+  const float scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
+  return launch_paged_select(c, a.cache.dtype == SBA_E4M3, D, a.q, a.q_stride, a.Hq, a.block_indices,
+                             a.block_counts, a.block_count_scalar, a.S, a.block_size,
+                             a.causal ? 1 : 0, scale, a.g_slc, a.out, a.lse,
+                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 int sba_l2_read_probe(const void* buf, size_t bytes, int reps, uint32_t* sink,

@@ -19,8 +19,9 @@
 //
 // Work unit: one page of one row, for one head of K, V or Q: its maximum is all that the
 // scale needs, so a unit is one block (or one warp) and nothing waits for another.  The
-// kernel is bound by memory: every input is read once and held in registers between the
+// kernels are bound by memory: every input is read once and held in registers between the
 // maximum and the store.
+#include <algorithm>
 #include <string>
 
 #include "paged.cuh"
@@ -42,20 +43,21 @@ struct AppendParams {
   long long k_tok, v_tok, q_tok, qo_tok;
   int Hq, rot, interleaved, max_pos;
   int units_per_row;  // pages a row's tokens can touch (cu == null)
+  int heads;          // heads a block works through
 };
 
-// x[0..8) and y[0..8): the thread's two chunks of 8 dimensions.  Half-split pairs are
-// (x[i], y[i]); neighbouring pairs lie inside each chunk.
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
   const float a2 = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
   const float b2 = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
   a = a2;
   b = b2;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
   x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
   x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  unpack8(__ldg(reinterpret_cast<const uint4*>(p)), x);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   uint4 w;
@@ -72,20 +74,193 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// kUnit threads work on one unit; a row (token) takes kD / 16 of them, each with two
-// chunks of 8 dimensions; kPasses passes cover the unit's rows.
-template <bool kF8, int kD, int kUnit, int kPasses>
-__global__ void __launch_bounds__(kUnit == 32 ? 128 : 256)
+// The unit's row, first token and positions [p0, p1); m = p1 - p0 <= 0: nothing to do.
+struct Unit {
+  int b, first, p0, m, page_slot;
+};
+__device__ __forceinline__ Unit unit_of(const PagedView& c, int b, int j, bool report) {
+  Unit u;
+  u.b = b;
+  u.m = 0;
+  u.first = u.p0 = u.page_slot = 0;
+  bool bad;
+  const PagedRow r = paged_row(c, b, &bad);
+  if (bad) {
+    if (report) atomicOr(&g_err_append, (unsigned)kDevErrInput);
+    return u;
+  }
+  if (r.n == 0) return u;
+  const int start = r.len - r.n;  // position of the row's first token; those left of 0 do not exist
+  u.page_slot = (max(start, 0) >> c.p_shift) + j;
+  u.p0 = max(max(start, 0), u.page_slot << c.p_shift);
+  u.m = min(r.len, (u.page_slot + 1) << c.p_shift) - u.p0;
+  u.first = r.t0 + (u.p0 - start);
+  return u;
+}
+__device__ __forceinline__ int page_of(const PagedView& c, const Unit& u, bool report) {
+  const int page = c.table[(long long)u.b * c.width + u.page_slot];
+  if ((unsigned)page < (unsigned)c.num_pages) return page;
+  if (report) atomicOr(&g_err_append, (unsigned)kDevErrInput);
+  return -1;
+}
+
+// A head of the call's queries, keys or values.
+struct Stream {
+  const __nv_bfloat16* src;
+  long long tok;
+  int h;
+  bool is_q, is_k;
+};
+template <int kD>
+__device__ __forceinline__ Stream stream_of(const AppendParams& p, int s) {
+  Stream t;
+  t.is_q = s < p.Hq;
+  t.is_k = !t.is_q && s < p.Hq + p.c.Hkv;
+  t.h = t.is_q ? s : (t.is_k ? s - p.Hq : s - p.Hq - p.c.Hkv);
+  t.src = (t.is_q ? p.q : (t.is_k ? p.k : p.v)) + (long long)t.h * kD;
+  t.tok = t.is_q ? p.q_tok : (t.is_k ? p.k_tok : p.v_tok);
+  return t;
+}
+
+// Chunks of 8 dimensions of the thread `rt` of a row: rotated ones first, a chunk with its
+// partner; then the rest two by two.
+__device__ __forceinline__ void chunks_of(int rt, int rot, int interleaved, int& c0, int& c1) {
+  if (rt < rot / 16 && !interleaved) {
+    c0 = rt;
+    c1 = rt + rot / 16;
+  } else {
+    c0 = 2 * rt;
+    c1 = 2 * rt + 1;
+  }
+}
+__device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int rt, float* cs, float* sn) {
+  if (pos >= p.max_pos) {
+    atomicOr(&g_err_append, (unsigned)kDevErrInput);
+    pos = p.max_pos - 1;
+  }
+  // of pairs 8 rt .. 8 rt + 7
+  const float4* cp = reinterpret_cast<const float4*>(p.cosp + (long long)pos * (p.rot / 2) + 8 * rt);
+  const float4* sp = reinterpret_cast<const float4*>(p.sinp + (long long)pos * (p.rot / 2) + 8 * rt);
+  *reinterpret_cast<float4*>(cs) = __ldg(cp);
+  *reinterpret_cast<float4*>(cs + 4) = __ldg(cp + 1);
+  *reinterpret_cast<float4*>(sn) = __ldg(sp);
+  *reinterpret_cast<float4*>(sn + 4) = __ldg(sp + 1);
+}
+__device__ __forceinline__ void rotate16(float* x, const float* cs, const float* sn, int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rotate_pair(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rotate_pair(x[e], x[e + 8], cs[e], sn[e]);
+  }
+}
+__device__ __forceinline__ float finite_max(const float* x, float top) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float a = fabsf(x[e]);
+    if (a <= 3.4028235e38f) top = fmaxf(top, a);  // infinities and NaN set no scale
+  }
+  return top;
+}
+// 16 codes that a page holds, from scale `old` to 1 / `inv`.
+__device__ __forceinline__ void rescale16(uint8_t* at, float old, float inv) {
+  uint4 w = *reinterpret_cast<uint4*>(at);
+  uint32_t* c = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x2(c[i], lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+    c[i] = f32x4_to_e4m3x4(__fmul_rn(__fmul_rn(a.x, old), inv), __fmul_rn(__fmul_rn(a.y, old), inv),
+                           __fmul_rn(__fmul_rn(b.x, old), inv), __fmul_rn(__fmul_rn(b.y, old), inv));
+  }
+  *reinterpret_cast<uint4*>(at) = w;
+}
+__device__ __forceinline__ void store_codes(uint8_t* row, int c0, int c1, float* x, float inv) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(x[e], inv);
+  *reinterpret_cast<uint2*>(row + 8 * c0) =
+      make_uint2(f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]), f32x4_to_e4m3x4(x[4], x[5], x[6], x[7]));
+  *reinterpret_cast<uint2*>(row + 8 * c1) =
+      make_uint2(f32x4_to_e4m3x4(x[8], x[9], x[10], x[11]), f32x4_to_e4m3x4(x[12], x[13], x[14], x[15]));
+}
+
+// Few tokens a row (at most 512 / kD): one warp for each (page, head); a row of kD / 16
+// threads, 16 dimensions each.
+template <bool kF8, int kD>
+__global__ void __launch_bounds__(128)
+paged_append_few_kernel(const AppendParams p) {
+  constexpr int kRowThreads = kD / 16;
+  constexpr int kRows = 32 / kRowThreads;
+  const PagedView& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const int stream = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (stream >= p.Hq + 2 * c.Hkv) return;
+  const int b = blockIdx.x / p.units_per_row;
+  const Unit u = unit_of(c, b, blockIdx.x - b * p.units_per_row, lane == 0);
+  if (u.m <= 0) return;
+  const Stream t = stream_of<kD>(p, stream);
+  const int rt = lane % kRowThreads, row = lane / kRowThreads;
+  const int rot = t.is_q || t.is_k ? p.rot : 0;
+  const bool mine = row < u.m, turn = rt < rot / 16;
+  int c0, c1;
+  chunks_of(rt, rot, p.interleaved, c0, c1);
+  float x[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = 0.f;
+  if (mine) {
+    const __nv_bfloat16* s = t.src + (long long)(u.first + row) * t.tok;
+    load8(s + 8 * c0, x);
+    load8(s + 8 * c1, x + 8);
+  }
+  const int page = t.is_q ? 0 : page_of(c, u, lane == 0);
+  if (page < 0) return;
+  if (mine && turn) {
+    float cs[8], sn[8];
+    load_angles(p, u.p0 + row, rt, cs, sn);
+    rotate16(x, cs, sn, p.interleaved);
+  }
+  const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
+  uint8_t* tile = (t.is_k ? c.k : c.v) + page * c.page_bytes + (long long)t.h * P * (kD * (kF8 ? 1 : 2));
+  if (t.is_q || !kF8) {
+    if (!mine) return;
+    __nv_bfloat16* o = t.is_q ? p.q_out + (long long)(u.first + row) * p.qo_tok + (long long)t.h * kD
+                              : reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
+    store8(o + 8 * c0, x);
+    store8(o + 8 * c1, x + 8);
+    return;
+  }
+  float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
+  const float old = off > 0 ? *scale_at : 0.f;
+  float amax = finite_max(x, 0.f);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  const float need = pow2_scale(amax);
+  const float scale = need > old ? need : old;
+  const float inv = __frcp_rn(scale);
+  if (scale != old) {
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale_at = scale;
+#pragma unroll 4
+    for (int i = row; i < off; i += kRows) rescale16(tile + i * kD + 16 * rt, old, inv);
+  }
+  if (mine) store_codes(tile + (off + row) * kD, c0, c1, x, inv);
+}
+
+// Any number of tokens: one block of P kD / 32 threads for a page and `heads` heads, so a
+// page's rows take two passes; the angles of its positions stay in registers from head to
+// head, and a head's values are loaded while the one before is worked on.
+template <bool kF8, int kD>
+__global__ void __launch_bounds__(512)
 paged_append_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
-  constexpr int kRows = kUnit / kRowThreads;
+  constexpr int kPasses = 2;
   const PagedView& c = p.c;
-  const int tid = kUnit == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  const int stream = kUnit == 32 ? blockIdx.y * 4 + (threadIdx.x >> 5) : blockIdx.y;
-  const int streams = p.Hq + 2 * c.Hkv;
-  const int P = 1 << c.p_shift;
-
-  // ---- the unit: page number j of row b's new tokens
+  const int tid = threadIdx.x;
+  __shared__ int s_b;
+  __shared__ float s_max[2][16];
   int b, j;
   if (c.cu == nullptr) {
     b = blockIdx.x / p.units_per_row;
@@ -93,11 +268,10 @@ paged_append_kernel(const AppendParams p) {
   } else {
     // Row b owns units from floor(cu[b] / P) + 2 b on: n tokens touch at most
     // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.
-    __shared__ int s_b;
-    if (threadIdx.x == 0) s_b = -1;
+    if (tid == 0) s_b = -1;
     __syncthreads();
     const int u = blockIdx.x;
-    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+    for (int i = tid; i < c.B; i += blockDim.x) {
       const int lo = (min(max(c.cu[i], 0), c.N) >> c.p_shift) + 2 * i;
       const int hi = (min(max(c.cu[i + 1], 0), c.N) >> c.p_shift) + 2 * i + 2;
       if (u >= lo && u < hi) s_b = i;
@@ -107,200 +281,108 @@ paged_append_kernel(const AppendParams p) {
     if (b < 0) return;
     j = u - (min(max(c.cu[b], 0), c.N) >> c.p_shift) - 2 * b;
   }
-  if (stream >= streams) return;
-  bool bad;
-  const PagedRow r = paged_row(c, b, &bad);
-  if (bad) {
-    if (tid == 0) atomicOr(&g_err_append, (unsigned)kDevErrInput);
-    return;
-  }
-  const int start = r.len - r.n;  // position of the row's first token; those left of 0 do not exist
-  const int pj = (max(start, 0) >> c.p_shift) + j;
-  const int p0 = max(max(start, 0), pj << c.p_shift);
-  const int p1 = min(r.len, (pj + 1) << c.p_shift);
-  const int m = p1 - p0;
-  if (r.n == 0 || m <= 0) return;
-
-  // ---- the stream: a query head, a key head or a value head
-  const bool is_q = stream < p.Hq;
-  const bool is_k = !is_q && stream < p.Hq + c.Hkv;
-  const int h = is_q ? stream : (is_k ? stream - p.Hq : stream - p.Hq - c.Hkv);
-  const __nv_bfloat16* src = is_q ? p.q : (is_k ? p.k : p.v);
-  const long long tok = is_q ? p.q_tok : (is_k ? p.k_tok : p.v_tok);
-  const int first = r.t0 + (p0 - start);  // token at position p0
-  const int rot = (is_q || is_k) ? p.rot : 0;
-  int page = 0;
-  if (!is_q) {
-    page = c.table[(long long)b * c.width + pj];
-    if ((unsigned)page >= (unsigned)c.num_pages) {
-      if (tid == 0) atomicOr(&g_err_append, (unsigned)kDevErrInput);
-      return;
-    }
-  }
-
+  const Unit u = unit_of(c, b, j, tid == 0 && blockIdx.y == 0);
+  if (u.m <= 0) return;
+  const int rows = blockDim.x / kRowThreads;
   const int rt = tid % kRowThreads, slot = tid / kRowThreads;
-  // rotated dimensions first, a chunk with its partner; then the rest two by two
-  int c0, c1;
-  const bool turn = rt < rot / 16;
-  if (turn && !p.interleaved) {
-    c0 = rt;
-    c1 = rt + rot / 16;
-  } else {
-    c0 = 2 * rt;
-    c1 = 2 * rt + 1;
-  }
-  float x[kPasses][16];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = i * kRows + slot;
-    if (row >= m) continue;
-    const __nv_bfloat16* s = src + (long long)(first + row) * tok + (long long)h * kD;
-    load8(s + 8 * c0, x[i]);
-    load8(s + 8 * c1, x[i] + 8);
-  }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = i * kRows + slot;
-    if (row >= m) continue;
-    if (turn) {
-      int pos = p0 + row;
-      if (pos >= p.max_pos) {
-        atomicOr(&g_err_append, (unsigned)kDevErrInput);
-        pos = p.max_pos - 1;
-      }
-      // 8 angles: of pairs 8 c0 .. 8 c0 + 7 (half split) or of the 16 neighbours
-      const float4* cp = reinterpret_cast<const float4*>(p.cosp + (long long)pos * (rot / 2) + 8 * rt);
-      const float4* sp = reinterpret_cast<const float4*>(p.sinp + (long long)pos * (rot / 2) + 8 * rt);
-      const float4 ca = __ldg(cp), cb = __ldg(cp + 1), sa = __ldg(sp), sb = __ldg(sp + 1);
-      const float cs[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-      const float sn[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-      if (p.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rotate_pair(x[i][2 * e], x[i][2 * e + 1], cs[e], sn[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rotate_pair(x[i][e], x[i][e + 8], cs[e], sn[e]);
-      }
-    }
-    if (kF8 && !is_q) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = fabsf(x[i][e]);
-        if (a <= 3.4028235e38f) amax = fmaxf(amax, a);  // infinities and NaN set no scale
-      }
-    }
-  }
+  const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
+  const int s_end = min((int)(blockIdx.y + 1) * p.heads, p.Hq + 2 * c.Hkv);
+  int s = blockIdx.y * p.heads;
+  const int page = s_end > p.Hq ? page_of(c, u, tid == 0) : 0;
+  if (page < 0) return;
 
-  if (is_q) {
+  bool mine[kPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int row = i * kRows + slot;
-      if (row >= m) continue;
-      __nv_bfloat16* o = p.q_out + (long long)(first + row) * p.qo_tok + (long long)h * kD;
-      store8(o + 8 * c0, x[i]);
-      store8(o + 8 * c1, x[i] + 8);
-    }
-    return;
+  for (int i = 0; i < kPasses; ++i) mine[i] = i * rows + slot < u.m;
+  const bool turns = rt < p.rot / 16;
+  float cs[kPasses][8], sn[kPasses][8];
+  if (turns && s < p.Hq + c.Hkv) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (mine[i]) load_angles(p, u.p0 + i * rows + slot, rt, cs[i], sn[i]);
   }
-  const int off = p0 & (P - 1);
-  uint8_t* tile = (is_k ? c.k : c.v) + page * c.page_bytes + (long long)h * P * (kD * (kF8 ? 1 : 2));
-  if constexpr (!kF8) {
+  uint4 next[kPasses][2];
+  auto fetch = [&](int stream) {
+    const Stream t = stream_of<kD>(p, stream);
+    int c0, c1;
+    chunks_of(rt, t.is_q || t.is_k ? p.rot : 0, p.interleaved, c0, c1);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (mine[i]) {
+        const __nv_bfloat16* src = t.src + (long long)(u.first + i * rows + slot) * t.tok;
+        next[i][0] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c0));
+        next[i][1] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c1));
+      }
+  };
+  fetch(s);
+  for (; s < s_end; ++s) {
+    const Stream t = stream_of<kD>(p, s);
+    const int rot = t.is_q || t.is_k ? p.rot : 0;
+    int c0, c1;
+    chunks_of(rt, rot, p.interleaved, c0, c1);
+    float x[kPasses][16];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int row = i * kRows + slot;
-      if (row >= m) continue;
-      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
-      store8(o + 8 * c0, x[i]);
-      store8(o + 8 * c1, x[i] + 8);
+      unpack8(next[i][0], x[i]);
+      unpack8(next[i][1], x[i] + 8);
     }
-    return;
-  } else {
-    float* scale_at = (is_k ? c.ks : c.vs) + (long long)page * c.Hkv + h;
+    if (s + 1 < s_end) fetch(s + 1);
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (mine[i]) {
+        if (rt < rot / 16) rotate16(x[i], cs[i], sn[i], p.interleaved);
+        if (kF8 && !t.is_q) amax = finite_max(x[i], amax);
+      }
+    uint8_t* tile = (t.is_k ? c.k : c.v) + page * c.page_bytes + (long long)t.h * P * (kD * (kF8 ? 1 : 2));
+    if (t.is_q || !kF8) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        if (mine[i]) {
+          const int row = i * rows + slot;
+          __nv_bfloat16* o = t.is_q ? p.q_out + (long long)(u.first + row) * p.qo_tok + (long long)t.h * kD
+                                    : reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
+          store8(o + 8 * c0, x[i]);
+          store8(o + 8 * c1, x[i] + 8);
+        }
+      continue;
+    }
+    float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
     const float old = off > 0 ? *scale_at : 0.f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if constexpr (kUnit > 32) {
-      __shared__ float s_max[kUnit / 32];
-      if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-      __syncthreads();
-      amax = s_max[0];
-#pragma unroll
-      for (int w = 1; w < kUnit / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    } else {
-      __syncwarp();
-    }
+    float* most = s_max[s & 1];  // two in turn: a head's readers are behind the next barrier
+    if ((tid & 31) == 0) most[tid >> 5] = amax;
+    __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, most[w]);
     const float need = pow2_scale(amax);
     const float scale = need > old ? need : old;
     const float inv = __frcp_rn(scale);
     if (scale != old) {
       if (tid == 0) *scale_at = scale;  // every thread has read the old one
-      // codes that the page holds already, to the new scale
-      for (int row = slot; row < off; row += kRows) {
-        uint2* at = reinterpret_cast<uint2*>(tile + row * kD + 16 * rt);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint2 w = at[half];
-          uint2 o;
-          float f[8];
-          uint32_t lo, hi;
-          e4m3x4_to_f16x2(w.x, lo, hi);
-          float2 t = __half22float2(*reinterpret_cast<__half2*>(&lo));
-          f[0] = t.x; f[1] = t.y;
-          t = __half22float2(*reinterpret_cast<__half2*>(&hi));
-          f[2] = t.x; f[3] = t.y;
-          e4m3x4_to_f16x2(w.y, lo, hi);
-          t = __half22float2(*reinterpret_cast<__half2*>(&lo));
-          f[4] = t.x; f[5] = t.y;
-          t = __half22float2(*reinterpret_cast<__half2*>(&hi));
-          f[6] = t.x; f[7] = t.y;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn(f[e], old), inv);
-          o.x = f32x4_to_e4m3x4(f[0], f[1], f[2], f[3]);
-          o.y = f32x4_to_e4m3x4(f[4], f[5], f[6], f[7]);
-          at[half] = o;
-        }
-      }
+      for (int i = slot; i < off; i += rows) rescale16(tile + i * kD + 16 * rt, old, inv);
     }
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int row = i * kRows + slot;
-      if (row >= m) continue;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[i][e] = __fmul_rn(x[i][e], inv);
-      uint8_t* o = tile + (off + row) * kD;
-      *reinterpret_cast<uint2*>(o + 8 * c0) =
-          make_uint2(f32x4_to_e4m3x4(x[i][0], x[i][1], x[i][2], x[i][3]),
-                     f32x4_to_e4m3x4(x[i][4], x[i][5], x[i][6], x[i][7]));
-      *reinterpret_cast<uint2*>(o + 8 * c1) =
-          make_uint2(f32x4_to_e4m3x4(x[i][8], x[i][9], x[i][10], x[i][11]),
-                     f32x4_to_e4m3x4(x[i][12], x[i][13], x[i][14], x[i][15]));
-    }
+    for (int i = 0; i < kPasses; ++i)
+      if (mine[i]) store_codes(tile + (off + i * rows + slot) * kD, c0, c1, x[i], inv);
   }
 }
 
 template <bool kF8, int kD>
-void launch_append(const AppendParams& p, cudaStream_t st) {
+void launch_append(AppendParams p, cudaStream_t st) {
   const PagedView& c = p.c;
   const int streams = p.Hq + 2 * c.Hkv;
-  constexpr int kWarpRows = 32 / (kD / 16);
-  if (c.cu == nullptr && c.Qn <= kWarpRows) {
-    // decode steps: a unit has at most kWarpRows tokens, one warp each
+  if (c.cu == nullptr && c.Qn <= 512 / kD) {
     dim3 grid((unsigned)c.B * p.units_per_row, (streams + 3) / 4);
-    paged_append_kernel<kF8, kD, 32, 1><<<grid, 128, 0, st>>>(p);
+    paged_append_few_kernel<kF8, kD><<<grid, 128, 0, st>>>(p);
     return;
   }
   const long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row
                                           : ((long long)c.N >> c.p_shift) + 2LL * c.B;
-  dim3 grid((unsigned)units, streams);
-  constexpr int kRows = 256 / (kD / 16);
-  const int passes = ((1 << c.p_shift) + kRows - 1) / kRows;
-  if (passes == 1)
-    paged_append_kernel<kF8, kD, 256, 1><<<grid, 256, 0, st>>>(p);
-  else if (passes == 2)
-    paged_append_kernel<kF8, kD, 256, 2><<<grid, 256, 0, st>>>(p);
-  else
-    paged_append_kernel<kF8, kD, 256, 4><<<grid, 256, 0, st>>>(p);
+  // up to 8 heads a block, as long as there are blocks enough to fill the GPU
+  p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
+  dim3 grid((unsigned)units, (streams + p.heads - 1) / p.heads);
+  paged_append_kernel<kF8, kD><<<grid, (kD << c.p_shift) / 32, 0, st>>>(p);
 }
 
 }  // namespace

@@ -6,14 +6,16 @@
 // window_right (a bound < 0 is open) or k < num_sinks.  Logit scale <q, k>, then cap
 // tanh(. / cap), then + sink bias; the softmax is kept in fp32.
 //
-// Split.  An item is (batch row, KV head, 16 (query, head) rows); its keys are tiles of 32
-// (e4m3) or 16 (bf16).  All items' tiles in order form one line that is cut into equal
-// runs, one for each of kCtas CTAs (three per SM), so every CTA reads the same amount
-// whatever the lengths are; each finds its place from the lengths on the device, and the
-// grid does not depend on them.  A run that holds an item whole writes its output; else
-// the item's partials (o, m, l) go to the workspace, two slots per CTA, and the CTA that
-// counts the item complete merges them in the order of the line, so results do not
-// depend on timing.  The counters are cleared by a small kernel that this one overlaps.
+// Split.  An item is (batch row, KV head, 16 (query, head) rows); its keys are tiles of
+// 4 KB of keys and 4 KB of values.  All items' tiles in order form one line that is cut
+// into equal runs, one for each of kCtas CTAs (three per SM), so every CTA reads the same
+// amount whatever the lengths are; each finds its place from the lengths on the device, and
+// the grid does not depend on them.  An item's fixed cost (its queries, the merge of the
+// CTA's warps) is kItemCost empty tiles ahead of its own, so that a run of many short items
+// takes no longer than a run inside a long one.  A run that holds an item whole writes its
+// output; else the item's partials (o, m, l) go to the workspace, two slots per CTA, and
+// paged_merge_kernel, launched behind this one with its start overlapped, adds them up in
+// the order of the line, so results do not depend on timing.
 #include <string>
 
 #include "paged_core.cuh"
@@ -27,6 +29,7 @@ namespace {
 constexpr int kThreads = kPagedWarps * 32;
 constexpr int kCtas = 456;    // three for each of 152 SMs
 constexpr int kMinTiles = 4;  // tiles of a run, at least: one for each warp
+constexpr int kItemCost = 8;  // tiles that an item's fixed cost is worth
 
 struct PagedAttnParams {
   PagedView c;
@@ -35,12 +38,19 @@ struct PagedAttnParams {
   const float* sink_bias;
   __nv_bfloat16* out;  // [N, Hq, D]
   float* lse;          // [N, Hq] or null
-  int* counters;       // [kCtas]
+  struct SplitItem* split;  // [kCtas]
   float* part_ml;      // [2 kCtas][16][2]
   float* part_o;       // [2 kCtas][16][D]
   int Hq, G;
   float scale, cap;
   int window_left, window_right, num_sinks, sink_per_head;
+};
+
+// The item that a CTA begins but does not end: its partials are slot 2 cta + 1 and the
+// slots 2 (cta + i), 0 < i < n.  n = 0: there is none.
+struct SplitItem {
+  int n, n_rows, first, t0, h;  // rows first .. first + n_rows of the row's (query, head) rows
+  int pad[3];
 };
 
 // The tiles of a row's items: all items of a row get the same number, that of the union
@@ -69,12 +79,17 @@ __device__ __forceinline__ RowTiles row_tiles(const PagedAttnParams& p, int b, b
 template <bool kF8, int kD, bool kHi, bool kCap>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_attention_kernel(const PagedAttnParams p) {
-  using W = PagedWarp<kF8, kD, kHi, kCap>;
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_sum[kPagedWarps];
   __shared__ long long s_total, s_off;
-  __shared__ int s_row, s_last;
+  __shared__ int s_row;
+  // what the CTA needs again after an item's tiles; kept here to leave registers to them
+  __shared__ struct {
+    long long cur, off, item_at;
+    int b, units, h, first, n_rows, t0, begins, whole;
+  } s_it;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
 
@@ -88,7 +103,7 @@ paged_attention_kernel(const PagedAttnParams p) {
       bool x;
       const RowTiles t = row_tiles<kKeys>(p, b, &x);
       bad |= x;
-      sum += (long long)t.tiles * t.groups * p.c.Hkv;
+      sum += (long long)(t.tiles + kItemCost) * t.groups * p.c.Hkv;
     }
     if (bad && cta == 0) atomicOr(&g_err_paged, (unsigned)kDevErrInput);
     long long pre = sum;
@@ -114,7 +129,7 @@ paged_attention_kernel(const PagedAttnParams p) {
       for (;; ++b) {
         bool x;
         const RowTiles t = row_tiles<kKeys>(p, b, &x);
-        const long long n = (long long)t.tiles * t.groups * p.c.Hkv;
+        const long long n = (long long)(t.tiles + kItemCost) * t.groups * p.c.Hkv;
         if (off < n) break;
         off -= n;
       }
@@ -124,33 +139,38 @@ paged_attention_kernel(const PagedAttnParams p) {
     if (tid == 0) s_total = total;
     __syncthreads();
   }
-  const long long total = s_total;
-  const long long per = max((total + kCtas - 1) / kCtas, (long long)kMinTiles);
-  long long cur = (long long)cta * per;
-  const long long end = min(cur + per, total);
+  auto run_length = [&]() { return max((s_total + kCtas - 1) / kCtas, (long long)kMinTiles); };
+  long long cur = cta * run_length();
   int b = s_row;
   long long off = s_off;
-  // The counters were cleared by the launch before this one, which may still be running.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (cur >= end) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) p.split[cta].n = 0;
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * W::kWarpBytes;
   float* so = reinterpret_cast<float*>(smem);          // [warps][16][kSmemRow]
   float* sm = so + kPagedWarps * 16 * W::kSmemRow;     // [warps][16][3]
   float* sw = sm + kPagedWarps * 16 * 3;               // [16][warps + 2]: weights, max, sum
 
-  while (cur < end) {
+  while (true) {
+    const long long end = min((cta + 1) * run_length(), s_total);
+    if (cur >= end) return;
     bool bad;
     const RowTiles rt = row_tiles<kKeys>(p, b, &bad);
-    const long long row_total = (long long)rt.tiles * rt.groups * p.c.Hkv;
+    const int units = rt.tiles + kItemCost;
+    const long long row_total = (long long)units * rt.groups * p.c.Hkv;
     if (off >= row_total) {
       off -= row_total;
       ++b;
       continue;
     }
-    const int item = (int)(off / rt.tiles);
-    const int s0 = (int)(off - (long long)item * rt.tiles);
-    const int s1 = (int)min((long long)rt.tiles, s0 + (end - cur));
+    const int item = (int)(off / units);
+    const int x0 = (int)(off - (long long)item * units);
+    const int x1 = (int)min((long long)units, x0 + (end - cur));
+    const long long item_at = cur - x0;  // the item's place on the line
+    cur += x1 - x0;
+    off += x1 - x0;
+    if (x1 <= kItemCost) continue;  // nothing but the empty tiles
+    const int s0 = max(x0 - kItemCost, 0), s1 = x1 - kItemCost;
     const int h = item / rt.groups, group = item - h * rt.groups;
     const int n_rows = min(16, rt.r.n * p.G - group * 16);
     const int first_pos = rt.r.len - rt.r.n;  // position of query 0
@@ -191,6 +211,19 @@ paged_attention_kernel(const PagedAttnParams p) {
     const int count = (with_sink ? 1 : 0) + max(wb - max(wa, 0), 0);
     const int w_first = max(wa, 0) - (with_sink ? 1 : 0);  // window tile of index t: w_first + t
 
+    if (tid == 0) {
+      s_it.cur = cur;
+      s_it.off = off;
+      s_it.item_at = item_at;
+      s_it.b = b;
+      s_it.units = units;
+      s_it.h = h;
+      s_it.first = group * 16;
+      s_it.n_rows = n_rows;
+      s_it.t0 = rt.r.t0;
+      s_it.begins = s0 == 0;
+      s_it.whole = s0 == 0 && s1 == rt.tiles;
+    }
     W w;
     w.init(p.c, b, h, ring, p.scale, p.cap, &g_err_paged);
     w.load_q(ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr,
@@ -209,7 +242,8 @@ paged_attention_kernel(const PagedAttnParams p) {
     __syncthreads();  // the rings become the merge buffer
     w.park(so, sm, warp);
     __syncthreads();
-    if (tid < n_rows) {
+    const int rows = s_it.n_rows;
+    if (tid < rows) {
       float M, L, wt[kPagedWarps];
       paged_merge_row(sm, tid, M, L, wt);
 #pragma unroll
@@ -218,10 +252,10 @@ paged_attention_kernel(const PagedAttnParams p) {
       sw[tid * (kPagedWarps + 2) + kPagedWarps + 1] = L;
     }
     __syncthreads();
-    const bool begins = s0 == 0, whole = begins && s1 == rt.tiles;
+    const bool begins = s_it.begins, whole = s_it.whole;
     auto out_row = [&](int r) -> long long {
-      const int rr = group * 16 + r;
-      return (long long)(rt.r.t0 + rr / p.G) * p.Hq + h * p.G + rr % p.G;
+      const int rr = s_it.first + r;
+      return (long long)(s_it.t0 + rr / p.G) * p.Hq + s_it.h * p.G + rr % p.G;
     };
     auto write = [&](int r, int pos, float O, float M, float L) {
       const long long row = out_row(r);
@@ -229,7 +263,7 @@ paged_attention_kernel(const PagedAttnParams p) {
       if (p.lse != nullptr && pos == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
     };
     const int slot = cta * 2 + (begins ? 1 : 0);
-    for (int x = tid; x < n_rows * kD; x += kThreads) {
+    for (int x = tid; x < rows * kD; x += kThreads) {
       const int r = x / kD, pos = x % kD;
       const float* wt = sw + r * (kPagedWarps + 2);
       float O = 0.f;
@@ -244,71 +278,81 @@ paged_attention_kernel(const PagedAttnParams p) {
         if (pos == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(M, L);
       }
     }
-    if (!whole) {
-      // Partials visible before the count; the CTA that counts the last one merges.
-      const long long g0 = cur - s0;  // the item's first tile
-      const int ca = (int)(g0 / per), cb = (int)((g0 + rt.tiles - 1) / per);
-      const int n = cb - ca + 1;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(p.counters + ca, 1) == n - 1;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        auto slot_of = [&](int i) { return i == 0 ? ca * 2 + 1 : (ca + i) * 2; };
-        // eight lanes to a row: the common max and sum
-        float* st = so;  // [16][2]
-        {
-          const int r = tid >> 3, k = tid & 7;
-          float M = -INFINITY, L = 0.f;
-          if (r < n_rows)
-            for (int i = k; i < n; i += 8) M = fmaxf(M, __ldcg(p.part_ml + (slot_of(i) * 16 + r) * 2));
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-          if (r < n_rows)
-            for (int i = k; i < n; i += 8) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot_of(i) * 16 + r) * 2));
-              if (ml.y != 0.f) L = fmaf(ptx::ex2(ml.x - M), ml.y, L);
-            }
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-          if (k == 0) {
-            st[r * 2] = M;
-            st[r * 2 + 1] = L;
-          }
-        }
-        __syncthreads();
-        for (int x = tid; x < n_rows * kD; x += kThreads) {
-          const int r = x / kD, pos = x % kD;
-          const float M = st[r * 2], L = st[r * 2 + 1];
-          float O = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const int s = slot_of(i);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (s * 16 + r) * 2));
-            const float v = __ldcg(p.part_o + ((long long)s * 16 + r) * kD + pos);
-            if (ml.y != 0.f) O = fmaf(ptx::ex2(ml.x - M), v, O);
-          }
-          write(r, pos, O, M, L);
-        }
-      }
+    if (begins && !whole && tid == 0) {
+      const int last = (int)((s_it.item_at + s_it.units - 1) / run_length());  // the CTA that ends the item
+      SplitItem it;
+      it.n = last - cta + 1;
+      it.n_rows = rows;
+      it.first = s_it.first;
+      it.t0 = s_it.t0;
+      it.h = s_it.h;
+      p.split[cta] = it;
     }
+    cur = s_it.cur;
+    off = s_it.off;
+    b = s_it.b;
     __syncthreads();  // the merge buffer becomes the rings again
-    cur += s1 - s0;
-    off += s1 - s0;
   }
 }
 
-// Clears the counters; the attention kernel may start meanwhile (programmatic dependent
-// launch) and waits for this one before it counts.
-__global__ void paged_clear_kernel(int* counters) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < kCtas; i += blockDim.x) counters[i] = 0;
+// One warp for each row of an item that a CTA begins and others continue: the partials'
+// common max, their weights, and the weighted sum, four (kD = 64: two) columns a lane.
+template <bool kF8, int kD>
+__global__ void __launch_bounds__(128)
+paged_merge_kernel(const PagedAttnParams p) {
+  using W = PagedWarp<kF8, kD, 32, true, false>;
+  constexpr int kCols = kD / 32;
+  const int cta = blockIdx.x, r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitItem it = p.split[cta];
+  if (it.n == 0 || r >= it.n_rows) return;
+  auto ml_of = [&](int i) {
+    const int slot = i == 0 ? cta * 2 + 1 : (cta + i) * 2;
+    return *reinterpret_cast<const float2*>(p.part_ml + (slot * 16 + r) * 2);
+  };
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < it.n; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float O[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) O[c] = 0.f;
+  for (int base = 0; base < it.n; base += 32) {
+    const float2 ml = base + lane < it.n ? ml_of(base + lane) : make_float2(0.f, 0.f);
+    const float f = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
+    if (ml.y != 0.f) L = fmaf(f, ml.y, L);
+    const int n = min(32, it.n - base);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const int slot = base + i == 0 ? cta * 2 + 1 : (cta + base + i) * 2;
+      const float* src = p.part_o + ((long long)slot * 16 + r) * kD + lane * kCols;
+      float v[kCols];
+      if constexpr (kCols == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(src);
+        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(src);
+        v[0] = w.x; v[1] = w.y;
+      }
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        if (fi != 0.f) O[c] = fmaf(fi, v[c], O[c]);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  const int rr = it.first + r;
+  const long long row = (long long)(it.t0 + rr / p.G) * p.Hq + it.h * p.G + rr % p.G;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+    p.out[row * kD + W::dim_of(lane * kCols + c)] = __float2bfloat16_rn(L == 0.f ? 0.f : O[c] / L);
+  if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
 }
 
 template <bool kF8, int kD, bool kHi, bool kCap>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
-  using W = PagedWarp<kF8, kD, kHi, kCap>;
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
   constexpr int ring = kPagedWarps * W::kWarpBytes;
   constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kPagedWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
@@ -322,20 +366,19 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) set |= 1ull << dev;
   }
-  paged_clear_kernel<<<1, 512, 0, st>>>(p.counters);
+  kernel<<<kCtas, kThreads, bytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.gridDim = dim3(kCtas, kHi ? 4 : 2);
+  cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<kF8, kD>, p);
 }
 
 template <bool kF8, int kD>
@@ -345,14 +388,13 @@ cudaError_t launch_d(const PagedAttnParams& p, bool hi, cudaStream_t st) {
   return cap ? launch<kF8, kD, false, true>(p, st) : launch<kF8, kD, false, false>(p, st);
 }
 
-constexpr size_t kCounterBytes = 2048;
-static_assert(kCounterBytes >= kCtas * sizeof(int), "one counter per CTA");
+constexpr size_t kItemBytes = sizeof(SplitItem) * kCtas;
 constexpr size_t kMlBytes = sizeof(float) * 2 * 2 * kCtas * 16;
 
 }  // namespace
 
 size_t paged_attention_workspace_bytes(int D) {
-  return kCounterBytes + kMlBytes + sizeof(float) * 2 * kCtas * 16 * (size_t)D;
+  return kItemBytes + kMlBytes + sizeof(float) * 2 * kCtas * 16 * (size_t)D;
 }
 
 unsigned read_and_clear_error_paged(cudaStream_t, std::string* where) {
@@ -377,9 +419,9 @@ int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, lon
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.counters = reinterpret_cast<int*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + kCounterBytes);
-  p.part_o = reinterpret_cast<float*>(ws + kCounterBytes + kMlBytes);
+  p.split = reinterpret_cast<SplitItem*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + kItemBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kItemBytes + kMlBytes);
   p.Hq = Hq;
   p.G = Hq / c.Hkv;
   p.scale = scale;

@@ -1,8 +1,7 @@
 // One warp's walk over key tiles of a paged cache: 16 query rows, an online softmax.
 //
 // Rows are (query, head) pairs of one KV head, the 16 rows of an m16n8k16 MMA.  A tile is
-// 32 keys (e4m3) or 16 keys (bf16), whole 16-key subtiles of one page each, brought into
-// shared memory with 16-byte cp.async through a ring of kStages tiles per warp.
+// kTileKeys keys, whole 16-key subtiles of one page each, brought into shared memory with 16-byte cp.async through a ring of kStages tiles per warp.
 //
 // e4m3 operands.  The tensor instruction takes fp16 pairs.  Codes become fp16 exactly
 // (one conversion per pair); the query row is multiplied by a power of two that puts its
@@ -79,9 +78,9 @@ struct PagedMask {
   const float* bias1;
 };
 
-template <bool kF8, int kD, bool kHi, bool kCap>
+template <bool kF8, int kD, int kTileKeys, bool kHi, bool kCap>
 struct PagedWarp {
-  static constexpr int kKeys = kF8 ? 32 : 16;
+  static constexpr int kKeys = kTileKeys;
   static constexpr int kSub = kKeys / 16;
   static constexpr int kRowBytes = kD * (kF8 ? 1 : 2);
   static constexpr int kTileBytes = kKeys * kRowBytes;
@@ -301,12 +300,14 @@ struct PagedWarp {
       const int mi = lane >> 3, ri = lane & 7;
       const int row = (mi >> 1) * 8 + ri;
 #pragma unroll
-      for (int s = 0; s < kKS; ++s) {
-        uint32_t b00, b01, b10, b11;
-        ptx::ldsm_x4(kt + at(row, 2 * s + (mi & 1)), b00, b01, b10, b11);
-        paged_mma<false>(sc[0][0], qa[s], b00, b01);
-        paged_mma<false>(sc[0][1], qa[s], b10, b11);
-      }
+      for (int t = 0; t < kSub; ++t)
+#pragma unroll
+        for (int s = 0; s < kKS; ++s) {
+          uint32_t b00, b01, b10, b11;
+          ptx::ldsm_x4(kt + at(16 * t + row, 2 * s + (mi & 1)), b00, b01, b10, b11);
+          paged_mma<false>(sc[t][0], qa[s], b00, b01);
+          paged_mma<false>(sc[t][1], qa[s], b10, b11);
+        }
     }
 
     // ---- logits (log2 units), masks, maxima
@@ -454,12 +455,14 @@ struct PagedWarp {
       const int mi = lane >> 3, ri = lane & 7;
       const int row = (mi & 1) * 8 + ri;
 #pragma unroll
-      for (int dn = 0; dn < kNT; dn += 2) {
-        uint32_t b00, b01, b10, b11;
-        ptx::ldsm_x4_t(vt + at(row, dn + (mi >> 1)), b00, b01, b10, b11);
-        paged_mma<false>(o[dn], pa[0], b00, b01);
-        paged_mma<false>(o[dn + 1], pa[0], b10, b11);
-      }
+      for (int t = 0; t < kSub; ++t)
+#pragma unroll
+        for (int dn = 0; dn < kNT; dn += 2) {
+          uint32_t b00, b01, b10, b11;
+          ptx::ldsm_x4_t(vt + at(16 * t + row, dn + (mi >> 1)), b00, b01, b10, b11);
+          paged_mma<false>(o[dn], pa[t], b00, b01);
+          paged_mma<false>(o[dn + 1], pa[t], b10, b11);
+        }
     }
   }
 

@@ -25,6 +25,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = kPagedWarps * 32;
 constexpr int kMaxBlocks = 32;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster, at most (the portable limit)
 
 struct PagedSelectParams {
   PagedView c;
@@ -43,7 +44,7 @@ struct PagedSelectParams {
 template <bool kF8, int kD, bool kHi>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_select_kernel(const PagedSelectParams p) {
-  using W = PagedWarp<kF8, kD, kHi, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_key[kMaxBlocks * 128 / kKeys];  // first key of each tile
@@ -127,22 +128,33 @@ paged_select_kernel(const PagedSelectParams p) {
     }
   }
   cluster.sync();
-  for (int x = part * kThreads + tid; x < p.G * kD; x += split * kThreads) {
-    const int row = x / kD, col = x % kD;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int i = 0; i < split; ++i) M = fmaxf(M, cluster.map_shared_rank(sl, i)[row * 2]);
-    for (int i = 0; i < split; ++i) {
-      const float* ml = cluster.map_shared_rank(sl, i) + row * 2;
-      if (ml[1] != 0.f) {
-        const float f = ptx::ex2(ml[0] - M);
-        L = fmaf(f, ml[1], L);
-        O = fmaf(f, cluster.map_shared_rank(sp, i)[row * kD + col], O);
-      }
+  for (int x = part * kThreads + tid; x < p.G * (kD / 4); x += split * kThreads) {
+    const int row = x / (kD / 4), col = x % (kD / 4) * 4;
+    float2 ml[kMaxSplit];
+    float4 v[kMaxSplit];
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) {
+      if (i >= split) break;
+      ml[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sl, i) + row * 2);
+      v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sp, i) + row * kD + col);
+    }
+    float M = -INFINITY, L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i)
+      if (i < split) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i) {
+      if (i >= split || ml[i].y == 0.f) continue;
+      const float f = ptx::ex2(ml[i].x - M);
+      L = fmaf(f, ml[i].y, L);
+      O[0] = fmaf(f, v[i].x, O[0]); O[1] = fmaf(f, v[i].y, O[1]);
+      O[2] = fmaf(f, v[i].z, O[2]); O[3] = fmaf(f, v[i].w, O[3]);
     }
     const long long at = (long long)token * p.Hq + h * p.G + row;
-    float y = L == 0.f ? 0.f : O / L;
-    if (p.gate != nullptr) y *= __bfloat162float(p.gate[at]);
-    p.out[at * kD + W::dim_of(col)] = __float2bfloat16_rn(y);
+    float inv = L == 0.f ? 0.f : 1.f / L;
+    if (p.gate != nullptr) inv *= __bfloat162float(p.gate[at]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.out[at * kD + W::dim_of(col + i)] = __float2bfloat16_rn(O[i] * inv);
     if (p.lse != nullptr && col == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
   }
   cluster.sync();  // no CTA leaves while others read its shared memory
@@ -150,7 +162,7 @@ paged_select_kernel(const PagedSelectParams p) {
 
 template <bool kF8, int kD, bool kHi>
 cudaError_t launch(const PagedSelectParams& p, cudaStream_t st) {
-  using W = PagedWarp<kF8, kD, kHi, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
   constexpr int ring = kPagedWarps * W::kWarpBytes;
   constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
@@ -215,7 +227,7 @@ int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long l
   const long long items = (long long)c.B * c.Qn * c.Hkv;
   const int tiles = S * block_size / (f8 ? 32 : 16);
   int split = 1;
-  while (split < 8 && items * split < 456 && tiles > split * kPagedWarps) split *= 2;
+  while (split < kMaxSplit && items * split < 456 && tiles > split * kPagedWarps) split *= 2;
   p.split = split;
   const bool hi = p.G > 8;
   cudaError_t e;

@@ -18,30 +18,65 @@ def lib():
     return sba.load_library()
 
 
-POOL = dict(k_pages=FAKE, v_pages=FAKE, k_scales=FAKE, v_scales=FAKE, page_stride=2 * 64 * 128, num_pages=4,
-            page_size=64, page_table=FAKE, table_width=8, seq_lens=FAKE)
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales", "page_table", "seq_lens",
+                                               "cu")] + [("page_stride", ctypes.c_longlong)]
+    _fields_ += [(n, ctypes.c_int) for n in ("num_pages", "page_size", "Hkv", "D", "dt", "table_width", "B", "Q", "N")]
+
+
+def struct(name, pointers, longs, rest):
+    p, ll = ctypes.c_void_p, ctypes.c_longlong
+    fields = [("cache", Cache)] + [(n, p) for n in pointers] + [(n, ll) for n in longs]
+    fields += [(n, ctypes.c_float if n in ("scale", "cap") else ctypes.c_int) for n in rest]
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+APPEND = struct("Append", ("k", "v", "q", "qo", "cos", "sin"), ("ks", "vs", "qs", "qos"), ("Hq", "rot", "max_pos", "inter"))
+ATTEND = struct("Attend", ("q", "bias", "out", "lse", "ws"), ("ws_bytes", "qs"),
+                ("Hq", "scale", "left", "right", "cap", "sinks", "per_head"))
+SELECT = struct("Select", ("q", "idx", "cnt", "gate", "out", "lse"), ("qs",),
+                ("Hq", "n", "S", "bs", "causal", "scale"))
+POOL = dict(k_pages=FAKE, v_pages=FAKE, k_scales=FAKE, v_scales=FAKE, page_table=FAKE, seq_lens=FAKE, cu=None,
+            page_stride=2 * 64 * 128, num_pages=4, page_size=64, Hkv=2, D=128, dt=2, table_width=8, B=3, Q=2, N=6)
+
+
+def call(fn, kind, defaults, change):
+    own = [n for n, _ in kind._fields_]
+    cache = Cache(**{**POOL, **{n: v for n, v in change.items() if n in POOL}})
+    args = kind(cache=cache, **{**defaults, **{n: v for n, v in change.items() if n in own}})
+    return fn(ctypes.string_at(ctypes.addressof(args), ctypes.sizeof(args)), None)
 
 
 def append(lib, **kw):
-    a = dict(k=FAKE, ks=256, v=FAKE, vs=256, q=FAKE, qs=1024, qo=FAKE, qos=1024, cos=FAKE, sin=FAKE, rot=128,
-             max_pos=512, inter=0, **POOL, cu=None, B=3, Q=2, N=6, Hq=8, Hkv=2, D=128, dt=2, stream=None)
-    a.update(kw)
-    return lib.sba_paged_kv_append(*a.values())
+    d = dict(k=FAKE, ks=256, v=FAKE, vs=256, q=FAKE, qs=1024, qo=FAKE, qos=1024, cos=FAKE, sin=FAKE, rot=128,
+             max_pos=512, inter=0, Hq=8)
+    return call(lib.sba_paged_kv_append, APPEND, d, kw)
 
 
 def attend(lib, **kw):
-    need = lib.sba_paged_attention_workspace_size(128)
-    a = dict(q=FAKE, qs=1024, **POOL, cu=None, B=3, Q=2, N=6, Hq=8, Hkv=2, D=128, dt=2, scale=0.0, left=-1, right=-1,
-             cap=0.0, bias=None, sinks=0, per_head=0, out=FAKE, lse=None, ws=FAKE, ws_bytes=need, stream=None)
-    a.update(kw)
-    return lib.sba_paged_attention_fwd(*a.values())
+    d = dict(q=FAKE, qs=1024, Hq=8, scale=0.0, left=-1, right=-1, cap=0.0, bias=None, sinks=0, per_head=0, out=FAKE,
+             lse=None, ws=FAKE, ws_bytes=lib.sba_paged_attention_workspace_size(128))
+    return call(lib.sba_paged_attention_fwd, ATTEND, d, kw)
 
 
 def select(lib, **kw):
-    a = dict(q=FAKE, qs=1024, **POOL, B=3, Q=2, Hq=8, Hkv=2, D=128, dt=2, idx=FAKE, cnt=None, n=4, S=4, bs=64,
-             causal=1, scale=0.0, gate=None, out=FAKE, lse=None, stream=None)
-    a.update(kw)
-    return lib.sba_nsa_select_paged_fwd(*a.values())
+    d = dict(q=FAKE, qs=1024, Hq=8, idx=FAKE, cnt=None, n=4, S=4, bs=64, causal=1, scale=0.0, gate=None, out=FAKE,
+             lse=None)
+    return call(lib.sba_nsa_select_paged_fwd, SELECT, d, kw)
+
+
+def test_binding_packs_the_structs():
+    """The binding's formats have the layout of the structs as the C compiler lays them out."""
+    import selected_block_attention_gb300 as sba
+
+    for fmt, kind in ((sba._APPEND_ARGS, APPEND), (sba._ATTENTION_ARGS, ATTEND), (sba._SELECT_ARGS, SELECT)):
+        n = len(fmt.unpack(bytes(fmt.size)))
+        flat = [(f, t) for f, t in Cache._fields_] + list(kind._fields_[1:])
+        assert n == len(flat)
+        vals = [float(i) if t is ctypes.c_float else i for i, (_, t) in enumerate(flat, 1)]
+        got = kind.from_buffer_copy(fmt.pack(*vals).ljust(ctypes.sizeof(kind), b"\0"))
+        for i, (f, _) in enumerate(flat, 1):
+            assert getattr(got.cache if i <= len(Cache._fields_) else got, f) == i, f
 
 
 COMMON = [(dict(k_pages=None), -1, b"null"), (dict(page_table=None), -1, b"null"), (dict(seq_lens=None), -1, b"null"),
@@ -55,8 +90,8 @@ COMMON = [(dict(k_pages=None), -1, b"null"), (dict(page_table=None), -1, b"null"
 
 @pytest.mark.parametrize("change,code,text", COMMON)
 def test_cache_arguments(lib, change, code, text):
-    for call in (append, attend, select):
-        assert call(lib, **change) == code, call.__name__
+    for entry in (append, attend, select):
+        assert entry(lib, **change) == code, entry.__name__
         assert text in lib.sba_last_error()
 
 
