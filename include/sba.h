@@ -56,8 +56,8 @@ SBA_API const char* sba_last_error(void);
 
 /*
  * sba_set_wait_timeout_cycles -- limit, in SM clock cycles, on every internal wait of
- * the warp-specialised kernels (the NSA selection forward on tensor cores and the
- * block-sparse / ragged block attention).  No counterpart on the pages: it is the
+ * the warp-specialised kernels (the NSA selection forward on tensor cores, the
+ * block-sparse / ragged block attention and the paged attention of many rows).  No counterpart on the pages: it is the
  * library's failure detection.  A wait that runs past the limit records the kernel,
  * role, barrier and work item in the device error word, makes every other wait of its
  * CTA return at once, drains the copies already issued, frees its tensor memory and
@@ -495,9 +495,10 @@ SBA_API int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t 
 
 /*
  * sba_paged_attention_workspace_size -- bytes of device workspace sba_paged_attention_fwd
- * needs: it depends on the head dimension only.  Returns 0 for an unsupported D.
+ * needs for B rows with N query tokens in all (it does not depend on the lengths).  Returns
+ * 0 for invalid sizes.
  */
-SBA_API size_t sba_paged_attention_workspace_size(int D);
+SBA_API size_t sba_paged_attention_workspace_size(int B, int N, int Hq, int Hkv, int D);
 
 /*
  * sba_paged_attention_fwd -- attention of one or several query tokens per row over a paged
@@ -512,8 +513,12 @@ SBA_API size_t sba_paged_attention_workspace_size(int D);
  * Pages wholly left of every query's window, but for the sinks', are not read, so a server
  * may give them back.  The grid does not depend on the lengths, which the kernel reads on
  * the device: a captured call serves whatever seq_lens holds when it is replayed.
- * Results do not depend on timing.  Internally, on `stream`: the attention kernel and a
- * kernel that merges the items it cut into runs.
+ * Results do not depend on timing.  A key that some query of the row sees takes part with
+ * weight 0 in the products of the row's other queries, so its value must be finite.
+ * Internally, on `stream`: the attention kernel (with 64 or more (query, head) rows for each
+ * row and KV head on average and no sinks the one with accumulators in tensor memory, whose
+ * waits are bounded, see sba_set_wait_timeout_cycles) and a kernel that merges the items it
+ * cut into runs.
  */
 typedef struct sba_paged_attention_args {
   sba_paged_cache cache; /* read only */
@@ -525,7 +530,7 @@ typedef struct sba_paged_attention_args {
   void* out;              /* [N, Hq, D] bf16 (written) */
   float* lse;             /* [N, Hq] (written) or NULL */
   void* workspace;        /* device scratch, 16-byte aligned, caller-owned, of at least
-                             sba_paged_attention_workspace_size(D) bytes; needs no
+                             sba_paged_attention_workspace_size() bytes; needs no
                              initialisation.  Calls that may overlap on the GPU need one
                              each. */
   size_t workspace_bytes;

@@ -121,7 +121,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sba_nsa_select_bwd.argtypes = [vp, vp, vp, vp, f32p, vp, i32p, i32p, ci, ci, i32p, ci, ci, ci,
                                        ci, ci, ci, ci, ci, cf, ci, vp, vp, vp, vp, csz, vp]
     lib.sba_nsa_select_bwd.restype = ci
-    lib.sba_paged_attention_workspace_size.argtypes = [ci]
+    lib.sba_paged_attention_workspace_size.argtypes = [ci] * 5
     lib.sba_paged_attention_workspace_size.restype = csz
     for fn in (lib.sba_paged_kv_append, lib.sba_paged_attention_fwd, lib.sba_nsa_select_paged_fwd):
         fn.argtypes = [ctypes.c_char_p, vp]  # the packed argument struct, the stream
@@ -595,8 +595,9 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=No
     return q_out
 
 
-def paged_attention_workspace_size(D) -> int:
-    return int(load_library().sba_paged_attention_workspace_size(D))
+def paged_attention_workspace_size(B, N, Hq, Hkv, D) -> int:
+    """Bytes for B rows with N query tokens in all."""
+    return int(load_library().sba_paged_attention_workspace_size(B, N, Hq, Hkv, D))
 
 
 def _results(q, index, out, lse, return_lse):
@@ -632,7 +633,7 @@ def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=N
         bias_p = _at(sink_bias, "sink_bias", index, torch.float32, (hq, num_sinks) if per_head else (num_sinks,))
     out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
     if workspace is None:
-        workspace = torch.empty(lib.sba_paged_attention_workspace_size(d) or 16, dtype=torch.uint8,
+        workspace = torch.empty(lib.sba_paged_attention_workspace_size(batch, N, hq, hkv, d) or 16, dtype=torch.uint8,
                                 device=q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")

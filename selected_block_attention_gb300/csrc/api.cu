@@ -617,8 +617,9 @@ int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) 
                              a.max_pos, a.interleaved ? 1 : 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t sba_paged_attention_workspace_size(int D) {
-  return D == 64 || D == 128 ? paged_attention_workspace_bytes(D) : 0;
+size_t sba_paged_attention_workspace_size(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 1 || N < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return paged_attention_workspace_bytes(B, N, Hq, Hkv, D);
 }
 
 int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_stream_t stream) {
@@ -640,7 +641,7 @@ int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_stream_t s
   SBA_SUPPORT(a.num_sinks <= 16, "num_sinks must be <= 16");
   SBA_SUPPORT((long long)c.N * a.Hq < (1LL << 31), "tokens * Hq must be < 2^31");
   SBA_REQUIRE(a.workspace != nullptr && aligned16(a.workspace) &&
-                  a.workspace_bytes >= paged_attention_workspace_bytes(D),
+                  a.workspace_bytes >= paged_attention_workspace_bytes(c.B, c.N, a.Hq, c.Hkv, D),
               "workspace missing, misaligned or smaller than sba_paged_attention_workspace_size()");
   const float scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
   return launch_paged_attention(c, a.cache.dtype == SBA_E4M3, D, a.q, a.q_stride, a.Hq, scale,
@@ -697,7 +698,8 @@ int sba_check_error(sba_stream_t stream) {
   unsigned w = read_and_clear_error_nsa(s, &where) | read_and_clear_error_mask(s, &where) |
                read_and_clear_error_blocksparse(s, &where) | read_and_clear_error_decode(s, &where) |
                read_and_clear_error_nsa_bwd(s, &where) | read_and_clear_error_append(s, &where) |
-               read_and_clear_error_paged(s, &where) | read_and_clear_error_select(s, &where);
+               read_and_clear_error_paged(s, &where) | read_and_clear_error_select(s, &where) |
+               read_and_clear_error_chunk(s, &where);
   if (w & kDevErrTimeout)
     return set_error(SBA_ERR_TIMEOUT, "a kernel gave up on a bounded internal wait" + where);
   if (w & kDevErrInput)

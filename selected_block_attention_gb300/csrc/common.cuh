@@ -39,6 +39,7 @@ unsigned read_and_clear_error_decode(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_nsa_bwd(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_append(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_paged(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_chunk(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_select(cudaStream_t s, std::string* where);
 
 // Launch entry points implemented by the kernel files (arguments already validated).
@@ -92,7 +93,12 @@ int launch_paged_append(const PagedView& c, int f8, int D, const void* k, long l
                         const void* v, long long v_tok, const void* q, long long q_tok, void* q_out,
                         long long qo_tok, int Hq, const float* cosp, const float* sinp, int rot,
                         int max_pos, int interleaved, cudaStream_t stream);
-size_t paged_attention_workspace_bytes(int D);
+bool paged_many_rows(int B, int N, int Hq, int Hkv);
+size_t paged_chunk_workspace_bytes(int D);
+int launch_paged_chunk(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq, float scale,
+                       int window_left, int window_right, float cap, void* out, float* lse,
+                       void* workspace, cudaStream_t stream);
+size_t paged_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq,
                            float scale, int window_left, int window_right, float cap,
                            const float* sink_bias, int num_sinks, int sink_per_head, void* out,

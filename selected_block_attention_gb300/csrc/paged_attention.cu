@@ -16,6 +16,7 @@
 // output; else the item's partials (o, m, l) go to the workspace, two slots per CTA, and
 // paged_merge_kernel, launched behind this one with its start overlapped, adds them up in
 // the order of the line, so results do not depend on timing.
+#include <algorithm>
 #include <string>
 
 #include "paged_core.cuh"
@@ -393,8 +394,15 @@ constexpr size_t kMlBytes = sizeof(float) * 2 * 2 * kCtas * 16;
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(int D) {
-  return kItemBytes + kMlBytes + sizeof(float) * 2 * kCtas * 16 * (size_t)D;
+// Whether a call's rows have (query, head) rows enough for the kernel with tensor-memory
+// accumulators (paged_chunk.cu).
+bool paged_many_rows(int B, int N, int Hq, int Hkv) {
+  return (long long)N * (Hq / Hkv) >= 64LL * B;
+}
+
+size_t paged_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+  const size_t few = kItemBytes + kMlBytes + sizeof(float) * 2 * kCtas * 16 * (size_t)D;
+  return paged_many_rows(B, N, Hq, Hkv) ? std::max(few, paged_chunk_workspace_bytes(D)) : few;
 }
 
 unsigned read_and_clear_error_paged(cudaStream_t, std::string* where) {
@@ -411,6 +419,9 @@ int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, lon
                            float scale, int window_left, int window_right, float cap,
                            const float* sink_bias, int num_sinks, int sink_per_head, void* out,
                            float* lse, void* workspace, cudaStream_t stream) {
+  if (num_sinks == 0 && paged_many_rows(c.B, c.N, Hq, c.Hkv))
+    return launch_paged_chunk(c, f8, D, q, q_tok, Hq, scale, window_left, window_right, cap, out, lse, workspace,
+                              stream);
   PagedAttnParams p;
   p.c = c;
   p.q = static_cast<const __nv_bfloat16*>(q);

@@ -1,0 +1,1012 @@
+// Attention of many query tokens per row over a paged cache, on the tensor cores' own
+// memory: paged_chunk_kernel (prompts and chunks of prompts; few tokens a row run in
+// paged_attention.cu, which this file's definitions follow).
+//
+// An item is (batch row, KV head, group of 256 (query, head) rows); its two halves of 128
+// rows read the same keys, walked in tiles of 64.  As in paged_attention.cu the items'
+// tiles form one line cut into equal runs, here one for each of kCtas CTAs (one per SM),
+// and a second kernel merges the items that were cut.  A CTA's warps:
+//   warps 0..3   loaders: pairs take the tiles in turn, a warp half a tile.  e4m3: 16-byte
+//                loads into registers (a pair's next tile is on its way while the other
+//                pair's is stored), codes to fp16 (exact), stored in the 128-byte swizzle
+//                that the MMA reads; bf16: cp.async straight into it.  The pages' scales
+//                travel with the value tile.
+//   warps 4, 5   MMA issuers, one for each half w: S_w = Q_w K^T into one of two buffers,
+//                O_w += P_w V with P_w in tensor memory over the S it came from, in the
+//                order S(0) S(1) | PV(t) S(t + 2) | ...
+//   warp 6       scheduler: finds the run's items and publishes them (warp 7 idle)
+//   warps 8..15  softmax, four for each half, one thread per row: it brings its query row
+//                in (e4m3: times a power of two into fp16, see paged_core.cuh), takes its
+//                64 scores out of tensor memory, keeps (m, l, u) as described there,
+//                writes P, and at the end of the item writes the row or its partial.
+// Tensor memory: S_w,0 S_w,1 (64 columns each) for w = 0, 1, then O_0, O_1: 512 columns.
+//
+// The MMAs bound it: per tile and half an S of N = 64 costs 8 x 50 cycles and a PV of
+// N = 128 4 x 64; the conversion of a tile (2 x 8 loads, 128 conversions and 32 stores a
+// thread) and the softmax of 256 rows run beside them.
+#include <climits>
+#include <cstdio>
+#include <string>
+
+#include "paged_core.cuh"
+#include "sync.cuh"
+
+namespace sba {
+
+static __device__ DevError g_err_chunk = {0u, 0u, 0};
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 512;
+constexpr int kCtas = 152;    // one for each SM
+constexpr int kM = 128;       // rows of a half
+constexpr int kRows = 2 * kM;
+constexpr int kKT = 64;       // keys of a tile
+constexpr int kMinTiles = 4;  // tiles of a run, at least
+constexpr int kItemCost = 6;  // tiles that an item's queries and output are worth
+constexpr float kRaise = 8.f;
+constexpr float kRaiseU = 6.f;
+
+struct ChunkParams {
+  PagedView c;
+  const __nv_bfloat16* q;
+  long long q_tok;
+  __nv_bfloat16* out;
+  float* lse;
+  struct SplitChunk* split;  // [kCtas]
+  float* part_ml;            // [2 kCtas][kRows][2]
+  float* part_o;             // [2 kCtas][D][kRows]
+  int Hq, G;
+  float scale, cap;
+  int window_left, window_right;
+  long long wait_limit;
+};
+
+// The item that a CTA begins but does not end (n > 1 partials: slot 2 cta + 1, then
+// 2 (cta + i)); n = 0: none.
+struct SplitChunk {
+  int n, rows, first, t0, h;
+  int pad[3];
+};
+
+enum Role : unsigned { kRoleLoader = 1, kRoleMma = 2, kRoleSoftmax = 3, kRoleScheduler = 4 };
+enum BarId : unsigned { kBarQ = 1, kBarKFull, kBarKEmpty, kBarVFull, kBarVEmpty, kBarS, kBarP, kBarPvTile, kBarPvLast, kBarO, kBarSegFull, kBarSegEmpty };
+
+// Key tiles [ka, kb) that a group's queries see, and its place on the line: max(kb - ka,
+// 1) tiles after kItemCost empty ones.
+struct GroupTiles {
+  int ka, kb, units;
+};
+__device__ __forceinline__ int win_lo(const ChunkParams& p, const PagedRow& r, int i) {
+  return p.window_left < 0 ? 0 : (int)min(max((long long)r.len - r.n + i - p.window_left, 0LL), (long long)r.len);
+}
+__device__ __forceinline__ int win_end(const ChunkParams& p, const PagedRow& r, int i) {  // one past the last key
+  return p.window_right < 0 ? r.len
+                            : (int)min(max((long long)r.len - r.n + i + p.window_right + 1, 0LL), (long long)r.len);
+}
+__device__ __forceinline__ GroupTiles group_tiles(const ChunkParams& p, const PagedRow& r, int g) {
+  const int rows = r.n * p.G, r0 = g * kRows, r1 = min(r0 + kRows, rows) - 1;
+  const int lo = win_lo(p, r, r0 / p.G), hi = win_end(p, r, r1 / p.G);
+  GroupTiles t;
+  t.ka = lo / kKT;
+  t.kb = hi > lo ? (hi + kKT - 1) / kKT : t.ka;
+  t.units = kItemCost + max(t.kb - t.ka, 1);
+  return t;
+}
+__device__ __forceinline__ int groups_of(const ChunkParams& p, const PagedRow& r) {
+  return (int)(((long long)r.n * p.G + kRows - 1) / kRows);
+}
+__device__ __forceinline__ long long row_units(const ChunkParams& p, const PagedRow& r) {
+  const int n = groups_of(p, r);
+  long long s = 0;
+  for (int g = 0; g < n; ++g) s += group_tiles(p, r, g).units;
+  return s;  // of one KV head
+}
+
+// One item's part of the CTA's run, as the scheduler publishes it.
+struct Segment {
+  PagedRow r;
+  int b, h, g, rows;   // rows of the group
+  int t0, nt;          // key tiles [t0, t0 + nt)
+  int lo;              // first key of the row that may be read
+  int begins, whole;
+  int n;               // CTAs of the item, when it begins here
+  int end;             // no more items
+};
+constexpr int kSegs = 4;  // slots; each is read by 4 loader, 2 MMA and 8 softmax warps
+// Walks the run.
+struct Walker {
+  long long cur, end, per;
+  int b, h, g, off, groups;
+  PagedRow r;
+  __device__ __forceinline__ void row(const ChunkParams& p) {
+    bool bad;
+    r = paged_row(p.c, b, &bad);
+    groups = groups_of(p, r);
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p, int cta, Segment& s) {
+    while (cur < end) {
+      while (g >= groups) {  // also rows without tokens
+        g = 0;
+        if (groups == 0 || ++h == p.c.Hkv) {
+          h = 0;
+          ++b;
+          row(p);
+        }
+      }
+      const GroupTiles t = group_tiles(p, r, g);
+      const int x0 = off, x1 = (int)min((long long)t.units, x0 + (end - cur));
+      const long long at = cur - x0;
+      cur += x1 - x0;
+      off = x1;
+      s.g = g;
+      if (x1 == t.units) {
+        off = 0;
+        ++g;
+      }
+      if (x1 <= kItemCost) continue;  // nothing but the empty tiles
+      const int s0 = max(x0 - kItemCost, 0), s1 = x1 - kItemCost;
+      s.r = r;
+      s.b = b;
+      s.h = h;
+      s.rows = min(kRows, r.n * p.G - s.g * kRows);
+      s.t0 = t.ka + s0;
+      s.nt = max(min(t.ka + s1, t.kb) - s.t0, 0);
+      s.begins = s0 == 0;
+      s.whole = s.begins && x1 == t.units;
+      s.n = (int)((at + t.units - 1) / per) - cta + 1;
+      s.lo = win_lo(p, r, 0);
+      s.end = 0;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kQPanel = kM * 128;
+  static constexpr int kQBytes = kPanels * kQPanel;
+  static constexpr int kTPanel = kKT * 128;
+  static constexpr int kTBytes = kPanels * kTPanel;
+  static constexpr int kStagesK = 3;
+  static constexpr int kStages = 4;
+  static constexpr int kOffK = 2 * kQBytes;
+  static constexpr int kOffV = kOffK + kStagesK * kTBytes;
+  static constexpr int kOffMeta = kOffV + kStages * kTBytes;  // per V stage: 4 key, 4 value scales
+  static constexpr int kOffSegs = kOffMeta + kStages * 32;
+  static constexpr int kOffBars = (kOffSegs + kSegs * (int)sizeof(Segment) + 7) & ~7;
+  static constexpr int kNumBars = 2 * kSegs + 2 + 2 * kStagesK + 2 * kStages + 4 + 4 + 2 + 2 + 2 + 2;
+  static constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static constexpr int kOCol = 4 * kKT;
+  static constexpr int kTmemCols = 512;
+  static_assert(kOCol + 2 * D <= kTmemCols, "tensor memory");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void mask_columns(float (&x)[kKT], int jlo, int jhi) {
+  const uint32_t w0 = (jlo <= 31 && jhi >= 0)
+      ? ((jhi >= 31 ? 0xffffffffu : ((2u << jhi) - 1u)) & (0xffffffffu << min(max(jlo, 0), 31))) : 0u;
+  const uint32_t w1 = (jhi >= 32 && jlo <= 63)
+      ? ((jhi >= 63 ? 0xffffffffu : ((2u << (jhi - 32)) - 1u)) & (0xffffffffu << max(jlo - 32, 0))) : 0u;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[j] = (w0 & (1u << j)) ? x[j] : -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[32 + j] = (w1 & (1u << j)) ? x[32 + j] : -INFINITY;
+}
+
+// Log2 logits under the cap: see PagedWarp::logit.
+__device__ __forceinline__ float capped(float y, float c1k) {
+  const float e = ex2(y * (2.f * kPagedLog2e));
+  float rc;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
+  const float far = fmaf(-2.f, rc, 1.f);
+  const float y2 = y * y;
+  float pl = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
+  pl = fmaf(y2, pl, 2.f / 15.f);
+  pl = fmaf(y2, pl, -1.f / 3.f);
+  const float near = fmaf(y * y2, pl, y);
+  return c1k * (fabsf(y) < 0.25f ? near : far);
+}
+
+template <bool kF8, int D, bool kCap>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_chunk_kernel(const ChunkParams p) {
+  using C = Cfg<D>;
+  constexpr uint32_t kFmt = kF8 ? 0u : 1u;  // operands: fp16 or bf16
+  constexpr uint32_t kIdescQK = make_idesc(128, kKT, kFmt, false, false);
+  constexpr uint32_t kIdescPV = make_idesc(128, D, kFmt, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ long long s_sum[kThreads / 32], s_total, s_at;
+  __shared__ int s_row;
+  uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+  uint64_t* seg_full = bb;  bb += kSegs;
+  uint64_t* seg_empty = bb; bb += kSegs;
+  uint64_t* q_full = bb;   bb += 2;
+  uint64_t* k_full = bb;   bb += C::kStagesK;
+  uint64_t* k_empty = bb;  bb += C::kStagesK;
+  uint64_t* v_full = bb;   bb += C::kStages;
+  uint64_t* v_empty = bb;  bb += C::kStages;
+  uint64_t* s_full = bb;   bb += 4;  // [2 w + buffer]
+  uint64_t* p_full = bb;   bb += 4;
+  uint64_t* pv_tile = bb;  bb += 2;
+  uint64_t* pv_last = bb;  bb += 2;
+  uint64_t* o_empty = bb;  bb += 2;
+  uint64_t* mma_done = bb; bb += 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const Abort ab{abort_flag, &g_err_chunk, 5u, p.wait_limit};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+
+  // ---- the CTA's run
+  {
+    const int chunk = (p.c.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * chunk, p.c.B), b1 = min(b0 + chunk, p.c.B);
+    long long sum = 0;
+    bool any_bad = false;
+    for (int b = b0; b < b1; ++b) {
+      bool bad;
+      const PagedRow r = paged_row(p.c, b, &bad);
+      any_bad |= bad;
+      sum += row_units(p, r) * p.c.Hkv;
+    }
+    if (any_bad && cta == 0) atomicOr(&g_err_chunk.flags, (unsigned)kDevErrInput);
+    long long pre = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, pre, d);
+      if (lane >= d) pre += x;
+    }
+    if (lane == 31) s_sum[warp] = pre;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i == warp) pre += total;
+      total += s_sum[i];
+    }
+    pre -= sum;
+    const long long per = max((total + kCtas - 1) / kCtas, (long long)(kMinTiles + kItemCost));
+    const long long t0 = (long long)cta * per;
+    if (t0 >= pre && t0 < pre + sum) {
+      long long off = t0 - pre;
+      int b = b0;
+      for (;; ++b) {
+        bool bad;
+        const long long n = row_units(p, paged_row(p.c, b, &bad)) * p.c.Hkv;
+        if (off < n) break;
+        off -= n;
+      }
+      s_row = b;
+      s_at = off;
+    }
+    if (tid == 0) s_total = total;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSegs; ++i) { mbar_init(&seg_full[i], 1); mbar_init(&seg_empty[i], 14); }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&q_full[w], 4);
+      mbar_init(&pv_tile[w], 1); mbar_init(&pv_last[w], 1);
+      mbar_init(&o_empty[w], 4); mbar_init(&mma_done[w], 1);
+    }
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); }
+    // both loader warps fill a stage, both MMA warps release it
+    for (int i = 0; i < C::kStagesK; ++i) { mbar_init(&k_full[i], 2); mbar_init(&k_empty[i], 2); }
+    for (int i = 0; i < C::kStages; ++i) { mbar_init(&v_full[i], 2); mbar_init(&v_empty[i], 2); }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(tmem_holder, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t smem_base = smem_u32(smem);
+  auto seg_at = [&](int slot) -> Segment& {
+    return *reinterpret_cast<Segment*>(smem + C::kOffSegs + slot * (int)sizeof(Segment));
+  };
+
+  // registers of the four warpgroups: 104 + 72 + 168 + 168 = 4 x 128
+  if (warp < 4) {
+    // ------------------------------------------------------------------ loaders
+    setmaxnreg_dec<104>();
+    constexpr int kItem = kF8 ? 1 : 2;
+    constexpr int kCpr = D * kItem / 16;  // 16-byte chunks of a row
+    constexpr int kStep = 32 / kCpr;      // rows of a warp-wide access
+    constexpr int kN = 32 / kStep;        // accesses for the warp's 32 keys
+    const int pair = warp >> 1, half = warp & 1;
+    const int chunk = lane % kCpr, row0 = lane / kCpr;
+    const int pmask = (1 << p.c.p_shift) - 1;
+    int ks = 0; uint32_t kphase = 0;
+    int vs = 0; uint32_t vphase = 0;
+    auto next_k = [&]() { if (++ks == C::kStagesK) { ks = 0; kphase ^= 1; } };
+    auto next_v = [&]() { if (++vs == C::kStages) { vs = 0; vphase ^= 1; } };
+    // ---- the run's tiles in order; this pair's are every second one
+    int slot = -1; uint32_t sphase = 1;  // before slot 0 of phase 0
+    int t = -1, nt = 0;
+    bool have = true;
+    auto step = [&]() {
+      ++t;
+      while (have && t >= nt) {
+        if (slot >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&seg_empty[slot]);
+        }
+        if (slot < 0 || ++slot == kSegs) { slot = 0; sphase ^= 1; }
+        have = warp_wait(&seg_full[slot], sphase, ab, kRoleLoader, kBarSegFull, cta) && !seg_at(slot).end;
+        nt = have ? seg_at(slot).nt : 0;
+        t = 0;
+      }
+    };
+    // the tile that is fetched next: its keys (clamped to owned slots) and pages
+    int key0 = 0, cl = 0, ch = 0, h = 0, pg[2] = {0, 0};
+    auto look = [&]() {
+      if (!have) return;
+      const Segment& sg = seg_at(slot);
+      key0 = (sg.t0 + t) * kKT + half * 32;
+      cl = sg.lo;
+      ch = sg.r.len - 1;
+      h = sg.h;
+      const int* table = p.c.table + (long long)sg.b * p.c.width;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) pg[i] = __ldg(table + (min(max(key0 + 16 * i, cl), ch) >> p.c.p_shift));
+    };
+    auto page_at = [&](int i) -> int {
+      if ((unsigned)pg[i] < (unsigned)p.c.num_pages) return pg[i];
+      if (lane == 0) atomicOr(&g_err_chunk.flags, (unsigned)kDevErrInput);
+      return 0;  // any page that exists: the row's result is undefined, the read is not
+    };
+    auto byte_of = [&](int page) -> long long {
+      return page * p.c.page_bytes + (((long long)h << p.c.p_shift) * D) * kItem + chunk * 16;
+    };
+    auto row_off = [&](int i) -> int {  // of access i
+      return (min(max(key0 + row0 + i * kStep, cl), ch) & pmask) * (D * kItem);
+    };
+    if constexpr (kF8) {
+      uint4 rk[kN], rv[kN];
+      float kc[2], vc[2];
+      auto load = [&]() {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int page = page_at(x);
+          const uint8_t* k = p.c.k + byte_of(page);
+          const uint8_t* v = p.c.v + byte_of(page);
+#pragma unroll
+          for (int i = x * kN / 2; i < (x + 1) * kN / 2; ++i) {
+            rk[i] = __ldg(reinterpret_cast<const uint4*>(k + row_off(i)));
+            rv[i] = __ldg(reinterpret_cast<const uint4*>(v + row_off(i)));
+          }
+          kc[x] = __ldg(p.c.ks + (long long)page * p.c.Hkv + h);
+          vc[x] = __ldg(p.c.vs + (long long)page * p.c.Hkv + h);
+        }
+      };
+      // 16 codes as two 16-byte chunks of fp16; the halves go out in an order that spreads
+      // eight lanes over all banks
+      auto put = [&](uint8_t* tile, const uint4 (&raw)[kN]) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int row = half * 32 + row0 + i * kStep;
+          uint4 a, c;
+          e4m3x4_to_f16x2(raw[i].x, a.x, a.y);
+          e4m3x4_to_f16x2(raw[i].y, a.z, a.w);
+          e4m3x4_to_f16x2(raw[i].z, c.x, c.y);
+          e4m3x4_to_f16x2(raw[i].w, c.z, c.w);
+          uint8_t* dst = tile + (chunk >> 2) * C::kTPanel + row * 128;
+          const int first = (chunk & 3) * 2, flip = (chunk >> 2) & 1;
+          *reinterpret_cast<uint4*>(dst + (((first + flip) ^ (row & 7)) << 4)) = flip ? c : a;
+          *reinterpret_cast<uint4*>(dst + (((first + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : c;
+        }
+      };
+      step();
+      if (pair == 1) {
+        step();
+        next_k();
+        next_v();
+      }
+      look();
+      if (have) load();
+      bool more = have;  // a tile is in registers
+      step();
+      step();
+      look();
+      while (more) {
+        if (!warp_wait(&k_empty[ks], kphase ^ 1, ab, kRoleLoader, kBarKEmpty, cta)) break;
+        put(smem + C::kOffK + ks * C::kTBytes, rk);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[ks]);
+        if (!warp_wait(&v_empty[vs], vphase ^ 1, ab, kRoleLoader, kBarVEmpty, cta)) break;
+        put(smem + C::kOffV + vs * C::kTBytes, rv);
+        if (lane < 2) {
+          float* meta = reinterpret_cast<float*>(smem + C::kOffMeta + vs * 32);
+          meta[half * 2 + lane] = lane ? kc[1] : kc[0];
+          meta[4 + half * 2 + lane] = lane ? vc[1] : vc[0];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[vs]);
+        next_k(); next_k();
+        next_v(); next_v();
+        more = have;
+        if (have) load();
+        step();
+        step();
+        look();
+      }
+    } else {
+      auto copy = [&](uint8_t* tile, const uint8_t* pool) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* src = pool + byte_of(page_at(x));
+#pragma unroll
+          for (int i = x * kN / 2; i < (x + 1) * kN / 2; ++i) {
+            const int row = half * 32 + row0 + i * kStep;
+            paged_cp16(smem_u32(tile + (chunk >> 3) * C::kTPanel + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)),
+                       src + row_off(i));
+          }
+        }
+        paged_cp_commit();
+      };
+      step();
+      if (pair == 1) {
+        step();
+        next_k();
+        next_v();
+      }
+      look();
+      while (have) {
+        if (!warp_wait(&k_empty[ks], kphase ^ 1, ab, kRoleLoader, kBarKEmpty, cta)) break;
+        copy(smem + C::kOffK + ks * C::kTBytes, p.c.k);
+        if (!warp_wait(&v_empty[vs], vphase ^ 1, ab, kRoleLoader, kBarVEmpty, cta)) break;
+        copy(smem + C::kOffV + vs * C::kTBytes, p.c.v);
+        step();
+        step();
+        look();
+        paged_cp_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[ks]);
+        paged_cp_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[vs]);
+        next_k(); next_k();
+        next_v(); next_v();
+      }
+      paged_cp_wait<0>();
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ MMA issuer of half w
+    setmaxnreg_dec<72>();
+    if (warp < 6) {
+      const int w = warp - 4;
+      const uint32_t leader = elect_one();
+      uint32_t qph = 0u, oph = 0u, pph = 0u;
+      int ks = 0; uint32_t kphase = 0;
+      int vs = 0; uint32_t vphase = 0;
+      bool ok = true;
+      const uint64_t q_desc = make_sdesc(smem_base + w * C::kQBytes, 16, 1024, kLayoutSW128);
+      const uint64_t k_desc0 = make_sdesc(smem_base + C::kOffK, 16, 1024, kLayoutSW128);
+      const uint64_t v_desc0 = make_sdesc(smem_base + C::kOffV, C::kTPanel, 1024, kLayoutSW128);
+      const uint32_t o_tmem = tmem + C::kOCol + w * D;
+      auto s_tmem = [&](int buf) { return tmem + (2 * w + buf) * kKT; };
+      auto kstep = [](int kk, int panel) -> uint64_t {
+        return static_cast<uint64_t>(((kk / 4) * panel + (kk % 4) * 32) >> 4);
+      };
+      auto next_k = [&]() { if (++ks == C::kStagesK) { ks = 0; kphase ^= 1; } };
+      auto next_v = [&]() { if (++vs == C::kStages) { vs = 0; vphase ^= 1; } };
+      auto issue_s = [&](int buf) -> bool {
+        if (!warp_wait(&k_full[ks], kphase, ab, kRoleMma, kBarKFull, cta)) return false;
+        tc_fence_after();
+        const uint64_t kd = k_desc0 + static_cast<uint64_t>((ks * C::kTBytes) >> 4);
+  #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss_by(leader, s_tmem(buf), q_desc + kstep(kk, C::kQPanel), kd + kstep(kk, C::kTPanel), kIdescQK,
+                        kk > 0 ? 1u : 0u);
+        mma_commit_by(leader, &s_full[2 * w + buf]);
+        mma_commit_by(leader, &k_empty[ks]);
+        next_k();
+        return true;
+      };
+      for (int slot = 0, phase = 0; ok; phase ^= ++slot == kSegs, slot %= kSegs) {
+        if (!warp_wait(&seg_full[slot], phase, ab, kRoleMma, kBarSegFull, cta)) break;
+        const int nt = seg_at(slot).nt, rows = seg_at(slot).rows, last = seg_at(slot).end;
+        if (last) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[slot]);
+        if (nt == 0) continue;
+        if (rows <= w * kM) {
+          // no row in this half: release the stages so the rings stay in step
+          for (int t = 0; t < nt && ok; ++t) {
+            if (!warp_wait(&k_full[ks], kphase, ab, kRoleMma, kBarKFull, cta)) { ok = false; break; }
+            if (lane == 0) mbar_arrive(&k_empty[ks]);
+            next_k();
+            if (!warp_wait(&v_full[vs], vphase, ab, kRoleMma, kBarVFull, cta)) { ok = false; break; }
+            if (lane == 0) mbar_arrive(&v_empty[vs]);
+            next_v();
+          }
+          continue;
+        }
+        if (!warp_wait(&q_full[w], qph, ab, kRoleMma, kBarQ, cta)) break;
+        qph ^= 1;
+        for (int t = 0; t < 2 && t < nt && ok; ++t)
+          if (!issue_s(t)) ok = false;
+        for (int t = 0; t < nt && ok; ++t) {
+          const int buf = t & 1;
+          if (!warp_wait(&v_full[vs], vphase, ab, kRoleMma, kBarVFull, cta)) { ok = false; break; }
+          if (t == 0) {
+            if (!warp_wait(&o_empty[w], oph ^ 1, ab, kRoleMma, kBarO, cta)) { ok = false; break; }
+            oph ^= 1;
+          }
+          if (!warp_wait(&p_full[2 * w + buf], (pph >> buf) & 1u, ab, kRoleMma, kBarP, cta)) { ok = false; break; }
+          pph ^= 1u << buf;
+          tc_fence_after();
+          const uint64_t vd = v_desc0 + static_cast<uint64_t>((vs * C::kTBytes) >> 4);
+  #pragma unroll
+          for (int kk = 0; kk < kKT / 16; ++kk)
+            mma_f16_ts_by(leader, o_tmem, s_tmem(buf) + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4),
+                          kIdescPV, (t == 0 && kk == 0) ? 0u : 1u);
+          mma_commit_by(leader, &pv_tile[w]);
+          if (t == nt - 1) mma_commit_by(leader, &pv_last[w]);
+          mma_commit_by(leader, &v_empty[vs]);
+          next_v();
+          if (t + 2 < nt && !issue_s(buf)) { ok = false; break; }
+        }
+      }
+      mma_commit_by(leader, &mma_done[w]);
+      drain_wait(&mma_done[w], 0);
+      __syncwarp();
+    } else if (warp == 6) {
+      // ---------------------------------------------------------------- scheduler
+      const long long per = max((s_total + kCtas - 1) / kCtas, (long long)(kMinTiles + kItemCost));
+      Walker walk;
+      walk.per = per;
+      walk.cur = (long long)cta * per;
+      walk.end = min(walk.cur + per, s_total);
+      if (lane == 0) p.split[cta].n = 0;
+      if (walk.cur < walk.end) {
+        walk.b = s_row;
+        walk.row(p);
+        const long long one = row_units(p, walk.r);
+        walk.h = (int)(s_at / one);
+        long long off = s_at - walk.h * one;
+        walk.g = 0;
+        for (;; ++walk.g) {
+          const int u = group_tiles(p, walk.r, walk.g).units;
+          if (off < u) break;
+          off -= u;
+        }
+        walk.off = (int)off;
+      }
+      int slot = 0; uint32_t phase = 0;
+      while (true) {
+        Segment sg;
+        sg.end = walk.next(p, cta, sg) ? 0 : 1;
+        if (!warp_wait(&seg_empty[slot], phase ^ 1, ab, kRoleScheduler, kBarSegEmpty, cta)) break;
+        if (lane == 0) {
+          seg_at(slot) = sg;
+          mbar_arrive(&seg_full[slot]);
+        }
+        __syncwarp();
+        if (sg.end) break;
+        if (++slot == kSegs) { slot = 0; phase ^= 1; }
+      }
+    }
+  } else {
+    setmaxnreg_inc<168>();
+    // ------------------------------------------------------------------ softmax and output
+    const int w = (warp - 8) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row of the half = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t o_col = tmem + lane_off + C::kOCol + w * D;
+    uint8_t* my_q = smem + w * C::kQBytes + r * 128;
+    int vs = 0; uint32_t vphase = 0;
+    uint32_t sph = 0u, pvt_ph = 0u, pvl_ph = 0u;
+    for (int slot = 0, phase = 0;; phase ^= ++slot == kSegs, slot %= kSegs) {
+      if (!warp_wait(&seg_full[slot], phase, ab, kRoleSoftmax, kBarSegFull, cta)) break;
+      const Segment& sg = seg_at(slot);  // until this warp releases the slot
+      if (sg.end) break;
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[slot]);
+      };
+      const int nt = sg.nt;
+      const bool active = sg.rows > w * kM;
+      const int rr = sg.g * kRows + w * kM + r;
+      const bool row_ok = w * kM + r < sg.rows;
+      const int qi = row_ok ? rr / p.G : 0, hq = sg.h * p.G + (row_ok ? rr - qi * p.G : 0);
+      const int klo = win_lo(p, sg.r, qi), khi = row_ok ? win_end(p, sg.r, qi) - 1 : -1;  // the row's keys
+      // every row of the group sees [full_lo, full_end)
+      const int ia = sg.g * kRows / p.G, ib = (sg.g * kRows + sg.rows - 1) / p.G;
+      const int full_lo = win_lo(p, sg.r, ib), full_end = win_end(p, sg.r, ia);
+      float m = -INFINITY, l = 0.f, u = -INFINITY;
+      bool ok = true;
+      if (active && nt > 0) {
+        // ---- the query row, into the swizzle that the MMA reads
+        float f = kCap ? p.scale / p.cap : p.scale * kPagedLog2e;
+        const __nv_bfloat16* src = p.q + (long long)(sg.r.t0 + qi) * p.q_tok + (long long)hq * D;
+        uint4 raw[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          raw[i] = row_ok ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kF8) {
+          uint32_t top = 0u;  // of bf16 magnitudes as integers
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            top = __vmaxu2(top, raw[i].x & 0x7FFF7FFFu); top = __vmaxu2(top, raw[i].y & 0x7FFF7FFFu);
+            top = __vmaxu2(top, raw[i].z & 0x7FFF7FFFu); top = __vmaxu2(top, raw[i].w & 0x7FFF7FFFu);
+          }
+          const int ex = (int)(max(top & 0xFFFFu, top >> 16) >> 7);
+          const int fe = (ex == 0 || ex == 255) ? 127 : min(127 + 14 - (ex - 127), 253);
+          const float up = __uint_as_float((uint32_t)fe << 23);
+          f *= __uint_as_float((uint32_t)(254 - fe) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            raw[i].x = pack_f16x2(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up);
+            raw[i].y = pack_f16x2(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up);
+            raw[i].z = pack_f16x2(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up);
+            raw[i].w = pack_f16x2(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4*>(my_q + (i >> 3) * C::kQPanel + (((i & 7) ^ (r & 7)) << 4)) = raw[i];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[w]);
+
+        for (int t = 0; t < nt; ++t) {
+          const int buf = t & 1, key0 = (sg.t0 + t) * kKT;
+          const uint32_t s_col = tmem + lane_off + (2 * w + buf) * kKT;
+          if (!warp_wait(&s_full[2 * w + buf], (sph >> buf) & 1u, ab, kRoleSoftmax, kBarS, cta)) { ok = false; break; }
+          sph ^= 1u << buf;
+          float mult[4], vexp[4], vman[4];
+          if constexpr (kF8) {
+            // the scales arrived with the values
+            if (!warp_wait(&v_full[vs], vphase, ab, kRoleSoftmax, kBarVFull, cta)) { ok = false; break; }
+            const float4* meta = reinterpret_cast<const float4*>(smem + C::kOffMeta + vs * 32);
+            const float4 kc = meta[0], vc = meta[1];
+            mult[0] = f * kc.x; mult[1] = f * kc.y; mult[2] = f * kc.z; mult[3] = f * kc.w;
+            const float vv[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t bits = __float_as_uint(vv[s]), field = (bits >> 23) & 255u;
+              vexp[s] = (float)((int)field - 127);
+              vman[s] = field == 0 ? 0.f : __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
+            }
+          } else {
+            mult[0] = mult[1] = mult[2] = mult[3] = f;
+          }
+          if (++vs == C::kStages) { vs = 0; vphase ^= 1; }
+          float x[kKT];
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kKT / 32; ++c) tmem_ld_32x32b_x32_nw(s_col + c * 32, x + c * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < kKT; ++j) tmem_ld_ready(x[j]);
+          if constexpr (kCap) {
+            const float c1k = p.cap * kPagedLog2e;
+#pragma unroll
+            for (int j = 0; j < kKT; ++j) x[j] = capped(x[j] * mult[j >> 4], c1k);
+          }
+          if (key0 < full_lo || key0 + kKT > full_end)
+            mask_columns(x, min(max(klo - key0, 0), kKT), max(min(khi - key0, kKT - 1), -1));
+          // maxima by subtile, in log2 units
+          float tmax = -INFINITY, dmax = -INFINITY;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            float a = fmaxf(x[16 * s], x[16 * s + 1]), b = fmaxf(x[16 * s + 2], x[16 * s + 3]);
+#pragma unroll
+            for (int j = 4; j < 16; j += 4) {
+              a = fmax3f(a, x[16 * s + j], x[16 * s + j + 1]);
+              b = fmax3f(b, x[16 * s + j + 2], x[16 * s + j + 3]);
+            }
+            const float top = kCap ? fmaxf(a, b) : fmaxf(a, b) * mult[s];
+            tmax = fmaxf(tmax, top);
+            if constexpr (kF8) dmax = fmaxf(dmax, top + vexp[s]);
+          }
+          const bool move = tmax > m + kRaise || (m == -INFINITY && tmax != -INFINITY);
+          const float m_new = move ? tmax : m;
+          l *= (move && m != -INFINITY) ? ex2(m - m_new) : 1.f;
+          bool rescale;
+          float alpha;
+          if constexpr (kF8) {
+            const bool mu = dmax > u + kRaiseU || (u == -INFINITY && dmax != -INFINITY);
+            rescale = mu && u != -INFINITY;
+            alpha = rescale ? ex2(u - dmax) : 1.f;
+            if (mu) u = dmax;
+          } else {
+            rescale = move && m != -INFINITY;
+            alpha = rescale ? ex2(m - m_new) : 1.f;
+          }
+          m = m_new;
+          const float mm = m == -INFINITY ? 0.f : m;
+          uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+          const uint64_t negm2 = pack_f32x2(-mm, -mm);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int s = 2 * c; s < 2 * c + 2; ++s) {
+              const float w1 = !kF8 ? 1.f : m == -INFINITY ? 0.f : vman[s] * ex2(fminf(vexp[s] + m - u + 8.f, 126.f));
+              const uint64_t w2 = pack_f32x2(w1, w1);
+              const float ms = kCap ? 1.f : mult[s];
+              const uint64_t m2 = pack_f32x2(ms, ms);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float a0, a1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(x[16 * s + j], x[16 * s + j + 1]), m2, negm2), a0, a1);
+                uint64_t e2 = pack_f32x2(ex2(a0), ex2(a1));
+                sum2[(j >> 1) & 3] = add_f32x2(sum2[(j >> 1) & 3], e2);
+                if constexpr (kF8) e2 = mul_f32x2(e2, w2);
+                float e0, e1;
+                unpack_f32x2(e2, e0, e1);
+                pk[8 * (s - 2 * c) + (j >> 1)] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+              }
+            }
+            tmem_st_32x32b_x16_u_nw(s_col + c * 16, pk);
+          }
+          tmem_wait_st();
+          {
+            float lo, hi;
+            unpack_f32x2(add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3])), lo, hi);
+            l += lo + hi;
+          }
+          if (t > 0) {
+            // O_w holds PV(0 .. t - 2); a rescale also waits for PV(t - 1)
+            if (__any_sync(0xffffffffu, rescale)) {
+              if (!warp_wait(&pv_tile[w], pvt_ph, ab, kRoleSoftmax, kBarPvTile, cta)) { ok = false; break; }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                float ov[32];
+                tmem_ld_32x32b_x32(o_col + c * 32, ov);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) ov[j] *= alpha;
+                tmem_st_32x32b_x32(o_col + c * 32, ov);
+              }
+            }
+            pvt_ph ^= 1u;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * w + buf]);
+        }
+        if (!ok) break;
+        if (!warp_wait(&pv_last[w], pvl_ph, ab, kRoleSoftmax, kBarPvLast, cta)) break;
+        pvl_ph ^= 1u;
+        pvt_ph ^= 1u;
+        tc_fence_after();
+      } else {
+        for (int t = 0; t < nt; ++t)
+          if (++vs == C::kStages) { vs = 0; vphase ^= 1; }
+      }
+
+      // ---- the row's result, or its partial
+      const float ref = kF8 ? u - 8.f : m;  // o stands for o 2^ref
+      const bool some = active && nt > 0 && l != 0.f;
+      const int part = cta * 2 + (sg.begins ? 1 : 0);
+      if (sg.begins && !sg.whole && warp == 8 && lane == 0) {
+        SplitChunk s;
+        s.n = sg.n;
+        s.rows = sg.rows;
+        s.first = sg.g * kRows;
+        s.t0 = sg.r.t0;
+        s.h = sg.h;
+        p.split[cta] = s;
+      }
+      if (!active) {
+        release();
+        continue;
+      }
+      const long long orow = (long long)(sg.r.t0 + qi) * p.Hq + hq;
+      // whole: o / l; partial: o relative to 2^m
+      const float factor = !some ? 0.f : sg.whole ? ex2(ref - m) / l : ex2(ref - m);
+      if (!sg.whole) {
+        *reinterpret_cast<float2*>(p.part_ml + ((long long)part * kRows + w * kM + r) * 2) =
+            make_float2(some ? m : -INFINITY, some ? l : 0.f);
+      } else if (p.lse != nullptr && row_ok) {
+        p.lse[orow] = some ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+      }
+      float* po = p.part_o + (long long)part * D * kRows + w * kM + r;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float ov[32];
+        if (nt > 0) {
+          tmem_ld_32x32b_x32_nw(o_col + c * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) tmem_ld_ready(ov[j]);
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[w]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) ov[j] = some ? ov[j] * factor : 0.f;
+        if (!sg.whole) {
+          // lanes are rows: one coalesced store a column
+#pragma unroll
+          for (int j = 0; j < 32; ++j) po[(long long)(c * 32 + j) * kRows] = ov[j];
+        } else {
+          // this row's part of the (consumed) query buffer
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            *reinterpret_cast<uint4*>(my_q + (c >> 1) * C::kQPanel + ((((c & 1) * 4 + (j >> 3)) ^ (r & 7)) << 4)) =
+                make_uint4(pack_bf16x2(ov[j], ov[j + 1]), pack_bf16x2(ov[j + 2], ov[j + 3]),
+                           pack_bf16x2(ov[j + 4], ov[j + 5]), pack_bf16x2(ov[j + 6], ov[j + 7]));
+        }
+      }
+      if (sg.whole) {
+        __syncwarp();
+        constexpr int kCh = D / 8;  // 16-byte chunks of an output row
+        const long long mine = row_ok ? orow : -1;
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) {
+          const int x = i * 32 + lane, row = x / kCh, ch = x % kCh;
+          const long long to = __shfl_sync(0xffffffffu, mine, row);
+          const int rq = q4 * 32 + row;
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + w * C::kQBytes + (ch >> 3) * C::kQPanel + rq * 128 +
+                                                          (((ch & 7) ^ (rq & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * D + ch * 8) = v;
+        }
+      }
+      release();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// 32 rows of an item that was cut: lanes are rows, a warp a quarter of the columns; the
+// result goes out through shared memory in whole rows.
+template <int D>
+__global__ void __launch_bounds__(128)
+paged_chunk_merge_kernel(const ChunkParams p) {
+  constexpr int kCols = D / 4;
+  __shared__ __align__(16) __nv_bfloat16 s_out[32][D + 8];
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitChunk it = p.split[cta];
+  const int r0 = blockIdx.y * 32, r = r0 + lane;
+  if (it.n == 0 || r0 >= it.rows) return;
+  auto slot_of = [&](int i) -> long long { return i == 0 ? cta * 2 + 1 : (cta + i) * 2; };
+  auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(p.part_ml + (slot_of(i) * kRows + r) * 2); };
+  float M = -INFINITY, L = 0.f;
+  for (int i = 0; i < it.n; ++i) M = fmaxf(M, ml_of(i).x);
+  float o[kCols];
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) o[j] = 0.f;
+  for (int i = 0; i < it.n; ++i) {
+    const float2 ml = ml_of(i);
+    const float f = ml.y != 0.f ? ex2(ml.x - M) : 0.f;
+    if (ml.y != 0.f) L = fmaf(f, ml.y, L);
+    const float* src = p.part_o + (slot_of(i) * D + warp * kCols) * kRows + r;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const float v = src[(long long)j * kRows];
+      if (f != 0.f) o[j] = fmaf(f, v, o[j]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int j = 0; j < kCols; j += 2)
+    *reinterpret_cast<uint32_t*>(&s_out[lane][warp * kCols + j]) = pack_bf16x2(o[j] * inv, o[j + 1] * inv);
+  auto row_at = [&](int x) -> long long {
+    const int rr = it.first + x;
+    return (long long)(it.t0 + rr / p.G) * p.Hq + it.h * p.G + rr % p.G;
+  };
+  if (warp == 0 && r < it.rows && p.lse != nullptr)
+    p.lse[row_at(r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+  __syncthreads();
+  constexpr int kCh = D / 8;
+  for (int x = threadIdx.x; x < 32 * kCh; x += 128) {
+    const int row = x / kCh, ch = x % kCh;
+    if (r0 + row < it.rows)
+      *reinterpret_cast<uint4*>(p.out + row_at(r0 + row) * D + ch * 8) = *reinterpret_cast<const uint4*>(&s_out[row][ch * 8]);
+  }
+}
+
+template <bool kF8, int D, bool kCap>
+cudaError_t launch(const ChunkParams& p, cudaStream_t st) {
+  using C = Cfg<D>;
+  auto* kernel = paged_chunk_kernel<kF8, D, kCap>;
+  static thread_local unsigned long long set = 0;  // devices whose limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((set >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set |= 1ull << dev;
+  }
+  kernel<<<kCtas, kThreads, C::kSmemBytes, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas, kRows / 32);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_chunk_merge_kernel<D>, p);
+}
+
+constexpr size_t kItemBytes = sizeof(SplitChunk) * kCtas;
+constexpr size_t kMlBytes = sizeof(float) * 2 * 2 * kCtas * kRows;
+
+}  // namespace
+
+size_t paged_chunk_workspace_bytes(int D) {
+  return kItemBytes + kMlBytes + sizeof(float) * 2 * kCtas * kRows * (size_t)D;
+}
+
+unsigned read_and_clear_error_chunk(cudaStream_t, std::string* where) {
+  DevError w{0u, 0u, 0}, zero{0u, 0u, 0};
+  cudaMemcpyFromSymbol(&w, g_err_chunk, sizeof(w));
+  if (w.flags) {
+    cudaMemcpyToSymbol(g_err_chunk, &zero, sizeof(zero));
+    char buf[128];
+    if (w.where)
+      snprintf(buf, sizeof(buf), " [paged attention chunk role %u barrier %u CTA %d]", (w.where >> 16) & 0xFFu,
+               w.where & 0xFFFFu, w.item);
+    else
+      snprintf(buf, sizeof(buf), " (paged attention: a length, a token offset or a page number out of range)");
+    *where += buf;
+  }
+  return w.flags;
+}
+
+int launch_paged_chunk(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq, float scale,
+                       int window_left, int window_right, float cap, void* out, float* lse,
+                       void* workspace, cudaStream_t stream) {
+  ChunkParams p;
+  p.c = c;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_tok = q_tok;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.split = reinterpret_cast<SplitChunk*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + kItemBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kItemBytes + kMlBytes);
+  p.Hq = Hq;
+  p.G = Hq / c.Hkv;
+  p.scale = scale;
+  p.cap = cap;
+  p.window_left = window_left;
+  p.window_right = window_right;
+  p.wait_limit = wait_timeout_cycles();
+  cudaError_t e;
+  const bool capped = cap > 0.f;
+  if (D == 128)
+    e = f8 ? (capped ? launch<true, 128, true>(p, stream) : launch<true, 128, false>(p, stream))
+           : (capped ? launch<false, 128, true>(p, stream) : launch<false, 128, false>(p, stream));
+  else
+    e = f8 ? (capped ? launch<true, 64, true>(p, stream) : launch<true, 64, false>(p, stream))
+           : (capped ? launch<false, 64, true>(p, stream) : launch<false, 64, false>(p, stream));
+  if (e != cudaSuccess) return cuda_error(e, "paged attention chunk launch");
+  return SBA_OK;
+}
+
+}  // namespace sba

@@ -25,6 +25,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = kPagedWarps * 32;
 constexpr int kMaxBlocks = 32;
+constexpr int kResident = 456;  // three CTAs on each of 152 SMs
 constexpr int kMaxSplit = 8;  // CTAs of a cluster, at most (the portable limit)
 
 struct PagedSelectParams {
@@ -223,11 +224,20 @@ int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long l
   p.Hq = Hq;
   p.G = Hq / c.Hkv;
   p.scale = scale;
-  // CTAs per item: enough to fill the GPU three times over, each warp with a tile or more.
+  // CTAs per item: the choice with the least (waves of resident CTAs) x (a CTA's fixed time,
+  // worth about 8 tiles of a warp, + its warps' tiles).
   const long long items = (long long)c.B * c.Qn * c.Hkv;
-  const int tiles = S * block_size / (f8 ? 32 : 16);
+  const int tiles = S * block_size / (f8 || D == 64 ? 32 : 16);
   int split = 1;
-  while (split < kMaxSplit && items * split < 456 && tiles > split * kPagedWarps) split *= 2;
+  long long best = LLONG_MAX;
+  for (int s = 1; s <= kMaxSplit; s *= 2) {
+    const long long waves = (items * s + kResident - 1) / kResident;
+    const long long cost = waves * (8 + (tiles + s * kPagedWarps - 1) / (s * kPagedWarps));
+    if (cost < best) {
+      best = cost;
+      split = s;
+    }
+  }
   p.split = split;
   const bool hi = p.G > 8;
   cudaError_t e;

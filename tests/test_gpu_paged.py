@@ -546,7 +546,7 @@ def test_prompt_then_decode(sba, f8):
 
     qs, ks, vs = (torch.empty((B, h, D), dtype=torch.bfloat16, device=DEV) for h in (H * G, H, H))
     idx = torch.empty((B, H, 3), dtype=torch.int32, device=DEV)
-    ws = torch.empty(sba.paged_attention_workspace_size(D), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(sba.paged_attention_workspace_size(B, B, H * G, H, D), dtype=torch.uint8, device=DEV)
     qr, out, sel = (torch.empty_like(qs) for _ in range(3))
     lse, sel_lse = (torch.empty((B, H * G), device=DEV) for _ in range(2))
 
@@ -587,7 +587,7 @@ def test_two_streams(sba):
     alone = [sba.paged_attention_fwd(q, *c.pool(), **c.kw()) for c, q in zip(cs, qs)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
-    ws = [torch.empty(sba.paged_attention_workspace_size(128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    ws = [torch.empty(sba.paged_attention_workspace_size(3, 3, 16, 4, 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
     got = [None, None]
     for _ in range(30):
         for i in range(2):
@@ -601,7 +601,7 @@ def test_two_streams(sba):
 def test_workspace_needs_no_initialisation_and_may_be_shared_in_order(sba):
     c = Cache([4000, 900, 17], 4, 128, 64, True, 830)
     q = c.q((3, 16, 128), 61)
-    ws = torch.full((sba.paged_attention_workspace_size(128),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((sba.paged_attention_workspace_size(3, 3, 16, 4, 128),), 0xFF, dtype=torch.uint8, device=DEV)
     want = sba.paged_attention_fwd(q, *c.pool(), **c.kw())
     graphs, outs = [], []
     for i in range(2):

@@ -55,7 +55,7 @@ def append(lib, **kw):
 
 def attend(lib, **kw):
     d = dict(q=FAKE, qs=1024, Hq=8, scale=0.0, left=-1, right=-1, cap=0.0, bias=None, sinks=0, per_head=0, out=FAKE,
-             lse=None, ws=FAKE, ws_bytes=lib.sba_paged_attention_workspace_size(128))
+             lse=None, ws=FAKE, ws_bytes=lib.sba_paged_attention_workspace_size(3, 6, 8, 2, 128))
     return call(lib.sba_paged_attention_fwd, ATTEND, d, kw)
 
 
@@ -119,9 +119,12 @@ def test_selection_arguments(lib, change, code):
 
 
 def test_workspace_size(lib):
-    a, b = (lib.sba_paged_attention_workspace_size(d) for d in (64, 128))
-    assert 0 < a < b < 16 << 20
-    assert lib.sba_paged_attention_workspace_size(96) == 0
+    size = lib.sba_paged_attention_workspace_size
+    few, many = size(64, 64, 32, 8, 128), size(4, 2048, 32, 8, 128)
+    assert 0 < size(64, 64, 32, 8, 64) < few < many < 64 << 20
+    assert few == size(1, 15, 32, 8, 128) and many == size(1, 16, 32, 8, 128)  # 64 rows a KV head
+    for bad in ((0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 1, 8, 8, 96), (1, 1, 9, 8, 128), (1, 1, 4, 8, 128)):
+        assert size(*bad) == 0
 
 
 def test_binding_refuses_host_tensors():
