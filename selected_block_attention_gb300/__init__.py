@@ -476,17 +476,19 @@ _APPEND_ARGS = struct.Struct("@" + _CACHE + "6P4q4i")
 _ATTENTION_ARGS = struct.Struct("@" + _CACHE + "5PNqif2if2i")
 _SELECT_ARGS = struct.Struct("@" + _CACHE + "6Pq5if")
 _CACHE_DTYPES = {torch.float8_e4m3fn: SBA_E4M3, torch.bfloat16: SBA_BF16}
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+# The raw forms of torch.cuda.current_device() and current_stream(): the latter builds a
+# Stream object, which takes longer than the launch.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _paged_call(index, fn, args):
     """_call with a device index; most calls find their device current already."""
-    # the raw handle: torch.cuda.current_stream() builds a Stream object first
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
-        code = fn(args, stream)
+    if _current_device() == index:
+        code = fn(args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            code = fn(args, stream)
+            code = fn(args, _raw_stream(index))
     if code:
         _check(code)
 
@@ -507,8 +509,9 @@ def _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens, cu_
     index = k_pages.get_device()
     if index < 0:
         raise ValueError("libsba works on CUDA tensors only (no CPU path)")
-    dtype = _CACHE_DTYPES.get(k_pages.dtype)
-    if dtype is None or v_pages.dtype != k_pages.dtype:
+    kind = k_pages.dtype
+    dtype = _CACHE_DTYPES.get(kind)
+    if dtype is None or v_pages.dtype != kind:
         raise TypeError("k_pages and v_pages must both be float8_e4m3fn or both bfloat16")
     shape, st = k_pages.shape, k_pages.stride()
     if len(shape) != 4 or v_pages.shape != shape or v_pages.get_device() != index:
@@ -517,17 +520,16 @@ def _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens, cu_
     for s in (st, v_pages.stride()):
         if s[3] != 1 or s[2] != d or (s[1] != size * d and hkv > 1) or (s[0] != st[0] and pages > 1):
             raise ValueError("k_pages, v_pages: pages must be dense and lie as far apart in both pools")
-    if page_table.dim() != 2:
+    table_shape = page_table.shape
+    if len(table_shape) != 2:
         raise ValueError("page_table must be [B, width]")
-    batch, width = table_shape = page_table.shape
+    batch, width = table_shape
     scale_shape = (pages, hkv)
     return index, hkv, d, batch, (
-        k_pages.data_ptr(), v_pages.data_ptr(),
-        _at(k_scales, "k_scales", index, torch.float32, scale_shape),
-        _at(v_scales, "v_scales", index, torch.float32, scale_shape),
-        _at(page_table, "page_table", index, torch.int32, table_shape),
-        _at(seq_lens, "seq_lens", index, torch.int32, (batch,)),
-        0 if cu_seqlens is None else _at(cu_seqlens, "cu_seqlens", index, torch.int32, (batch + 1,)),
+        k_pages.data_ptr(), v_pages.data_ptr(), _at(k_scales, "k_scales", index, _F32, scale_shape),
+        _at(v_scales, "v_scales", index, _F32, scale_shape),
+        _at(page_table, "page_table", index, _I32, table_shape), _at(seq_lens, "seq_lens", index, _I32, (batch,)),
+        0 if cu_seqlens is None else _at(cu_seqlens, "cu_seqlens", index, _I32, (batch + 1,)),
         st[0] if pages > 1 else hkv * size * d, pages, size, hkv, d, dtype, width, batch)
 
 
@@ -535,10 +537,11 @@ def _token_rows(t, name, index, d, batch):
     """(address, Q, N, heads, token stride) of bf16 token rows: [N, H, D] with cu_seqlens
     (``batch`` None), else [batch, H, D] (one token per row) or [batch, Q, H, D].  Heads are
     dense inside a token, tokens equally far apart."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _BF16:
         raise TypeError(f"{name} must be bfloat16")
     shape, st = t.shape, t.stride()
-    if t.get_device() != index or shape[-1] != d or (st[-1] != 1 or (st[-2] != d and shape[-2] > 1)):
+    heads = shape[-2]
+    if t.get_device() != index or shape[-1] != d or st[-1] != 1 or (st[-2] != d and heads > 1):
         raise ValueError(f"{name} must be on the cache's device, with its head dimension and dense heads")
     if len(shape) == 3:
         n, q, stride = shape[0], 1, st[0]
@@ -551,7 +554,7 @@ def _token_rows(t, name, index, d, batch):
         raise ValueError(f"{name} must be [B, H, D] or [B, Q, H, D], or [N, H, D] with cu_seqlens")
     if batch is not None and shape[0] != batch:
         raise ValueError(f"{name} must have one entry per row of page_table")
-    return t.data_ptr(), q, n, shape[-2], stride if n > 1 else shape[-2] * d
+    return t.data_ptr(), q, n, heads, stride if n > 1 else heads * d
 
 
 def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
@@ -567,9 +570,9 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=No
                                                seq_lens, cu_seqlens)
     rows = batch if cu_seqlens is None else None
     kp, Q, N, heads, k_stride = _token_rows(k, "k", index, d, rows)
-    vp, _, _, _, v_stride = _token_rows(v, "v", index, d, rows)
-    if v.shape != k.shape or heads != hkv:
-        raise ValueError("k and v must have the same shape and the cache's heads")
+    vp, vq, vn, v_heads, v_stride = _token_rows(v, "v", index, d, rows)
+    if heads != hkv or v_heads != hkv or vq != Q or vn != N:
+        raise ValueError("k and v must have the same tokens and the cache's heads")
     qp = op = hq = q_stride = o_stride = rot = max_pos = 0
     if q is not None:
         qp, qq, qn, hq, q_stride = _token_rows(q, "q", index, d, rows)
@@ -577,21 +580,24 @@ def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=No
             raise ValueError("q must have k's tokens")
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        op, _, _, _, o_stride = _token_rows(q_out, "q_out", index, d, rows)
+            op, o_stride = q_out.data_ptr(), hq * d
+        else:
+            op, oq, on, o_heads, o_stride = _token_rows(q_out, "q_out", index, d, rows)
+            if oq != Q or on != N or o_heads != hq:
+                raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out needs q")
+    cos_p = sin_p = 0
     if cos is not None or sin is not None:
-        if cos is None or sin is None or cos.dim() != 2:
+        if cos is None or sin is None or len(cos.shape) != 2:
             raise ValueError("cos and sin go together, [max_pos, rot_dim / 2]")
-        max_pos, rot = cos.shape
+        table = cos.shape
+        max_pos, rot = table
         rot *= 2
-    _paged_call(index, load_library().sba_paged_kv_append, _APPEND_ARGS.pack(
-        *cache, Q, N, kp, vp, qp, op,
-        0 if cos is None else _at(cos, "cos", index, torch.float32, cos.shape),
-        0 if cos is None else _at(sin, "sin", index, torch.float32, cos.shape),
-        k_stride, v_stride, q_stride, o_stride, hq, rot, max_pos, 1 if interleaved else 0))
+        cos_p, sin_p = _at(cos, "cos", index, _F32, table), _at(sin, "sin", index, _F32, table)
+    _paged_call(index, (_lib or load_library()).sba_paged_kv_append, _APPEND_ARGS.pack(
+        *cache, Q, N, kp, vp, qp, op, cos_p, sin_p, k_stride, v_stride, q_stride, o_stride, hq, rot, max_pos,
+        1 if interleaved else 0))
     return q_out
 
 
@@ -607,11 +613,11 @@ def _results(q, index, out, lse, return_lse):
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         out_p = out.data_ptr()
     else:
-        out_p = _at(out, "out", index, torch.bfloat16, shape)
+        out_p = _at(out, "out", index, _BF16, shape)
     if lse is None and return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(shape[:-1], dtype=_F32, device=q.device)
         return out, lse, out_p, lse.data_ptr()
-    return out, lse, out_p, _at(lse, "lse", index, torch.float32, shape[:-1])
+    return out, lse, out_p, _at(lse, "lse", index, _F32, shape[:-1])
 
 
 def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
@@ -625,12 +631,12 @@ def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=N
     index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
                                                seq_lens, cu_seqlens)
     qp, Q, N, hq, q_stride = _token_rows(q, "q", index, d, batch if cu_seqlens is None else None)
-    lib = load_library()
+    lib = _lib or load_library()
     bias_p = num_sinks = per_head = 0
     if sink_bias is not None:
         per_head = 1 if sink_bias.dim() == 2 else 0
         num_sinks = sink_bias.shape[-1]
-        bias_p = _at(sink_bias, "sink_bias", index, torch.float32, (hq, num_sinks) if per_head else (num_sinks,))
+        bias_p = _at(sink_bias, "sink_bias", index, _F32, (hq, num_sinks) if per_head else (num_sinks,))
     out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
     if workspace is None:
         workspace = torch.empty(lib.sba_paged_attention_workspace_size(batch, N, hq, hkv, d) or 16, dtype=torch.uint8,
@@ -657,11 +663,11 @@ def nsa_select_paged_fwd(q, k_pages, v_pages, page_table, seq_lens, block_indice
     lead = q.shape[:-2]
     S = block_indices.shape[-1]
     counts = isinstance(block_counts, torch.Tensor)
-    idx_p = _at(block_indices, "block_indices", index, torch.int32, (*lead, hkv, S))
-    cnt_p = _at(block_counts, "block_counts", index, torch.int32, (*lead, hkv)) if counts else 0
-    gate_p = 0 if g_slc is None else _at(g_slc, "g_slc", index, torch.bfloat16, q.shape[:-1])
+    idx_p = _at(block_indices, "block_indices", index, _I32, (*lead, hkv, S))
+    cnt_p = _at(block_counts, "block_counts", index, _I32, (*lead, hkv)) if counts else 0
+    gate_p = 0 if g_slc is None else _at(g_slc, "g_slc", index, _BF16, q.shape[:-1])
     out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
-    _paged_call(index, load_library().sba_nsa_select_paged_fwd, _SELECT_ARGS.pack(
+    _paged_call(index, (_lib or load_library()).sba_nsa_select_paged_fwd, _SELECT_ARGS.pack(
         *cache, Q, N, qp, idx_p, cnt_p, gate_p, out_p, lse_p, q_stride, hq,
         0 if counts else int(block_counts), S, int(block_size), 1 if causal else 0,
         softmax_scale or 0.0))

@@ -213,9 +213,12 @@ __device__ __forceinline__ float capped(float y, float c1k) {
   return c1k * (fabsf(y) < 0.25f ? near : far);
 }
 
-template <bool kF8, int D, bool kCap>
+// kSub: groups of a tile's keys with one scale each: 1 for pages of 64 and more (and bf16),
+// 4 for smaller ones.
+template <bool kF8, int D, bool kCap, int kSub>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const ChunkParams p) {
+  constexpr int kCols = kKT / kSub;
   using C = Cfg<D>;
   constexpr uint32_t kFmt = kF8 ? 0u : 1u;  // operands: fp16 or bf16
   constexpr uint32_t kIdescQK = make_idesc(128, kKT, kFmt, false, false);
@@ -316,16 +319,19 @@ paged_chunk_kernel(const ChunkParams p) {
     return *reinterpret_cast<Segment*>(smem + C::kOffSegs + slot * (int)sizeof(Segment));
   };
 
-  // registers of the four warpgroups: 104 + 72 + 168 + 168 = 4 x 128
+  // registers of the four warpgroups: 120 + 72 + 160 + 160 = 4 x 128
   if (warp < 4) {
     // ------------------------------------------------------------------ loaders
-    setmaxnreg_dec<104>();
+    setmaxnreg_dec<120>();
     constexpr int kItem = kF8 ? 1 : 2;
     constexpr int kCpr = D * kItem / 16;  // 16-byte chunks of a row
     constexpr int kStep = 32 / kCpr;      // rows of a warp-wide access
     constexpr int kN = 32 / kStep;        // accesses for the warp's 32 keys
     const int pair = warp >> 1, half = warp & 1;
-    const int chunk = lane % kCpr, row0 = lane / kCpr;
+    // A lane's chunk and first row.  e4m3 at D = 128: eight lanes write chunks 0..3 (or 4..7)
+    // of two rows, whose fp16 halves then lie in different banks.
+    const int chunk = kF8 && D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane % kCpr;
+    const int row0 = kF8 && D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane / kCpr;
     const int pmask = (1 << p.c.p_shift) - 1;
     int ks = 0; uint32_t kphase = 0;
     int vs = 0; uint32_t vphase = 0;
@@ -369,42 +375,47 @@ paged_chunk_kernel(const ChunkParams p) {
     auto byte_of = [&](int page) -> long long {
       return page * p.c.page_bytes + (((long long)h << p.c.p_shift) * D) * kItem + chunk * 16;
     };
-    auto row_off = [&](int i) -> int {  // of access i
-      return (min(max(key0 + row0 + i * kStep, cl), ch) & pmask) * (D * kItem);
+    // Byte offset in the page of access j of subtile x; inside the owned keys it steps by a
+    // constant.
+    constexpr int kHalf = kN / 2;  // accesses of a subtile
+    auto row_off = [&](int x, int j, bool inside) -> int {
+      const int first = key0 + 16 * x;
+      if (inside) return ((first & pmask) + row0) * (D * kItem) + j * kStep * (D * kItem);
+      return (min(max(first + row0 + j * kStep, cl), ch) & pmask) * (D * kItem);
     };
     if constexpr (kF8) {
       uint4 rk[kN], rv[kN];
-      float kc[2], vc[2];
-      auto load = [&]() {
+      float kc[2], vc[2], kc_next[2];
+      auto load = [&](const uint8_t* pool, const float* scales, uint4 (&raw)[kN], float (&sc)[2]) {
+        const bool inside = key0 >= cl && key0 + 31 <= ch;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int page = page_at(x);
-          const uint8_t* k = p.c.k + byte_of(page);
-          const uint8_t* v = p.c.v + byte_of(page);
+          const uint8_t* src = pool + byte_of(page);
+          auto rows = [&](bool in) {
 #pragma unroll
-          for (int i = x * kN / 2; i < (x + 1) * kN / 2; ++i) {
-            rk[i] = __ldg(reinterpret_cast<const uint4*>(k + row_off(i)));
-            rv[i] = __ldg(reinterpret_cast<const uint4*>(v + row_off(i)));
-          }
-          kc[x] = __ldg(p.c.ks + (long long)page * p.c.Hkv + h);
-          vc[x] = __ldg(p.c.vs + (long long)page * p.c.Hkv + h);
+            for (int j = 0; j < kHalf; ++j)
+              raw[x * kHalf + j] = __ldg(reinterpret_cast<const uint4*>(src + row_off(x, j, in)));
+          };
+          if (inside) rows(true); else rows(false);
+          sc[x] = __ldg(scales + (long long)page * p.c.Hkv + h);
         }
       };
-      // 16 codes as two 16-byte chunks of fp16; the halves go out in an order that spreads
-      // eight lanes over all banks
-      auto put = [&](uint8_t* tile, const uint4 (&raw)[kN]) {
+      // 16 codes as two 16-byte chunks of fp16
+      const uint32_t s0 = (((chunk & 3) * 2) ^ (row0 & 7)) << 4;
+      auto put = [&](uint32_t tile, const uint4 (&raw)[kN]) {
+        const uint32_t dst = tile + (chunk >> 2) * C::kTPanel + (half * 32 + row0) * 128;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int row = half * 32 + row0 + i * kStep;
+          // row & 7 is row0 (kStep = 8) or row0 + 4 (i & 1) with row0 < 4
+          const uint32_t at = dst + i * (kStep * 128), x = kStep == 8 ? 0u : (i & 1) * 64u;
           uint4 a, c;
           e4m3x4_to_f16x2(raw[i].x, a.x, a.y);
           e4m3x4_to_f16x2(raw[i].y, a.z, a.w);
           e4m3x4_to_f16x2(raw[i].z, c.x, c.y);
           e4m3x4_to_f16x2(raw[i].w, c.z, c.w);
-          uint8_t* dst = tile + (chunk >> 2) * C::kTPanel + row * 128;
-          const int first = (chunk & 3) * 2, flip = (chunk >> 2) & 1;
-          *reinterpret_cast<uint4*>(dst + (((first + flip) ^ (row & 7)) << 4)) = flip ? c : a;
-          *reinterpret_cast<uint4*>(dst + (((first + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : c;
+          paged_sts16(at + (s0 ^ x), a);
+          paged_sts16(at + (s0 ^ x ^ 16u), c);
         }
       };
       step();
@@ -414,19 +425,26 @@ paged_chunk_kernel(const ChunkParams p) {
         next_v();
       }
       look();
-      if (have) load();
+      if (have) {
+        load(p.c.k, p.c.ks, rk, kc);
+        load(p.c.v, p.c.vs, rv, vc);
+      }
       bool more = have;  // a tile is in registers
       step();
       step();
       look();
+      // The next tile's keys are on their way while this one's values are stored, its
+      // values while the next one's keys are.
       while (more) {
         if (!warp_wait(&k_empty[ks], kphase ^ 1, ab, kRoleLoader, kBarKEmpty, cta)) break;
-        put(smem + C::kOffK + ks * C::kTBytes, rk);
+        put(smem_base + C::kOffK + ks * C::kTBytes, rk);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[ks]);
+        more = have;
+        if (have) load(p.c.k, p.c.ks, rk, kc_next);
         if (!warp_wait(&v_empty[vs], vphase ^ 1, ab, kRoleLoader, kBarVEmpty, cta)) break;
-        put(smem + C::kOffV + vs * C::kTBytes, rv);
+        put(smem_base + C::kOffV + vs * C::kTBytes, rv);
         if (lane < 2) {
           float* meta = reinterpret_cast<float*>(smem + C::kOffMeta + vs * 32);
           meta[half * 2 + lane] = lane ? kc[1] : kc[0];
@@ -435,10 +453,11 @@ paged_chunk_kernel(const ChunkParams p) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[vs]);
+        if (have) load(p.c.v, p.c.vs, rv, vc);
+        kc[0] = kc_next[0];
+        kc[1] = kc_next[1];
         next_k(); next_k();
         next_v(); next_v();
-        more = have;
-        if (have) load();
         step();
         step();
         look();
@@ -448,11 +467,12 @@ paged_chunk_kernel(const ChunkParams p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint8_t* src = pool + byte_of(page_at(x));
+          const bool inside = key0 >= cl && key0 + 31 <= ch;
 #pragma unroll
-          for (int i = x * kN / 2; i < (x + 1) * kN / 2; ++i) {
-            const int row = half * 32 + row0 + i * kStep;
+          for (int j = 0; j < kHalf; ++j) {
+            const int row = half * 32 + row0 + (x * kHalf + j) * kStep;
             paged_cp16(smem_u32(tile + (chunk >> 3) * C::kTPanel + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)),
-                       src + row_off(i));
+                       src + row_off(x, j, inside));
           }
         }
         paged_cp_commit();
@@ -603,7 +623,7 @@ paged_chunk_kernel(const ChunkParams p) {
       }
     }
   } else {
-    setmaxnreg_inc<168>();
+    setmaxnreg_inc<160>();
     // ------------------------------------------------------------------ softmax and output
     const int w = (warp - 8) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the half = TMEM lane
@@ -670,22 +690,18 @@ paged_chunk_kernel(const ChunkParams p) {
           const uint32_t s_col = tmem + lane_off + (2 * w + buf) * kKT;
           if (!warp_wait(&s_full[2 * w + buf], (sph >> buf) & 1u, ab, kRoleSoftmax, kBarS, cta)) { ok = false; break; }
           sph ^= 1u << buf;
-          float mult[4], vexp[4], vman[4];
+          float mult[kSub], lgv[kSub];  // logit factors, log2 of the value scales
           if constexpr (kF8) {
             // the scales arrived with the values
             if (!warp_wait(&v_full[vs], vphase, ab, kRoleSoftmax, kBarVFull, cta)) { ok = false; break; }
-            const float4* meta = reinterpret_cast<const float4*>(smem + C::kOffMeta + vs * 32);
-            const float4 kc = meta[0], vc = meta[1];
-            mult[0] = f * kc.x; mult[1] = f * kc.y; mult[2] = f * kc.z; mult[3] = f * kc.w;
-            const float vv[4] = {vc.x, vc.y, vc.z, vc.w};
+            const float* meta = reinterpret_cast<const float*>(smem + C::kOffMeta + vs * 32);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const uint32_t bits = __float_as_uint(vv[s]), field = (bits >> 23) & 255u;
-              vexp[s] = (float)((int)field - 127);
-              vman[s] = field == 0 ? 0.f : __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
+            for (int g = 0; g < kSub; ++g) {
+              mult[g] = f * meta[g];
+              asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lgv[g]) : "f"(meta[4 + g]));
             }
           } else {
-            mult[0] = mult[1] = mult[2] = mult[3] = f;
+            mult[0] = f;
           }
           if (++vs == C::kStages) { vs = 0; vphase ^= 1; }
           float x[kKT];
@@ -698,23 +714,25 @@ paged_chunk_kernel(const ChunkParams p) {
           if constexpr (kCap) {
             const float c1k = p.cap * kPagedLog2e;
 #pragma unroll
-            for (int j = 0; j < kKT; ++j) x[j] = capped(x[j] * mult[j >> 4], c1k);
+            for (int j = 0; j < kKT; ++j) x[j] = capped(x[j] * mult[j / kCols], c1k);
           }
           if (key0 < full_lo || key0 + kKT > full_end)
             mask_columns(x, min(max(klo - key0, 0), kKT), max(min(khi - key0, kKT - 1), -1));
-          // maxima by subtile, in log2 units
+          // maxima of the groups, in log2 units
           float tmax = -INFINITY, dmax = -INFINITY;
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            float a = fmaxf(x[16 * s], x[16 * s + 1]), b = fmaxf(x[16 * s + 2], x[16 * s + 3]);
+          for (int g = 0; g < kSub; ++g) {
+            float a[4];
 #pragma unroll
-            for (int j = 4; j < 16; j += 4) {
-              a = fmax3f(a, x[16 * s + j], x[16 * s + j + 1]);
-              b = fmax3f(b, x[16 * s + j + 2], x[16 * s + j + 3]);
-            }
-            const float top = kCap ? fmaxf(a, b) : fmaxf(a, b) * mult[s];
+            for (int i = 0; i < 4; ++i) a[i] = fmaxf(x[g * kCols + 2 * i], x[g * kCols + 2 * i + 1]);
+#pragma unroll
+            for (int j = 8; j < kCols; j += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = fmax3f(a[i], x[g * kCols + j + 2 * i], x[g * kCols + j + 2 * i + 1]);
+            float top = fmaxf(fmax3f(a[0], a[1], a[2]), a[3]);
+            if constexpr (!kCap) top *= mult[g];
             tmax = fmaxf(tmax, top);
-            if constexpr (kF8) dmax = fmaxf(dmax, top + vexp[s]);
+            if constexpr (kF8) dmax = fmaxf(dmax, top + lgv[g]);
           }
           const bool move = tmax > m + kRaise || (m == -INFINITY && tmax != -INFINITY);
           const float m_new = move ? tmax : m;
@@ -731,38 +749,38 @@ paged_chunk_kernel(const ChunkParams p) {
             alpha = rescale ? ex2(m - m_new) : 1.f;
           }
           m = m_new;
+          // P = 2^(x mult - m + lw): lw takes the probability to the reference u (e4m3).  Below
+          // 2^-40 it is zero in fp16 whatever its size, so lw stops there and the sum of P
+          // 2^-lw keeps every probability.
+          float lw[kSub], tile_sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < kSub; ++g)
+            lw[g] = kF8 && m != -INFINITY ? fminf(fmaxf(lgv[g] + (m - u) + 8.f, -40.f), 100.f) : 0.f;
           const float mm = m == -INFINITY ? 0.f : m;
-          uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-          const uint64_t negm2 = pack_f32x2(-mm, -mm);
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
+          for (int g = 0; g < kSub; ++g) {
+            uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+            const uint64_t base2 = pack_f32x2(lw[g] - mm, lw[g] - mm);
+            const float ms = kCap ? 1.f : mult[g];
+            const uint64_t m2 = pack_f32x2(ms, ms);
 #pragma unroll
-            for (int s = 2 * c; s < 2 * c + 2; ++s) {
-              const float w1 = !kF8 ? 1.f : m == -INFINITY ? 0.f : vman[s] * ex2(fminf(vexp[s] + m - u + 8.f, 126.f));
-              const uint64_t w2 = pack_f32x2(w1, w1);
-              const float ms = kCap ? 1.f : mult[s];
-              const uint64_t m2 = pack_f32x2(ms, ms);
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float a0, a1;
-                unpack_f32x2(fma_f32x2(pack_f32x2(x[16 * s + j], x[16 * s + j + 1]), m2, negm2), a0, a1);
-                uint64_t e2 = pack_f32x2(ex2(a0), ex2(a1));
-                sum2[(j >> 1) & 3] = add_f32x2(sum2[(j >> 1) & 3], e2);
-                if constexpr (kF8) e2 = mul_f32x2(e2, w2);
-                float e0, e1;
-                unpack_f32x2(e2, e0, e1);
-                pk[8 * (s - 2 * c) + (j >> 1)] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-              }
+            for (int j = 0; j < kCols; j += 2) {
+              const int col = g * kCols + j;
+              float a0, a1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[col], x[col + 1]), m2, base2), a0, a1);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              sum2[(j >> 1) & 3] = add_f32x2(sum2[(j >> 1) & 3], pack_f32x2(a0, a1));
+              pk[(col >> 1) & 15] = kF8 ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
+              if ((col & 31) == 30) tmem_st_32x32b_x16_u_nw(s_col + (col >> 5) * 16, pk);
             }
-            tmem_st_32x32b_x16_u_nw(s_col + c * 16, pk);
-          }
-          tmem_wait_st();
-          {
             float lo, hi;
             unpack_f32x2(add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3])), lo, hi);
-            l += lo + hi;
+            tile_sum += kF8 ? (lo + hi) * ex2(-lw[g]) : lo + hi;
           }
+          tmem_wait_st();
+          l += tile_sum;
           if (t > 0) {
             // O_w holds PV(0 .. t - 2); a rescale also waits for PV(t - 1)
             if (__any_sync(0xffffffffu, rescale)) {
@@ -924,10 +942,10 @@ paged_chunk_merge_kernel(const ChunkParams p) {
   }
 }
 
-template <bool kF8, int D, bool kCap>
+template <bool kF8, int D, bool kCap, int kSub>
 cudaError_t launch(const ChunkParams& p, cudaStream_t st) {
   using C = Cfg<D>;
-  auto* kernel = paged_chunk_kernel<kF8, D, kCap>;
+  auto* kernel = paged_chunk_kernel<kF8, D, kCap, kSub>;
   static thread_local unsigned long long set = 0;  // devices whose limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -950,6 +968,17 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, paged_chunk_merge_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t launch_f8(const ChunkParams& p, cudaStream_t st) {
+  const bool cap = p.cap > 0.f;
+  if (p.c.p_shift >= 6) return cap ? launch<true, D, true, 1>(p, st) : launch<true, D, false, 1>(p, st);
+  return cap ? launch<true, D, true, 4>(p, st) : launch<true, D, false, 4>(p, st);
+}
+template <int D>
+cudaError_t launch_bf16(const ChunkParams& p, cudaStream_t st) {
+  return p.cap > 0.f ? launch<false, D, true, 1>(p, st) : launch<false, D, false, 1>(p, st);
 }
 
 constexpr size_t kItemBytes = sizeof(SplitChunk) * kCtas;
@@ -998,13 +1027,10 @@ int launch_paged_chunk(const PagedView& c, int f8, int D, const void* q, long lo
   p.window_right = window_right;
   p.wait_limit = wait_timeout_cycles();
   cudaError_t e;
-  const bool capped = cap > 0.f;
   if (D == 128)
-    e = f8 ? (capped ? launch<true, 128, true>(p, stream) : launch<true, 128, false>(p, stream))
-           : (capped ? launch<false, 128, true>(p, stream) : launch<false, 128, false>(p, stream));
+    e = f8 ? launch_f8<128>(p, stream) : launch_bf16<128>(p, stream);
   else
-    e = f8 ? (capped ? launch<true, 64, true>(p, stream) : launch<true, 64, false>(p, stream))
-           : (capped ? launch<false, 64, true>(p, stream) : launch<false, 64, false>(p, stream));
+    e = f8 ? launch_f8<64>(p, stream) : launch_bf16<64>(p, stream);
   if (e != cudaSuccess) return cuda_error(e, "paged attention chunk launch");
   return SBA_OK;
 }
