@@ -195,6 +195,7 @@ paged_append_few_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
   constexpr int kRows = 32 / kRowThreads;
   const PagedView& c = p.c;
+  paged_wait_before();
   const int lane = threadIdx.x & 31;
   const int stream = blockIdx.y * 4 + (threadIdx.x >> 5);
   if (stream >= p.Hq + 2 * c.Hkv) return;
@@ -261,6 +262,7 @@ paged_append_kernel(const AppendParams p) {
   const int tid = threadIdx.x;
   __shared__ int s_b;
   __shared__ float s_max[2][16];
+  paged_wait_before();
   int b, j;
   if (c.cu == nullptr) {
     b = blockIdx.x / p.units_per_row;
@@ -369,20 +371,19 @@ paged_append_kernel(const AppendParams p) {
 }
 
 template <bool kF8, int kD>
-void launch_append(AppendParams p, cudaStream_t st) {
+cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const PagedView& c = p.c;
   const int streams = p.Hq + 2 * c.Hkv;
   if (c.cu == nullptr && c.Qn <= 512 / kD) {
     dim3 grid((unsigned)c.B * p.units_per_row, (streams + 3) / 4);
-    paged_append_few_kernel<kF8, kD><<<grid, 128, 0, st>>>(p);
-    return;
+    return paged_launch(paged_append_few_kernel<kF8, kD>, grid, 128, 0, st, p);
   }
   const long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row
                                           : ((long long)c.N >> c.p_shift) + 2LL * c.B;
   // up to 8 heads a block, as long as there are blocks enough to fill the GPU
   p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
   dim3 grid((unsigned)units, (streams + p.heads - 1) / p.heads);
-  paged_append_kernel<kF8, kD><<<grid, (kD << c.p_shift) / 32, 0, st>>>(p);
+  return paged_launch(paged_append_kernel<kF8, kD>, grid, (kD << c.p_shift) / 32, 0, st, p);
 }
 
 }  // namespace
@@ -416,11 +417,11 @@ int launch_paged_append(const PagedView& c, int f8, int D, const void* k, long l
   p.max_pos = max_pos;
   // n tokens in a row lie in at most floor((n - 2) / P) + 2 pages (n >= 2), one for n = 1
   p.units_per_row = c.Qn <= 1 ? 1 : ((c.Qn - 2) >> c.p_shift) + 2;
+  cudaError_t e;
   if (D == 128)
-    f8 ? launch_append<true, 128>(p, stream) : launch_append<false, 128>(p, stream);
+    e = f8 ? launch_append<true, 128>(p, stream) : launch_append<false, 128>(p, stream);
   else
-    f8 ? launch_append<true, 64>(p, stream) : launch_append<false, 64>(p, stream);
-  const cudaError_t e = cudaGetLastError();
+    e = f8 ? launch_append<true, 64>(p, stream) : launch_append<false, 64>(p, stream);
   if (e != cudaSuccess) return cuda_error(e, "paged append launch");
   return SBA_OK;
 }

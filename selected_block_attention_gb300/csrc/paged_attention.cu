@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = kPagedWarps * 32;
 constexpr int kCtas = 456;    // three for each of 152 SMs
 constexpr int kMinTiles = 4;  // tiles of a run, at least: one for each warp
-constexpr int kItemCost = 8;  // tiles that an item's fixed cost is worth
+constexpr int kItemCost = 12;  // tiles that an item's fixed cost is worth
 
 struct PagedAttnParams {
   PagedView c;
@@ -93,6 +93,7 @@ paged_attention_kernel(const PagedAttnParams p) {
   } s_it;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
+  paged_wait_before();
 
   // ---- this CTA's run [t0, t1) of the line, and the row it begins in
   {
@@ -144,7 +145,7 @@ paged_attention_kernel(const PagedAttnParams p) {
   long long cur = cta * run_length();
   int b = s_row;
   long long off = s_off;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  paged_let_next();
   if (tid == 0) p.split[cta].n = 0;
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * W::kWarpBytes;
@@ -304,7 +305,7 @@ paged_merge_kernel(const PagedAttnParams p) {
   using W = PagedWarp<kF8, kD, 32, true, false>;
   constexpr int kCols = kD / 32;
   const int cta = blockIdx.x, r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  paged_wait_before();
   const SplitItem it = p.split[cta];
   if (it.n == 0 || r >= it.n_rows) return;
   auto ml_of = [&](int i) {
@@ -323,22 +324,27 @@ paged_merge_kernel(const PagedAttnParams p) {
     const float f = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
     if (ml.y != 0.f) L = fmaf(f, ml.y, L);
     const int n = min(32, it.n - base);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const int slot = base + i == 0 ? cta * 2 + 1 : (cta + base + i) * 2;
-      const float* src = p.part_o + ((long long)slot * 16 + r) * kD + lane * kCols;
-      float v[kCols];
-      if constexpr (kCols == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(src);
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-      } else {
-        const float2 w = *reinterpret_cast<const float2*>(src);
-        v[0] = w.x; v[1] = w.y;
-      }
-      const float fi = __shfl_sync(0xffffffffu, f, i);
+    // sixteen partials in flight (a few of the last group are read twice, with weight 0)
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      float v[16][kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        if (fi != 0.f) O[c] = fmaf(fi, v[c], O[c]);
+      for (int x = 0; x < 16; ++x) {
+        const int i = base + min(i0 + x, n - 1);
+        const int slot = i == 0 ? cta * 2 + 1 : (cta + i) * 2;
+        const float* src = p.part_o + ((long long)slot * 16 + r) * kD + lane * kCols;
+        if constexpr (kCols == 4)
+          *reinterpret_cast<float4*>(v[x]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v[x]) = *reinterpret_cast<const float2*>(src);
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float fi = __shfl_sync(0xffffffffu, f, (i0 + x) & 31);
+        if (i0 + x < n && fi != 0.f) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) O[c] = fmaf(fi, v[x][c], O[c]);
+        }
+      }
     }
   }
 #pragma unroll
@@ -358,28 +364,11 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kPagedWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
   auto* kernel = paged_attention_kernel<kF8, kD, kHi, kCap>;
-  static thread_local unsigned long long set = 0;  // devices whose limit is raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((set >> dev) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) set |= 1ull << dev;
-  }
-  kernel<<<kCtas, kThreads, bytes, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas, kHi ? 4 : 2);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<kF8, kD>, p);
+  static thread_local unsigned long long devices = 0;
+  cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
+  if (e == cudaSuccess) e = paged_launch(kernel, dim3(kCtas), kThreads, bytes, st, p);
+  if (e == cudaSuccess) e = paged_launch(paged_merge_kernel<kF8, kD>, dim3(kCtas, kHi ? 4 : 2), 128, 0, st, p);
+  return e;
 }
 
 template <bool kF8, int kD>

@@ -247,6 +247,7 @@ paged_chunk_kernel(const ChunkParams p) {
   const Abort ab{abort_flag, &g_err_chunk, 5u, p.wait_limit};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
+  paged_wait_before();
 
   // ---- the CTA's run
   {
@@ -312,7 +313,7 @@ paged_chunk_kernel(const ChunkParams p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  paged_let_next();
   const uint32_t tmem = *tmem_holder;
   const uint32_t smem_base = smem_u32(smem);
   auto seg_at = [&](int slot) -> Segment& {
@@ -901,7 +902,7 @@ paged_chunk_merge_kernel(const ChunkParams p) {
   constexpr int kCols = D / 4;
   __shared__ __align__(16) __nv_bfloat16 s_out[32][D + 8];
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  paged_wait_before();
   const SplitChunk it = p.split[cta];
   const int r0 = blockIdx.y * 32, r = r0 + lane;
   if (it.n == 0 || r0 >= it.rows) return;
@@ -946,28 +947,11 @@ template <bool kF8, int D, bool kCap, int kSub>
 cudaError_t launch(const ChunkParams& p, cudaStream_t st) {
   using C = Cfg<D>;
   auto* kernel = paged_chunk_kernel<kF8, D, kCap, kSub>;
-  static thread_local unsigned long long set = 0;  // devices whose limit is raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((set >> dev) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) set |= 1ull << dev;
-  }
-  kernel<<<kCtas, kThreads, C::kSmemBytes, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas, kRows / 32);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_chunk_merge_kernel<D>, p);
+  static thread_local unsigned long long devices = 0;
+  cudaError_t e = paged_allow_smem(kernel, C::kSmemBytes, &devices);
+  if (e == cudaSuccess) e = paged_launch(kernel, dim3(kCtas), kThreads, C::kSmemBytes, st, p);
+  if (e == cudaSuccess) e = paged_launch(paged_chunk_merge_kernel<D>, dim3(kCtas, kRows / 32), 128, 0, st, p);
+  return e;
 }
 
 template <int D>

@@ -33,22 +33,6 @@ constexpr float kPagedLn2 = 0.6931471805599453f;
 constexpr int kPagedWarps = 4;
 constexpr int kPagedStages = 2;
 
-__device__ __forceinline__ void paged_cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void paged_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void paged_cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 paged_lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void paged_sts16(uint32_t a, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 __device__ __forceinline__ uint2 paged_lds8(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -57,13 +41,13 @@ __device__ __forceinline__ uint2 paged_lds8(uint32_t a) {
 template <bool kHalf>
 __device__ __forceinline__ void paged_mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (kHalf)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -280,24 +264,22 @@ struct PagedWarp {
 #pragma unroll
       for (int n = 0; n < 2; ++n) sc[s][n][0] = sc[s][n][1] = sc[s][n][2] = sc[s][n][3] = 0.f;
     if constexpr (kF8) {
+      // four accumulators in turn: a step of one chain waits for nothing
 #pragma unroll
-      for (int s = 0; s < kSub; ++s)
+      for (int s0 = 0; s0 < kSub; s0 += 2)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int row = 16 * s + 8 * n + g;
+        for (int i = 0; i < kKS / 4; ++i) {
+          uint4 w[4];
 #pragma unroll
-          for (int i = 0; i < kKS / 4; ++i) {
-            const uint4 w = paged_lds16(kt + at(row, c + 4 * i));
-            uint32_t b0, b1;
-            e4m3x4_to_f16x2(w.x, b0, b1);
-            paged_mma<true>(sc[s][n], qa[4 * i], b0, b1);
-            e4m3x4_to_f16x2(w.y, b0, b1);
-            paged_mma<true>(sc[s][n], qa[4 * i + 1], b0, b1);
-            e4m3x4_to_f16x2(w.z, b0, b1);
-            paged_mma<true>(sc[s][n], qa[4 * i + 2], b0, b1);
-            e4m3x4_to_f16x2(w.w, b0, b1);
-            paged_mma<true>(sc[s][n], qa[4 * i + 3], b0, b1);
-          }
+          for (int x = 0; x < 4; ++x) w[x] = paged_lds16(kt + at(16 * (s0 + (x >> 1)) + 8 * (x & 1) + g, c + 4 * i));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16x2(k == 0 ? w[x].x : k == 1 ? w[x].y : k == 2 ? w[x].z : w[x].w, b0, b1);
+              paged_mma<true>(sc[s0 + (x >> 1)][x & 1], qa[4 * i + k], b0, b1);
+            }
         }
     } else {
       const int mi = lane >> 3, ri = lane & 7;

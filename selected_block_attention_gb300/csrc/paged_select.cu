@@ -56,6 +56,7 @@ paged_select_kernel(const PagedSelectParams p) {
   const int h = blockIdx.x / split % p.c.Hkv, token = blockIdx.x / split / p.c.Hkv;
   const int b = token / p.c.Qn, qi = token - b * p.c.Qn;
 
+  paged_wait_before();
   bool bad;
   const PagedRow r = paged_row(p.c, b, &bad);
   if (bad && tid == 0) atomicOr(&g_err_select, (unsigned)kDevErrInput);
@@ -168,28 +169,11 @@ cudaError_t launch(const PagedSelectParams& p, cudaStream_t st) {
   constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
   auto* kernel = paged_select_kernel<kF8, kD, kHi>;
-  static thread_local unsigned long long set = 0;  // devices whose limit is raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static thread_local unsigned long long devices = 0;
+  cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((set >> dev) & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) set |= 1ull << dev;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.c.B * p.c.Qn * p.c.Hkv * p.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  const long long items = (long long)p.c.B * p.c.Qn * p.c.Hkv;
+  return paged_launch(kernel, dim3((unsigned)(items * p.split)), kThreads, bytes, st, p, p.split);
 }
 
 }  // namespace
