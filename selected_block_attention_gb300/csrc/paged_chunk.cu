@@ -45,7 +45,7 @@ constexpr int kM = 128;       // rows of a half
 constexpr int kRows = 2 * kM;
 constexpr int kKT = 64;       // keys of a tile
 constexpr int kMinTiles = 4;  // tiles of a run, at least
-constexpr int kItemCost = 6;  // tiles that an item's queries and output are worth
+constexpr int kItemCost = 12;  // tiles that an item's queries and output are worth
 constexpr float kRaise = 8.f;
 constexpr float kRaiseU = 6.f;
 
@@ -115,6 +115,7 @@ struct Segment {
   int n;               // CTAs of the item, when it begins here
   int end;             // no more items
 };
+constexpr int kMetas = 8;  // tiles whose scales are kept
 constexpr int kSegs = 4;  // slots; each is read by 4 loader, 2 MMA and 8 softmax warps
 // Walks the run.
 struct Walker {
@@ -176,8 +177,8 @@ struct Cfg {
   static constexpr int kStages = 4;
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kStagesK * kTBytes;
-  static constexpr int kOffMeta = kOffV + kStages * kTBytes;  // per V stage: 4 key, 4 value scales
-  static constexpr int kOffSegs = kOffMeta + kStages * 32;
+  static constexpr int kOffMeta = kOffV + kStages * kTBytes;  // per tile: 4 key, 4 value scales
+  static constexpr int kOffSegs = kOffMeta + kMetas * 32;
   static constexpr int kOffBars = (kOffSegs + kSegs * (int)sizeof(Segment) + 7) & ~7;
   static constexpr int kNumBars = 2 * kSegs + 2 + 2 * kStagesK + 2 * kStages + 4 + 4 + 2 + 2 + 2 + 2;
   static constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) & ~15;
@@ -226,8 +227,8 @@ paged_chunk_kernel(const ChunkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ long long s_sum[kThreads / 32], s_total, s_at;
-  __shared__ int s_row;
+  __shared__ long long s_sum[kThreads / 32], s_total;
+  __shared__ int s_b, s_h, s_g, s_off;  // where the CTA's run begins
   uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
   uint64_t* seg_full = bb;  bb += kSegs;
   uint64_t* seg_empty = bb; bb += kSegs;
@@ -249,46 +250,85 @@ paged_chunk_kernel(const ChunkParams p) {
   const int cta = blockIdx.x;
   paged_wait_before();
 
-  // ---- the CTA's run
+  // ---- the CTA's run: each warp adds up a share of the rows, lanes over a row's groups
+  // (few rows: they are long) or over rows
   {
-    const int chunk = (p.c.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * chunk, p.c.B), b1 = min(b0 + chunk, p.c.B);
-    long long sum = 0;
+    const bool by_row = p.c.B > 4 * (kThreads / 32);
+    const int chunk = (p.c.B + kThreads / 32 - 1) / (kThreads / 32);
+    const int b0 = min(warp * chunk, p.c.B), b1 = min(b0 + chunk, p.c.B);
     bool any_bad = false;
-    for (int b = b0; b < b1; ++b) {
+    // units of one KV head of row b, in every lane
+    auto row_sum = [&](const PagedRow& r) {
+      const int n = groups_of(p, r);
+      long long x = 0;
+      for (int g = lane; g < n; g += 32) x += group_tiles(p, r, g).units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      return x;
+    };
+    auto units_of_lane = [&](int b) {  // of row b, all KV heads
       bool bad;
       const PagedRow r = paged_row(p.c, b, &bad);
       any_bad |= bad;
-      sum += row_units(p, r) * p.c.Hkv;
+      return row_units(p, r) * p.c.Hkv;
+    };
+    long long sum = 0;
+    if (by_row) {
+      for (int b = b0 + lane; b < b1; b += 32) sum += units_of_lane(b);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    } else {
+      for (int b = b0; b < b1; ++b) {
+        bool bad;
+        const PagedRow r = paged_row(p.c, b, &bad);
+        any_bad |= bad;
+        sum += row_sum(r) * p.c.Hkv;
+      }
     }
     if (any_bad && cta == 0) atomicOr(&g_err_chunk.flags, (unsigned)kDevErrInput);
-    long long pre = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, pre, d);
-      if (lane >= d) pre += x;
-    }
-    if (lane == 31) s_sum[warp] = pre;
+    if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
-    long long total = 0;
+    long long total = 0, pre = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
-      if (i == warp) pre += total;
+      if (i == warp) pre = total;
       total += s_sum[i];
     }
-    pre -= sum;
-    const long long per = max((total + kCtas - 1) / kCtas, (long long)(kMinTiles + kItemCost));
-    const long long t0 = (long long)cta * per;
+    const long long t0 = (long long)cta * max((total + kCtas - 1) / kCtas, (long long)(kMinTiles + kItemCost));
     if (t0 >= pre && t0 < pre + sum) {
       long long off = t0 - pre;
       int b = b0;
+      PagedRow r;
+      long long one;
       for (;; ++b) {
         bool bad;
-        const long long n = row_units(p, paged_row(p.c, b, &bad)) * p.c.Hkv;
-        if (off < n) break;
-        off -= n;
+        r = paged_row(p.c, b, &bad);
+        one = row_sum(r);
+        if (off < one * p.c.Hkv) break;
+        off -= one * p.c.Hkv;
       }
-      s_row = b;
-      s_at = off;
+      const int h = (int)(off / one);
+      off -= h * one;
+      for (int g0 = 0;; g0 += 32) {  // the group: 32 at a time
+        const int g = g0 + lane, u = g < groups_of(p, r) ? group_tiles(p, r, g).units : 0;
+        int end = u;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, end, d);
+          if (lane >= d) end += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, end, 31);
+        if (off >= all) {
+          off -= all;
+          continue;
+        }
+        if (off >= end - u && off < end) {
+          s_b = b;
+          s_h = h;
+          s_g = g;
+          s_off = (int)off - (end - u);
+        }
+        break;
+      }
     }
     if (tid == 0) s_total = total;
   }
@@ -299,7 +339,8 @@ paged_chunk_kernel(const ChunkParams p) {
       mbar_init(&pv_tile[w], 1); mbar_init(&pv_last[w], 1);
       mbar_init(&o_empty[w], 4); mbar_init(&mma_done[w], 1);
     }
-    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); }
+    // the MMA's completion, and the issuing warp itself: it has seen the tile's scales
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 2); mbar_init(&p_full[i], 4); }
     // both loader warps fill a stage, both MMA warps release it
     for (int i = 0; i < C::kStagesK; ++i) { mbar_init(&k_full[i], 2); mbar_init(&k_empty[i], 2); }
     for (int i = 0; i < C::kStages; ++i) { mbar_init(&v_full[i], 2); mbar_init(&v_empty[i], 2); }
@@ -336,6 +377,7 @@ paged_chunk_kernel(const ChunkParams p) {
     const int pmask = (1 << p.c.p_shift) - 1;
     int ks = 0; uint32_t kphase = 0;
     int vs = 0; uint32_t vphase = 0;
+    int ms = pair;  // the tile's place among the scales
     auto next_k = [&]() { if (++ks == C::kStagesK) { ks = 0; kphase ^= 1; } };
     auto next_v = [&]() { if (++vs == C::kStages) { vs = 0; vphase ^= 1; } };
     // ---- the run's tiles in order; this pair's are every second one
@@ -386,20 +428,26 @@ paged_chunk_kernel(const ChunkParams p) {
     };
     if constexpr (kF8) {
       uint4 rk[kN], rv[kN];
-      float kc[2], vc[2], kc_next[2];
-      auto load = [&](const uint8_t* pool, const float* scales, uint4 (&raw)[kN], float (&sc)[2]) {
+      float kc[2], vc[2];
+      auto load_scales = [&]() {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const long long at = (long long)page_at(x) * p.c.Hkv + h;
+          kc[x] = __ldg(p.c.ks + at);
+          vc[x] = __ldg(p.c.vs + at);
+        }
+      };
+      auto load = [&](const uint8_t* pool, uint4 (&raw)[kN]) {
         const bool inside = key0 >= cl && key0 + 31 <= ch;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int page = page_at(x);
-          const uint8_t* src = pool + byte_of(page);
+          const uint8_t* src = pool + byte_of(page_at(x));
           auto rows = [&](bool in) {
 #pragma unroll
             for (int j = 0; j < kHalf; ++j)
               raw[x * kHalf + j] = __ldg(reinterpret_cast<const uint4*>(src + row_off(x, j, in)));
           };
           if (inside) rows(true); else rows(false);
-          sc[x] = __ldg(scales + (long long)page * p.c.Hkv + h);
         }
       };
       // 16 codes as two 16-byte chunks of fp16
@@ -427,8 +475,9 @@ paged_chunk_kernel(const ChunkParams p) {
       }
       look();
       if (have) {
-        load(p.c.k, p.c.ks, rk, kc);
-        load(p.c.v, p.c.vs, rv, vc);
+        load_scales();
+        load(p.c.k, rk);
+        load(p.c.v, rv);
       }
       bool more = have;  // a tile is in registers
       step();
@@ -438,25 +487,27 @@ paged_chunk_kernel(const ChunkParams p) {
       // values while the next one's keys are.
       while (more) {
         if (!warp_wait(&k_empty[ks], kphase ^ 1, ab, kRoleLoader, kBarKEmpty, cta)) break;
+        if (lane < 2) {
+          float* meta = reinterpret_cast<float*>(smem + C::kOffMeta + ms * 32);
+          meta[half * 2 + lane] = lane ? kc[1] : kc[0];
+          meta[4 + half * 2 + lane] = lane ? vc[1] : vc[0];
+        }
         put(smem_base + C::kOffK + ks * C::kTBytes, rk);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[ks]);
         more = have;
-        if (have) load(p.c.k, p.c.ks, rk, kc_next);
+        if (have) {
+          load_scales();
+          load(p.c.k, rk);
+        }
         if (!warp_wait(&v_empty[vs], vphase ^ 1, ab, kRoleLoader, kBarVEmpty, cta)) break;
         put(smem_base + C::kOffV + vs * C::kTBytes, rv);
-        if (lane < 2) {
-          float* meta = reinterpret_cast<float*>(smem + C::kOffMeta + vs * 32);
-          meta[half * 2 + lane] = lane ? kc[1] : kc[0];
-          meta[4 + half * 2 + lane] = lane ? vc[1] : vc[0];
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[vs]);
-        if (have) load(p.c.v, p.c.vs, rv, vc);
-        kc[0] = kc_next[0];
-        kc[1] = kc_next[1];
+        if (have) load(p.c.v, rv);
+        ms = (ms + 2) % kMetas;
         next_k(); next_k();
         next_v(); next_v();
         step();
@@ -535,6 +586,7 @@ paged_chunk_kernel(const ChunkParams p) {
           mma_f16_ss_by(leader, s_tmem(buf), q_desc + kstep(kk, C::kQPanel), kd + kstep(kk, C::kTPanel), kIdescQK,
                         kk > 0 ? 1u : 0u);
         mma_commit_by(leader, &s_full[2 * w + buf]);
+        if (lane == 0) mbar_arrive(&s_full[2 * w + buf]);
         mma_commit_by(leader, &k_empty[ks]);
         next_k();
         return true;
@@ -596,18 +648,11 @@ paged_chunk_kernel(const ChunkParams p) {
       walk.end = min(walk.cur + per, s_total);
       if (lane == 0) p.split[cta].n = 0;
       if (walk.cur < walk.end) {
-        walk.b = s_row;
+        walk.b = s_b;
+        walk.h = s_h;
+        walk.g = s_g;
+        walk.off = s_off;
         walk.row(p);
-        const long long one = row_units(p, walk.r);
-        walk.h = (int)(s_at / one);
-        long long off = s_at - walk.h * one;
-        walk.g = 0;
-        for (;; ++walk.g) {
-          const int u = group_tiles(p, walk.r, walk.g).units;
-          if (off < u) break;
-          off -= u;
-        }
-        walk.off = (int)off;
       }
       int slot = 0; uint32_t phase = 0;
       while (true) {
@@ -631,7 +676,7 @@ paged_chunk_kernel(const ChunkParams p) {
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t o_col = tmem + lane_off + C::kOCol + w * D;
     uint8_t* my_q = smem + w * C::kQBytes + r * 128;
-    int vs = 0; uint32_t vphase = 0;
+    int ms = 0;  // the tile's place among the scales
     uint32_t sph = 0u, pvt_ph = 0u, pvl_ph = 0u;
     for (int slot = 0, phase = 0;; phase ^= ++slot == kSegs, slot %= kSegs) {
       if (!warp_wait(&seg_full[slot], phase, ab, kRoleSoftmax, kBarSegFull, cta)) break;
@@ -693,9 +738,7 @@ paged_chunk_kernel(const ChunkParams p) {
           sph ^= 1u << buf;
           float mult[kSub], lgv[kSub];  // logit factors, log2 of the value scales
           if constexpr (kF8) {
-            // the scales arrived with the values
-            if (!warp_wait(&v_full[vs], vphase, ab, kRoleSoftmax, kBarVFull, cta)) { ok = false; break; }
-            const float* meta = reinterpret_cast<const float*>(smem + C::kOffMeta + vs * 32);
+            const float* meta = reinterpret_cast<const float*>(smem + C::kOffMeta + ms * 32);
 #pragma unroll
             for (int g = 0; g < kSub; ++g) {
               mult[g] = f * meta[g];
@@ -704,7 +747,7 @@ paged_chunk_kernel(const ChunkParams p) {
           } else {
             mult[0] = f;
           }
-          if (++vs == C::kStages) { vs = 0; vphase ^= 1; }
+          ms = (ms + 1) % kMetas;
           float x[kKT];
           tc_fence_after();
 #pragma unroll
@@ -808,8 +851,7 @@ paged_chunk_kernel(const ChunkParams p) {
         pvt_ph ^= 1u;
         tc_fence_after();
       } else {
-        for (int t = 0; t < nt; ++t)
-          if (++vs == C::kStages) { vs = 0; vphase ^= 1; }
+        ms = (ms + nt) % kMetas;
       }
 
       // ---- the row's result, or its partial
