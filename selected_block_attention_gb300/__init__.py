@@ -18,8 +18,8 @@ Entry points (same names as the C ABI without the ``sba_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -124,7 +124,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sba_paged_attention_workspace_size.argtypes = [ci] * 5
     lib.sba_paged_attention_workspace_size.restype = csz
     for fn in (lib.sba_paged_kv_append, lib.sba_paged_attention_fwd, lib.sba_nsa_select_paged_fwd):
-        fn.argtypes = [ctypes.c_char_p, vp]  # the packed argument struct, the stream
+        fn.argtypes = [vp, vp]  # the argument struct, the stream
         fn.restype = ci
     lib.sba_set_wait_timeout_cycles.argtypes = [ctypes.c_longlong]
     lib.sba_set_wait_timeout_cycles.restype = ci
@@ -468,210 +468,46 @@ def ragged_flash_attention_fwd(q, k, v, sequence_start, sequence_end, *, softmax
 
 
 # ---------------------------------------------------------------- paged caches
-# A decode step makes these calls once per layer on small batches, so their host time
-# counts: arguments travel as one packed struct (32 ctypes arguments take 5 us, packing
-# them 0.3 us), and every tensor attribute is read once.
-_CACHE = "7Pq9i"  # sba_paged_cache
-_APPEND_ARGS = struct.Struct("@" + _CACHE + "6P4q4i")
-_ATTENTION_ARGS = struct.Struct("@" + _CACHE + "5PNqif2if2i")
-_SELECT_ARGS = struct.Struct("@" + _CACHE + "6Pq5if")
-_CACHE_DTYPES = {torch.float8_e4m3fn: SBA_E4M3, torch.bfloat16: SBA_BF16}
-_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
-# The raw forms of torch.cuda.current_device() and current_stream(): the latter builds a
-# Stream object, which takes longer than the launch.
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# A decode step makes these calls once per layer on small batches, where the host's time
+# counts, so their checks, allocations and calls are in C++ (csrc/binding.cpp).
+_PAGED_CALLS = ("paged_kv_append", "paged_attention_fwd", "nsa_select_paged_fwd")
+_paged = None
 
 
-def _paged_call(index, fn, args):
-    """_call with a device index; most calls find their device current already."""
-    if _current_device() == index:
-        code = fn(args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            code = fn(args, _raw_stream(index))
-    if code:
-        _check(code)
+def _paged_module():
+    """The built module; its functions take the place of the ones that loaded it."""
+    global _paged
+    if _paged is None:
+        load_library()
+        if not os.path.exists(_build.MODULE_PATH):
+            raise RuntimeError(f"{_build.MODULE_PATH} not found; build it with "
+                               "selected_block_attention_gb300._build.build()")
+        spec = importlib.util.spec_from_file_location(f"{__name__}._paged", _build.MODULE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(SBAError)
+        for name in _PAGED_CALLS:
+            globals()[name] = getattr(module, name)
+        _paged = module
+    return _paged
 
 
-def _at(t, name, index, dtype, shape):
-    """Address of a contiguous CUDA tensor on device ``index``; 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.get_device() != index or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)} on the cache's device")
-    return t.data_ptr()
+def _first_call(name):
+    def call(*args, **kwargs):
+        return getattr(_paged_module(), name)(*args, **kwargs)
+
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = f"{name} of the paged caches (loads the built module on the first call)."
+    return call
 
 
-def _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table, seq_lens, cu_seqlens):
-    """(device index, Hkv, D, B, the fields of sba_paged_cache before Q)."""
-    index = k_pages.get_device()
-    if index < 0:
-        raise ValueError("libsba works on CUDA tensors only (no CPU path)")
-    kind = k_pages.dtype
-    dtype = _CACHE_DTYPES.get(kind)
-    if dtype is None or v_pages.dtype != kind:
-        raise TypeError("k_pages and v_pages must both be float8_e4m3fn or both bfloat16")
-    shape, st = k_pages.shape, k_pages.stride()
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.get_device() != index:
-        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D] on one device")
-    pages, hkv, size, d = shape
-    for s in (st, v_pages.stride()):
-        if s[3] != 1 or s[2] != d or (s[1] != size * d and hkv > 1) or (s[0] != st[0] and pages > 1):
-            raise ValueError("k_pages, v_pages: pages must be dense and lie as far apart in both pools")
-    table_shape = page_table.shape
-    if len(table_shape) != 2:
-        raise ValueError("page_table must be [B, width]")
-    batch, width = table_shape
-    scale_shape = (pages, hkv)
-    return index, hkv, d, batch, (
-        k_pages.data_ptr(), v_pages.data_ptr(), _at(k_scales, "k_scales", index, _F32, scale_shape),
-        _at(v_scales, "v_scales", index, _F32, scale_shape),
-        _at(page_table, "page_table", index, _I32, table_shape), _at(seq_lens, "seq_lens", index, _I32, (batch,)),
-        0 if cu_seqlens is None else _at(cu_seqlens, "cu_seqlens", index, _I32, (batch + 1,)),
-        st[0] if pages > 1 else hkv * size * d, pages, size, hkv, d, dtype, width, batch)
-
-
-def _token_rows(t, name, index, d, batch):
-    """(address, Q, N, heads, token stride) of bf16 token rows: [N, H, D] with cu_seqlens
-    (``batch`` None), else [batch, H, D] (one token per row) or [batch, Q, H, D].  Heads are
-    dense inside a token, tokens equally far apart."""
-    if t.dtype != _BF16:
-        raise TypeError(f"{name} must be bfloat16")
-    shape, st = t.shape, t.stride()
-    heads = shape[-2]
-    if t.get_device() != index or shape[-1] != d or st[-1] != 1 or (st[-2] != d and heads > 1):
-        raise ValueError(f"{name} must be on the cache's device, with its head dimension and dense heads")
-    if len(shape) == 3:
-        n, q, stride = shape[0], 1, st[0]
-    elif len(shape) == 4 and batch is not None:
-        q = shape[1]
-        n, stride = shape[0] * q, st[1] if q > 1 else st[0]
-        if q > 1 and shape[0] > 1 and st[0] != q * stride:
-            raise ValueError(f"{name}: tokens must lie equally far apart")
-    else:
-        raise ValueError(f"{name} must be [B, H, D] or [B, Q, H, D], or [N, H, D] with cu_seqlens")
-    if batch is not None and shape[0] != batch:
-        raise ValueError(f"{name} must have one entry per row of page_table")
-    return t.data_ptr(), q, n, heads, stride if n > 1 else heads * d
-
-
-def paged_kv_append(k, v, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
-                    cu_seqlens=None, q=None, cos=None, sin=None, interleaved=False, q_out=None):
-    """Write the rows' last tokens into a paged cache.  k / v bf16 [B, Hkv, D] (one token
-    per row), [B, Q, Hkv, D], or [N, Hkv, D] with cu_seqlens int32 [B + 1]; token strides
-    may be those of a slice.  k_pages / v_pages [num_pages, Hkv, page_size, D]
-    float8_e4m3fn (with fp32 scales [num_pages, Hkv]) or bfloat16, page_table int32
-    [B, width], seq_lens int32 [B] with the new tokens counted.  cos / sin fp32
-    [max_pos, rot_dim / 2] turn keys (and q, [..., Hq, D]) by their positions.  Returns
-    q_out (new unless given; may be q), or None without q."""
-    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
-                                               seq_lens, cu_seqlens)
-    rows = batch if cu_seqlens is None else None
-    kp, Q, N, heads, k_stride = _token_rows(k, "k", index, d, rows)
-    vp, vq, vn, v_heads, v_stride = _token_rows(v, "v", index, d, rows)
-    if heads != hkv or v_heads != hkv or vq != Q or vn != N:
-        raise ValueError("k and v must have the same tokens and the cache's heads")
-    qp = op = hq = q_stride = o_stride = rot = max_pos = 0
-    if q is not None:
-        qp, qq, qn, hq, q_stride = _token_rows(q, "q", index, d, rows)
-        if qq != Q or qn != N:
-            raise ValueError("q must have k's tokens")
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            op, o_stride = q_out.data_ptr(), hq * d
-        else:
-            op, oq, on, o_heads, o_stride = _token_rows(q_out, "q_out", index, d, rows)
-            if oq != Q or on != N or o_heads != hq:
-                raise ValueError("q_out must have q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    cos_p = sin_p = 0
-    if cos is not None or sin is not None:
-        if cos is None or sin is None or len(cos.shape) != 2:
-            raise ValueError("cos and sin go together, [max_pos, rot_dim / 2]")
-        table = cos.shape
-        max_pos, rot = table
-        rot *= 2
-        cos_p, sin_p = _at(cos, "cos", index, _F32, table), _at(sin, "sin", index, _F32, table)
-    _paged_call(index, (_lib or load_library()).sba_paged_kv_append, _APPEND_ARGS.pack(
-        *cache, Q, N, kp, vp, qp, op, cos_p, sin_p, k_stride, v_stride, q_stride, o_stride, hq, rot, max_pos,
-        1 if interleaved else 0))
-    return q_out
+for _name in _PAGED_CALLS:
+    globals()[_name] = _first_call(_name)
 
 
 def paged_attention_workspace_size(B, N, Hq, Hkv, D) -> int:
     """Bytes for B rows with N query tokens in all."""
     return int(load_library().sba_paged_attention_workspace_size(B, N, Hq, Hkv, D))
-
-
-def _results(q, index, out, lse, return_lse):
-    """(out, lse, their addresses) of a call on queries q."""
-    shape = q.shape
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        out_p = out.data_ptr()
-    else:
-        out_p = _at(out, "out", index, _BF16, shape)
-    if lse is None and return_lse:
-        lse = torch.empty(shape[:-1], dtype=_F32, device=q.device)
-        return out, lse, out_p, lse.data_ptr()
-    return out, lse, out_p, _at(lse, "lse", index, _F32, shape[:-1])
-
-
-def paged_attention_fwd(q, k_pages, v_pages, page_table, seq_lens, *, k_scales=None, v_scales=None,
-                        cu_seqlens=None, softmax_scale=None, window_left=-1, window_right=-1,
-                        logits_soft_cap=None, sink_bias=None, out=None, lse=None, workspace=None,
-                        return_lse=True):
-    """Attention of the rows' last tokens over a paged cache (as paged_kv_append fills it).
-    q bf16 [B, Hq, D], [B, Q, Hq, D], or [N, Hq, D] with cu_seqlens; windows, soft cap and
-    sink_bias as in ragged_flash_attention_fwd (window_right=0 is causal).  Returns
-    (out, lse) in q's shape and [..., Hq]."""
-    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
-                                               seq_lens, cu_seqlens)
-    qp, Q, N, hq, q_stride = _token_rows(q, "q", index, d, batch if cu_seqlens is None else None)
-    lib = _lib or load_library()
-    bias_p = num_sinks = per_head = 0
-    if sink_bias is not None:
-        per_head = 1 if sink_bias.dim() == 2 else 0
-        num_sinks = sink_bias.shape[-1]
-        bias_p = _at(sink_bias, "sink_bias", index, _F32, (hq, num_sinks) if per_head else (num_sinks,))
-    out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
-    if workspace is None:
-        workspace = torch.empty(lib.sba_paged_attention_workspace_size(batch, N, hq, hkv, d) or 16, dtype=torch.uint8,
-                                device=q.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    _paged_call(index, lib.sba_paged_attention_fwd, _ATTENTION_ARGS.pack(
-        *cache, Q, N, qp, bias_p, out_p, lse_p, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), q_stride, hq, softmax_scale or 0.0, window_left,
-        window_right, logits_soft_cap or 0.0, num_sinks, per_head))
-    return out, lse
-
-
-def nsa_select_paged_fwd(q, k_pages, v_pages, page_table, seq_lens, block_indices, block_counts,
-                         block_size, *, k_scales=None, v_scales=None, causal=True, softmax_scale=None,
-                         g_slc=None, out=None, lse=None, return_lse=True):
-    """Selection-branch NSA of the rows' last tokens over a paged cache: the decode form of
-    nsa_select_fwd.  q bf16 [B, Hq, D] or [B, Q, Hq, D], block_indices int32 [B, (Q,) Hkv, S],
-    block_counts int or int32 [B, (Q,) Hkv], g_slc bf16 [B, (Q,) Hq] or None.  Returns
-    (out, lse)."""
-    index, hkv, d, batch, cache = _paged_cache(k_pages, v_pages, k_scales, v_scales, page_table,
-                                               seq_lens, None)
-    qp, Q, N, hq, q_stride = _token_rows(q, "q", index, d, batch)
-    lead = q.shape[:-2]
-    S = block_indices.shape[-1]
-    counts = isinstance(block_counts, torch.Tensor)
-    idx_p = _at(block_indices, "block_indices", index, _I32, (*lead, hkv, S))
-    cnt_p = _at(block_counts, "block_counts", index, _I32, (*lead, hkv)) if counts else 0
-    gate_p = 0 if g_slc is None else _at(g_slc, "g_slc", index, _BF16, q.shape[:-1])
-    out, lse, out_p, lse_p = _results(q, index, out, lse, return_lse)
-    _paged_call(index, (_lib or load_library()).sba_nsa_select_paged_fwd, _SELECT_ARGS.pack(
-        *cache, Q, N, qp, idx_p, cnt_p, gate_p, out_p, lse_p, q_stride, hq,
-        0 if counts else int(block_counts), S, int(block_size), 1 if causal else 0,
-        softmax_scale or 0.0))
-    return out, lse
 
 
 def l2_read_probe(buf, reps, sink):

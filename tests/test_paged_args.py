@@ -44,7 +44,7 @@ def call(fn, kind, defaults, change):
     own = [n for n, _ in kind._fields_]
     cache = Cache(**{**POOL, **{n: v for n, v in change.items() if n in POOL}})
     args = kind(cache=cache, **{**defaults, **{n: v for n, v in change.items() if n in own}})
-    return fn(ctypes.string_at(ctypes.addressof(args), ctypes.sizeof(args)), None)
+    return fn(ctypes.addressof(args), None)
 
 
 def append(lib, **kw):
@@ -63,20 +63,6 @@ def select(lib, **kw):
     d = dict(q=FAKE, qs=1024, Hq=8, idx=FAKE, cnt=None, n=4, S=4, bs=64, causal=1, scale=0.0, gate=None, out=FAKE,
              lse=None)
     return call(lib.sba_nsa_select_paged_fwd, SELECT, d, kw)
-
-
-def test_binding_packs_the_structs():
-    """The binding's formats have the layout of the structs as the C compiler lays them out."""
-    import selected_block_attention_gb300 as sba
-
-    for fmt, kind in ((sba._APPEND_ARGS, APPEND), (sba._ATTENTION_ARGS, ATTEND), (sba._SELECT_ARGS, SELECT)):
-        n = len(fmt.unpack(bytes(fmt.size)))
-        flat = [(f, t) for f, t in Cache._fields_] + list(kind._fields_[1:])
-        assert n == len(flat)
-        vals = [float(i) if t is ctypes.c_float else i for i, (_, t) in enumerate(flat, 1)]
-        got = kind.from_buffer_copy(fmt.pack(*vals).ljust(ctypes.sizeof(kind), b"\0"))
-        for i, (f, _) in enumerate(flat, 1):
-            assert getattr(got.cache if i <= len(Cache._fields_) else got, f) == i, f
 
 
 COMMON = [(dict(k_pages=None), -1, b"null"), (dict(page_table=None), -1, b"null"), (dict(seq_lens=None), -1, b"null"),
@@ -127,7 +113,7 @@ def test_workspace_size(lib):
         assert size(*bad) == 0
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_refuses_host_tensors(lib):
     import selected_block_attention_gb300 as sba
 
     k = torch.zeros((2, 1, 16, 64), dtype=torch.bfloat16)
@@ -137,3 +123,16 @@ def test_binding_refuses_host_tensors():
                  lambda: sba.nsa_select_paged_fwd(x, k, k, t, n, t.view(1, 1, 2), 2, 32)):
         with pytest.raises(ValueError):
             call()
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            call()
+    with pytest.raises(TypeError, match="misses the argument 'seq_lens'"):
+        sba.paged_attention_fwd(x, k, k, t)
+    with pytest.raises(TypeError, match="unexpected argument 'scale'"):
+        sba.paged_attention_fwd(x, k, k, t, n, scale=1.0)
+    with pytest.raises(TypeError, match="second argument 'q'"):
+        sba.paged_attention_fwd(x, k, k, t, n, q=x)
+    with pytest.raises(TypeError, match="at most 6 positional"):
+        sba.paged_kv_append(x, x, k, k, t, n, None)
+    with pytest.raises(TypeError, match="k_pages must be a tensor"):
+        sba.paged_attention_fwd(x, None, k, t, n)
+    assert "page_table" in sba.paged_kv_append.__doc__
