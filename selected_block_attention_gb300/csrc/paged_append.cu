@@ -164,8 +164,7 @@ __device__ __forceinline__ float finite_max(const float* x, float top) {
   return top;
 }
 // 16 codes that a page holds, from scale `old` to 1 / `inv`.
-__device__ __forceinline__ void rescale16(uint8_t* at, float old, float inv) {
-  uint4 w = *reinterpret_cast<uint4*>(at);
+__device__ __forceinline__ uint4 rescaled16(uint4 w, float old, float inv) {
   uint32_t* c = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -176,7 +175,7 @@ __device__ __forceinline__ void rescale16(uint8_t* at, float old, float inv) {
     c[i] = f32x4_to_e4m3x4(__fmul_rn(__fmul_rn(a.x, old), inv), __fmul_rn(__fmul_rn(a.y, old), inv),
                            __fmul_rn(__fmul_rn(b.x, old), inv), __fmul_rn(__fmul_rn(b.y, old), inv));
   }
-  *reinterpret_cast<uint4*>(at) = w;
+  return w;
 }
 __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int c1, float* x, float inv) {
 #pragma unroll
@@ -187,25 +186,26 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int c1, float*
       make_uint2(f32x4_to_e4m3x4(x[8], x[9], x[10], x[11]), f32x4_to_e4m3x4(x[12], x[13], x[14], x[15]));
 }
 
-// Few tokens a row (at most 512 / kD): one warp for each (page, head); a row of kD / 16
-// threads, 16 dimensions each.
-template <bool kF8, int kD>
+// Few tokens a row: a row of a head is kD / 16 threads, 16 dimensions each.  kOne (one token
+// a row): a warp takes 512 / kD heads; else it takes one head, up to 512 / kD tokens.
+template <bool kF8, int kD, bool kOne>
 __global__ void __launch_bounds__(128)
 paged_append_few_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
   constexpr int kRows = 32 / kRowThreads;
   const PagedView& c = p.c;
   paged_wait_before();
-  const int lane = threadIdx.x & 31;
-  const int stream = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (stream >= p.Hq + 2 * c.Hkv) return;
+  const int lane = threadIdx.x & 31, rt = lane % kRowThreads;
+  const int warp = blockIdx.y * 4 + (threadIdx.x >> 5), streams = p.Hq + 2 * c.Hkv;
+  const int stream = kOne ? warp * kRows + lane / kRowThreads : warp;
+  const int row = kOne ? 0 : lane / kRowThreads;
+  if (warp * (kOne ? kRows : 1) >= streams) return;
   const int b = blockIdx.x / p.units_per_row;
   const Unit u = unit_of(c, b, blockIdx.x - b * p.units_per_row, lane == 0);
   if (u.m <= 0) return;
-  const Stream t = stream_of<kD>(p, stream);
-  const int rt = lane % kRowThreads, row = lane / kRowThreads;
+  const Stream t = stream_of<kD>(p, min(stream, streams - 1));
   const int rot = t.is_q || t.is_k ? p.rot : 0;
-  const bool mine = row < u.m, turn = rt < rot / 16;
+  const bool mine = row < u.m && stream < streams;
   int c0, c1;
   chunks_of(rt, rot, p.interleaved, c0, c1);
   float x[16];
@@ -216,38 +216,56 @@ paged_append_few_kernel(const AppendParams p) {
     load8(s + 8 * c0, x);
     load8(s + 8 * c1, x + 8);
   }
-  const int page = t.is_q ? 0 : page_of(c, u, lane == 0);
+  const bool any_kv = (kOne ? min(warp * kRows + kRows, streams) : warp + 1) > p.Hq;
+  const int page = any_kv ? page_of(c, u, lane == 0) : 0;
   if (page < 0) return;
-  if (mine && turn) {
+  if (mine && rt < rot / 16) {
     float cs[8], sn[8];
     load_angles(p, u.p0 + row, rt, cs, sn);
     rotate16(x, cs, sn, p.interleaved);
   }
   const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
   uint8_t* tile = (t.is_k ? c.k : c.v) + page * c.page_bytes + (long long)t.h * P * (kD * (kF8 ? 1 : 2));
-  if (t.is_q || !kF8) {
-    if (!mine) return;
+  if ((t.is_q || !kF8) && mine) {
     __nv_bfloat16* o = t.is_q ? p.q_out + (long long)(u.first + row) * p.qo_tok + (long long)t.h * kD
                               : reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
     store8(o + 8 * c0, x);
     store8(o + 8 * c1, x + 8);
-    return;
   }
-  float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
-  const float old = off > 0 ? *scale_at : 0.f;
-  float amax = finite_max(x, 0.f);
+  if constexpr (kF8) {
+    const bool stores = !t.is_q && (!kOne || mine);  // this head's values are quantised
+    if (!__any_sync(0xffffffffu, stores)) return;
+    float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
+    const float old = stores && off > 0 ? *scale_at : 0.f;
+    float amax = finite_max(x, 0.f);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  const float need = pow2_scale(amax);
-  const float scale = need > old ? need : old;
-  const float inv = __frcp_rn(scale);
-  if (scale != old) {
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale_at = scale;
-#pragma unroll 4
-    for (int i = row; i < off; i += kRows) rescale16(tile + i * kD + 16 * rt, old, inv);
+    for (int d = (kOne ? kRowThreads : 32) / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    const float need = pow2_scale(amax);
+    const float scale = need > old ? need : old;
+    const float inv = __frcp_rn(scale);
+    // Heads whose scale grows: the whole warp takes their codes along, one head after the
+    // other, eight loads in flight.
+    const bool grow = stores && scale != old;
+    unsigned heads = __ballot_sync(0xffffffffu, grow && rt == 0 && (kOne || lane == 0));
+    if (grow && rt == 0 && (kOne || lane == 0)) *scale_at = scale;
+    while (heads) {
+      const int from = __ffs(heads) - 1;
+      heads &= heads - 1;
+      uint8_t* const at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(tile), from));
+      const float was = __shfl_sync(0xffffffffu, old, from), now = __shfl_sync(0xffffffffu, inv, from);
+      const int n = off * (kD / 16);  // 16-byte pieces held already
+      for (int i0 = 0; i0 < n; i0 += 256) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + j * 32 + lane < n) w[j] = reinterpret_cast<const uint4*>(at)[i0 + j * 32 + lane];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i0 + j * 32 + lane < n) reinterpret_cast<uint4*>(at)[i0 + j * 32 + lane] = rescaled16(w[j], was, now);
+      }
+    }
+    if (stores && mine) store_codes(tile + (off + row) * kD, c0, c1, x, inv);
   }
-  if (mine) store_codes(tile + (off + row) * kD, c0, c1, x, inv);
 }
 
 // Any number of tokens: one block of P kD / 32 threads for a page and `heads` heads, so a
@@ -362,7 +380,10 @@ paged_append_kernel(const AppendParams p) {
     const float inv = __frcp_rn(scale);
     if (scale != old) {
       if (tid == 0) *scale_at = scale;  // every thread has read the old one
-      for (int i = slot; i < off; i += rows) rescale16(tile + i * kD + 16 * rt, old, inv);
+      for (int i = slot; i < off; i += rows) {
+        uint4* at = reinterpret_cast<uint4*>(tile + i * kD + 16 * rt);
+        *at = rescaled16(*at, old, inv);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
@@ -375,8 +396,12 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const PagedView& c = p.c;
   const int streams = p.Hq + 2 * c.Hkv;
   if (c.cu == nullptr && c.Qn <= 512 / kD) {
-    dim3 grid((unsigned)c.B * p.units_per_row, (streams + 3) / 4);
-    return paged_launch(paged_append_few_kernel<kF8, kD>, grid, 128, 0, st, p);
+    constexpr int kHeads = 512 / kD;  // of a warp, when rows have one token
+    if (c.Qn == 1)
+      return paged_launch(paged_append_few_kernel<kF8, kD, true>,
+                          dim3((unsigned)c.B, (streams + 4 * kHeads - 1) / (4 * kHeads)), 128, 0, st, p);
+    return paged_launch(paged_append_few_kernel<kF8, kD, false>,
+                        dim3((unsigned)c.B * p.units_per_row, (streams + 3) / 4), 128, 0, st, p);
   }
   const long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row
                                           : ((long long)c.N >> c.p_shift) + 2LL * c.B;

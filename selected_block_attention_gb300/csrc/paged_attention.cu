@@ -27,7 +27,8 @@ static __device__ unsigned g_err_paged = 0;
 
 namespace {
 
-constexpr int kThreads = kPagedWarps * 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kCtas = 456;    // three for each of 152 SMs
 constexpr int kMinTiles = 4;  // tiles of a run, at least: one for each warp
 constexpr int kItemCost = 12;  // tiles that an item's fixed cost is worth
@@ -83,7 +84,7 @@ paged_attention_kernel(const PagedAttnParams p) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_sum[kPagedWarps];
+  __shared__ long long s_sum[kWarps];
   __shared__ long long s_total, s_off;
   __shared__ int s_row;
   // what the CTA needs again after an item's tiles; kept here to leave registers to them
@@ -118,7 +119,7 @@ paged_attention_kernel(const PagedAttnParams p) {
     __syncthreads();
     long long total = 0;
 #pragma unroll
-    for (int i = 0; i < kPagedWarps; ++i) {
+    for (int i = 0; i < kWarps; ++i) {
       if (i == warp) pre += total;
       total += s_sum[i];
     }
@@ -150,8 +151,8 @@ paged_attention_kernel(const PagedAttnParams p) {
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * W::kWarpBytes;
   float* so = reinterpret_cast<float*>(smem);          // [warps][16][kSmemRow]
-  float* sm = so + kPagedWarps * 16 * W::kSmemRow;     // [warps][16][3]
-  float* sw = sm + kPagedWarps * 16 * 3;               // [16][warps + 2]: weights, max, sum
+  float* sm = so + kWarps * 16 * W::kSmemRow;     // [warps][16][3]
+  float* sw = sm + kWarps * 16 * 3;               // [16][warps + 2]: weights, max, sum
 
   while (true) {
     const long long end = min((cta + 1) * run_length(), s_total);
@@ -231,7 +232,7 @@ paged_attention_kernel(const PagedAttnParams p) {
     w.load_q(ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr,
              ok1 ? p.q + (rt.r.t0 + i1) * p.q_tok + (long long)h1 * kD : nullptr);
     w.walk(
-        warp, kPagedWarps, rt.r.len > 0 ? count : 0,
+        warp, kWarps, rt.r.len > 0 ? count : 0,
         [&](int t) { return (with_sink && t == 0) ? 0 : rt.base + (w_first + t) * kKeys; },
         [&](int t, int& c0, int& c1) {
           const bool s = with_sink && t == 0;
@@ -245,39 +246,26 @@ paged_attention_kernel(const PagedAttnParams p) {
     w.park(so, sm, warp);
     __syncthreads();
     const int rows = s_it.n_rows;
-    if (tid < rows) {
-      float M, L, wt[kPagedWarps];
-      paged_merge_row(sm, tid, M, L, wt);
-#pragma unroll
-      for (int i = 0; i < kPagedWarps; ++i) sw[tid * (kPagedWarps + 2) + i] = wt[i];
-      sw[tid * (kPagedWarps + 2) + kPagedWarps] = M;
-      sw[tid * (kPagedWarps + 2) + kPagedWarps + 1] = L;
-    }
+    if (tid < rows) paged_merge_row<kWarps>(sm, tid, sw + tid * (kWarps + 2));
     __syncthreads();
     const bool begins = s_it.begins, whole = s_it.whole;
-    auto out_row = [&](int r) -> long long {
-      const int rr = s_it.first + r;
-      return (long long)(s_it.t0 + rr / p.G) * p.Hq + s_it.h * p.G + rr % p.G;
-    };
-    auto write = [&](int r, int pos, float O, float M, float L) {
-      const long long row = out_row(r);
-      p.out[row * kD + W::dim_of(pos)] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
-      if (p.lse != nullptr && pos == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
-    };
     const int slot = cta * 2 + (begins ? 1 : 0);
-    for (int x = tid; x < rows * kD; x += kThreads) {
-      const int r = x / kD, pos = x % kD;
-      const float* wt = sw + r * (kPagedWarps + 2);
-      float O = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPagedWarps; ++i)
-        if (wt[i] != 0.f) O = fmaf(wt[i], so[(i * 16 + r) * W::kSmemRow + pos], O);
-      const float M = wt[kPagedWarps], L = wt[kPagedWarps + 1];
+    for (int x = tid; x < rows * (kD / 8); x += kThreads) {
+      const int r = x / (kD / 8), d0 = x % (kD / 8) * 8;
+      const float* wt = sw + r * (kWarps + 2);
+      const float M = wt[kWarps], L = wt[kWarps + 1];
+      float O[8];
+      paged_merge_dims<W, kWarps>(so, wt, r, d0, O);
       if (whole) {
-        write(r, pos, O, M, L);
+        const int rr = s_it.first + r;
+        const long long row = (long long)(s_it.t0 + rr / p.G) * p.Hq + s_it.h * p.G + rr % p.G;
+        paged_store_row(p.out + row * kD + d0, O, L == 0.f ? 0.f : 1.f / L);
+        if (p.lse != nullptr && d0 == 0) p.lse[row] = paged_lse(M, L);
       } else {
-        p.part_o[((long long)slot * 16 + r) * kD + pos] = O;
-        if (pos == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(M, L);
+        float4* to = reinterpret_cast<float4*>(p.part_o + ((long long)slot * 16 + r) * kD + d0);
+        to[0] = make_float4(O[0], O[1], O[2], O[3]);
+        to[1] = make_float4(O[4], O[5], O[6], O[7]);
+        if (d0 == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(M, L);
       }
     }
     if (begins && !whole && tid == 0) {
@@ -299,28 +287,29 @@ paged_attention_kernel(const PagedAttnParams p) {
 
 // One warp for each row of an item that a CTA begins and others continue: the partials'
 // common max, their weights, and the weighted sum, four (kD = 64: two) columns a lane.
-template <bool kF8, int kD>
+template <int kD>
 __global__ void __launch_bounds__(128)
 paged_merge_kernel(const PagedAttnParams p) {
-  using W = PagedWarp<kF8, kD, 32, true, false>;
   constexpr int kCols = kD / 32;
   const int cta = blockIdx.x, r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   paged_wait_before();
-  const SplitItem it = p.split[cta];
-  if (it.n == 0 || r >= it.n_rows) return;
   auto ml_of = [&](int i) {
     const int slot = i == 0 ? cta * 2 + 1 : (cta + i) * 2;
     return *reinterpret_cast<const float2*>(p.part_ml + (slot * 16 + r) * 2);
   };
-  float M = -INFINITY, L = 0.f;
-  for (int i = lane; i < it.n; i += 32) M = fmaxf(M, ml_of(i).x);
+  // the first 32 partials' (max, sum) are on their way before it is known how many there are
+  const float2 first = cta + lane < kCtas ? ml_of(lane) : make_float2(0.f, 0.f);
+  const SplitItem it = p.split[cta];
+  if (it.n == 0 || r >= it.n_rows) return;
+  float M = lane < it.n ? first.x : -INFINITY, L = 0.f;
+  for (int i = 32 + lane; i < it.n; i += 32) M = fmaxf(M, ml_of(i).x);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   float O[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) O[c] = 0.f;
   for (int base = 0; base < it.n; base += 32) {
-    const float2 ml = base + lane < it.n ? ml_of(base + lane) : make_float2(0.f, 0.f);
+    const float2 ml = base + lane < it.n ? (base == 0 ? first : ml_of(base + lane)) : make_float2(0.f, 0.f);
     const float f = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
     if (ml.y != 0.f) L = fmaf(f, ml.y, L);
     const int n = min(32, it.n - base);
@@ -351,23 +340,24 @@ paged_merge_kernel(const PagedAttnParams p) {
   for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   const int rr = it.first + r;
   const long long row = (long long)(it.t0 + rr / p.G) * p.Hq + it.h * p.G + rr % p.G;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t* to = reinterpret_cast<uint32_t*>(p.out + row * kD + lane * kCols);
 #pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    p.out[row * kD + W::dim_of(lane * kCols + c)] = __float2bfloat16_rn(L == 0.f ? 0.f : O[c] / L);
-  if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+  for (int c = 0; c < kCols; c += 2) to[c / 2] = pack_bf16x2(O[c] * inv, O[c + 1] * inv);
+  if (p.lse != nullptr && lane == 0) p.lse[row] = paged_lse(M, L);
 }
 
 template <bool kF8, int kD, bool kHi, bool kCap>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
-  constexpr int ring = kPagedWarps * W::kWarpBytes;
-  constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kPagedWarps + 2)) * 4;
+  constexpr int ring = kWarps * W::kWarpBytes;
+  constexpr int merge = (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
   auto* kernel = paged_attention_kernel<kF8, kD, kHi, kCap>;
   static thread_local unsigned long long devices = 0;
   cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
   if (e == cudaSuccess) e = paged_launch(kernel, dim3(kCtas), kThreads, bytes, st, p);
-  if (e == cudaSuccess) e = paged_launch(paged_merge_kernel<kF8, kD>, dim3(kCtas, kHi ? 4 : 2), 128, 0, st, p);
+  if (e == cudaSuccess) e = paged_launch(paged_merge_kernel<kD>, dim3(kCtas, kHi ? 4 : 2), 128, 0, st, p);
   return e;
 }
 

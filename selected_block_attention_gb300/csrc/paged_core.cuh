@@ -30,7 +30,6 @@ namespace sba {
 
 constexpr float kPagedLog2e = 1.4426950408889634f;
 constexpr float kPagedLn2 = 0.6931471805599453f;
-constexpr int kPagedWarps = 4;
 constexpr int kPagedStages = 2;
 
 __device__ __forceinline__ uint2 paged_lds8(uint32_t a) {
@@ -67,6 +66,7 @@ struct PagedMask {
 
 template <bool kF8, int kD, int kTileKeys, bool kHi, bool kCap>
 struct PagedWarp {
+  static constexpr bool kCodes = kF8;
   static constexpr int kKeys = kTileKeys;
   static constexpr int kSub = kKeys / 16;
   static constexpr int kRowBytes = kD * (kF8 ? 1 : 2);
@@ -497,11 +497,6 @@ struct PagedWarp {
     paged_cp_wait<0>();
   }
 
-  // Dimension of merge-buffer position `pos`.
-  static __device__ __forceinline__ int dim_of(int pos) {
-    return kF8 ? kNT * (pos & 7) + (pos >> 3) : pos;
-  }
-
   // The warp's state into the merge buffer: o rows at so[(warp * 16 + row) * kSmemRow +
   // 8 j + n], (max, sum, exponent that multiplies o) at sm[(warp * 16 + row) * 3].
   __device__ __forceinline__ void park(float* so, float* sm, int warp) {
@@ -524,19 +519,44 @@ struct PagedWarp {
   }
 };
 
-// Merge of the CTA's warps for row r: the common max, the sum, and each warp's weight.
-__device__ __forceinline__ void paged_merge_row(const float* sm, int r, float& M, float& L, float* w) {
-  M = -INFINITY;
+// Merge of the CTA's warps for row r: each warp's weight, the common max, the sum.
+template <int kWarps>
+__device__ __forceinline__ void paged_merge_row(const float* sm, int r, float* w) {
+  float M = -INFINITY, L = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPagedWarps; ++i) M = fmaxf(M, sm[(i * 16 + r) * 3]);
-  L = 0.f;
+  for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm[(i * 16 + r) * 3]);
 #pragma unroll
-  for (int i = 0; i < kPagedWarps; ++i) {
+  for (int i = 0; i < kWarps; ++i) {
     const float* s = sm + (i * 16 + r) * 3;
     const bool some = s[1] != 0.f;  // a NaN sum has to reach the output
     w[i] = some ? ptx::ex2(s[2] - M) : 0.f;
     L += some ? ptx::ex2(s[0] - M) * s[1] : 0.f;
   }
+  w[kWarps] = M;
+  w[kWarps + 1] = L;
+}
+// Dimensions d0 .. d0 + 7 of row r over the CTA's warps with weights w.
+template <class W, int kWarps>
+__device__ __forceinline__ void paged_merge_dims(const float* so, const float* w, int r, int d0, float (&o)[8]) {
+  // e4m3: dimension kNT n + j is at 8 j + n
+  const int n = d0 / W::kNT, j0 = d0 % W::kNT;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const float* s = so + (i * 16 + r) * W::kSmemRow;
+    if (w[i] == 0.f) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = fmaf(w[i], s[W::kCodes ? 8 * (j0 + e) + n : d0 + e], o[e]);
+  }
+}
+__device__ __forceinline__ void paged_store_row(__nv_bfloat16* at, const float (&o)[8], float f) {
+  *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f),
+                                             pack_bf16x2(o[4] * f, o[5] * f), pack_bf16x2(o[6] * f, o[7] * f));
+}
+// LSE of a row from its max (log2 units) and sum.
+__device__ __forceinline__ float paged_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
 }
 
 }  // namespace sba

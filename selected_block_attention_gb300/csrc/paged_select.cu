@@ -23,9 +23,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = kPagedWarps * 32;
 constexpr int kMaxBlocks = 32;
-constexpr int kResident = 456;  // three CTAs on each of 152 SMs
 constexpr int kMaxSplit = 8;  // CTAs of a cluster, at most (the portable limit)
 
 struct PagedSelectParams {
@@ -42,9 +40,10 @@ struct PagedSelectParams {
   float scale;
 };
 
-template <bool kF8, int kD, bool kHi>
-__global__ void __launch_bounds__(kThreads, 3)
+template <bool kF8, int kD, bool kHi, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 12 / kWarps)
 paged_select_kernel(const PagedSelectParams p) {
+  constexpr int kThreads = kWarps * 32;
   using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -100,35 +99,42 @@ paged_select_kernel(const PagedSelectParams p) {
   const int tiles = s_tiles;
   const int a = (int)((long long)tiles * part / split), e = (int)((long long)tiles * (part + 1) / split);
   w.walk(
-      a + warp, kPagedWarps, e, [&](int t) { return s_key[t]; },
+      a + warp, kWarps, e, [&](int t) { return s_key[t]; },
       [&](int, int& cl, int& ch) {
         cl = 0;
         ch = limit - 1;
       },
       mk);
 
-  // ---- the CTA's partial, then the cluster's result
-  float* so = reinterpret_cast<float*>(smem);       // [warps][16][kSmemRow]
-  float* sm = so + kPagedWarps * 16 * W::kSmemRow;  // [warps][16][3]
-  float* sp = sm + kPagedWarps * 16 * 3;            // [16][kD] the CTA's o
-  float* sl = sp + 16 * kD;                         // [16][2] its max and sum
+  // ---- the CTA's result, or its partial and the cluster's
+  float* so = reinterpret_cast<float*>(smem);    // [warps][16][kSmemRow]
+  float* sm = so + kWarps * 16 * W::kSmemRow;    // [warps][16][3]
+  float* sw = sm + kWarps * 16 * 3;              // [16][warps + 2]: weights, max, sum
+  float* sp = sw + 16 * (kWarps + 2);            // [16][kD] the CTA's o
   __syncthreads();
   w.park(so, sm, warp);
   __syncthreads();
-  for (int x = tid; x < p.G * kD; x += kThreads) {
-    const int row = x / kD, col = x % kD;
-    float M, L, wt[kPagedWarps];
-    paged_merge_row(sm, row, M, L, wt);
-    float O = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPagedWarps; ++i)
-      if (wt[i] != 0.f) O = fmaf(wt[i], so[(i * 16 + row) * W::kSmemRow + col], O);
-    sp[row * kD + col] = O;
-    if (col == 0) {
-      sl[row * 2] = M;
-      sl[row * 2 + 1] = L;
+  if (tid < p.G) paged_merge_row<kWarps>(sm, tid, sw + tid * (kWarps + 2));
+  __syncthreads();
+  const long long row0 = (long long)token * p.Hq + h * p.G;
+  auto factor = [&](int row, float L) {  // of o, in the output
+    return (L == 0.f ? 0.f : 1.f / L) * (p.gate != nullptr ? __bfloat162float(p.gate[row0 + row]) : 1.f);
+  };
+  for (int x = tid; x < p.G * (kD / 8); x += kThreads) {
+    const int row = x / (kD / 8), d0 = x % (kD / 8) * 8;
+    const float* wt = sw + row * (kWarps + 2);
+    float O[8];
+    paged_merge_dims<W, kWarps>(so, wt, row, d0, O);
+    if (split == 1) {
+      paged_store_row(p.out + (row0 + row) * kD + d0, O, factor(row, wt[kWarps + 1]));
+      if (p.lse != nullptr && d0 == 0) p.lse[row0 + row] = paged_lse(wt[kWarps], wt[kWarps + 1]);
+    } else {
+      float4* to = reinterpret_cast<float4*>(sp + row * kD + d0);
+      to[0] = make_float4(O[0], O[1], O[2], O[3]);
+      to[1] = make_float4(O[4], O[5], O[6], O[7]);
     }
   }
+  if (split == 1) return;
   cluster.sync();
   for (int x = part * kThreads + tid; x < p.G * (kD / 4); x += split * kThreads) {
     const int row = x / (kD / 4), col = x % (kD / 4) * 4;
@@ -137,7 +143,7 @@ paged_select_kernel(const PagedSelectParams p) {
 #pragma unroll
     for (int i = 0; i < kMaxSplit; ++i) {
       if (i >= split) break;
-      ml[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sl, i) + row * 2);
+      ml[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sw, i) + row * (kWarps + 2) + kWarps);
       v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sp, i) + row * kD + col);
     }
     float M = -INFINITY, L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
@@ -152,28 +158,30 @@ paged_select_kernel(const PagedSelectParams p) {
       O[0] = fmaf(f, v[i].x, O[0]); O[1] = fmaf(f, v[i].y, O[1]);
       O[2] = fmaf(f, v[i].z, O[2]); O[3] = fmaf(f, v[i].w, O[3]);
     }
-    const long long at = (long long)token * p.Hq + h * p.G + row;
-    float inv = L == 0.f ? 0.f : 1.f / L;
-    if (p.gate != nullptr) inv *= __bfloat162float(p.gate[at]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p.out[at * kD + W::dim_of(col + i)] = __float2bfloat16_rn(O[i] * inv);
-    if (p.lse != nullptr && col == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+    const float f = factor(row, L);
+    *reinterpret_cast<uint2*>(p.out + (row0 + row) * kD + col) =
+        make_uint2(pack_bf16x2(O[0] * f, O[1] * f), pack_bf16x2(O[2] * f, O[3] * f));
+    if (p.lse != nullptr && col == 0) p.lse[row0 + row] = paged_lse(M, L);
   }
   cluster.sync();  // no CTA leaves while others read its shared memory
 }
 
-template <bool kF8, int kD, bool kHi>
-cudaError_t launch(const PagedSelectParams& p, cudaStream_t st) {
+template <bool kF8, int kD, bool kHi, int kWarps>
+cudaError_t launch_w(const PagedSelectParams& p, cudaStream_t st) {
   using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
-  constexpr int ring = kPagedWarps * W::kWarpBytes;
-  constexpr int merge = (kPagedWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + 2)) * 4;
+  constexpr int ring = kWarps * W::kWarpBytes;
+  constexpr int merge = (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + kWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
-  auto* kernel = paged_select_kernel<kF8, kD, kHi>;
+  auto* kernel = paged_select_kernel<kF8, kD, kHi, kWarps>;
   static thread_local unsigned long long devices = 0;
   cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.c.B * p.c.Qn * p.c.Hkv;
-  return paged_launch(kernel, dim3((unsigned)(items * p.split)), kThreads, bytes, st, p, p.split);
+  return paged_launch(kernel, dim3((unsigned)(items * p.split)), kWarps * 32, bytes, st, p, p.split);
+}
+template <bool kF8, int kD, bool kHi>
+cudaError_t launch(const PagedSelectParams& p, int warps, cudaStream_t st) {
+  return warps == 4 ? launch_w<kF8, kD, kHi, 4>(p, st) : launch_w<kF8, kD, kHi, 6>(p, st);
 }
 
 }  // namespace
@@ -208,29 +216,32 @@ int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long l
   p.Hq = Hq;
   p.G = Hq / c.Hkv;
   p.scale = scale;
-  // CTAs per item: the choice with the least (waves of resident CTAs) x (a CTA's fixed time,
-  // worth about 8 tiles of a warp, + its warps' tiles).
+  // Warps a CTA (4, three CTAs on an SM, or 6, two) and CTAs an item: the choice with the
+  // least (waves of resident CTAs) x (a CTA's fixed time, worth about 2 tiles of a warp, +
+  // its warps' tiles).
   const long long items = (long long)c.B * c.Qn * c.Hkv;
   const int tiles = S * block_size / (f8 || D == 64 ? 32 : 16);
-  int split = 1;
+  int split = 1, warps = 4;
   long long best = LLONG_MAX;
-  for (int s = 1; s <= kMaxSplit; s *= 2) {
-    const long long waves = (items * s + kResident - 1) / kResident;
-    const long long cost = waves * (8 + (tiles + s * kPagedWarps - 1) / (s * kPagedWarps));
-    if (cost < best) {
-      best = cost;
-      split = s;
+  for (int w = 4; w <= 6; w += 2)
+    for (int s = 1; s <= kMaxSplit; s *= 2) {
+      const long long resident = 152 * (12 / w), waves = (items * s + resident - 1) / resident;
+      const long long cost = waves * (2 + (tiles + s * w - 1) / (s * w));
+      if (cost < best) {
+        best = cost;
+        split = s;
+        warps = w;
+      }
     }
-  }
   p.split = split;
   const bool hi = p.G > 8;
   cudaError_t e;
   if (D == 128)
-    e = f8 ? (hi ? launch<true, 128, true>(p, stream) : launch<true, 128, false>(p, stream))
-           : (hi ? launch<false, 128, true>(p, stream) : launch<false, 128, false>(p, stream));
+    e = f8 ? (hi ? launch<true, 128, true>(p, warps, stream) : launch<true, 128, false>(p, warps, stream))
+           : (hi ? launch<false, 128, true>(p, warps, stream) : launch<false, 128, false>(p, warps, stream));
   else
-    e = f8 ? (hi ? launch<true, 64, true>(p, stream) : launch<true, 64, false>(p, stream))
-           : (hi ? launch<false, 64, true>(p, stream) : launch<false, 64, false>(p, stream));
+    e = f8 ? (hi ? launch<true, 64, true>(p, warps, stream) : launch<true, 64, false>(p, warps, stream))
+           : (hi ? launch<false, 64, true>(p, warps, stream) : launch<false, 64, false>(p, warps, stream));
   if (e != cudaSuccess) return cuda_error(e, "paged selection launch");
   return SBA_OK;
 }
