@@ -527,7 +527,7 @@ typedef struct sba_paged_attention_args {
                              hq / (Hq / Hkv) */
   const float* sink_bias; /* [Hq, num_sinks] (sink_bias_per_head != 0) or [num_sinks]; NULL
                              with num_sinks == 0 for none.  num_sinks <= 16. */
-  void* out;              /* [N, Hq, D] bf16 (written) */
+  void* out;              /* [N, Hq, D] bf16 (written); must not overlap q */
   float* lse;             /* [N, Hq] (written) or NULL */
   void* workspace;        /* device scratch, 16-byte aligned, caller-owned, of at least
                              sba_paged_attention_workspace_size() bytes; needs no
@@ -557,7 +557,7 @@ typedef struct sba_nsa_select_paged_args {
   const int32_t* block_indices;  /* [B, Q, Hkv, S]: as in sba_nsa_select_fwd */
   const int32_t* block_counts;   /* [B, Q, Hkv], or NULL for block_count_scalar */
   const void* g_slc;             /* [B, Q, Hq] bf16, or NULL */
-  void* out;                     /* [B, Q, Hq, D] bf16 (written) */
+  void* out;                     /* [B, Q, Hq, D] bf16 (written); must not overlap q */
   float* lse;                    /* [B, Q, Hq] (written) or NULL */
   long long q_stride;
   int Hq;                        /* Hq / Hkv <= 16 */

@@ -634,6 +634,7 @@ int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_stream_t s
   SBA_REQUIRE(a.num_sinks >= 0 && (a.num_sinks == 0 || a.sink_bias != nullptr),
               "num_sinks > 0 needs sink_bias");
   SBA_REQUIRE(aligned16(a.q) && aligned16(a.out), "q and out must be 16-byte aligned");
+  SBA_REQUIRE(a.q != a.out, "out must not be q: other blocks still read it");
   SBA_REQUIRE(token_stride_ok(a.q_stride, a.Hq, D, c.N),
               "the token stride of q must cover its heads and be a multiple of 8 elements");
   SBA_REQUIRE(std::isfinite(a.softmax_scale) && std::isfinite(a.logits_soft_cap),
@@ -663,6 +664,7 @@ int sba_nsa_select_paged_fwd(const sba_nsa_select_paged_args* args, sba_stream_t
   SBA_REQUIRE(a.block_counts != nullptr || a.block_count_scalar >= 0,
               "block_count_scalar must be >= 0");
   SBA_REQUIRE(aligned16(a.q) && aligned16(a.out), "q and out must be 16-byte aligned");
+  SBA_REQUIRE(a.q != a.out, "out must not be q: other blocks still read it");
   SBA_REQUIRE(token_stride_ok(a.q_stride, a.Hq, D, c.N),
               "the token stride of q must cover its heads and be a multiple of 8 elements");
   SBA_REQUIRE(std::isfinite(a.softmax_scale), "softmax_scale must be finite");

@@ -278,7 +278,6 @@ paged_append_kernel(const AppendParams p) {
   constexpr int kPasses = 2;
   const PagedView& c = p.c;
   const int tid = threadIdx.x;
-  __shared__ int s_b;
   __shared__ float s_max[2][16];
   paged_wait_before();
   int b, j;
@@ -287,19 +286,20 @@ paged_append_kernel(const AppendParams p) {
     j = blockIdx.x - b * p.units_per_row;
   } else {
     // Row b owns units from floor(cu[b] / P) + 2 b on: n tokens touch at most
-    // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.
-    if (tid == 0) s_b = -1;
-    __syncthreads();
-    const int u = blockIdx.x;
-    for (int i = tid; i < c.B; i += blockDim.x) {
-      const int lo = (min(max(c.cu[i], 0), c.N) >> c.p_shift) + 2 * i;
-      const int hi = (min(max(c.cu[i + 1], 0), c.N) >> c.p_shift) + 2 * i + 2;
-      if (u >= lo && u < hi) s_b = i;
+    // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.  The row
+    // is the last one that begins at or before this unit: 32 probes a round.
+    const int unit = blockIdx.x, lane = tid & 31;
+    auto begin_of = [&](int i) { return (min(max(c.cu[i], 0), c.N) >> c.p_shift) + 2 * i; };
+    b = 0;
+    for (int range = c.B; range > 1;) {
+      const int step = (range + 31) / 32, i = b + lane * step;
+      const unsigned before = __ballot_sync(0xffffffffu, lane * step < range && begin_of(min(i, c.B - 1)) <= unit);
+      const int hit = before ? 31 - __clz(before) : 0;
+      b += hit * step;
+      range = min(step, range - hit * step);
     }
-    __syncthreads();
-    b = s_b;
-    if (b < 0) return;
-    j = u - (min(max(c.cu[b], 0), c.N) >> c.p_shift) - 2 * b;
+    j = unit - begin_of(b);
+    if (j < 0) return;  // offsets that decrease
   }
   const Unit u = unit_of(c, b, j, tid == 0 && blockIdx.y == 0);
   if (u.m <= 0) return;

@@ -484,6 +484,15 @@ def test_append_fixed(sba, f8, Q, D):
     check_append(sba, c, [Q] * len(lens), 4, D, False, 41, fixed=Q)
 
 
+@pytest.mark.parametrize("B", [33, 700, 1500])
+def test_append_many_ragged_rows(sba, B):
+    """The row of a page is searched among the offsets, 32 at a time."""
+    rng = np.random.default_rng(B)
+    n = rng.integers(0, 4, B)
+    c = Cache(rng.integers(0, 40, B) + n, 1, 64, 16, True, 735)
+    check_append(sba, c, n, 1, 0, False, 46)
+
+
 @pytest.mark.parametrize("size", [1e-3, 40.0, 1e30])
 def test_append_grows_and_keeps_scales(sba, size):
     """Tokens much larger (codes in the page move to the new scale), much smaller (it
@@ -518,6 +527,27 @@ def test_append_rotates_in_place(sba):
     got = sba.paged_kv_append(kv, kv, *c.pool(), **c.kw(), q=q, cos=cos, sin=sin, q_out=q)
     sba.check_error()
     assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
+def test_waits_of_the_many_row_kernel_run_out(sba):
+    """With a limit far below a wait's normal time the launch returns, is reported with its
+    place, and the next launch on the same context is right: nothing hangs, every wait and
+    drain is bounded."""
+    c = Cache([700, 300], 2, 128, 64, True, 780)
+    q = c.q((2, 200, 8, 128), 47)
+    want = sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
+    sba.check_error()
+    try:
+        sba.set_wait_timeout_cycles(100)
+        sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
+        with pytest.raises(sba.SBAError) as e:
+            sba.check_error()
+        assert e.value.code == -4 and "paged attention chunk role" in str(e.value)
+    finally:
+        sba.set_wait_timeout_cycles(0)
+    got = sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
+    sba.check_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 # ------------------------------------------------------------------ as they are used

@@ -36,6 +36,7 @@ ATTEND = struct("Attend", ("q", "bias", "out", "lse", "ws"), ("ws_bytes", "qs"),
                 ("Hq", "scale", "left", "right", "cap", "sinks", "per_head"))
 SELECT = struct("Select", ("q", "idx", "cnt", "gate", "out", "lse"), ("qs",),
                 ("Hq", "n", "S", "bs", "causal", "scale"))
+OUT = 0x20000
 POOL = dict(k_pages=FAKE, v_pages=FAKE, k_scales=FAKE, v_scales=FAKE, page_table=FAKE, seq_lens=FAKE, cu=None,
             page_stride=2 * 64 * 128, num_pages=4, page_size=64, Hkv=2, D=128, dt=2, table_width=8, B=3, Q=2, N=6)
 
@@ -54,13 +55,13 @@ def append(lib, **kw):
 
 
 def attend(lib, **kw):
-    d = dict(q=FAKE, qs=1024, Hq=8, scale=0.0, left=-1, right=-1, cap=0.0, bias=None, sinks=0, per_head=0, out=FAKE,
+    d = dict(q=FAKE, qs=1024, Hq=8, scale=0.0, left=-1, right=-1, cap=0.0, bias=None, sinks=0, per_head=0, out=OUT,
              lse=None, ws=FAKE, ws_bytes=lib.sba_paged_attention_workspace_size(3, 6, 8, 2, 128))
     return call(lib.sba_paged_attention_fwd, ATTEND, d, kw)
 
 
 def select(lib, **kw):
-    d = dict(q=FAKE, qs=1024, Hq=8, idx=FAKE, cnt=None, n=4, S=4, bs=64, causal=1, scale=0.0, gate=None, out=FAKE,
+    d = dict(q=FAKE, qs=1024, Hq=8, idx=FAKE, cnt=None, n=4, S=4, bs=64, causal=1, scale=0.0, gate=None, out=OUT,
              lse=None)
     return call(lib.sba_nsa_select_paged_fwd, SELECT, d, kw)
 
@@ -92,14 +93,15 @@ def test_append_arguments(lib, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(q=None), -1), (dict(out=None), -1), (dict(N=5), -1), (dict(Hq=7), -1), (dict(left=-2), -1), (dict(right=-2), -1),
     (dict(sinks=2), -1), (dict(bias=FAKE, sinks=17), -2), (dict(cap=float("inf")), -1), (dict(scale=float("nan")), -1),
-    (dict(ws=None), -1), (dict(ws_bytes=16), -1), (dict(ws=FAKE + 8), -1), (dict(qs=1004), -1), (dict(out=FAKE + 4), -1)])
+    (dict(ws=None), -1), (dict(ws_bytes=16), -1), (dict(ws=FAKE + 8), -1), (dict(qs=1004), -1), (dict(out=FAKE + 4), -1), (dict(out=FAKE), -1)])
 def test_attention_arguments(lib, change, code):
     assert attend(lib, **change) == code
 
 
 @pytest.mark.parametrize("change,code", [
     (dict(idx=None), -1), (dict(S=0), -1), (dict(S=33), -2), (dict(bs=48), -2), (dict(bs=16), -2), (dict(n=-1), -1),
-    (dict(Hq=34, qs=34 * 128), -2), (dict(Hq=9), -1), (dict(out=None), -1), (dict(q=FAKE + 8), -1), (dict(scale=float("inf")), -1)])
+    (dict(Hq=34, qs=34 * 128), -2), (dict(Hq=9), -1), (dict(out=None), -1), (dict(q=FAKE + 8), -1), (dict(scale=float("inf")), -1),
+    (dict(out=FAKE), -1), (dict(cu=FAKE), -1)])
 def test_selection_arguments(lib, change, code):
     assert select(lib, **change) == code
 
