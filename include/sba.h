@@ -515,10 +515,10 @@ SBA_API size_t sba_paged_attention_workspace_size(int B, int N, int Hq, int Hkv,
  * the device: a captured call serves whatever seq_lens holds when it is replayed.
  * Results do not depend on timing.  A key that some query of the row sees takes part with
  * weight 0 in the products of the row's other queries, so its value must be finite.
- * Internally, on `stream`: the attention kernel (with 64 or more (query, head) rows for each
- * row and KV head on average and no sinks the one with accumulators in tensor memory, whose
- * waits are bounded, see sba_set_wait_timeout_cycles) and a kernel that merges the items it
- * cut into runs.
+ * Internally, on `stream`: the attention kernel and a kernel that merges the items it cut
+ * into runs.  Without sinks, calls with many (query, head) rows for each row and KV head (17
+ * to 97 on average, by head dimension, dtype and table size) use the kernel with
+ * accumulators in tensor memory, whose waits are bounded (sba_set_wait_timeout_cycles).
  */
 typedef struct sba_paged_attention_args {
   sba_paged_cache cache; /* read only */

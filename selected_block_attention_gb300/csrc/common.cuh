@@ -93,7 +93,6 @@ int launch_paged_append(const PagedView& c, int f8, int D, const void* k, long l
                         const void* v, long long v_tok, const void* q, long long q_tok, void* q_out,
                         long long qo_tok, int Hq, const float* cosp, const float* sinp, int rot,
                         int max_pos, int interleaved, cudaStream_t stream);
-bool paged_many_rows(int B, int N, int Hq, int Hkv);
 size_t paged_chunk_workspace_bytes(int D);
 int launch_paged_chunk(const PagedView& c, int f8, int D, const void* q, long long q_tok, int Hq, float scale,
                        int window_left, int window_right, float cap, void* out, float* lse,

@@ -373,15 +373,26 @@ constexpr size_t kMlBytes = sizeof(float) * 2 * 2 * kCtas * 16;
 
 }  // namespace
 
-// Whether a call's rows have (query, head) rows enough for the kernel with tensor-memory
-// accumulators (paged_chunk.cu).
-bool paged_many_rows(int B, int N, int Hq, int Hkv) {
-  return (long long)N * (Hq / Hkv) >= 64LL * B;
+// (query, head) rows of a batch row and KV head, on average, from which a call may go to the
+// kernel with tensor-memory accumulators (paged_chunk.cu).
+static bool may_have_many_rows(int B, int N, int Hq, int Hkv) { return (long long)N * (Hq / Hkv) > 16LL * B; }
+
+// Whether it does.  This file's kernel reads the keys once for each 16 rows, the other one
+// once for 256 at a higher price a tile.  32 rows of 7000 to 8000 keys, 8 KV heads, by
+// (query, head) rows (us, here / there): e4m3 D = 128 16: 94 / 214, 32: 170 / 217,
+// 40: 247 / 217; bf16 D = 128 16: 160 / 189, 24: 288 / 189; e4m3 D = 64 48: 154 / 164,
+// 64: 199 / 164; bf16 D = 64 32: 120 / 150, 40: 226 / 150.  Two such rows: e4m3 D = 128
+// 40: 26 / 40, 96: 41 / 40: with few keys this file's finer runs win; the tables bound the
+// keys, and the lines cross near half a million.
+static bool many_rows(const PagedView& c, int f8, int D, int Hq) {
+  const long long rows = (long long)c.N * (Hq / c.Hkv), keys = (long long)c.B * c.Hkv * c.width << c.p_shift;
+  const int from = keys < (1 << 19) ? 96 : (f8 ? (D == 128 ? 32 : 48) : (D == 128 ? 16 : 32));
+  return rows > (long long)from * c.B;
 }
 
 size_t paged_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   const size_t few = kItemBytes + kMlBytes + sizeof(float) * 2 * kCtas * 16 * (size_t)D;
-  return paged_many_rows(B, N, Hq, Hkv) ? std::max(few, paged_chunk_workspace_bytes(D)) : few;
+  return may_have_many_rows(B, N, Hq, Hkv) ? std::max(few, paged_chunk_workspace_bytes(D)) : few;
 }
 
 unsigned read_and_clear_error_paged(cudaStream_t, std::string* where) {
@@ -398,7 +409,7 @@ int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, lon
                            float scale, int window_left, int window_right, float cap,
                            const float* sink_bias, int num_sinks, int sink_per_head, void* out,
                            float* lse, void* workspace, cudaStream_t stream) {
-  if (num_sinks == 0 && paged_many_rows(c.B, c.N, Hq, c.Hkv))
+  if (num_sinks == 0 && many_rows(c, f8, D, Hq))
     return launch_paged_chunk(c, f8, D, q, q_tok, Hq, scale, window_left, window_right, cap, out, lse, workspace,
                               stream);
   PagedAttnParams p;

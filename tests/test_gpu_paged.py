@@ -178,6 +178,78 @@ def test_equal_chunks(sba, D):
                     window_left=200)
 
 
+@pytest.mark.parametrize("f8,P", [(True, 16), (True, 64), (True, 128), (False, 16), (False, 64)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("left,right,cap", [(-1, 0, 0.0), (70, 0, 0.0), (-1, 2, 7.0), (0, 0, 0.0)])
+def test_many_rows(sba, f8, P, D, left, right, cap):
+    """The kernel for many rows: rows without a sequence and without tokens, rows shorter
+    than their tokens, one token among many, a group of 256 rows filled to one row."""
+    lens, n = [0, 300, 64, 515, 40, 128, 1], [3, 129, 0, 1, 65, 128, 2]
+    c = Cache(lens, 2, D, P, f8, 415 + P)
+    check_attention(sba, c, n, 6, 24, what="many rows", window_left=left, window_right=right, logits_soft_cap=cap)
+
+
+def test_many_rows_of_many_sequences(sba):
+    """More batch rows than warps look at one by one, runs that hold several items."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 150, 100)
+    n = np.minimum(rng.integers(0, 90, 100), np.maximum(lens, 1))
+    c = Cache(lens, 1, 128, 32, True, 416)
+    check_attention(sba, c, list(n), 4, 25, what="many sequences", window_right=0)
+
+
+def test_many_rows_of_one_long_sequence(sba):
+    """One item row cut into as many runs as there are."""
+    c = Cache([20000], 1, 128, 64, True, 417)
+    q = c.q((1, 40, 4, 128), 26)
+    out, lse = sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
+    few, few_lse = sba.paged_attention_fwd(q[:, -1].contiguous(), *c.pool(), **c.kw())
+    sba.check_error()
+    ref, rl, mag = oracle.paged_attention(np64(q[:, -1]), c.host(), c.table.cpu().numpy(), [20000], [0, 1])
+    close(out[:, -1], lse[:, -1], ref, rl, mag, True, "last token among 40")
+    close(few, few_lse, ref, rl, mag, True, "last token alone")
+    ref, rl, mag = oracle.paged_attention(np64(q[0, :1]), c.host(), c.table.cpu().numpy(), [20000 - 39], [0, 1])
+    close(out[:, 0], lse[:, 0], ref, rl, mag, True, "first token")
+
+
+@pytest.mark.parametrize("P", [16, 64])
+def test_many_rows_scales_far_apart(sba, P):
+    """As test_scales_far_apart, in the kernel for many rows."""
+    c = Cache([200, 333], 2, 128, P, True, 418)
+    rng = np.random.default_rng(8)
+    shape = tuple(c.ks.shape)
+    c.vs = torch.from_numpy((2.0 ** rng.integers(-60, 60, shape) * 1.37).astype(np.float32)).to(DEV)
+    check_attention(sba, c, [60, 150], 8, 27, what="value scales", window_right=0)
+    zero = torch.from_numpy(rng.random(shape[0]) < 0.5).to(DEV)
+    c.k.view(torch.uint8)[zero] = 0
+    c.v.view(torch.uint8)[zero] = 0
+    c.ks[zero] = 2.0 ** -126
+    c.vs = torch.where(zero[:, None], torch.full_like(c.vs, 2.0 ** -126), torch.full_like(c.vs, 0.02))
+    check_attention(sba, c, [60, 150], 8, 27, what="zero pages", window_right=0)
+
+
+def test_many_rows_give_pages_back_and_leave_rows_alone(sba):
+    lens, left, n = [900, 400], 60, 100
+    c = Cache(lens, 1, 128, 16, True, 419)
+    for b, L in enumerate(lens):
+        c.table[b, :max(0, L - n - left) // 16] = -1
+    q = c.q((2 * n + 5, 4, 128), 28)
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device=DEV)
+    out, lse = torch.full_like(q, 3.0), torch.full((2 * n + 5, 4), 5.0, device=DEV)
+    sba.paged_attention_fwd(q, *c.pool(), **c.kw(), cu_seqlens=cu, window_left=left, window_right=0, out=out, lse=lse)
+    sba.check_error()
+    ref, rl, mag = oracle.paged_attention(np64(q)[:2 * n], c.host(), c.table.clamp(min=0).cpu().numpy(), lens,
+                                          [0, n, 2 * n], window_left=left, window_right=0)
+    close(out[:2 * n], lse[:2 * n], ref, rl, mag, True, "window pages")
+    assert (out[2 * n:] == 3).all() and (lse[2 * n:] == 5).all()
+    bad = c.table.clone()
+    bad[0, -1] = c.k.shape[0]
+    sba.paged_attention_fwd(q, c.k, c.v, bad, c.lens, **c.kw(), cu_seqlens=cu, window_left=left, window_right=0)
+    with pytest.raises(sba.SBAError) as e:
+        sba.check_error()
+    assert e.value.code == -5 and "out of range" in str(e.value)
+
+
 def test_caps_at_both_ends(sba):
     """A huge cap is none; a tiny one leaves the mean of the values (fp32 throughout)."""
     c = Cache([900, 77], 2, 128, 64, True, 420)
@@ -316,6 +388,11 @@ def test_results_repeat(sba):
     a, la = sba.paged_attention_fwd(q, *c.pool(), **c.kw())
     for _ in range(20):
         b, lb = sba.paged_attention_fwd(q, *c.pool(), **c.kw())
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    q = c.q((4, 50, 16, 128), 21)
+    a, la = sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
+    for _ in range(20):
+        b, lb = sba.paged_attention_fwd(q, *c.pool(), **c.kw(), window_right=0)
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
