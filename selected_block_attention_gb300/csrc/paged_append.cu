@@ -43,7 +43,7 @@ struct AppendParams {
   long long k_tok, v_tok, q_tok, qo_tok;
   int Hq, rot, interleaved, max_pos;
   int units_per_row;  // pages a row's tokens can touch (cu == null)
-  int heads;          // heads a block works through
+  int heads, groups;  // heads a block works through, blocks of a unit
 };
 
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
@@ -280,15 +280,17 @@ paged_append_kernel(const AppendParams p) {
   const int tid = threadIdx.x;
   __shared__ float s_max[2][16];
   paged_wait_before();
+  // a unit's blocks follow one another: their heads' rows are neighbours in memory
+  const int unit = blockIdx.x / p.groups, group = blockIdx.x - unit * p.groups;
   int b, j;
   if (c.cu == nullptr) {
-    b = blockIdx.x / p.units_per_row;
-    j = blockIdx.x - b * p.units_per_row;
+    b = unit / p.units_per_row;
+    j = unit - b * p.units_per_row;
   } else {
     // Row b owns units from floor(cu[b] / P) + 2 b on: n tokens touch at most
     // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.  The row
     // is the last one that begins at or before this unit: 32 probes a round.
-    const int unit = blockIdx.x, lane = tid & 31;
+    const int lane = tid & 31;
     auto begin_of = [&](int i) { return (min(max(c.cu[i], 0), c.N) >> c.p_shift) + 2 * i; };
     b = 0;
     for (int range = c.B; range > 1;) {
@@ -301,13 +303,13 @@ paged_append_kernel(const AppendParams p) {
     j = unit - begin_of(b);
     if (j < 0) return;  // offsets that decrease
   }
-  const Unit u = unit_of(c, b, j, tid == 0 && blockIdx.y == 0);
+  const Unit u = unit_of(c, b, j, tid == 0 && group == 0);
   if (u.m <= 0) return;
   const int rows = blockDim.x / kRowThreads;
   const int rt = tid % kRowThreads, slot = tid / kRowThreads;
   const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
-  const int s_end = min((int)(blockIdx.y + 1) * p.heads, p.Hq + 2 * c.Hkv);
-  int s = blockIdx.y * p.heads;
+  const int s_end = min((group + 1) * p.heads, p.Hq + 2 * c.Hkv);
+  int s = group * p.heads;
   const int page = s_end > p.Hq ? page_of(c, u, tid == 0) : 0;
   if (page < 0) return;
 
@@ -407,7 +409,8 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
                                           : ((long long)c.N >> c.p_shift) + 2LL * c.B;
   // up to 8 heads a block, as long as there are blocks enough to fill the GPU
   p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
-  dim3 grid((unsigned)units, (streams + p.heads - 1) / p.heads);
+  p.groups = (streams + p.heads - 1) / p.heads;
+  const dim3 grid((unsigned)(units * p.groups));
   return paged_launch(paged_append_kernel<kF8, kD>, grid, (kD << c.p_shift) / 32, 0, st, p);
 }
 

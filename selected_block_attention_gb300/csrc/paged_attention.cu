@@ -229,8 +229,8 @@ paged_attention_kernel(const PagedAttnParams p) {
     }
     W w;
     w.init(p.c, b, h, ring, p.scale, p.cap, &g_err_paged);
-    w.load_q(ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr,
-             ok1 ? p.q + (rt.r.t0 + i1) * p.q_tok + (long long)h1 * kD : nullptr);
+    const __nv_bfloat16* q0 = ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr;
+    const __nv_bfloat16* q1 = ok1 ? p.q + (rt.r.t0 + i1) * p.q_tok + (long long)h1 * kD : nullptr;
     w.walk(
         warp, kWarps, rt.r.len > 0 ? count : 0,
         [&](int t) { return (with_sink && t == 0) ? 0 : rt.base + (w_first + t) * kKeys; },
@@ -239,7 +239,7 @@ paged_attention_kernel(const PagedAttnParams p) {
           c0 = s ? 0 : cl;
           c1 = s ? min(p.num_sinks, rt.r.len) - 1 : rt.r.len - 1;
         },
-        mk);
+        [&] { w.load_q(q0, q1); }, mk);
 
     // ---- the CTA's warps become one partial
     __syncthreads();  // the rings become the merge buffer

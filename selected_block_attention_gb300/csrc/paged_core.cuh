@@ -452,9 +452,10 @@ struct PagedWarp {
   }
 
   // Tiles first, first + step, ... below count; key_of(t) is tile t's first key and
-  // lim_of(t, cl, ch) the keys that may be read for it.
-  template <class KeyOf, class LimOf>
-  __device__ __forceinline__ void walk(int first, int step, int count, KeyOf key_of, LimOf lim_of,
+  // lim_of(t, cl, ch) the keys that may be read for it.  queries() brings the query rows in
+  // while the first tile is on its way.
+  template <class KeyOf, class LimOf, class Queries>
+  __device__ __forceinline__ void walk(int first, int step, int count, KeyOf key_of, LimOf lim_of, Queries queries,
                                        const PagedMask& mk) {
     if (first >= count) return;
     int cl, ch;
@@ -471,6 +472,7 @@ struct PagedWarp {
       lim_of(first + step, ncl, nch);
       pg = fetch(nkey, ncl, nch);
     }
+    queries();
     int stage = 0;
     for (int t = first; t < count; t += step) {
       Scales sn = sl;

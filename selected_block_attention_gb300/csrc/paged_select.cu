@@ -104,7 +104,7 @@ paged_select_kernel(const PagedSelectParams p) {
         cl = 0;
         ch = limit - 1;
       },
-      mk);
+      [] {}, mk);  // the queries came while the blocks were looked through
 
   // ---- the CTA's result, or its partial and the cluster's
   float* so = reinterpret_cast<float*>(smem);    // [warps][16][kSmemRow]
