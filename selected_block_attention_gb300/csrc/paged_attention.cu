@@ -1,5 +1,5 @@
 // Attention of one or several query tokens per row over a paged cache:
-// paged_attention_kernel.
+// paged_attention_kernel, paged_merge_kernel and, for few keys, paged_small_kernel.
 //
 // Row b's n_b query tokens are the last of its len_b tokens: query i sits at position
 // p_i = len_b - n_b + i and sees key k < len_b iff p_i - window_left <= k <= p_i +
@@ -32,6 +32,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kCtas = 456;    // three for each of 152 SMs
 constexpr int kMinTiles = 4;  // tiles of a run, at least: one for each warp
 constexpr int kItemCost = 12;  // tiles that an item's fixed cost is worth
+// Tiles of a warp, at most, in paged_small_kernel.  Line and cluster, us, e4m3 D = 128, 8 KV
+// heads, equal lengths: one row of 2000 keys 10.7 / 7.0, of 8000 17.9 / 13.3, of 16000
+// 20.2 / 21.9; 16 rows of 2000 20.1 / 16.7, of 8000 50.5 / 51.8; 48 rows of 300 16.7 / 9.4.
+// Past 8 tiles a warp the two come level, and the cluster's fixed shares lose to the line
+// once the rows' lengths differ.
+constexpr int kSmallTiles = 8;
 
 struct PagedAttnParams {
   PagedView c;
@@ -46,6 +52,7 @@ struct PagedAttnParams {
   int Hq, G;
   float scale, cap;
   int window_left, window_right, num_sinks, sink_per_head;
+  int cluster, groups;  // few keys: CTAs of an item and items of a KV head (else cluster = 0)
 };
 
 // The item that a CTA begins but does not end: its partials are slot 2 cta + 1 and the
@@ -78,7 +85,77 @@ __device__ __forceinline__ RowTiles row_tiles(const PagedAttnParams& p, int b, b
   return t;
 }
 
-template <bool kF8, int kD, bool kHi, bool kCap>
+// The 16 rows of an item, what they see, and the item's tiles of [s0, s1) that they need.
+template <int kD>
+struct Group {
+  PagedMask mk;
+  const __nv_bfloat16* q0;  // the thread's rows g and g + 8, or null
+  const __nv_bfloat16* q1;
+  int n_rows;
+  int count, key_first;  // tile t < count is the keys from key_first + t kKeys on ...
+  bool with_sink;        // ... but for tile 0, which is the sinks'
+  int cl, ch;            // keys that may be read; of the sinks' tile, 0 .. sink_ch
+  int sink_ch;
+  template <int kKeys>
+  __device__ __forceinline__ int key_of(int t) const {
+    return with_sink && t == 0 ? 0 : key_first + t * kKeys;
+  }
+  __device__ __forceinline__ void limits(int t, int& lo, int& hi) const {
+    const bool s = with_sink && t == 0;
+    lo = s ? 0 : cl;
+    hi = s ? sink_ch : ch;
+  }
+};
+template <int kKeys, bool kHi, int kD>
+__device__ __forceinline__ Group<kD> group_of(const PagedAttnParams& p, const RowTiles& rt, int h, int group, int s0,
+                                              int s1) {
+  Group<kD> gr;
+  const int lane = threadIdx.x & 31, rows = rt.r.n * p.G;
+  const int first_pos = rt.r.len - rt.r.n;  // position of query 0
+  gr.n_rows = min(16, rows - group * 16);
+  PagedMask& mk = gr.mk;
+  mk.len = rt.r.len;
+  mk.num_sinks = p.num_sinks;
+  const int ra = group * 16 + (lane >> 2), rb = ra + 8;
+  const bool ok0 = ra < rows, ok1 = kHi && rb < rows;
+  const int i0 = ok0 ? ra / p.G : 0, i1 = ok1 ? rb / p.G : 0;
+  const int h0 = h * p.G + (ok0 ? ra - i0 * p.G : 0), h1 = h * p.G + (ok1 ? rb - i1 * p.G : 0);
+  auto win_lo = [&](int i) {
+    return p.window_left < 0 ? 0 : (int)max((long long)first_pos + i - p.window_left, 0LL);
+  };
+  auto win_hi = [&](int i) {
+    return p.window_right < 0 ? INT_MAX : (int)min((long long)first_pos + i + p.window_right, (long long)INT_MAX);
+  };
+  mk.wlo0 = win_lo(i0);
+  mk.whi0 = ok0 ? win_hi(i0) : -1;
+  mk.wlo1 = win_lo(i1);
+  mk.whi1 = ok1 ? win_hi(i1) : -1;
+  const int ia = group * 16 / p.G, ib = (group * 16 + gr.n_rows - 1) / p.G;  // queries of the group
+  mk.all_lo = win_lo(ib);
+  mk.all_hi = win_hi(ia);
+  mk.bias0 = p.sink_bias + (p.sink_per_head ? (long long)h0 * p.num_sinks : 0);
+  mk.bias_step = p.sink_per_head ? (h1 - h0) * p.num_sinks : 0;
+  // tiles this group needs: [ka, kb) of the window's
+  const bool sinks_at_base = p.num_sinks > 0 && !rt.sink;
+  const int lo = sinks_at_base ? 0 : min(win_lo(ia), rt.r.len);
+  int hi = (int)min((long long)max(win_hi(ib), -1) + 1, (long long)rt.r.len);
+  if (sinks_at_base) hi = max(hi, min(p.num_sinks, rt.r.len));
+  const int ka = (lo - rt.base) / kKeys;
+  const int kb = hi > lo ? (hi - rt.base + kKeys - 1) / kKeys : ka;
+  // of the segment [s0, s1): the sinks' tile, then the window's
+  gr.with_sink = rt.sink && s0 == 0;
+  const int wa = max(max(s0 - rt.sink, ka), 0), wb = min(s1 - rt.sink, kb);
+  gr.count = rt.r.len > 0 ? (gr.with_sink ? 1 : 0) + max(wb - wa, 0) : 0;
+  gr.key_first = rt.base + (wa - (gr.with_sink ? 1 : 0)) * kKeys;
+  gr.cl = sinks_at_base ? 0 : rt.lo;
+  gr.ch = rt.r.len - 1;
+  gr.sink_ch = min(p.num_sinks, rt.r.len) - 1;
+  gr.q0 = ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr;
+  gr.q1 = ok1 ? p.q + (rt.r.t0 + i1) * p.q_tok + (long long)h1 * kD : nullptr;
+  return gr;
+}
+
+template <bool kF8, int kD, bool kHi, int kCap>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_attention_kernel(const PagedAttnParams p) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
@@ -175,44 +252,7 @@ paged_attention_kernel(const PagedAttnParams p) {
     if (x1 <= kItemCost) continue;  // nothing but the empty tiles
     const int s0 = max(x0 - kItemCost, 0), s1 = x1 - kItemCost;
     const int h = item / rt.groups, group = item - h * rt.groups;
-    const int n_rows = min(16, rt.r.n * p.G - group * 16);
-    const int first_pos = rt.r.len - rt.r.n;  // position of query 0
-
-    PagedMask mk;
-    mk.len = rt.r.len;
-    mk.num_sinks = p.num_sinks;
-    const int ra = group * 16 + (lane >> 2), rb = ra + 8;
-    const bool ok0 = ra < rt.r.n * p.G, ok1 = kHi && rb < rt.r.n * p.G;
-    const int i0 = ok0 ? ra / p.G : 0, i1 = ok1 ? rb / p.G : 0;
-    const int h0 = h * p.G + (ok0 ? ra - i0 * p.G : 0), h1 = h * p.G + (ok1 ? rb - i1 * p.G : 0);
-    auto win_lo = [&](int i) {
-      return p.window_left < 0 ? 0 : (int)max((long long)first_pos + i - p.window_left, 0LL);
-    };
-    auto win_hi = [&](int i) {
-      return p.window_right < 0 ? INT_MAX : (int)min((long long)first_pos + i + p.window_right, (long long)INT_MAX);
-    };
-    mk.wlo0 = win_lo(i0);
-    mk.whi0 = ok0 ? win_hi(i0) : -1;
-    mk.wlo1 = win_lo(i1);
-    mk.whi1 = ok1 ? win_hi(i1) : -1;
-    const int ia = group * 16 / p.G, ib = (group * 16 + n_rows - 1) / p.G;  // queries of the group
-    mk.all_lo = win_lo(ib);
-    mk.all_hi = win_hi(ia);
-    mk.bias0 = p.sink_bias + (p.sink_per_head ? (long long)h0 * p.num_sinks : 0);
-    mk.bias1 = p.sink_bias + (p.sink_per_head ? (long long)h1 * p.num_sinks : 0);
-    // tiles this group needs: [ka, kb) of the window's
-    const bool sinks_at_base = p.num_sinks > 0 && !rt.sink;
-    const int lo = sinks_at_base ? 0 : min(win_lo(ia), rt.r.len);
-    int hi = (int)min((long long)max(win_hi(ib), -1) + 1, (long long)rt.r.len);
-    if (sinks_at_base) hi = max(hi, min(p.num_sinks, rt.r.len));
-    const int ka = (lo - rt.base) / kKeys;
-    const int kb = hi > lo ? (hi - rt.base + kKeys - 1) / kKeys : ka;
-    const int cl = sinks_at_base ? 0 : rt.lo;
-    // tiles of the segment [s0, s1): the sinks' tile, then the window's
-    const bool with_sink = rt.sink && s0 == 0;
-    const int wa = max(s0 - rt.sink, ka), wb = min(s1 - rt.sink, kb);
-    const int count = (with_sink ? 1 : 0) + max(wb - max(wa, 0), 0);
-    const int w_first = max(wa, 0) - (with_sink ? 1 : 0);  // window tile of index t: w_first + t
+    const Group<kD> gr = group_of<kKeys, kHi, kD>(p, rt, h, group, s0, s1);
 
     if (tid == 0) {
       s_it.cur = cur;
@@ -222,24 +262,16 @@ paged_attention_kernel(const PagedAttnParams p) {
       s_it.units = units;
       s_it.h = h;
       s_it.first = group * 16;
-      s_it.n_rows = n_rows;
+      s_it.n_rows = gr.n_rows;
       s_it.t0 = rt.r.t0;
       s_it.begins = s0 == 0;
       s_it.whole = s0 == 0 && s1 == rt.tiles;
     }
     W w;
     w.init(p.c, b, h, ring, p.scale, p.cap, &g_err_paged);
-    const __nv_bfloat16* q0 = ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr;
-    const __nv_bfloat16* q1 = ok1 ? p.q + (rt.r.t0 + i1) * p.q_tok + (long long)h1 * kD : nullptr;
     w.walk(
-        warp, kWarps, rt.r.len > 0 ? count : 0,
-        [&](int t) { return (with_sink && t == 0) ? 0 : rt.base + (w_first + t) * kKeys; },
-        [&](int t, int& c0, int& c1) {
-          const bool s = with_sink && t == 0;
-          c0 = s ? 0 : cl;
-          c1 = s ? min(p.num_sinks, rt.r.len) - 1 : rt.r.len - 1;
-        },
-        [&] { w.load_q(q0, q1); }, mk);
+        warp, kWarps, gr.count, [&](int t) { return gr.template key_of<kKeys>(t); },
+        [&](int t, int& lo, int& hi) { gr.limits(t, lo, hi); }, [&] { w.load_q(gr.q0, gr.q1); }, gr.mk);
 
     // ---- the CTA's warps become one partial
     __syncthreads();  // the rings become the merge buffer
@@ -347,13 +379,53 @@ paged_merge_kernel(const PagedAttnParams p) {
   if (p.lse != nullptr && lane == 0) p.lse[row] = paged_lse(M, L);
 }
 
-template <bool kF8, int kD, bool kHi, bool kCap>
+// Few keys: an item's tiles are shared evenly by the `split` CTAs of one cluster, which merge
+// through distributed shared memory, so there is neither a line to find a place on nor a
+// second launch.
+template <bool kF8, int kD, bool kHi, int kCap>
+__global__ void __launch_bounds__(kThreads, 3)
+paged_small_kernel(const PagedAttnParams p) {
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
+  constexpr int kKeys = W::kKeys;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int split = p.cluster, part = blockIdx.x % split, warp = threadIdx.x >> 5;
+  const int item = blockIdx.x / split, groups = p.groups;
+  const int group = item % groups, h = item / groups % p.c.Hkv, b = item / groups / p.c.Hkv;
+  paged_wait_before();
+  bool bad;
+  const RowTiles rt = row_tiles<kKeys>(p, b, &bad);
+  if (bad && threadIdx.x == 0) atomicOr(&g_err_paged, (unsigned)kDevErrInput);
+  const Group<kD> gr = group_of<kKeys, kHi, kD>(p, rt, h, group, 0, rt.tiles);
+  W w;
+  w.init(p.c, b, h, ptx::smem_u32(smem) + warp * W::kWarpBytes, p.scale, p.cap, &g_err_paged);
+  const int a = (int)((long long)gr.count * part / split), e = (int)((long long)gr.count * (part + 1) / split);
+  w.walk(
+      a + warp, kWarps, e, [&](int t) { return gr.template key_of<kKeys>(t); },
+      [&](int t, int& lo, int& hi) { gr.limits(t, lo, hi); }, [&] { w.load_q(gr.q0, gr.q1); }, gr.mk);
+  const int first = group * 16;
+  paged_cluster_finish<W, kWarps, kD>(
+      w, smem, split, part, gr.n_rows,
+      [&](int r) -> long long {
+        return (long long)(rt.r.t0 + (first + r) / p.G) * p.Hq + h * p.G + (first + r) % p.G;
+      },
+      [](int, float L) { return L == 0.f ? 0.f : 1.f / L; }, p.out, p.lse);
+}
+
+template <bool kF8, int kD, bool kHi, int kCap>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
   constexpr int ring = kWarps * W::kWarpBytes;
   constexpr int merge = (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
   auto* kernel = paged_attention_kernel<kF8, kD, kHi, kCap>;
+  if (p.cluster > 0) {
+    constexpr int finish = paged_finish_bytes<W, kWarps, kD>(), need = ring > finish ? ring : finish;
+    static thread_local unsigned long long devices = 0;
+    auto* small = paged_small_kernel<kF8, kD, kHi, kCap>;
+    const cudaError_t e = paged_allow_smem(small, need, &devices);
+    if (e != cudaSuccess) return e;
+    return paged_launch(small, dim3((unsigned)(p.c.B * p.c.Hkv * p.groups * p.cluster)), kThreads, need, st, p, p.cluster);
+  }
   static thread_local unsigned long long devices = 0;
   cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
   if (e == cudaSuccess) e = paged_launch(kernel, dim3(kCtas), kThreads, bytes, st, p);
@@ -363,9 +435,9 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
 
 template <bool kF8, int kD>
 cudaError_t launch_d(const PagedAttnParams& p, bool hi, cudaStream_t st) {
-  const bool cap = p.cap > 0.f;
-  if (hi) return cap ? launch<kF8, kD, true, true>(p, st) : launch<kF8, kD, true, false>(p, st);
-  return cap ? launch<kF8, kD, false, true>(p, st) : launch<kF8, kD, false, false>(p, st);
+  const int cap = p.cap <= 0.f ? 0 : p.cap <= kPagedSmallCap ? 1 : 2;
+  if (hi) return cap == 0 ? launch<kF8, kD, true, 0>(p, st) : cap == 1 ? launch<kF8, kD, true, 1>(p, st) : launch<kF8, kD, true, 2>(p, st);
+  return cap == 0 ? launch<kF8, kD, false, 0>(p, st) : cap == 1 ? launch<kF8, kD, false, 1>(p, st) : launch<kF8, kD, false, 2>(p, st);
 }
 
 constexpr size_t kItemBytes = sizeof(SplitItem) * kCtas;
@@ -431,6 +503,22 @@ int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, lon
   p.window_right = window_right;
   p.num_sinks = num_sinks;
   p.sink_per_head = sink_per_head;
+  p.cluster = 0;
+  p.groups = 0;
+  if (c.cu == nullptr) {
+    // Every row has Qn tokens, so the items are known here; the tables bound their keys.
+    const int tile = 4096 / (D * (f8 ? 1 : 2));
+    long long keys = (long long)c.width << c.p_shift;
+    if (window_left >= 0) keys = std::min(keys, (long long)window_left + c.Qn + 2 * tile + (num_sinks > 0 ? tile : 0));
+    const long long tiles = (keys + tile - 1) / tile, groups = ((long long)c.Qn * p.G + 15) / 16;
+    const long long items = (long long)c.B * c.Hkv * groups;
+    int split = 1;
+    while (split < kPagedMaxSplit && items * split * 2 <= kCtas && tiles > split * kWarps) split *= 2;
+    if (items * split <= kCtas && tiles <= kSmallTiles * kWarps * split) {
+      p.cluster = split;
+      p.groups = (int)groups;
+    }
+  }
   // A group of 16 (query, head) rows uses rows 8..15 unless a row has at most 8 of them.
   const bool hi = c.cu != nullptr || (long long)c.Qn * p.G > 8;
   cudaError_t e;

@@ -23,7 +23,10 @@
 //
 // The MMAs bound it: per tile and half an S of N = 64 costs 8 x 50 cycles and a PV of
 // N = 128 4 x 64; the conversion of a tile (2 x 8 loads, 128 conversions and 32 stores a
-// thread) and the softmax of 256 rows run beside them.
+// thread) and the softmax of 256 rows run beside them.  Four stages of keys and of values
+// keep the loaders ahead of an item's change (three of keys: 273 us where four take 264).
+// Tiles of 128 keys would halve the S instructions' fixed part, but leave one S buffer a
+// half and the softmax on the path of the MMAs: 333 us.
 #include <climits>
 #include <cstdio>
 #include <string>
@@ -173,7 +176,7 @@ struct Cfg {
   static constexpr int kQBytes = kPanels * kQPanel;
   static constexpr int kTPanel = kKT * 128;
   static constexpr int kTBytes = kPanels * kTPanel;
-  static constexpr int kStagesK = 3;
+  static constexpr int kStagesK = 4;
   static constexpr int kStages = 4;
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kStagesK * kTBytes;
@@ -198,20 +201,6 @@ __device__ __forceinline__ void mask_columns(float (&x)[kKT], int jlo, int jhi) 
   for (int j = 0; j < 32; ++j) x[j] = (w0 & (1u << j)) ? x[j] : -INFINITY;
 #pragma unroll
   for (int j = 0; j < 32; ++j) x[32 + j] = (w1 & (1u << j)) ? x[32 + j] : -INFINITY;
-}
-
-// Log2 logits under the cap: see PagedWarp::logit.
-__device__ __forceinline__ float capped(float y, float c1k) {
-  const float e = ex2(y * (2.f * kPagedLog2e));
-  float rc;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
-  const float far = fmaf(-2.f, rc, 1.f);
-  const float y2 = y * y;
-  float pl = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
-  pl = fmaf(y2, pl, 2.f / 15.f);
-  pl = fmaf(y2, pl, -1.f / 3.f);
-  const float near = fmaf(y * y2, pl, y);
-  return c1k * (fabsf(y) < 0.25f ? near : far);
 }
 
 // kSub: groups of a tile's keys with one scale each: 1 for pages of 64 and more (and bf16),
@@ -361,10 +350,9 @@ paged_chunk_kernel(const ChunkParams p) {
     return *reinterpret_cast<Segment*>(smem + C::kOffSegs + slot * (int)sizeof(Segment));
   };
 
-  // registers of the four warpgroups: 120 + 72 + 160 + 160 = 4 x 128
+  // registers of the four warpgroups: 128 + 64 + 160 + 160 = 4 x 128
   if (warp < 4) {
     // ------------------------------------------------------------------ loaders
-    setmaxnreg_dec<120>();
     constexpr int kItem = kF8 ? 1 : 2;
     constexpr int kCpr = D * kItem / 16;  // 16-byte chunks of a row
     constexpr int kStep = 32 / kCpr;      // rows of a warp-wide access
@@ -559,7 +547,7 @@ paged_chunk_kernel(const ChunkParams p) {
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ MMA issuer of half w
-    setmaxnreg_dec<72>();
+    setmaxnreg_dec<64>();
     if (warp < 6) {
       const int w = warp - 4;
       const uint32_t leader = elect_one();
@@ -758,7 +746,7 @@ paged_chunk_kernel(const ChunkParams p) {
           if constexpr (kCap) {
             const float c1k = p.cap * kPagedLog2e;
 #pragma unroll
-            for (int j = 0; j < kKT; ++j) x[j] = capped(x[j] * mult[j / kCols], c1k);
+            for (int j = 0; j < kKT; ++j) x[j] = paged_capped(x[j] * mult[j / kCols], c1k);
           }
           if (key0 < full_lo || key0 + kKT > full_end)
             mask_columns(x, min(max(klo - key0, 0), kKT), max(min(khi - key0, kKT - 1), -1));

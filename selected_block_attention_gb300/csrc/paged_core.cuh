@@ -22,6 +22,8 @@
 // spreads both reads over all banks (f below).
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include <climits>
 
 #include "paged.cuh"
@@ -60,11 +62,31 @@ struct PagedMask {
   int wlo1, whi1;  // window of row g + 8
   int all_lo, all_hi;  // the part of the window that every row shares
   int num_sinks;       // keys < num_sinks are always visible
-  const float* bias0;  // their biases, rows g and g + 8
-  const float* bias1;
+  const float* bias0;  // their biases for row g
+  int bias_step;       // distance to those for row g + 8
 };
 
-template <bool kF8, int kD, int kTileKeys, bool kHi, bool kCap>
+// log2(e) cap tanh(y) with an error relative to the value: near zero the odd series (its
+// next term is below 2^-28 of the sum at |y| = 0.25), elsewhere 1 - 2 / (1 + e^(2y)).
+__device__ __forceinline__ float paged_capped(float y, float c1k) {
+  const float e = ptx::ex2(y * (2.f * kPagedLog2e));
+  float rc;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
+  const float far = fmaf(-2.f, rc, 1.f);
+  const float y2 = y * y;
+  float pl = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
+  pl = fmaf(y2, pl, 2.f / 15.f);
+  pl = fmaf(y2, pl, -1.f / 3.f);
+  const float near = fmaf(y * y2, pl, y);
+  return c1k * (fabsf(y) < 0.25f ? near : far);
+}
+
+// kCap: 0 no soft cap, 1 a cap of at most kPagedSmallCap, 2 any cap.  An error of a few
+// 2^-24 of a small cap is one of at most 2^-14 in a logit, a hundredth of what rounding P
+// to 16 bits costs, so 1 leaves the series near zero out (a windowed call of 64 rows that
+// is bound by it: 97.4 us with the series, 93.7 without).
+constexpr float kPagedSmallCap = 256.f;
+template <bool kF8, int kD, int kTileKeys, bool kHi, int kCap>
 struct PagedWarp {
   static constexpr bool kCodes = kF8;
   static constexpr int kKeys = kTileKeys;
@@ -86,7 +108,7 @@ struct PagedWarp {
   float m0, m1, l0, l1;
   float u0, u1;    // e4m3: reference of the values' probabilities
   float r0, r1;    // logit factors of rows g, g + 8
-  float c1k, cap2; // cap: log2(e) cap, and 1 / cap
+  float c1k;       // log2(e) cap
   int lane, g, c;
   uint32_t ring;
   const uint8_t* kbase;
@@ -130,9 +152,8 @@ struct PagedWarp {
     for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m0 = m1 = u0 = u1 = -INFINITY;
     l0 = l1 = 0.f;
-    r0 = r1 = kCap ? scale : scale * kPagedLog2e;
+    r0 = r1 = kCap == 0 ? scale * kPagedLog2e : kCap == 1 ? scale * (2.f * kPagedLog2e / cap) : scale / cap;
     c1k = cap * kPagedLog2e;
-    cap2 = kCap ? 1.f / cap : 0.f;
   }
 
   // Query rows g and g + 8 (null: a row of zeros).
@@ -236,22 +257,16 @@ struct PagedWarp {
   }
 
   __device__ __forceinline__ float logit(float x, float f) const {
-    if constexpr (!kCap) {
+    // log2(e) cap tanh(y), y = x scale / cap
+    if constexpr (kCap == 0) {
       return x * f;
-    } else {
-      // log2(e) cap tanh(y), y = x f / cap.  Near zero the odd series (its next term is
-      // below 2^-28 of the sum at |y| = 0.25), elsewhere 1 - 2 / (1 + e^(2y)).
-      const float y = x * f * cap2;
-      const float e = ptx::ex2(y * (2.f * kPagedLog2e));
+    } else if constexpr (kCap == 1) {
+      // 1 - 2 / (1 + e^(2y)): off by a few 2^-24 of the cap
       float rc;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + e));
-      const float far = fmaf(-2.f, rc, 1.f);
-      const float y2 = y * y;
-      float pl = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
-      pl = fmaf(y2, pl, 2.f / 15.f);
-      pl = fmaf(y2, pl, -1.f / 3.f);
-      const float near = fmaf(y * y2, pl, y);
-      return c1k * (fabsf(y) < 0.25f ? near : far);
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ptx::ex2(x * f)));
+      return fmaf(-2.f * c1k, rc, c1k);
+    } else {
+      return paged_capped(x * f, c1k);
     }
   }
 
@@ -316,7 +331,7 @@ struct PagedWarp {
             const bool sink = key < mk.num_sinks;
             if (sink) {
               x0 = fmaf(mk.bias0[key], kPagedLog2e, x0);
-              if constexpr (kHi) x1 = fmaf(mk.bias1[key], kPagedLog2e, x1);
+              if constexpr (kHi) x1 = fmaf(mk.bias0[mk.bias_step + key], kPagedLog2e, x1);
             }
             const bool here = key < mk.len;
             x0 = here && ((key >= mk.wlo0 && key <= mk.whi0) || sink) ? x0 : -INFINITY;
@@ -559,6 +574,76 @@ __device__ __forceinline__ void paged_store_row(__nv_bfloat16* at, const float (
 // LSE of a row from its max (log2 units) and sum.
 __device__ __forceinline__ float paged_lse(float M, float L) {
   return L == 0.f ? -INFINITY : (M + log2f(L)) * kPagedLn2;
+}
+
+// Result of an item whose tiles the `split` CTAs of a cluster shared: the CTA's warps merge
+// in shared memory, the CTAs through distributed shared memory.  Row r < rows goes to row
+// row_of(r) of out and lse, o times factor_of(r, sum).
+constexpr int kPagedMaxSplit = 8;  // CTAs of a cluster, at most (the portable limit)
+template <class W, int kWarps, int kD>
+constexpr int paged_finish_bytes() {
+  return (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + kWarps + 2)) * 4;
+}
+template <class W, int kWarps, int kD, class RowOf, class FactorOf>
+__device__ __forceinline__ void paged_cluster_finish(W& w, uint8_t* smem, int split, int part, int rows, RowOf row_of,
+                                                     FactorOf factor_of, __nv_bfloat16* out, float* lse) {
+  constexpr int kThreads = kWarps * 32;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x;
+  float* so = reinterpret_cast<float*>(smem);    // [warps][16][kSmemRow]
+  float* sm = so + kWarps * 16 * W::kSmemRow;    // [warps][16][3]
+  float* sw = sm + kWarps * 16 * 3;              // [16][warps + 2]: weights, max, sum
+  float* sp = sw + 16 * (kWarps + 2);            // [16][kD] the CTA's o
+  __syncthreads();
+  w.park(so, sm, tid >> 5);
+  __syncthreads();
+  if (tid < rows) paged_merge_row<kWarps>(sm, tid, sw + tid * (kWarps + 2));
+  __syncthreads();
+  for (int x = tid; x < rows * (kD / 8); x += kThreads) {
+    const int r = x / (kD / 8), d0 = x % (kD / 8) * 8;
+    const float* wt = sw + r * (kWarps + 2);
+    float O[8];
+    paged_merge_dims<W, kWarps>(so, wt, r, d0, O);
+    if (split == 1) {
+      paged_store_row(out + row_of(r) * kD + d0, O, factor_of(r, wt[kWarps + 1]));
+      if (lse != nullptr && d0 == 0) lse[row_of(r)] = paged_lse(wt[kWarps], wt[kWarps + 1]);
+    } else {
+      float4* to = reinterpret_cast<float4*>(sp + r * kD + d0);
+      to[0] = make_float4(O[0], O[1], O[2], O[3]);
+      to[1] = make_float4(O[4], O[5], O[6], O[7]);
+    }
+  }
+  if (split == 1) return;
+  cluster.sync();
+  for (int x = part * kThreads + tid; x < rows * (kD / 4); x += split * kThreads) {
+    const int r = x / (kD / 4), col = x % (kD / 4) * 4;
+    float2 ml[kPagedMaxSplit];
+    float4 v[kPagedMaxSplit];
+#pragma unroll
+    for (int i = 0; i < kPagedMaxSplit; ++i) {
+      if (i >= split) break;
+      ml[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sw, i) + r * (kWarps + 2) + kWarps);
+      v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sp, i) + r * kD + col);
+    }
+    float M = -INFINITY, L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kPagedMaxSplit; ++i)
+      if (i < split) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < kPagedMaxSplit; ++i) {
+      if (i >= split || ml[i].y == 0.f) continue;
+      const float f = ptx::ex2(ml[i].x - M);
+      L = fmaf(f, ml[i].y, L);
+      O[0] = fmaf(f, v[i].x, O[0]); O[1] = fmaf(f, v[i].y, O[1]);
+      O[2] = fmaf(f, v[i].z, O[2]); O[3] = fmaf(f, v[i].w, O[3]);
+    }
+    const float f = factor_of(r, L);
+    *reinterpret_cast<uint2*>(out + row_of(r) * kD + col) =
+        make_uint2(pack_bf16x2(O[0] * f, O[1] * f), pack_bf16x2(O[2] * f, O[3] * f));
+    if (lse != nullptr && col == 0) lse[row_of(r)] = paged_lse(M, L);
+  }
+  cluster.sync();  // no CTA leaves while others read its shared memory
 }
 
 }  // namespace sba

@@ -9,8 +9,6 @@
 // One item is (row, token, KV head) with its Hq / Hkv <= 16 query heads.  Its key set is
 // small (at most 32 blocks), so an item's tiles are shared evenly among the `split` CTAs of
 // one cluster, which merge through distributed shared memory: one launch, no workspace.
-#include <cooperative_groups.h>
-
 #include <string>
 
 #include "paged_core.cuh"
@@ -21,10 +19,7 @@ static __device__ unsigned g_err_select = 0;
 
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kMaxBlocks = 32;
-constexpr int kMaxSplit = 8;  // CTAs of a cluster, at most (the portable limit)
 
 struct PagedSelectParams {
   PagedView c;
@@ -43,13 +38,11 @@ struct PagedSelectParams {
 template <bool kF8, int kD, bool kHi, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, 12 / kWarps)
 paged_select_kernel(const PagedSelectParams p) {
-  constexpr int kThreads = kWarps * 32;
-  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_key[kMaxBlocks * 128 / kKeys];  // first key of each tile
   __shared__ int s_tiles;
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = p.split, part = blockIdx.x % split;  // a cluster is `split` blocks along x
   const int h = blockIdx.x / split % p.c.Hkv, token = blockIdx.x / split / p.c.Hkv;
@@ -87,7 +80,8 @@ paged_select_kernel(const PagedSelectParams p) {
   mk.num_sinks = 0;
   mk.wlo0 = mk.wlo1 = mk.all_lo = 0;
   mk.whi0 = mk.whi1 = mk.all_hi = INT_MAX;
-  mk.bias0 = mk.bias1 = nullptr;
+  mk.bias0 = nullptr;
+  mk.bias_step = 0;
   W w;
   w.init(p.c, b, h, ptx::smem_u32(smem) + warp * W::kWarpBytes, p.scale, 0.f, &g_err_select);
   {
@@ -106,71 +100,20 @@ paged_select_kernel(const PagedSelectParams p) {
       },
       [] {}, mk);  // the queries came while the blocks were looked through
 
-  // ---- the CTA's result, or its partial and the cluster's
-  float* so = reinterpret_cast<float*>(smem);    // [warps][16][kSmemRow]
-  float* sm = so + kWarps * 16 * W::kSmemRow;    // [warps][16][3]
-  float* sw = sm + kWarps * 16 * 3;              // [16][warps + 2]: weights, max, sum
-  float* sp = sw + 16 * (kWarps + 2);            // [16][kD] the CTA's o
-  __syncthreads();
-  w.park(so, sm, warp);
-  __syncthreads();
-  if (tid < p.G) paged_merge_row<kWarps>(sm, tid, sw + tid * (kWarps + 2));
-  __syncthreads();
   const long long row0 = (long long)token * p.Hq + h * p.G;
-  auto factor = [&](int row, float L) {  // of o, in the output
-    return (L == 0.f ? 0.f : 1.f / L) * (p.gate != nullptr ? __bfloat162float(p.gate[row0 + row]) : 1.f);
-  };
-  for (int x = tid; x < p.G * (kD / 8); x += kThreads) {
-    const int row = x / (kD / 8), d0 = x % (kD / 8) * 8;
-    const float* wt = sw + row * (kWarps + 2);
-    float O[8];
-    paged_merge_dims<W, kWarps>(so, wt, row, d0, O);
-    if (split == 1) {
-      paged_store_row(p.out + (row0 + row) * kD + d0, O, factor(row, wt[kWarps + 1]));
-      if (p.lse != nullptr && d0 == 0) p.lse[row0 + row] = paged_lse(wt[kWarps], wt[kWarps + 1]);
-    } else {
-      float4* to = reinterpret_cast<float4*>(sp + row * kD + d0);
-      to[0] = make_float4(O[0], O[1], O[2], O[3]);
-      to[1] = make_float4(O[4], O[5], O[6], O[7]);
-    }
-  }
-  if (split == 1) return;
-  cluster.sync();
-  for (int x = part * kThreads + tid; x < p.G * (kD / 4); x += split * kThreads) {
-    const int row = x / (kD / 4), col = x % (kD / 4) * 4;
-    float2 ml[kMaxSplit];
-    float4 v[kMaxSplit];
-#pragma unroll
-    for (int i = 0; i < kMaxSplit; ++i) {
-      if (i >= split) break;
-      ml[i] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sw, i) + row * (kWarps + 2) + kWarps);
-      v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sp, i) + row * kD + col);
-    }
-    float M = -INFINITY, L = 0.f, O[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kMaxSplit; ++i)
-      if (i < split) M = fmaxf(M, ml[i].x);
-#pragma unroll
-    for (int i = 0; i < kMaxSplit; ++i) {
-      if (i >= split || ml[i].y == 0.f) continue;
-      const float f = ptx::ex2(ml[i].x - M);
-      L = fmaf(f, ml[i].y, L);
-      O[0] = fmaf(f, v[i].x, O[0]); O[1] = fmaf(f, v[i].y, O[1]);
-      O[2] = fmaf(f, v[i].z, O[2]); O[3] = fmaf(f, v[i].w, O[3]);
-    }
-    const float f = factor(row, L);
-    *reinterpret_cast<uint2*>(p.out + (row0 + row) * kD + col) =
-        make_uint2(pack_bf16x2(O[0] * f, O[1] * f), pack_bf16x2(O[2] * f, O[3] * f));
-    if (p.lse != nullptr && col == 0) p.lse[row0 + row] = paged_lse(M, L);
-  }
-  cluster.sync();  // no CTA leaves while others read its shared memory
+  paged_cluster_finish<W, kWarps, kD>(
+      w, smem, split, part, p.G, [&](int r) { return row0 + r; },
+      [&](int r, float L) {
+        return (L == 0.f ? 0.f : 1.f / L) * (p.gate != nullptr ? __bfloat162float(p.gate[row0 + r]) : 1.f);
+      },
+      p.out, p.lse);
 }
 
 template <bool kF8, int kD, bool kHi, int kWarps>
 cudaError_t launch_w(const PagedSelectParams& p, cudaStream_t st) {
-  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0>;
   constexpr int ring = kWarps * W::kWarpBytes;
-  constexpr int merge = (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kD + kWarps + 2)) * 4;
+  constexpr int merge = paged_finish_bytes<W, kWarps, kD>();
   constexpr int bytes = ring > merge ? ring : merge;
   auto* kernel = paged_select_kernel<kF8, kD, kHi, kWarps>;
   static thread_local unsigned long long devices = 0;
@@ -224,7 +167,7 @@ int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long l
   int split = 1, warps = 4;
   long long best = LLONG_MAX;
   for (int w = 4; w <= 6; w += 2)
-    for (int s = 1; s <= kMaxSplit; s *= 2) {
+    for (int s = 1; s <= kPagedMaxSplit; s *= 2) {
       const long long resident = 152 * (12 / w), waves = (items * s + resident - 1) / resident;
       const long long cost = waves * (2 + (tiles + s * w - 1) / (s * w));
       if (cost < best) {

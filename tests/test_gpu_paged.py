@@ -260,6 +260,8 @@ def test_caps_at_both_ends(sba):
     assert (free[0].double() - huge[0].double()).abs().max() <= 2.0 ** -7 * free[0].double().abs().max()
     assert (free[1] - huge[1]).abs().max() < 2.0 ** -12
     check_attention(sba, c, [1, 1], 8, 12, what="tiny cap", logits_soft_cap=1e-3)
+    for cap in (256.0, 300.0):  # either side of where the formula changes
+        check_attention(sba, c, [1, 1], 8, 12, what=f"cap {cap}", logits_soft_cap=cap)
 
 
 def test_scales_far_apart(sba):
