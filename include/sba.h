@@ -478,7 +478,8 @@ typedef struct sba_paged_cache {
  * overflow to +-448, NaN kept.  SBA_BF16 stores the rounded value.
  * Tokens at negative positions are passed over: nothing is stored, q_out is not written.
  * Two rows that write the same page in one call race on it (rows may share pages that
- * they only read).  The call has no workspace and is one launch.
+ * they only read).  The pools must not overlap, and q_out overlaps nothing but q, with q's
+ * stride.  The call has no workspace and is one launch.
  */
 typedef struct sba_paged_append_args {
   sba_paged_cache cache;
@@ -516,7 +517,8 @@ SBA_API size_t sba_paged_attention_workspace_size(int B, int N, int Hq, int Hkv,
  * Results do not depend on timing.  A key that some query of the row sees takes part with
  * weight 0 in the products of the row's other queries, so its value must be finite.
  * Internally, on `stream`: the attention kernel and a kernel that merges the items it cut
- * into runs.  Without sinks, calls with many (query, head) rows for each row and KV head (17
+ * into runs; without cu_seqlens and with tables of few keys, one kernel whose clusters share
+ * an item.  Without sinks, calls with many (query, head) rows for each row and KV head (17
  * to 97 on average, by head dimension, dtype and table size) use the kernel with
  * accumulators in tensor memory, whose waits are bounded (sba_set_wait_timeout_cycles).
  */

@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <cstdio>
 #include <mutex>
 #include <string>
@@ -602,6 +603,16 @@ int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) 
   SBA_REQUIRE(token_stride_ok(a.k_stride, Hkv, D, N) && token_stride_ok(a.v_stride, Hkv, D, N) &&
                   (!a.q || (token_stride_ok(a.q_stride, a.Hq, D, N) && token_stride_ok(a.q_out_stride, a.Hq, D, N))),
               "token strides must cover the token's heads and be multiples of 8 elements");
+  SBA_REQUIRE(a.q == nullptr || (a.q_out != a.k && a.q_out != a.v), "q_out must not be k or v");
+  SBA_REQUIRE(a.q != a.q_out || a.q == nullptr || N == 1 || a.q_stride == a.q_out_stride,
+              "q_out in place of q needs q's token stride");
+  {
+    // pages of one pool may lie between the other's, as halves of one array do
+    const long long item = a.cache.dtype == SBA_E4M3 ? 1 : 2, page = (long long)Hkv * a.cache.page_size * D * item;
+    const long long stride = a.cache.page_stride * item, d = std::llabs(c.k - c.v);
+    SBA_REQUIRE(d >= stride * (c.num_pages - 1LL) + page || (d % stride >= page && stride - d % stride >= page),
+                "k_pages and v_pages overlap");
+  }
   SBA_REQUIRE(!a.cos == !a.sin, "cos and sin go together");
   if (a.cos != nullptr) {
     SBA_REQUIRE(a.rot_dim >= 16 && a.rot_dim <= D && a.rot_dim % 16 == 0,
@@ -610,8 +621,9 @@ int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) 
                 "cos and sin must be 16-byte aligned tables of at least one position");
   }
   SBA_SUPPORT((long long)Hkv * 2 + (a.q ? a.Hq : 0) <= 65535, "Hq + 2 Hkv must be <= 65535");
-  SBA_SUPPORT(c.cu != nullptr || (long long)c.B * ((c.Qn >> c.p_shift) + 2) < (1LL << 31),
-              "too many pages touched by one call");
+  const long long units = c.cu != nullptr ? ((long long)N >> c.p_shift) + 2LL * c.B
+                                          : (long long)c.B * ((c.Qn >> c.p_shift) + 2);
+  SBA_SUPPORT(units * ((Hkv * 2 + (a.q ? a.Hq : 0) + 7) / 8) < (1LL << 31), "too many pages touched by one call");
   return launch_paged_append(c, a.cache.dtype == SBA_E4M3, D, a.k, a.k_stride, a.v, a.v_stride, a.q,
                              a.q_stride, a.q_out, a.q_out_stride, a.Hq, a.cos, a.sin, a.rot_dim,
                              a.max_pos, a.interleaved ? 1 : 0, reinterpret_cast<cudaStream_t>(stream));

@@ -384,8 +384,24 @@ def test_batches(sba, B):
     check_attention(sba, c, list(n), 4, 20, what=f"B={B}")
 
 
-def test_results_repeat(sba):
-    c = Cache([5000, 17, 900, 3333], 4, 128, 64, True, 495)
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("B,n,G,D", [(5, 1, 4, 128), (300, 1, 4, 128), (5, 3, 3, 64), (130, 3, 9, 64), (300, 1, 16, 128)])
+def test_equal_token_counts(sba, f8, B, n, G, D):
+    """Few and many rows with as many tokens each: the kernel whose clusters share an item
+    and the one whose runs are cut, with windows, caps and sinks."""
+    rng = np.random.default_rng(B + n)
+    c = Cache(rng.integers(0, 400, B), 2, D, 32, f8, 496 + B + G)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    bias = torch.randn((2 * G, 5), generator=g, device=DEV)
+    for kw in (dict(window_right=0), dict(window_left=60, window_right=0, logits_soft_cap=4.0, sink_bias=bias),
+               dict(window_left=33, window_right=2, sink_bias=bias[0].contiguous()), dict(logits_soft_cap=400.0)):
+        check_attention(sba, c, [n] * B, 2 * G, 28, what=f"B={B} n={n} {list(kw)}", **kw)
+
+
+@pytest.mark.parametrize("long", [5000, 30000])
+def test_results_repeat(sba, long):
+    c = Cache([long, 17, 900, 3333], 4, 128, 64, True, 495)
     q = c.q((4, 16, 128), 21)
     a, la = sba.paged_attention_fwd(q, *c.pool(), **c.kw())
     for _ in range(20):
@@ -691,7 +707,7 @@ def test_prompt_then_decode(sba, f8):
 
 def test_two_streams(sba):
     """Calls that overlap, each with its own workspace, give what they give alone."""
-    cs = [Cache([4000, 900, 17], 4, 128, 64, True, 820 + i) for i in range(2)]
+    cs = [Cache([30000, 900, 17], 4, 128, 64, True, 820 + i) for i in range(2)]
     qs = [c.q((3, 16, 128), 60 + i) for i, c in enumerate(cs)]
     alone = [sba.paged_attention_fwd(q, *c.pool(), **c.kw()) for c, q in zip(cs, qs)]
     torch.cuda.synchronize()
@@ -708,7 +724,7 @@ def test_two_streams(sba):
 
 
 def test_workspace_needs_no_initialisation_and_may_be_shared_in_order(sba):
-    c = Cache([4000, 900, 17], 4, 128, 64, True, 830)
+    c = Cache([30000, 900, 17], 4, 128, 64, True, 830)
     q = c.q((3, 16, 128), 61)
     ws = torch.full((sba.paged_attention_workspace_size(3, 3, 16, 4, 128),), 0xFF, dtype=torch.uint8, device=DEV)
     want = sba.paged_attention_fwd(q, *c.pool(), **c.kw())

@@ -37,7 +37,7 @@ ATTEND = struct("Attend", ("q", "bias", "out", "lse", "ws"), ("ws_bytes", "qs"),
 SELECT = struct("Select", ("q", "idx", "cnt", "gate", "out", "lse"), ("qs",),
                 ("Hq", "n", "S", "bs", "causal", "scale"))
 OUT = 0x20000
-POOL = dict(k_pages=FAKE, v_pages=FAKE, k_scales=FAKE, v_scales=FAKE, page_table=FAKE, seq_lens=FAKE, cu=None,
+POOL = dict(k_pages=FAKE, v_pages=FAKE + 4 * 2 * 64 * 128, k_scales=FAKE, v_scales=FAKE, page_table=FAKE, seq_lens=FAKE, cu=None,
             page_stride=2 * 64 * 128, num_pages=4, page_size=64, Hkv=2, D=128, dt=2, table_width=8, B=3, Q=2, N=6)
 
 
@@ -49,7 +49,7 @@ def call(fn, kind, defaults, change):
 
 
 def append(lib, **kw):
-    d = dict(k=FAKE, ks=256, v=FAKE, vs=256, q=FAKE, qs=1024, qo=FAKE, qos=1024, cos=FAKE, sin=FAKE, rot=128,
+    d = dict(k=0x30000, ks=256, v=0x40000, vs=256, q=FAKE, qs=1024, qo=FAKE, qos=1024, cos=FAKE, sin=FAKE, rot=128,
              max_pos=512, inter=0, Hq=8)
     return call(lib.sba_paged_kv_append, APPEND, d, kw)
 
@@ -85,7 +85,11 @@ def test_cache_arguments(lib, change, code, text):
 @pytest.mark.parametrize("change,code", [
     (dict(k=None), -1), (dict(q=None), -1), (dict(qo=None), -1), (dict(N=7), -1), (dict(ks=128), -1), (dict(vs=260), -1),
     (dict(qos=1000), -1), (dict(k=FAKE + 2), -1), (dict(cos=None), -1), (dict(rot=24), -1), (dict(rot=144), -1),
-    (dict(rot=0), -1), (dict(max_pos=0), -1), (dict(sin=FAKE + 4), -1), (dict(Hq=0), -1), (dict(Hq=1 << 17, qs=1 << 24, qos=1 << 24), -2)])
+    (dict(rot=0), -1), (dict(max_pos=0), -1), (dict(sin=FAKE + 4), -1), (dict(Hq=0), -1), (dict(Hq=1 << 17, qs=1 << 24, qos=1 << 24), -2),
+    (dict(qs=2048), -1), (dict(qo=0x30000), -1), (dict(qo=0x40000), -1), (dict(v_pages=FAKE), -1),
+    (dict(v_pages=FAKE + 2 * 64 * 128), -1), (dict(v_pages=FAKE + 64, page_stride=4 * 64 * 128), -1),
+    (dict(v_pages=FAKE + 3 * 64 * 128, page_stride=4 * 64 * 128), -1),
+    (dict(cu=FAKE, B=1 << 24, N=1 << 28, Hkv=2000, page_stride=2000 * 64 * 128, v_pages=1 << 40, ks=256000, vs=256000), -2)])
 def test_append_arguments(lib, change, code):
     assert append(lib, **change) == code
 
