@@ -588,6 +588,7 @@ template <class W, int kWarps, int kD, class RowOf, class FactorOf>
 __device__ __forceinline__ void paged_cluster_finish(W& w, uint8_t* smem, int split, int part, int rows, RowOf row_of,
                                                      FactorOf factor_of, __nv_bfloat16* out, float* lse) {
   constexpr int kThreads = kWarps * 32;
+  static_assert(kWarps % 2 == 0, "(max, sum) of a row are read as 8 bytes");
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x;
