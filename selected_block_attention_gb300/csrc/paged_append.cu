@@ -43,7 +43,7 @@ struct AppendParams {
   long long k_tok, v_tok, q_tok, qo_tok;
   int Hq, rot, interleaved, max_pos;
   int units_per_row;  // pages a row's tokens can touch (cu == null)
-  int heads, groups;  // heads a block works through, blocks of a unit
+  int heads, groups;  // heads a block (few tokens: a warp) works through, blocks of a unit
 };
 
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
@@ -186,26 +186,19 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int c1, float*
       make_uint2(f32x4_to_e4m3x4(x[8], x[9], x[10], x[11]), f32x4_to_e4m3x4(x[12], x[13], x[14], x[15]));
 }
 
-// Few tokens a row: a row of a head is kD / 16 threads, 16 dimensions each.  kOne (one token
-// a row): a warp takes 512 / kD heads; else it takes one head, up to 512 / kD tokens.
-template <bool kF8, int kD, bool kOne>
-__global__ void __launch_bounds__(128)
-paged_append_few_kernel(const AppendParams p) {
+// Few tokens of a page (at most kFew = 512 / kD), one warp, heads first .. min(first + kFew >>
+// shift, end) - 1: a row of a head is kD / 16 threads, 16 dimensions each, and a head has
+// 2^shift rows of threads.
+template <bool kF8, int kD>
+__device__ __forceinline__ void append_few(const AppendParams& p, const Unit& u, int first, int end, int shift) {
   constexpr int kRowThreads = kD / 16;
-  constexpr int kRows = 32 / kRowThreads;
+  constexpr int kFew = 32 / kRowThreads;
   const PagedView& c = p.c;
-  paged_wait_before();
   const int lane = threadIdx.x & 31, rt = lane % kRowThreads;
-  const int warp = blockIdx.y * 4 + (threadIdx.x >> 5), streams = p.Hq + 2 * c.Hkv;
-  const int stream = kOne ? warp * kRows + lane / kRowThreads : warp;
-  const int row = kOne ? 0 : lane / kRowThreads;
-  if (warp * (kOne ? kRows : 1) >= streams) return;
-  const int b = blockIdx.x / p.units_per_row;
-  const Unit u = unit_of(c, b, blockIdx.x - b * p.units_per_row, lane == 0);
-  if (u.m <= 0) return;
-  const Stream t = stream_of<kD>(p, min(stream, streams - 1));
+  const int row = lane / kRowThreads & ((1 << shift) - 1), stream = first + (lane / kRowThreads >> shift);
+  const Stream t = stream_of<kD>(p, min(stream, end - 1));
   const int rot = t.is_q || t.is_k ? p.rot : 0;
-  const bool mine = row < u.m && stream < streams;
+  const bool mine = row < u.m && stream < end;
   int c0, c1;
   chunks_of(rt, rot, p.interleaved, c0, c1);
   float x[16];
@@ -216,7 +209,7 @@ paged_append_few_kernel(const AppendParams p) {
     load8(s + 8 * c0, x);
     load8(s + 8 * c1, x + 8);
   }
-  const bool any_kv = (kOne ? min(warp * kRows + kRows, streams) : warp + 1) > p.Hq;
+  const bool any_kv = min(first + (kFew >> shift), end) > p.Hq;
   const int page = any_kv ? page_of(c, u, lane == 0) : 0;
   if (page < 0) return;
   if (mine && rt < rot / 16) {
@@ -233,21 +226,21 @@ paged_append_few_kernel(const AppendParams p) {
     store8(o + 8 * c1, x + 8);
   }
   if constexpr (kF8) {
-    const bool stores = !t.is_q && (!kOne || mine);  // this head's values are quantised
+    const bool stores = !t.is_q && stream < end;  // this head's values are quantised
     if (!__any_sync(0xffffffffu, stores)) return;
     float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
     const float old = stores && off > 0 ? *scale_at : 0.f;
     float amax = finite_max(x, 0.f);
 #pragma unroll
-    for (int d = (kOne ? kRowThreads : 32) / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    for (int d = (kRowThreads << shift) / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     const float need = pow2_scale(amax);
     const float scale = need > old ? need : old;
     const float inv = __frcp_rn(scale);
     // Heads whose scale grows: the whole warp takes their codes along, one head after the
     // other, eight loads in flight.
     const bool grow = stores && scale != old;
-    unsigned heads = __ballot_sync(0xffffffffu, grow && rt == 0 && (kOne || lane == 0));
-    if (grow && rt == 0 && (kOne || lane == 0)) *scale_at = scale;
+    unsigned heads = __ballot_sync(0xffffffffu, grow && rt == 0 && row == 0);
+    if (grow && rt == 0 && row == 0) *scale_at = scale;
     while (heads) {
       const int from = __ffs(heads) - 1;
       heads &= heads - 1;
@@ -268,14 +261,45 @@ paged_append_few_kernel(const AppendParams p) {
   }
 }
 
+// The first and the last page of a row, where they get at most kFew tokens: all of a call's
+// pages when no row has more.  kOne: every row has one.
+template <bool kF8, int kD, bool kOne>
+__global__ void __launch_bounds__(128)
+paged_append_few_kernel(const AppendParams p) {
+  constexpr int kFew = 512 / kD;
+  const PagedView& c = p.c;
+  paged_wait_before();
+  const int heads = kOne ? kFew : p.heads, b = blockIdx.x;
+  const int first = (blockIdx.y * 4 + (threadIdx.x >> 5)) * heads, end = min(first + heads, p.Hq + 2 * c.Hkv);
+  if (first >= end) return;
+  const bool report = (threadIdx.x & 31) == 0;
+  const Unit u = unit_of(c, b, 0, report);
+  if (u.m <= 0) return;
+  if constexpr (kOne) {
+    append_few<kF8, kD>(p, u, first, end, 0);
+  } else {
+    auto put = [&](const Unit& x) {
+      const int shift = x.m > 4 ? 3 : x.m > 2 ? 2 : x.m - 1;
+      for (int s = first; s < end; s += kFew >> shift) append_few<kF8, kD>(p, x, s, end, shift);
+    };
+    if (u.m <= kFew) put(u);
+    const int last = ((c.lens[b] - 1) >> c.p_shift) - u.page_slot;
+    if (last > 0) {
+      const Unit v = unit_of(c, b, last, report);
+      if (v.m > 0 && v.m <= kFew) put(v);
+    }
+  }
+}
+
 // Any number of tokens: one block of P kD / 32 threads for a page and `heads` heads, so a
 // page's rows take two passes; the angles of its positions stay in registers from head to
 // head, and a head's values are loaded while the one before is worked on.
-template <bool kF8, int kD>
+// kBig: pages that get at most kFew tokens are paged_append_few_kernel's.
+template <bool kF8, int kD, bool kBig>
 __global__ void __launch_bounds__(512)
 paged_append_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
-  constexpr int kPasses = 2;
+  constexpr int kPasses = 2, kFew = 512 / kD;
   const PagedView& c = p.c;
   const int tid = threadIdx.x;
   __shared__ float s_max[2][16];
@@ -291,7 +315,11 @@ paged_append_kernel(const AppendParams p) {
     // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.  The row
     // is the last one that begins at or before this unit: 32 probes a round.
     const int lane = tid & 31;
-    auto begin_of = [&](int i) { return (min(max(c.cu[i], 0), c.N) >> c.p_shift) + 2 * i; };
+    // kBig: at most floor(n / (kFew + 1)) of a row's pages are this kernel's.
+    auto begin_of = [&](int i) {
+      const int t = min(max(c.cu[i], 0), c.N);
+      return kBig ? t / (kFew + 1) : (t >> c.p_shift) + 2 * i;
+    };
     b = 0;
     for (int range = c.B; range > 1;) {
       const int step = (range + 31) / 32, i = b + lane * step;
@@ -303,7 +331,13 @@ paged_append_kernel(const AppendParams p) {
     j = unit - begin_of(b);
     if (j < 0) return;  // offsets that decrease
   }
-  const Unit u = unit_of(c, b, j, tid == 0 && group == 0);
+  Unit u = unit_of(c, b, kBig ? 0 : j, tid == 0 && group == 0);
+  if constexpr (kBig) {
+    if (u.m <= 0) return;
+    const bool small = u.m <= kFew;  // the first page; those up to the last are full
+    if (small || j > 0) u = unit_of(c, b, j + small, false);
+    if (u.m <= kFew) return;
+  }
   if (u.m <= 0) return;
   const int rows = blockDim.x / kRowThreads;
   const int rt = tid % kRowThreads, slot = tid / kRowThreads;
@@ -396,22 +430,31 @@ paged_append_kernel(const AppendParams p) {
 template <bool kF8, int kD>
 cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const PagedView& c = p.c;
+  constexpr int kFew = 512 / kD;
   const int streams = p.Hq + 2 * c.Hkv;
-  if (c.cu == nullptr && c.Qn <= 512 / kD) {
-    constexpr int kHeads = 512 / kD;  // of a warp, when rows have one token
-    if (c.Qn == 1)
-      return paged_launch(paged_append_few_kernel<kF8, kD, true>,
-                          dim3((unsigned)c.B, (streams + 4 * kHeads - 1) / (4 * kHeads)), 128, 0, st, p);
-    return paged_launch(paged_append_few_kernel<kF8, kD, false>,
-                        dim3((unsigned)c.B * p.units_per_row, (streams + 3) / 4), 128, 0, st, p);
+  const bool few = c.cu == nullptr && c.Qn <= kFew;
+  // Token counts only the device knows: pages with few tokens go to the kernel that is made
+  // for them when the average row has few.  Rows of n tokens each, e4m3 D = 128 (kFew = 4),
+  // 48 heads, us with one kernel / with two: 256 rows n = 1: 36.4 / 10.0, 4: 35.9 / 15.4,
+  // 8: 37.1 / 39.6, 16: 47.4 / 58.7; 16 rows n = 1: 7.8 / 4.4, 8: 8.0 / 9.0.
+  const bool two = c.cu != nullptr && c.N <= (long long)kFew * c.B;
+  if (few || two) {
+    // a warp takes as many heads as it has threads for, going by the tokens of the average row
+    const int rows = std::min(kFew, (int)((c.N + (long long)c.B - 1) / c.B));
+    p.heads = kFew / (rows > 4 ? 8 : rows > 2 ? 4 : rows);
+    const dim3 grid((unsigned)c.B, (streams + 4 * p.heads - 1) / (4 * p.heads));
+    const cudaError_t e = few && c.Qn == 1 ? paged_launch(paged_append_few_kernel<kF8, kD, true>, grid, 128, 0, st, p)
+                                           : paged_launch(paged_append_few_kernel<kF8, kD, false>, grid, 128, 0, st, p);
+    if (e != cudaSuccess || few || c.N <= kFew) return e;
   }
-  const long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row
-                                          : ((long long)c.N >> c.p_shift) + 2LL * c.B;
+  long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row : ((long long)c.N >> c.p_shift) + 2LL * c.B;
+  if (two) units = c.N / (kFew + 1);
   // up to 8 heads a block, as long as there are blocks enough to fill the GPU
   p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
   p.groups = (streams + p.heads - 1) / p.heads;
   const dim3 grid((unsigned)(units * p.groups));
-  return paged_launch(paged_append_kernel<kF8, kD>, grid, (kD << c.p_shift) / 32, 0, st, p);
+  return two ? paged_launch(paged_append_kernel<kF8, kD, true>, grid, (kD << c.p_shift) / 32, 0, st, p)
+             : paged_launch(paged_append_kernel<kF8, kD, false>, grid, (kD << c.p_shift) / 32, 0, st, p);
 }
 
 }  // namespace

@@ -20,6 +20,7 @@ static __device__ unsigned g_err_select = 0;
 namespace {
 
 constexpr int kMaxBlocks = 32;
+constexpr int kWarps = 4;
 
 struct PagedSelectParams {
   PagedView c;
@@ -35,8 +36,8 @@ struct PagedSelectParams {
   float scale;
 };
 
-template <bool kF8, int kD, bool kHi, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, 12 / kWarps)
+template <bool kF8, int kD, bool kHi>
+__global__ void __launch_bounds__(kWarps * 32, 3)
 paged_select_kernel(const PagedSelectParams p) {
   using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0>;
   constexpr int kKeys = W::kKeys;
@@ -109,24 +110,19 @@ paged_select_kernel(const PagedSelectParams p) {
       p.out, p.lse);
 }
 
-template <bool kF8, int kD, bool kHi, int kWarps>
-cudaError_t launch_w(const PagedSelectParams& p, cudaStream_t st) {
+template <bool kF8, int kD, bool kHi>
+cudaError_t launch(const PagedSelectParams& p, cudaStream_t st) {
   using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0>;
   constexpr int ring = kWarps * W::kWarpBytes;
   constexpr int merge = paged_finish_bytes<W, kWarps, kD>();
   constexpr int bytes = ring > merge ? ring : merge;
-  auto* kernel = paged_select_kernel<kF8, kD, kHi, kWarps>;
+  auto* kernel = paged_select_kernel<kF8, kD, kHi>;
   static thread_local unsigned long long devices = 0;
   cudaError_t e = paged_allow_smem(kernel, bytes, &devices);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.c.B * p.c.Qn * p.c.Hkv;
   return paged_launch(kernel, dim3((unsigned)(items * p.split)), kWarps * 32, bytes, st, p, p.split);
 }
-template <bool kF8, int kD, bool kHi>
-cudaError_t launch(const PagedSelectParams& p, int warps, cudaStream_t st) {
-  return warps == 4 ? launch_w<kF8, kD, kHi, 4>(p, st) : launch_w<kF8, kD, kHi, 6>(p, st);
-}
-
 }  // namespace
 
 unsigned read_and_clear_error_select(cudaStream_t, std::string* where) {
@@ -159,32 +155,29 @@ int launch_paged_select(const PagedView& c, int f8, int D, const void* q, long l
   p.Hq = Hq;
   p.G = Hq / c.Hkv;
   p.scale = scale;
-  // Warps a CTA (4, three CTAs on an SM, or 6, two) and CTAs an item: the choice with the
-  // least (waves of resident CTAs) x (a CTA's fixed time, worth about 2 tiles of a warp, +
-  // its warps' tiles).
+  // CTAs an item: the choice with the least (waves of resident CTAs, three on an SM) x (a
+  // CTA's fixed time, worth about 2 tiles of a warp, + its warps' tiles).
   const long long items = (long long)c.B * c.Qn * c.Hkv;
   const int tiles = S * block_size / (f8 || D == 64 ? 32 : 16);
-  int split = 1, warps = 4;
+  int split = 1;
   long long best = LLONG_MAX;
-  for (int w = 4; w <= 6; w += 2)
-    for (int s = 1; s <= kPagedMaxSplit; s *= 2) {
-      const long long resident = 152 * (12 / w), waves = (items * s + resident - 1) / resident;
-      const long long cost = waves * (2 + (tiles + s * w - 1) / (s * w));
-      if (cost < best) {
-        best = cost;
-        split = s;
-        warps = w;
-      }
+  for (int s = 1; s <= kPagedMaxSplit; s *= 2) {
+    const long long waves = (items * s + 455) / 456;
+    const long long cost = waves * (2 + (tiles + s * kWarps - 1) / (s * kWarps));
+    if (cost < best) {
+      best = cost;
+      split = s;
     }
+  }
   p.split = split;
   const bool hi = p.G > 8;
   cudaError_t e;
   if (D == 128)
-    e = f8 ? (hi ? launch<true, 128, true>(p, warps, stream) : launch<true, 128, false>(p, warps, stream))
-           : (hi ? launch<false, 128, true>(p, warps, stream) : launch<false, 128, false>(p, warps, stream));
+    e = f8 ? (hi ? launch<true, 128, true>(p, stream) : launch<true, 128, false>(p, stream))
+           : (hi ? launch<false, 128, true>(p, stream) : launch<false, 128, false>(p, stream));
   else
-    e = f8 ? (hi ? launch<true, 64, true>(p, warps, stream) : launch<true, 64, false>(p, warps, stream))
-           : (hi ? launch<false, 64, true>(p, warps, stream) : launch<false, 64, false>(p, warps, stream));
+    e = f8 ? (hi ? launch<true, 64, true>(p, stream) : launch<true, 64, false>(p, stream))
+           : (hi ? launch<false, 64, true>(p, stream) : launch<false, 64, false>(p, stream));
   if (e != cudaSuccess) return cuda_error(e, "paged selection launch");
   return SBA_OK;
 }

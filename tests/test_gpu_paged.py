@@ -588,6 +588,21 @@ def test_append_many_ragged_rows(sba, B):
     check_append(sba, c, n, 1, 0, False, 46)
 
 
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("D,P", [(128, 16), (128, 64), (64, 32)])
+def test_append_long_rows_among_short(sba, f8, D, P):
+    """Few tokens on average: pages with few and with many, first, last and in between, are
+    different kernels' work; rows without tokens and rows shorter than theirs."""
+    rng = np.random.default_rng(D + P)
+    n = rng.integers(0, 3, 150)
+    n[[3, 40, 77, 120, 149]] = 512 // D + 1, 2 * P, P + 1, 3 * P - 1, 37
+    n[60:70] = np.arange(10)
+    lens = rng.integers(0, 40, 150) + n
+    lens[[9, 120, 65]] = 0, P + 2, 1
+    c = Cache(lens, 2, D, P, f8, 736 + P)
+    check_append(sba, c, n, 3, D, False, 49)
+
+
 @pytest.mark.parametrize("size", [1e-3, 40.0, 1e30])
 def test_append_grows_and_keeps_scales(sba, size):
     """Tokens much larger (codes in the page move to the new scale), much smaller (it
