@@ -18,9 +18,16 @@
 // step of the same page filled at once.
 //
 // Work unit: one page of one row, for one head of K, V or Q: its maximum is all that the
-// scale needs, so a unit is one block (or one warp) and nothing waits for another.  The
-// kernels are bound by memory: every input is read once and held in registers between the
-// maximum and the store.
+// scale needs, so a unit is one block (or one warp) and nothing waits for another.  Every
+// input is read once and held in registers between the maximum and the store.
+//
+// What bounds it.  Prompts: bytes.  12 rows of up to 2600 tokens, 32 + 2 * 8 heads of 128,
+// e4m3 pages of 64: 340 MB in 65.5 us (5.2 TB/s); the angles of a page's positions are
+// kept over the block's heads (79 us when each head reads them again), and the next head's
+// loads are under way (a ring of cp.async in shared memory instead: 67.3; blocks of 2, 4 or
+// 12 heads instead of 8: 77.9, 70.4, 71.1).  One token a row: the chain of length, table,
+// values, scale and store, 2.2 us for 8 rows and 2.8 for 256; a warp takes several heads
+// because one head each needs four times the waves of blocks (5.7).
 #include <algorithm>
 #include <string>
 
@@ -264,7 +271,7 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Unit& u,
 // The first and the last page of a row, where they get at most kFew tokens: all of a call's
 // pages when no row has more.  kOne: every row has one.
 template <bool kF8, int kD, bool kOne>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 6)  // 256 rows of 4 tokens: 8.3 us with 5 blocks an SM, 7.8 with 6, 12.0 with 8
 paged_append_few_kernel(const AppendParams p) {
   constexpr int kFew = 512 / kD;
   const PagedView& c = p.c;
@@ -291,18 +298,24 @@ paged_append_few_kernel(const AppendParams p) {
   }
 }
 
-// Any number of tokens: one block of P kD / 32 threads for a page and `heads` heads, so a
-// page's rows take two passes; the angles of its positions stay in registers from head to
-// head, and a head's values are loaded while the one before is worked on.
+// Rows of a page that a thread takes.  e4m3: fewer warps meet at the barrier between a
+// head's maximum and its codes (12 prompts as above: 65.1 us with two, 67.0 with one); bf16
+// has no barrier (6 MB of prompts into pages of 16: 11.6 / 10.8 us).
+template <bool kF8>
+constexpr int append_passes = kF8 ? 2 : 1;
+
+// Any number of tokens: one block for a page and `heads` heads; the angles of its positions
+// stay in registers from head to head, and a head's values are loaded while the one before
+// is worked on.
 // kBig: pages that get at most kFew tokens are paged_append_few_kernel's.
 template <bool kF8, int kD, bool kBig>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(kF8 ? 512 : 1024)
 paged_append_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
-  constexpr int kPasses = 2, kFew = 512 / kD;
+  constexpr int kPasses = append_passes<kF8>, kFew = 512 / kD;
   const PagedView& c = p.c;
   const int tid = threadIdx.x;
-  __shared__ float s_max[2][16];
+  __shared__ float s_max[2][32];
   paged_wait_before();
   // a unit's blocks follow one another: their heads' rows are neighbours in memory
   const int unit = blockIdx.x / p.groups, group = blockIdx.x - unit * p.groups;
@@ -435,8 +448,8 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const bool few = c.cu == nullptr && c.Qn <= kFew;
   // Token counts only the device knows: pages with few tokens go to the kernel that is made
   // for them when the average row has few.  Rows of n tokens each, e4m3 D = 128 (kFew = 4),
-  // 48 heads, us with one kernel / with two: 256 rows n = 1: 36.4 / 10.0, 4: 35.9 / 15.4,
-  // 8: 37.1 / 39.6, 16: 47.4 / 58.7; 16 rows n = 1: 7.8 / 4.4, 8: 8.0 / 9.0.
+  // 48 heads, us with one kernel / with two: 256 rows n = 1: 36.4 / 8.7, 4: 35.9 / 13.9,
+  // 8: 37.1 / 39.6, 16: 47.4 / 58.7; 16 rows n = 1: 7.8 / 4.3, 8: 8.0 / 9.0.
   const bool two = c.cu != nullptr && c.N <= (long long)kFew * c.B;
   if (few || two) {
     // a warp takes as many heads as it has threads for, going by the tokens of the average row
@@ -453,8 +466,9 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
   p.groups = (streams + p.heads - 1) / p.heads;
   const dim3 grid((unsigned)(units * p.groups));
-  return two ? paged_launch(paged_append_kernel<kF8, kD, true>, grid, (kD << c.p_shift) / 32, 0, st, p)
-             : paged_launch(paged_append_kernel<kF8, kD, false>, grid, (kD << c.p_shift) / 32, 0, st, p);
+  const int threads = (kD << c.p_shift) / (16 * append_passes<kF8>);
+  return two ? paged_launch(paged_append_kernel<kF8, kD, true>, grid, threads, 0, st, p)
+             : paged_launch(paged_append_kernel<kF8, kD, false>, grid, threads, 0, st, p);
 }
 
 }  // namespace

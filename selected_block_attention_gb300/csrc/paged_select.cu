@@ -9,6 +9,10 @@
 // One item is (row, token, KV head) with its Hq / Hkv <= 16 query heads.  Its key set is
 // small (at most 32 blocks), so an item's tiles are shared evenly among the `split` CTAs of
 // one cluster, which merge through distributed shared memory: one launch, no workspace.
+//
+// What bounds it: two rows, the chain of block ids, page table, keys and merge: 4.6 us.  64
+// rows of 16 blocks of 64 keys, 4 KV heads, D = 128, e4m3: 67 MB in 19.0 us, the same chain
+// and 13 us of reading (5.2 TB/s): every CTA is in the first wave, so nothing hides it.
 #include <string>
 
 #include "paged_core.cuh"
