@@ -621,9 +621,6 @@ int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) 
                 "cos and sin must be 16-byte aligned tables of at least one position");
   }
   SBA_SUPPORT((long long)Hkv * 2 + (a.q ? a.Hq : 0) <= 65535, "Hq + 2 Hkv must be <= 65535");
-  const long long units = c.cu != nullptr ? ((long long)N >> c.p_shift) + 2LL * c.B
-                                          : (long long)c.B * ((c.Qn >> c.p_shift) + 2);
-  SBA_SUPPORT(units * ((Hkv * 2 + (a.q ? a.Hq : 0) + 7) / 8) < (1LL << 31), "too many pages touched by one call");
   return launch_paged_append(c, a.cache.dtype == SBA_E4M3, D, a.k, a.k_stride, a.v, a.v_stride, a.q,
                              a.q_stride, a.q_out, a.q_out_stride, a.Hq, a.cos, a.sin, a.rot_dim,
                              a.max_pos, a.interleaved ? 1 : 0, reinterpret_cast<cudaStream_t>(stream));

@@ -23,9 +23,9 @@
 //
 // What bounds it.  Prompts: bytes.  12 rows of up to 2600 tokens, 32 + 2 * 8 heads of 128,
 // e4m3 pages of 64: 340 MB in 65.5 us (5.2 TB/s); the angles of a page's positions are
-// kept over the block's heads (79 us when each head reads them again), and the next head's
-// loads are under way (a ring of cp.async in shared memory instead: 67.3; blocks of 2, 4 or
-// 12 heads instead of 8: 77.9, 70.4, 71.1).  One token a row: the chain of length, table,
+// kept over the heads (79 us when each head reads them again), and the next head's
+// loads are under way (none: 81.7; a second head's as well: 66.4; a ring of cp.async in shared
+// memory instead: 67.3).  One token a row: the chain of length, table,
 // values, scale and store, 2.2 us for 8 rows and 2.8 for 256; a warp takes several heads
 // because one head each needs four times the waves of blocks (5.7).
 #include <algorithm>
@@ -49,8 +49,7 @@ struct AppendParams {
   const float* sinp;
   long long k_tok, v_tok, q_tok, qo_tok;
   int Hq, rot, interleaved, max_pos;
-  int units_per_row;  // pages a row's tokens can touch (cu == null)
-  int heads, groups;  // heads a block (few tokens: a warp) works through, blocks of a unit
+  int heads;  // few tokens: heads of a warp
 };
 
 __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
@@ -304,139 +303,205 @@ paged_append_few_kernel(const AppendParams p) {
 template <bool kF8>
 constexpr int append_passes = kF8 ? 2 : 1;
 
-// Any number of tokens: one block for a page and `heads` heads; the angles of its positions
-// stay in registers from head to head, and a head's values are loaded while the one before
-// is worked on.
-// kBig: pages that get at most kFew tokens are paged_append_few_kernel's.
+// The pages of a row that this kernel writes: `n` of them from the row's page `first` on.
+// kBig: pages that get at most kFew tokens are paged_append_few_kernel's (those between a
+// row's first and last are full).
+struct RowPages {
+  int first, n;
+};
+template <bool kBig, int kFew>
+__device__ __forceinline__ RowPages row_pages(const PagedView& c, int b, bool* bad) {
+  const PagedRow r = paged_row(c, b, bad);
+  const int start = max(r.len - r.n, 0);
+  RowPages w = {0, 0};
+  if (*bad || r.n == 0 || r.len <= start) return w;
+  const int p0 = start >> c.p_shift, p1 = (r.len - 1) >> c.p_shift;
+  w.n = p1 - p0 + 1;
+  if constexpr (kBig) {
+    if (min(r.len, (p0 + 1) << c.p_shift) - start <= kFew) {
+      w.first = 1;
+      --w.n;
+    }
+    if (p1 > p0 && r.len - (p1 << c.p_shift) <= kFew) --w.n;
+  }
+  return w;
+}
+
+// a / b, b > 0; a is nearly always small enough for the short division.
+__device__ __forceinline__ long long quotient(long long a, unsigned b) {
+  return a >> 32 ? a / b : (unsigned)a / b;
+}
+
+// Any number of tokens.  All pages in order, `streams` heads each, form one line that is cut
+// into equal runs, one for each block that is resident: no last wave with few blocks, and
+// no block for a page that a row might have had (blocks of 8 heads of each such page, found
+// by searching the offsets: 256 rows of 8 tokens 36.6 us, so 30.5; 16 of 32: 10.8 and 9.0;
+// long prompts alike).  In a page a block goes from head to head:
+// the angles of its positions stay in registers, and a head's values are loaded while the
+// one before is worked on.
 template <bool kF8, int kD, bool kBig>
 __global__ void __launch_bounds__(kF8 ? 512 : 1024)
 paged_append_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
   constexpr int kPasses = append_passes<kF8>, kFew = 512 / kD;
   const PagedView& c = p.c;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int streams = p.Hq + 2 * c.Hkv;
   __shared__ float s_max[2][32];
+  __shared__ long long s_sum[32], s_off;
+  __shared__ int s_row;
   paged_wait_before();
-  // a unit's blocks follow one another: their heads' rows are neighbours in memory
-  const int unit = blockIdx.x / p.groups, group = blockIdx.x - unit * p.groups;
-  int b, j;
-  if (c.cu == nullptr) {
-    b = unit / p.units_per_row;
-    j = unit - b * p.units_per_row;
-  } else {
-    // Row b owns units from floor(cu[b] / P) + 2 b on: n tokens touch at most
-    // floor(n / P) + 2 pages, and floor is superadditive, so rows never overlap.  The row
-    // is the last one that begins at or before this unit: 32 probes a round.
-    const int lane = tid & 31;
-    // kBig: at most floor(n / (kFew + 1)) of a row's pages are this kernel's.
-    auto begin_of = [&](int i) {
-      const int t = min(max(c.cu[i], 0), c.N);
-      return kBig ? t / (kFew + 1) : (t >> c.p_shift) + 2 * i;
-    };
-    b = 0;
-    for (int range = c.B; range > 1;) {
-      const int step = (range + 31) / 32, i = b + lane * step;
-      const unsigned before = __ballot_sync(0xffffffffu, lane * step < range && begin_of(min(i, c.B - 1)) <= unit);
-      const int hit = before ? 31 - __clz(before) : 0;
-      b += hit * step;
-      range = min(step, range - hit * step);
+
+  // ---- this block's run of the line, and the row it begins in
+  const int chunk = (c.B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(tid * chunk, c.B), b1 = min(b0 + chunk, c.B);
+  long long sum = 0;
+  bool wrong = false;
+  for (int b = b0; b < b1; ++b) {
+    bool x;
+    sum += row_pages<kBig, kFew>(c, b, &x).n;
+    wrong |= x;
+  }
+  if (wrong && blockIdx.x == 0) atomicOr(&g_err_append, (unsigned)kDevErrInput);
+  long long pre = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, pre, d);
+    if (lane >= d) pre += x;
+  }
+  if (lane == 31) s_sum[warp] = pre;
+  __syncthreads();
+  long long total = 0;
+  for (int i = 0; i < warps; ++i) {
+    if (i == warp) pre += total;
+    total += s_sum[i];
+  }
+  pre -= sum;  // pages before this thread's rows
+  const long long per = quotient(total * streams + gridDim.x - 1, gridDim.x);
+  long long cur = blockIdx.x * per;
+  const long long end = min(cur + per, total * streams);
+  if (cur >= end) return;
+  int b = b0;
+  long long at = cur - pre * streams;  // of the row's part of the line
+  if (at >= 0 && at < sum * streams) {
+    for (; b + 1 < b1; ++b) {
+      bool x;
+      const long long n = (long long)row_pages<kBig, kFew>(c, b, &x).n * streams;
+      if (at < n) break;
+      at -= n;
     }
-    j = unit - begin_of(b);
-    if (j < 0) return;  // offsets that decrease
+    s_row = b;
+    s_off = at;
   }
-  Unit u = unit_of(c, b, kBig ? 0 : j, tid == 0 && group == 0);
-  if constexpr (kBig) {
-    if (u.m <= 0) return;
-    const bool small = u.m <= kFew;  // the first page; those up to the last are full
-    if (small || j > 0) u = unit_of(c, b, j + small, false);
-    if (u.m <= kFew) return;
-  }
-  if (u.m <= 0) return;
+  __syncthreads();
+  b = s_row;
+  at = s_off;
+
   const int rows = blockDim.x / kRowThreads;
   const int rt = tid % kRowThreads, slot = tid / kRowThreads;
-  const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
-  const int s_end = min((group + 1) * p.heads, p.Hq + 2 * c.Hkv);
-  int s = group * p.heads;
-  const int page = s_end > p.Hq ? page_of(c, u, tid == 0) : 0;
-  if (page < 0) return;
-
-  bool mine[kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) mine[i] = i * rows + slot < u.m;
-  const bool turns = rt < p.rot / 16;
-  float cs[kPasses][8], sn[kPasses][8];
-  if (turns && s < p.Hq + c.Hkv) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (mine[i]) load_angles(p, u.p0 + i * rows + slot, rt, cs[i], sn[i]);
-  }
-  uint4 next[kPasses][2];
-  auto fetch = [&](int stream) {
-    const Stream t = stream_of<kD>(p, stream);
-    int c0, c1;
-    chunks_of(rt, t.is_q || t.is_k ? p.rot : 0, p.interleaved, c0, c1);
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (mine[i]) {
-        const __nv_bfloat16* src = t.src + (long long)(u.first + i * rows + slot) * t.tok;
-        next[i][0] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c0));
-        next[i][1] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c1));
+  while (cur < end) {
+    bool bad;
+    const RowPages w = row_pages<kBig, kFew>(c, b, &bad);
+    if (at >= (long long)w.n * streams) {
+      // on to the next row with a page, 32 looked at together
+      at = 0;
+      unsigned some = 0;
+      int i = b + 1;
+      for (; i < c.B; i += 32) {
+        some = __ballot_sync(0xffffffffu, i + lane < c.B && row_pages<kBig, kFew>(c, min(i + lane, c.B - 1), &bad).n > 0);
+        if (some) break;
       }
-  };
-  fetch(s);
-  for (; s < s_end; ++s) {
-    const Stream t = stream_of<kD>(p, s);
-    const int rot = t.is_q || t.is_k ? p.rot : 0;
-    int c0, c1;
-    chunks_of(rt, rot, p.interleaved, c0, c1);
-    float x[kPasses][16];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      unpack8(next[i][0], x[i]);
-      unpack8(next[i][1], x[i] + 8);
+      if (some == 0) return;  // only if lengths change under the call
+      b = i + __ffs(some) - 1;
+      continue;
     }
-    if (s + 1 < s_end) fetch(s + 1);
-    float amax = 0.f;
+    const int j = (int)quotient(at, streams), s0 = (int)(at - (long long)j * streams);
+    const int s_end = (int)min((long long)streams, s0 + (end - cur));
+    cur += s_end - s0;
+    at += s_end - s0;
+    const Unit u = unit_of(c, b, w.first + j, false);
+    const int P = 1 << c.p_shift, off = u.p0 & (P - 1);
+    const int page = s_end > p.Hq ? page_of(c, u, tid == 0) : 0;
+    if (page < 0) continue;
+
+    bool mine[kPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (mine[i]) {
-        if (rt < rot / 16) rotate16(x[i], cs[i], sn[i], p.interleaved);
-        if (kF8 && !t.is_q) amax = finite_max(x[i], amax);
-      }
-    uint8_t* tile = (t.is_k ? c.k : c.v) + page * c.page_bytes + (long long)t.h * P * (kD * (kF8 ? 1 : 2));
-    if (t.is_q || !kF8) {
+    for (int i = 0; i < kPasses; ++i) mine[i] = i * rows + slot < u.m;
+    const bool turns = rt < p.rot / 16;
+    float cs[kPasses][8], sn[kPasses][8];
+    if (turns && s0 < p.Hq + c.Hkv) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        if (mine[i]) load_angles(p, u.p0 + i * rows + slot, rt, cs[i], sn[i]);
+    }
+    uint4 next[kPasses][2];
+    auto fetch = [&](int stream) {
+      const Stream t = stream_of<kD>(p, stream);
+      int c0, c1;
+      chunks_of(rt, t.is_q || t.is_k ? p.rot : 0, p.interleaved, c0, c1);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
         if (mine[i]) {
-          const int row = i * rows + slot;
-          __nv_bfloat16* o = t.is_q ? p.q_out + (long long)(u.first + row) * p.qo_tok + (long long)t.h * kD
-                                    : reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
-          store8(o + 8 * c0, x[i]);
-          store8(o + 8 * c1, x[i] + 8);
+          const __nv_bfloat16* src = t.src + (long long)(u.first + i * rows + slot) * t.tok;
+          next[i][0] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c0));
+          next[i][1] = __ldg(reinterpret_cast<const uint4*>(src + 8 * c1));
         }
-      continue;
-    }
-    float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
-    const float old = off > 0 ? *scale_at : 0.f;
+    };
+    fetch(s0);
+    for (int s = s0; s < s_end; ++s) {
+      const Stream t = stream_of<kD>(p, s);
+      const int rot = t.is_q || t.is_k ? p.rot : 0;
+      int c0, c1;
+      chunks_of(rt, rot, p.interleaved, c0, c1);
+      float x[kPasses][16];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    float* most = s_max[s & 1];  // two in turn: a head's readers are behind the next barrier
-    if ((tid & 31) == 0) most[tid >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, most[w]);
-    const float need = pow2_scale(amax);
-    const float scale = need > old ? need : old;
-    const float inv = __frcp_rn(scale);
-    if (scale != old) {
-      if (tid == 0) *scale_at = scale;  // every thread has read the old one
-      for (int i = slot; i < off; i += rows) {
-        uint4* at = reinterpret_cast<uint4*>(tile + i * kD + 16 * rt);
-        *at = rescaled16(*at, old, inv);
+      for (int i = 0; i < kPasses; ++i) {
+        unpack8(next[i][0], x[i]);
+        unpack8(next[i][1], x[i] + 8);
       }
-    }
+      if (s + 1 < s_end) fetch(s + 1);
+      float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (mine[i]) store_codes(tile + (off + i * rows + slot) * kD, c0, c1, x[i], inv);
+      for (int i = 0; i < kPasses; ++i)
+        if (mine[i]) {
+          if (rt < rot / 16) rotate16(x[i], cs[i], sn[i], p.interleaved);
+          if (kF8 && !t.is_q) amax = finite_max(x[i], amax);
+        }
+      uint8_t* tile = (t.is_k ? c.k : c.v) + page * c.page_bytes + (long long)t.h * P * (kD * (kF8 ? 1 : 2));
+      if (t.is_q || !kF8) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          if (mine[i]) {
+            const int row = i * rows + slot;
+            __nv_bfloat16* o = t.is_q ? p.q_out + (long long)(u.first + row) * p.qo_tok + (long long)t.h * kD
+                                      : reinterpret_cast<__nv_bfloat16*>(tile) + (off + row) * kD;
+            store8(o + 8 * c0, x[i]);
+            store8(o + 8 * c1, x[i] + 8);
+          }
+        continue;
+      }
+      float* scale_at = (t.is_k ? c.ks : c.vs) + (long long)page * c.Hkv + t.h;
+      const float old = off > 0 ? *scale_at : 0.f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      float* most = s_max[s & 1];  // two in turn: a head's readers are behind the next barrier
+      if ((tid & 31) == 0) most[tid >> 5] = amax;
+      __syncthreads();
+      for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, most[w]);
+      const float need = pow2_scale(amax);
+      const float scale = need > old ? need : old;
+      const float inv = __frcp_rn(scale);
+      if (scale != old) {
+        if (tid == 0) *scale_at = scale;  // every thread has read the old one
+        for (int i = slot; i < off; i += rows) {
+          uint4* at = reinterpret_cast<uint4*>(tile + i * kD + 16 * rt);
+          *at = rescaled16(*at, old, inv);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        if (mine[i]) store_codes(tile + (off + i * rows + slot) * kD, c0, c1, x[i], inv);
+    }
   }
 }
 
@@ -448,8 +513,8 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const bool few = c.cu == nullptr && c.Qn <= kFew;
   // Token counts only the device knows: pages with few tokens go to the kernel that is made
   // for them when the average row has few.  Rows of n tokens each, e4m3 D = 128 (kFew = 4),
-  // 48 heads, us with one kernel / with two: 256 rows n = 1: 36.4 / 8.7, 4: 35.9 / 13.9,
-  // 8: 37.1 / 39.6, 16: 47.4 / 58.7; 16 rows n = 1: 7.8 / 4.3, 8: 8.0 / 9.0.
+  // 48 heads, us with one kernel / with two: 256 rows n = 1: 30.2 / 5.3, 4: 29.4 / 10.6,
+  // 8: 30.5 / 34.1, 16: 39.5 / 43.1; 16 rows n = 1: 5.5 / 4.7, 8: 5.6 / 7.2.
   const bool two = c.cu != nullptr && c.N <= (long long)kFew * c.B;
   if (few || two) {
     // a warp takes as many heads as it has threads for, going by the tokens of the average row
@@ -460,13 +525,10 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
                                            : paged_launch(paged_append_few_kernel<kF8, kD, false>, grid, 128, 0, st, p);
     if (e != cudaSuccess || few || c.N <= kFew) return e;
   }
-  long long units = c.cu == nullptr ? (long long)c.B * p.units_per_row : ((long long)c.N >> c.p_shift) + 2LL * c.B;
-  if (two) units = c.N / (kFew + 1);
-  // up to 8 heads a block, as long as there are blocks enough to fill the GPU
-  p.heads = (int)std::max(1LL, std::min(8LL, units * streams / (152 * 8)));
-  p.groups = (streams + p.heads - 1) / p.heads;
-  const dim3 grid((unsigned)(units * p.groups));
+  // blocks that are resident together: two of 256 threads on an SM (e4m3, 122 registers),
+  // or 1024 threads (bf16)
   const int threads = (kD << c.p_shift) / (16 * append_passes<kF8>);
+  const dim3 grid(152 * ((kF8 ? 512 : 1024) / threads));
   return two ? paged_launch(paged_append_kernel<kF8, kD, true>, grid, threads, 0, st, p)
              : paged_launch(paged_append_kernel<kF8, kD, false>, grid, threads, 0, st, p);
 }
@@ -500,8 +562,6 @@ int launch_paged_append(const PagedView& c, int f8, int D, const void* k, long l
   p.rot = cosp ? rot : 0;
   p.interleaved = interleaved;
   p.max_pos = max_pos;
-  // n tokens in a row lie in at most floor((n - 2) / P) + 2 pages (n >= 2), one for n = 1
-  p.units_per_row = c.Qn <= 1 ? 1 : ((c.Qn - 2) >> c.p_shift) + 2;
   cudaError_t e;
   if (D == 128)
     e = f8 ? launch_append<true, 128>(p, stream) : launch_append<false, 128>(p, stream);

@@ -88,8 +88,7 @@ def test_cache_arguments(lib, change, code, text):
     (dict(rot=0), -1), (dict(max_pos=0), -1), (dict(sin=FAKE + 4), -1), (dict(Hq=0), -1), (dict(Hq=1 << 17, qs=1 << 24, qos=1 << 24), -2),
     (dict(qs=2048), -1), (dict(qo=0x30000), -1), (dict(qo=0x40000), -1), (dict(v_pages=FAKE), -1),
     (dict(v_pages=FAKE + 2 * 64 * 128), -1), (dict(v_pages=FAKE + 64, page_stride=4 * 64 * 128), -1),
-    (dict(v_pages=FAKE + 3 * 64 * 128, page_stride=4 * 64 * 128), -1),
-    (dict(cu=FAKE, B=1 << 24, N=1 << 28, Hkv=2000, page_stride=2000 * 64 * 128, v_pages=1 << 40, ks=256000, vs=256000), -2)])
+    (dict(v_pages=FAKE + 3 * 64 * 128, page_stride=4 * 64 * 128), -1)])
 def test_append_arguments(lib, change, code):
     assert append(lib, **change) == code
 
