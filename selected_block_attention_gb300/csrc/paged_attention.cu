@@ -215,7 +215,7 @@ paged_attention_kernel(const PagedAttnParams p) {
     if (t0 >= pre && t0 < pre + sum) {
       long long off = t0 - pre;
       int b = b0;
-      for (;; ++b) {
+      for (; b + 1 < b1; ++b) {  // (bounded, should the lengths change under the call)
         bool x;
         const RowTiles t = row_tiles<kKeys>(p, b, &x);
         const long long n = (long long)(t.tiles + kItemCost) * t.groups * p.c.Hkv;
@@ -249,7 +249,7 @@ paged_attention_kernel(const PagedAttnParams p) {
     const long long row_total = (long long)units * rt.groups * p.c.Hkv;
     if (off >= row_total) {
       off -= row_total;
-      ++b;
+      if (++b >= p.c.B) return;
       continue;
     }
     const int item = (int)(off / units);
@@ -310,7 +310,8 @@ paged_attention_kernel(const PagedAttnParams p) {
       }
     }
     if (begins && !whole && tid == 0) {
-      const int last = (int)((s_it.item_at + s_it.units - 1) / run_length());  // the CTA that ends the item
+      // the CTA that ends the item
+      const int last = (int)min((s_it.item_at + s_it.units - 1) / run_length(), (long long)kCtas - 1);
       SplitItem it;
       it.n = last - cta + 1;
       it.n_rows = rows;

@@ -139,7 +139,10 @@ struct Walker {
         g = 0;
         if (groups == 0 || ++h == p.c.Hkv) {
           h = 0;
-          ++b;
+          if (++b >= p.c.B) {  // only if lengths change under the call
+            cur = end;
+            return false;
+          }
           row(p);
         }
       }
@@ -163,7 +166,7 @@ struct Walker {
       s.nt = max(min(t.ka + s1, t.kb) - s.t0, 0);
       s.begins = s0 == 0;
       s.whole = s.begins && x1 == t.units;
-      s.n = (int)((at + t.units - 1) / per) - cta + 1;
+      s.n = (int)min((at + t.units - 1) / per, (long long)kCtas - 1) - cta + 1;
       s.lo = win_lo(p, r, 0);
       s.end = 0;
       return true;
@@ -279,6 +282,7 @@ paged_chunk_kernel(const ChunkParams p) {
     }
     if (any_bad && cta == 0) atomicOr(&g_err_chunk.flags, (unsigned)kDevErrInput);
     if (lane == 0) s_sum[warp] = sum;
+    if (tid == 0) s_b = s_h = s_g = s_off = 0;
     __syncthreads();
     long long total = 0, pre = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
@@ -295,12 +299,12 @@ paged_chunk_kernel(const ChunkParams p) {
         bool bad;
         r = paged_row(p.c, b, &bad);
         one = row_sum(r);
-        if (off < one * p.c.Hkv) break;
+        if (off < one * p.c.Hkv || b + 1 >= b1) break;
         off -= one * p.c.Hkv;
       }
-      const int h = (int)(off / one);
+      const int h = one > 0 ? (int)min(off / one, (long long)p.c.Hkv - 1) : 0;
       off -= h * one;
-      for (int g0 = 0;; g0 += 32) {  // the group: 32 at a time
+      for (int g0 = 0; g0 < groups_of(p, r); g0 += 32) {  // the group: 32 at a time
         const int g = g0 + lane, u = g < groups_of(p, r) ? group_tiles(p, r, g).units : 0;
         int end = u;
 #pragma unroll
