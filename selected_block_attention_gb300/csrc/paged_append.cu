@@ -334,12 +334,12 @@ __device__ __forceinline__ long long quotient(long long a, unsigned b) {
 
 // Any number of tokens.  All pages in order, `streams` heads each, form one line that is cut
 // into equal runs, one for each block that is resident: no last wave with few blocks, and
-// no block for a page that a row might have had (blocks of 8 heads of each such page, found
-// by searching the offsets: 256 rows of 8 tokens 36.6 us, so 30.5; 16 of 32: 10.8 and 9.0;
-// long prompts alike).  In a page a block goes from head to head:
+// (few rows) no place for a page that a row might have had: blocks of 8 heads of each such
+// page take 36.6 us for 256 rows of 8 tokens, 10.8 for 16 of 32, this one 30.5 and 9.0; long
+// prompts alike.  In a page a block goes from head to head:
 // the angles of its positions stay in registers, and a head's values are loaded while the
 // one before is worked on.
-template <bool kF8, int kD, bool kBig>
+template <bool kF8, int kD, bool kBig, bool kCounted>
 __global__ void __launch_bounds__(kF8 ? 512 : 1024)
 paged_append_kernel(const AppendParams p) {
   constexpr int kRowThreads = kD / 16;
@@ -352,50 +352,88 @@ paged_append_kernel(const AppendParams p) {
   __shared__ int s_row;
   paged_wait_before();
 
-  // ---- this block's run of the line, and the row it begins in
-  const int chunk = (c.B + blockDim.x - 1) / blockDim.x;
-  const int b0 = min(tid * chunk, c.B), b1 = min(b0 + chunk, c.B);
-  long long sum = 0;
-  bool wrong = false;
-  for (int b = b0; b < b1; ++b) {
-    bool x;
-    sum += row_pages<kBig, kFew>(c, b, &x).n;
-    wrong |= x;
-  }
-  if (wrong && blockIdx.x == 0) atomicOr(&g_err_append, (unsigned)kDevErrInput);
-  long long pre = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, pre, d);
-    if (lane >= d) pre += x;
-  }
-  if (lane == 31) s_sum[warp] = pre;
-  __syncthreads();
-  long long total = 0;
-  for (int i = 0; i < warps; ++i) {
-    if (i == warp) pre += total;
-    total += s_sum[i];
-  }
-  pre -= sum;  // pages before this thread's rows
-  const long long per = quotient(total * streams + gridDim.x - 1, gridDim.x);
-  long long cur = blockIdx.x * per;
-  const long long end = min(cur + per, total * streams);
-  if (cur >= end) return;
-  int b = b0;
-  long long at = cur - pre * streams;  // of the row's part of the line
-  if (at >= 0 && at < sum * streams) {
-    for (; b + 1 < b1; ++b) {
+  // ---- this block's run of the line, and the row it begins in.  Few rows are counted; many
+  // get the most pages that they could have: n tokens touch at most floor(n / P) + 2 (kBig:
+  // fill floor(n / (kFew + 1))), and floor is superadditive, so that the row's part begins at
+  // begin_of(row) and parts never overlap.
+  auto begin_of = [&](int i) -> long long {
+    if (c.cu == nullptr) return (long long)i * (((c.Qn - 1) >> c.p_shift) + 2);
+    const int t = min(max(c.cu[i], 0), c.N);
+    return kBig ? t / (kFew + 1) : (t >> c.p_shift) + 2LL * i;
+  };
+  long long cur, end, at;  // at: of the row's part of the line
+  int b;
+  if constexpr (kCounted) {
+    const int chunk = (c.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(tid * chunk, c.B), b1 = min(b0 + chunk, c.B);
+    long long sum = 0;
+    bool wrong = false;
+    for (b = b0; b < b1; ++b) {
       bool x;
-      const long long n = (long long)row_pages<kBig, kFew>(c, b, &x).n * streams;
-      if (at < n) break;
-      at -= n;
+      sum += row_pages<kBig, kFew>(c, b, &x).n;
+      wrong |= x;
     }
-    s_row = b;
-    s_off = at;
+    if (wrong && blockIdx.x == 0) atomicOr(&g_err_append, (unsigned)kDevErrInput);
+    long long pre = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, pre, d);
+      if (lane >= d) pre += x;
+    }
+    if (lane == 31) s_sum[warp] = pre;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < warps; ++i) {
+      if (i == warp) pre += total;
+      total += s_sum[i];
+    }
+    pre -= sum;  // pages before this thread's rows
+    const long long per = quotient(total * streams + gridDim.x - 1, gridDim.x);
+    cur = blockIdx.x * per;
+    end = min(cur + per, total * streams);
+    if (cur >= end) return;
+    b = b0;
+    at = cur - pre * streams;
+    if (at >= 0 && at < sum * streams) {
+      for (; b + 1 < b1; ++b) {
+        bool x;
+        const long long n = (long long)row_pages<kBig, kFew>(c, b, &x).n * streams;
+        if (at < n) break;
+        at -= n;
+      }
+      s_row = b;
+      s_off = at;
+    }
+    __syncthreads();
+    b = s_row;
+    at = s_off;
+  } else {
+    for (int i = blockIdx.x * blockDim.x + tid; i < c.B; i += gridDim.x * blockDim.x) {
+      bool wrong;
+      paged_row(c, i, &wrong);
+      if (wrong) atomicOr(&g_err_append, (unsigned)kDevErrInput);
+    }
+    const long long total = c.cu == nullptr ? begin_of(c.B) : kBig ? c.N / (kFew + 1) : (c.N >> c.p_shift) + 2LL * c.B;
+    const long long per = quotient(total * streams + gridDim.x - 1, gridDim.x);
+    cur = blockIdx.x * per;
+    end = min(cur + per, total * streams);
+    if (cur >= end) return;
+    // the last row that begins at or before this place: 32 probes a round
+    const long long unit = quotient(cur, streams);
+    b = 0;
+    for (int range = c.B; range > 1;) {
+      const int step = (range + 31) / 32, i = b + lane * step;
+      const unsigned before = __ballot_sync(0xffffffffu, lane * step < range && begin_of(min(i, c.B - 1)) <= unit);
+      const int hit = before ? 31 - __clz(before) : 0;
+      b += hit * step;
+      range = min(step, range - hit * step);
+    }
+    at = cur - begin_of(b) * streams;
+    if (at < 0) {  // ahead of the first row's first token
+      cur -= at;
+      at = 0;
+    }
   }
-  __syncthreads();
-  b = s_row;
-  at = s_off;
 
   const int rows = blockDim.x / kRowThreads;
   const int rt = tid % kRowThreads, slot = tid / kRowThreads;
@@ -409,10 +447,11 @@ paged_append_kernel(const AppendParams p) {
       int i = b + 1;
       for (; i < c.B; i += 32) {
         some = __ballot_sync(0xffffffffu, i + lane < c.B && row_pages<kBig, kFew>(c, min(i + lane, c.B - 1), &bad).n > 0);
-        if (some) break;
+        if (some || (!kCounted && begin_of(i) * streams >= end)) break;
       }
-      if (some == 0) return;  // only if lengths change under the call
+      if (some == 0) return;
       b = i + __ffs(some) - 1;
+      if constexpr (!kCounted) cur = max(cur, begin_of(b) * streams);
       continue;
     }
     const int j = (int)quotient(at, streams), s0 = (int)(at - (long long)j * streams);
@@ -529,8 +568,12 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   // or 1024 threads (bf16)
   const int threads = (kD << c.p_shift) / (16 * append_passes<kF8>);
   const dim3 grid(152 * ((kF8 ? 512 : 1024) / threads));
-  return two ? paged_launch(paged_append_kernel<kF8, kD, true>, grid, threads, 0, st, p)
-             : paged_launch(paged_append_kernel<kF8, kD, false>, grid, threads, 0, st, p);
+  // Counting takes each block a pass over the rows: 4096 rows of one token, D = 64, pages of 16
+  // (32 threads) 82 us, where the search takes 19.8; 1000 rows, D = 128 (64 threads) 14.3 / 11.3.
+  const bool counted = c.B <= 4 * threads;
+  auto* kernel = two ? (counted ? paged_append_kernel<kF8, kD, true, true> : paged_append_kernel<kF8, kD, true, false>)
+                     : (counted ? paged_append_kernel<kF8, kD, false, true> : paged_append_kernel<kF8, kD, false, false>);
+  return paged_launch(kernel, grid, threads, 0, st, p);
 }
 
 }  // namespace

@@ -589,18 +589,51 @@ def test_append_many_ragged_rows(sba, B):
 
 
 @pytest.mark.parametrize("f8", [True, False])
-@pytest.mark.parametrize("D,P", [(128, 16), (128, 64), (64, 32)])
-def test_append_long_rows_among_short(sba, f8, D, P):
+@pytest.mark.parametrize("D,P,B", [(128, 16, 150), (128, 64, 150), (64, 32, 150), (64, 16, 600), (128, 16, 600)])
+def test_append_long_rows_among_short(sba, f8, D, P, B):
     """Few tokens on average: pages with few and with many, first, last and in between, are
     different kernels' work; rows without tokens and rows shorter than theirs."""
     rng = np.random.default_rng(D + P)
-    n = rng.integers(0, 3, 150)
-    n[[3, 40, 77, 120, 149]] = 512 // D + 1, 2 * P, P + 1, 3 * P - 1, 37
+    n = rng.integers(0, 3, B)
+    n[[3, 40, 77, 120, B - 1]] = 512 // D + 1, 2 * P, P + 1, 3 * P - 1, 37
     n[60:70] = np.arange(10)
-    lens = rng.integers(0, 40, 150) + n
+    lens = rng.integers(0, 40, B) + n
     lens[[9, 120, 65]] = 0, P + 2, 1
     c = Cache(lens, 2, D, P, f8, 736 + P)
     check_append(sba, c, n, 3, D, False, 49)
+
+
+@pytest.mark.parametrize("f8", [True, False])
+@pytest.mark.parametrize("fixed", [None, 11])
+def test_append_many_rows_of_several_tokens(sba, f8, fixed):
+    """More rows than a block counts, more tokens than the kernel for few takes."""
+    rng = np.random.default_rng(31)
+    n = np.full(300, fixed) if fixed else rng.integers(0, 30, 300)
+    c = Cache(rng.integers(0, 40, 300) + n, 1, 64, 16, f8, 745)
+    check_append(sba, c, n, 1, 64, False, 50, fixed=fixed)
+
+
+@pytest.mark.parametrize("n", [[1, 2, 0, 3], [40, 2, 0, 33], [1] * 200 + [50], [9] * 300])
+def test_token_rows_ahead_of_the_first_sequence(sba, n):
+    """Offsets that begin past 0: the token rows before belong to nobody either."""
+    rng = np.random.default_rng(len(n))
+    lens = rng.integers(0, 40, len(n)) + np.array(n)
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).to(DEV)
+    res = []
+    for ahead in (0, 70):
+        c = Cache(lens, 2, 64, 16, True, 746)
+        kv, q = c.q((sum(n), 2, 64), 51), c.q((sum(n), 8, 64), 52)
+        pad = lambda t: torch.cat([torch.full((ahead, *t.shape[1:]), 7.0, dtype=t.dtype, device=DEV), t])
+        sba.paged_kv_append(pad(kv), pad(kv), *c.pool(), **c.kw(), cu_seqlens=cu + ahead)
+        out, lse = (torch.full((ahead + sum(n), 8, *d), 5.0, dtype=t, device=DEV) for d, t in (((64,), torch.bfloat16), ((), torch.float32)))
+        sba.paged_attention_fwd(pad(q), *c.pool(), **c.kw(), cu_seqlens=cu + ahead, window_right=0, out=out, lse=lse)
+        sba.check_error()
+        assert (out[:ahead] == 5).all() and (lse[:ahead] == 5).all()
+        # the token count may choose another kernel, so its results are held to the oracle's
+        ref, rl, mag = oracle.paged_attention(np64(q), c.host(), c.table.cpu().numpy(), lens, cu.cpu().numpy(), window_right=0)
+        close(out[ahead:], lse[ahead:], ref, rl, mag, True, f"ahead {ahead}")
+        res.append((c.k.view(torch.uint8), c.v.view(torch.uint8), c.ks[c.own.any(1)]))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
 @pytest.mark.parametrize("size", [1e-3, 40.0, 1e30])
