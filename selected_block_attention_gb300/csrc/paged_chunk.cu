@@ -14,7 +14,8 @@
 //   warps 4, 5   MMA issuers, one for each half w: S_w = Q_w K^T into one of two buffers,
 //                O_w += P_w V with P_w in tensor memory over the S it came from, in the
 //                order S(0) S(1) | PV(t) S(t + 2) | ...
-//   warp 6       scheduler: finds the run's items and publishes them (warp 7 idle)
+//   warp 6       scheduler: finds the run's items and publishes them; items whose queries
+//                see no key it writes itself (warp 7 idle)
 //   warps 8..15  softmax, four for each half, one thread per row: it brings its query row
 //                in (e4m3: times a power of two into fp16, see paged_core.cuh), takes its
 //                64 scores out of tensor memory, keeps (m, l, u) as described there,
@@ -111,7 +112,8 @@ __device__ __forceinline__ long long row_units(const ChunkParams& p, const Paged
   return s;  // of one KV head
 }
 
-// One item's part of the CTA's run, as the scheduler publishes it.
+// One item's part of the CTA's run, as the scheduler publishes it: one key tile at least (an
+// item without any is whole, and the scheduler's own).
 struct Segment {
   PagedRow r;
   int b, h, g, rows;   // rows of the group
@@ -122,7 +124,12 @@ struct Segment {
   int end;             // no more items
 };
 constexpr int kMetas = 8;  // tiles whose scales are kept
-constexpr int kSegs = 4;  // slots; each is read by 4 loader, 2 MMA and 8 softmax warps
+// Slots; each is read by 4 loader, 2 MMA and 8 softmax warps.  A loader looks two tiles ahead
+// of the one that it has not delivered yet, and that one keeps its segment's slot from coming
+// round.  Every segment has a tile, so what it looks at is two slots ahead at most: three slots
+// would do; with fewer, or with segments without tiles, it would wait for itself.
+constexpr int kSegs = 4;
+static_assert(kSegs >= 3, "a loader's look-ahead");
 // Walks the run.
 struct Walker {
   long long cur, end, per;
@@ -592,7 +599,6 @@ paged_chunk_kernel(const ChunkParams p) {
         if (last) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[slot]);
-        if (nt == 0) continue;
         if (rows <= w * kM) {
           // no row in this half: release the stages so the rings stay in step
           for (int t = 0; t < nt && ok; ++t) {
@@ -649,10 +655,25 @@ paged_chunk_kernel(const ChunkParams p) {
         walk.off = s_off;
         walk.row(p);
       }
+      // output 0 and LSE -inf of an item whose queries see no key
+      auto write_empty = [&](const Segment& s) {
+        constexpr int kCh = D / 8;
+#pragma unroll 1  // unrolled it spills (64 registers)
+        for (int x = lane; x < s.rows * kCh; x += 32) {
+          const int row = x / kCh, rr = s.g * kRows + row, qi = rr / p.G;
+          const long long orow = (long long)(s.r.t0 + qi) * p.Hq + s.h * p.G + (rr - qi * p.G);
+          *reinterpret_cast<uint4*>(p.out + orow * D + x % kCh * 8) = make_uint4(0u, 0u, 0u, 0u);
+          if (x % kCh == 0 && p.lse != nullptr) p.lse[orow] = -INFINITY;
+        }
+      };
       int slot = 0; uint32_t phase = 0;
       while (true) {
         Segment sg;
         sg.end = walk.next(p, cta, sg) ? 0 : 1;
+        if (!sg.end && sg.nt == 0) {
+          write_empty(sg);
+          continue;
+        }
         if (!warp_wait(&seg_empty[slot], phase ^ 1, ab, kRoleScheduler, kBarSegEmpty, cta)) break;
         if (lane == 0) {
           seg_at(slot) = sg;
@@ -692,7 +713,7 @@ paged_chunk_kernel(const ChunkParams p) {
       const int full_lo = win_lo(p, sg.r, ib), full_end = win_end(p, sg.r, ia);
       float m = -INFINITY, l = 0.f, u = -INFINITY;
       bool ok = true;
-      if (active && nt > 0) {
+      if (active) {
         // ---- the query row, into the swizzle that the MMA reads
         float f = kCap ? p.scale / p.cap : p.scale * kPagedLog2e;
         const __nv_bfloat16* src = p.q + (long long)(sg.r.t0 + qi) * p.q_tok + (long long)hq * D;
@@ -851,7 +872,7 @@ paged_chunk_kernel(const ChunkParams p) {
 
       // ---- the row's result, or its partial
       const float ref = kF8 ? u - 8.f : m;  // o stands for o 2^ref
-      const bool some = active && nt > 0 && l != 0.f;
+      const bool some = active && l != 0.f;
       const int part = cta * 2 + (sg.begins ? 1 : 0);
       if (sg.begins && !sg.whole && warp == 8 && lane == 0) {
         SplitChunk s;
@@ -879,16 +900,14 @@ paged_chunk_kernel(const ChunkParams p) {
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         float ov[32];
-        if (nt > 0) {
-          tmem_ld_32x32b_x32_nw(o_col + c * 32, ov);
-          tmem_wait_ld();
+        tmem_ld_32x32b_x32_nw(o_col + c * 32, ov);
+        tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) tmem_ld_ready(ov[j]);
-          if (c == D / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[w]);
-          }
+        for (int j = 0; j < 32; ++j) tmem_ld_ready(ov[j]);
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_empty[w]);
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j) ov[j] = some ? ov[j] * factor : 0.f;
