@@ -103,7 +103,7 @@ struct Group {
   int n_rows;
   int count, key_first;  // tile t < count is the keys from key_first + t kKeys on ...
   bool with_sink;        // ... but for tile 0, which is the sinks'
-  int cl, ch;            // keys that may be read; of the sinks' tile, 0 .. sink_ch
+  int cl, ch;            // keys that may be read, besides sinks; of the sinks' tile, 0 .. sink_ch
   int sink_ch;
   template <int kKeys>
   __device__ __forceinline__ int key_of(int t) const {
@@ -156,7 +156,7 @@ __device__ __forceinline__ Group<kD> group_of(const PagedAttnParams& p, const Ro
   const int wa = max(max(s0 - rt.sink, ka), 0), wb = min(s1 - rt.sink, kb);
   gr.count = rt.r.len > 0 ? (gr.with_sink ? 1 : 0) + max(wb - wa, 0) : 0;
   gr.key_first = rt.base + (wa - (gr.with_sink ? 1 : 0)) * kKeys;
-  gr.cl = sinks_at_base ? 0 : rt.lo;
+  gr.cl = rt.lo;
   gr.ch = rt.r.len - 1;
   gr.sink_ch = min(p.num_sinks, rt.r.len) - 1;
   gr.q0 = ok0 ? p.q + (rt.r.t0 + i0) * p.q_tok + (long long)h0 * kD : nullptr;
@@ -164,10 +164,10 @@ __device__ __forceinline__ Group<kD> group_of(const PagedAttnParams& p, const Ro
   return gr;
 }
 
-template <bool kF8, int kD, bool kHi, int kCap>
+template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_attention_kernel(const PagedAttnParams p) {
-  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_sum[kWarps];
@@ -392,10 +392,10 @@ paged_merge_kernel(const PagedAttnParams p) {
 // Few keys: an item's tiles are shared evenly by the `split` CTAs of one cluster, which merge
 // through distributed shared memory, so there is neither a line to find a place on nor a
 // second launch.
-template <bool kF8, int kD, bool kHi, int kCap>
+template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_small_kernel(const PagedAttnParams p) {
-  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   const int split = p.cluster, part = blockIdx.x % split, warp = threadIdx.x >> 5;
@@ -421,17 +421,17 @@ paged_small_kernel(const PagedAttnParams p) {
       [](int, float L) { return L == 0.f ? 0.f : 1.f / L; }, p.out, p.lse);
 }
 
-template <bool kF8, int kD, bool kHi, int kCap>
+template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
-  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap>;
+  using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
   constexpr int ring = kWarps * W::kWarpBytes;
   constexpr int merge = (kWarps * 16 * (W::kSmemRow + 3) + 16 * (kWarps + 2)) * 4;
   constexpr int bytes = ring > merge ? ring : merge;
-  auto* kernel = paged_attention_kernel<kF8, kD, kHi, kCap>;
+  auto* kernel = paged_attention_kernel<kF8, kD, kHi, kCap, kSinks>;
   if (p.cluster > 0) {
     constexpr int finish = paged_finish_bytes<W, kWarps, kD>(), need = ring > finish ? ring : finish;
     static thread_local unsigned long long devices = 0;
-    auto* small = paged_small_kernel<kF8, kD, kHi, kCap>;
+    auto* small = paged_small_kernel<kF8, kD, kHi, kCap, kSinks>;
     const cudaError_t e = paged_allow_smem(small, need, &devices);
     if (e != cudaSuccess) return e;
     return paged_launch(small, dim3((unsigned)(p.c.B * p.c.Hkv * p.groups * p.cluster)), kThreads, need, st, p, p.cluster);
@@ -443,11 +443,16 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   return e;
 }
 
+template <bool kF8, int kD, bool kHi, int kCap>
+cudaError_t launch_sinks(const PagedAttnParams& p, cudaStream_t st) {
+  return p.num_sinks > 0 ? launch<kF8, kD, kHi, kCap, true>(p, st) : launch<kF8, kD, kHi, kCap, false>(p, st);
+}
 template <bool kF8, int kD>
 cudaError_t launch_d(const PagedAttnParams& p, bool hi, cudaStream_t st) {
   const int cap = p.cap <= 0.f ? 0 : p.cap <= kPagedSmallCap ? 1 : 2;
-  if (hi) return cap == 0 ? launch<kF8, kD, true, 0>(p, st) : cap == 1 ? launch<kF8, kD, true, 1>(p, st) : launch<kF8, kD, true, 2>(p, st);
-  return cap == 0 ? launch<kF8, kD, false, 0>(p, st) : cap == 1 ? launch<kF8, kD, false, 1>(p, st) : launch<kF8, kD, false, 2>(p, st);
+  if (hi)
+    return cap == 0 ? launch_sinks<kF8, kD, true, 0>(p, st) : cap == 1 ? launch_sinks<kF8, kD, true, 1>(p, st) : launch_sinks<kF8, kD, true, 2>(p, st);
+  return cap == 0 ? launch_sinks<kF8, kD, false, 0>(p, st) : cap == 1 ? launch_sinks<kF8, kD, false, 1>(p, st) : launch_sinks<kF8, kD, false, 2>(p, st);
 }
 
 constexpr size_t kItemBytes = sizeof(SplitItem) * kCtas;

@@ -86,7 +86,8 @@ __device__ __forceinline__ float paged_capped(float y, float c1k) {
 // to 16 bits costs, so 1 leaves the series near zero out (a windowed call of 64 rows that
 // is bound by it: 97.4 us with the series, 93.7 without).
 constexpr float kPagedSmallCap = 256.f;
-template <bool kF8, int kD, int kTileKeys, bool kHi, int kCap>
+// kSinks: there are sinks (a call without them needs no part of their masks and addresses).
+template <bool kF8, int kD, int kTileKeys, bool kHi, int kCap, bool kSinks>
 struct PagedWarp {
   static constexpr bool kCodes = kF8;
   static constexpr int kKeys = kTileKeys;
@@ -205,14 +206,19 @@ struct PagedWarp {
   struct Pages { int page[kSub]; };
   struct Scales { float k[kSub], v[kSub]; };
 
-  // Page numbers of the tile's subtiles; keys are clamped into [cl, ch].
-  __device__ __forceinline__ Pages fetch(int key0, int cl, int ch) const {
+  // The key read in place of `key`, of subtile s of the tile at key0: keys outside [cl, ch]
+  // repeat its ends, as slots that no query sees may hold anything and 0 * NaN would reach the
+  // output.  The sinks, all in the first subtile, lie left of cl where a window begins; that
+  // subtile's keys between them and cl repeat the last sink, so that all stay in its page.
+  __device__ __forceinline__ int read_for(int key, int s, int key0, int cl, int ch, int sinks) const {
+    if (kSinks && s == 0 && key0 < sinks && key < cl) return min(min(key, sinks - 1), ch);
+    return min(max(key, cl), ch);
+  }
+  // Page numbers of the tile's subtiles.
+  __device__ __forceinline__ Pages fetch(int key0, int cl, int ch, int sinks) const {
     Pages p;
 #pragma unroll
-    for (int s = 0; s < kSub; ++s) {
-      const int key = min(max(key0 + 16 * s, cl), ch);
-      p.page[s] = __ldg(table + (key >> p_shift));
-    }
+    for (int s = 0; s < kSub; ++s) p.page[s] = __ldg(table + (read_for(key0 + 16 * s, s, key0, cl, ch, sinks) >> p_shift));
     return p;
   }
   __device__ __forceinline__ void check(Pages& p) const {
@@ -232,9 +238,8 @@ struct PagedWarp {
     }
     return s;
   }
-  // Starts the copies of the tile at key0.  Keys outside [cl, ch] repeat its ends: slots
-  // that the row does not own may hold anything, and 0 * NaN would reach the output.
-  __device__ __forceinline__ void issue(int key0, int cl, int ch, const Pages& p, int stage) const {
+  // Starts the copies of the tile at key0.
+  __device__ __forceinline__ void issue(int key0, int cl, int ch, int sinks, const Pages& p, int stage) const {
     const uint32_t kd = ring + stage * kStageBytes, vd = kd + kTileBytes;
     const int chunk = lane % kChunks, row0 = lane / kChunks;
     const int pmask = (1 << p_shift) - 1;
@@ -248,7 +253,7 @@ struct PagedWarp {
       for (int i = 0; i < kCopies / kSub; ++i) {
         const int row = 16 * s + row0 + i * kStep;
         int key = key0 + row;
-        if (!inside) key = min(max(key, cl), ch);
+        if (!inside) key = read_for(key, s, key0, cl, ch, sinks);
         const int src = (key & pmask) * kRowBytes;
         paged_cp16(kd + at(row, chunk), kp + src);
         paged_cp16(vd + at(row, chunk), vp + src);
@@ -314,7 +319,7 @@ struct PagedWarp {
     float t0 = -INFINITY, t1 = -INFINITY;  // tile maxima of rows g, g + 8
     float d0 = -INFINITY, d1 = -INFINITY;  // e4m3: maxima of logit + value exponent
     float mant[kSub], expo[kSub];
-    const bool plain = key0 >= mk.num_sinks && key0 >= mk.all_lo && key0 + kKeys - 1 <= mk.all_hi &&
+    const bool plain = (!kSinks || key0 >= mk.num_sinks) && key0 >= mk.all_lo && key0 + kKeys - 1 <= mk.all_hi &&
                        key0 + kKeys <= mk.len;
 #pragma unroll
     for (int s = 0; s < kSub; ++s) {
@@ -328,7 +333,7 @@ struct PagedWarp {
           float x1 = kHi ? logit(sc[s][n][2 + e], f1) : -INFINITY;
           if (!plain) {
             const int key = key0 + 16 * s + 8 * n + 2 * c + e;
-            const bool sink = key < mk.num_sinks;
+            const bool sink = kSinks && key < mk.num_sinks;
             if (sink) {
               x0 = fmaf(mk.bias0[key], kPagedLog2e, x0);
               if constexpr (kHi) x1 = fmaf(mk.bias0[mk.bias_step + key], kPagedLog2e, x1);
@@ -476,16 +481,16 @@ struct PagedWarp {
     int cl, ch;
     int key = key_of(first);
     lim_of(first, cl, ch);
-    Pages pg = fetch(key, cl, ch);
+    Pages pg = fetch(key, cl, ch, mk.num_sinks);
     check(pg);
-    issue(key, cl, ch, pg, 0);
+    issue(key, cl, ch, mk.num_sinks, pg, 0);
     paged_cp_commit();
     Scales sl = scales(pg);
     int nkey = 0, ncl = 0, nch = 0;
     if (first + step < count) {
       nkey = key_of(first + step);
       lim_of(first + step, ncl, nch);
-      pg = fetch(nkey, ncl, nch);
+      pg = fetch(nkey, ncl, nch, mk.num_sinks);
     }
     queries();
     int stage = 0;
@@ -494,13 +499,13 @@ struct PagedWarp {
       const int this_key = key;
       if (t + step < count) {
         check(pg);
-        issue(nkey, ncl, nch, pg, stage ^ 1);
+        issue(nkey, ncl, nch, mk.num_sinks, pg, stage ^ 1);
         sn = scales(pg);
         key = nkey;
         if (t + 2 * step < count) {
           nkey = key_of(t + 2 * step);
           lim_of(t + 2 * step, ncl, nch);
-          pg = fetch(nkey, ncl, nch);
+          pg = fetch(nkey, ncl, nch, mk.num_sinks);
         }
       }
       paged_cp_commit();
