@@ -55,6 +55,10 @@ constexpr int kMinTiles = 4;  // tiles of a run, at least
 constexpr int kItemCost = 12;  // tiles that an item's queries and output are worth
 constexpr float kRaise = 8.f;
 constexpr float kRaiseU = 6.f;
+// e4m3: logit factors are not let below this.  A masked score is -inf before it is multiplied,
+// and -inf * 0 is no number, but a small query's factor times the scale of a page of zeros is 0
+// in fp32.  Scores are below 2^31, so what a larger factor makes of them is below 2^-94.
+constexpr float kLeastFactor = 1.17549435e-38f;  // 2^-126
 
 struct ChunkParams {
   PagedView c;
@@ -757,7 +761,7 @@ paged_chunk_kernel(const ChunkParams p) {
             const float* meta = reinterpret_cast<const float*>(smem + C::kOffMeta + ms * 32);
 #pragma unroll
             for (int g = 0; g < kSub; ++g) {
-              mult[g] = f * meta[g];
+              mult[g] = fmaxf(f * meta[g], kLeastFactor);
               asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lgv[g]) : "f"(meta[4 + g]));
             }
           } else {
