@@ -164,7 +164,7 @@ __device__ __forceinline__ Group<kD> group_of(const PagedAttnParams& p, const Ro
   return gr;
 }
 
-template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
+template <bool kF8, int kD, bool kHi, bool kCap, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_attention_kernel(const PagedAttnParams p) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
@@ -392,7 +392,7 @@ paged_merge_kernel(const PagedAttnParams p) {
 // Few keys: an item's tiles are shared evenly by the `split` CTAs of one cluster, which merge
 // through distributed shared memory, so there is neither a line to find a place on nor a
 // second launch.
-template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
+template <bool kF8, int kD, bool kHi, bool kCap, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 3)
 paged_small_kernel(const PagedAttnParams p) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
@@ -421,7 +421,7 @@ paged_small_kernel(const PagedAttnParams p) {
       [](int, float L) { return L == 0.f ? 0.f : 1.f / L; }, p.out, p.lse);
 }
 
-template <bool kF8, int kD, bool kHi, int kCap, bool kSinks>
+template <bool kF8, int kD, bool kHi, bool kCap, bool kSinks>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   using W = PagedWarp<kF8, kD, 4096 / (kD * (kF8 ? 1 : 2)), kHi, kCap, kSinks>;
   constexpr int ring = kWarps * W::kWarpBytes;
@@ -443,16 +443,15 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   return e;
 }
 
-template <bool kF8, int kD, bool kHi, int kCap>
-cudaError_t launch_sinks(const PagedAttnParams& p, cudaStream_t st) {
-  return p.num_sinks > 0 ? launch<kF8, kD, kHi, kCap, true>(p, st) : launch<kF8, kD, kHi, kCap, false>(p, st);
+template <bool kF8, int kD, bool kHi>
+cudaError_t launch_hi(const PagedAttnParams& p, cudaStream_t st) {
+  const bool sinks = p.num_sinks > 0;
+  if (p.cap > 0.f) return sinks ? launch<kF8, kD, kHi, true, true>(p, st) : launch<kF8, kD, kHi, true, false>(p, st);
+  return sinks ? launch<kF8, kD, kHi, false, true>(p, st) : launch<kF8, kD, kHi, false, false>(p, st);
 }
 template <bool kF8, int kD>
 cudaError_t launch_d(const PagedAttnParams& p, bool hi, cudaStream_t st) {
-  const int cap = p.cap <= 0.f ? 0 : p.cap <= kPagedSmallCap ? 1 : 2;
-  if (hi)
-    return cap == 0 ? launch_sinks<kF8, kD, true, 0>(p, st) : cap == 1 ? launch_sinks<kF8, kD, true, 1>(p, st) : launch_sinks<kF8, kD, true, 2>(p, st);
-  return cap == 0 ? launch_sinks<kF8, kD, false, 0>(p, st) : cap == 1 ? launch_sinks<kF8, kD, false, 1>(p, st) : launch_sinks<kF8, kD, false, 2>(p, st);
+  return hi ? launch_hi<kF8, kD, true>(p, st) : launch_hi<kF8, kD, false>(p, st);
 }
 
 constexpr size_t kItemBytes = sizeof(SplitItem) * kCtas;

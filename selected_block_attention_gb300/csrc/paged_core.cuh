@@ -67,7 +67,7 @@ struct PagedMask {
 };
 
 // log2(e) cap tanh(y) with an error relative to the value: near zero the odd series (its
-// next term is below 2^-28 of the sum at |y| = 0.25), elsewhere 1 - 2 / (1 + e^(2y)).
+// next term is below 2^-26 of the sum at |y| = 0.25), elsewhere 1 - 2 / (1 + e^(2y)).
 __device__ __forceinline__ float paged_capped(float y, float c1k) {
   const float e = ptx::ex2(y * (2.f * kPagedLog2e));
   float rc;
@@ -80,14 +80,28 @@ __device__ __forceinline__ float paged_capped(float y, float c1k) {
   const float near = fmaf(y * y2, pl, y);
   return c1k * (fabsf(y) < 0.25f ? near : far);
 }
+// The same of two scores times f = 2 log2(e) scale / cap, the exponent of e^(2y), two at a time
+// where the instructions are; the series has a term less and ends at |y| = 1/8 (next one 2^-22).
+__device__ __forceinline__ void paged_capped2(float& x0, float& x1, float f, float c1k, float half_cap) {
+  using namespace ptx;
+  constexpr float k2 = 4.f * kPagedLog2e * kPagedLog2e;  // (exponent / y)^2
+  const uint64_t w = mul_f32x2(pack_f32x2(x0, x1), pack_f32x2(f, f));
+  float w0, w1, rc0, rc1, far0, far1, near0, near1;
+  unpack_f32x2(w, w0, w1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc0) : "f"(1.f + ex2(w0)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc1) : "f"(1.f + ex2(w1)));
+  unpack_f32x2(fma_f32x2(pack_f32x2(rc0, rc1), pack_f32x2(-2.f * c1k, -2.f * c1k), pack_f32x2(c1k, c1k)), far0, far1);
+  const uint64_t u = mul_f32x2(w, w), z = mul_f32x2(w, pack_f32x2(half_cap, half_cap));
+  constexpr float a = 2.f / 15.f / (k2 * k2), b = -1.f / 3.f / k2;
+  unpack_f32x2(fma_f32x2(mul_f32x2(z, u), fma_f32x2(u, pack_f32x2(a, a), pack_f32x2(b, b)), z), near0, near1);
+  constexpr float end = 2.f * kPagedLog2e / 8.f;
+  x0 = fabsf(w0) < end ? near0 : far0;
+  x1 = fabsf(w1) < end ? near1 : far1;
+}
 
-// kCap: 0 no soft cap, 1 a cap of at most kPagedSmallCap, 2 any cap.  An error of a few
-// 2^-24 of a small cap is one of at most 2^-14 in a logit, a hundredth of what rounding P
-// to 16 bits costs, so 1 leaves the series near zero out (a windowed call of 64 rows that
-// is bound by it: 97.4 us with the series, 93.7 without).
-constexpr float kPagedSmallCap = 256.f;
+// kCap: there is a soft cap.
 // kSinks: there are sinks (a call without them needs no part of their masks and addresses).
-template <bool kF8, int kD, int kTileKeys, bool kHi, int kCap, bool kSinks>
+template <bool kF8, int kD, int kTileKeys, bool kHi, bool kCap, bool kSinks>
 struct PagedWarp {
   static constexpr bool kCodes = kF8;
   static constexpr int kKeys = kTileKeys;
@@ -109,7 +123,7 @@ struct PagedWarp {
   float m0, m1, l0, l1;
   float u0, u1;    // e4m3: reference of the values' probabilities
   float r0, r1;    // logit factors of rows g, g + 8
-  float c1k;       // log2(e) cap
+  float c1k, half_cap;  // log2(e) cap, cap / 2
   int lane, g, c;
   uint32_t ring;
   const uint8_t* kbase;
@@ -153,7 +167,8 @@ struct PagedWarp {
     for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m0 = m1 = u0 = u1 = -INFINITY;
     l0 = l1 = 0.f;
-    r0 = r1 = kCap == 0 ? scale * kPagedLog2e : kCap == 1 ? scale * (2.f * kPagedLog2e / cap) : scale / cap;
+    r0 = r1 = kCap ? scale * (2.f * kPagedLog2e / cap) : scale * kPagedLog2e;
+    half_cap = 0.5f * cap;
     c1k = cap * kPagedLog2e;
   }
 
@@ -261,20 +276,6 @@ struct PagedWarp {
     }
   }
 
-  __device__ __forceinline__ float logit(float x, float f) const {
-    // log2(e) cap tanh(y), y = x scale / cap
-    if constexpr (kCap == 0) {
-      return x * f;
-    } else if constexpr (kCap == 1) {
-      // 1 - 2 / (1 + e^(2y)): off by a few 2^-24 of the cap
-      float rc;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ptx::ex2(x * f)));
-      return fmaf(-2.f * c1k, rc, c1k);
-    } else {
-      return paged_capped(x * f, c1k);
-    }
-  }
-
   // Scores of the tile in `stage` into the softmax, its values into o.
   __device__ __forceinline__ void consume(int key0, const Scales& sl, int stage, const PagedMask& mk) {
     const uint32_t kt = ring + stage * kStageBytes, vt = kt + kTileBytes;
@@ -324,13 +325,20 @@ struct PagedWarp {
 #pragma unroll
     for (int s = 0; s < kSub; ++s) {
       const float f0 = kF8 ? r0 * sl.k[s] : r0, f1 = kF8 ? r1 * sl.k[s] : r1;
+      if constexpr (kCap) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          paged_capped2(sc[s][n][0], sc[s][n][1], f0, c1k, half_cap);
+          if constexpr (kHi) paged_capped2(sc[s][n][2], sc[s][n][3], f1, c1k, half_cap);
+        }
+      }
       float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x0 = logit(sc[s][n][e], f0);
-          float x1 = kHi ? logit(sc[s][n][2 + e], f1) : -INFINITY;
+          float x0 = kCap ? sc[s][n][e] : sc[s][n][e] * f0;
+          float x1 = !kHi ? -INFINITY : kCap ? sc[s][n][2 + e] : sc[s][n][2 + e] * f1;
           if (!plain) {
             const int key = key0 + 16 * s + 8 * n + 2 * c + e;
             const bool sink = kSinks && key < mk.num_sinks;

@@ -43,7 +43,7 @@ struct PagedSelectParams {
 template <bool kF8, int kD, bool kHi>
 __global__ void __launch_bounds__(kWarps * 32, 3)
 paged_select_kernel(const PagedSelectParams p) {
-  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false, false>;
   constexpr int kKeys = W::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_key[kMaxBlocks * 128 / kKeys];  // first key of each tile
@@ -116,7 +116,7 @@ paged_select_kernel(const PagedSelectParams p) {
 
 template <bool kF8, int kD, bool kHi>
 cudaError_t launch(const PagedSelectParams& p, cudaStream_t st) {
-  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, 0, false>;
+  using W = PagedWarp<kF8, kD, kF8 || kD == 64 ? 32 : 16, kHi, false, false>;
   constexpr int ring = kWarps * W::kWarpBytes;
   constexpr int merge = paged_finish_bytes<W, kWarps, kD>();
   constexpr int bytes = ring > merge ? ring : merge;
