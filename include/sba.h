@@ -478,8 +478,8 @@ typedef struct sba_paged_cache {
  * overflow to +-448, NaN kept.  SBA_BF16 stores the rounded value.
  * Tokens at negative positions are passed over: nothing is stored, q_out is not written.
  * Two rows that write the same page in one call race on it (rows may share pages that
- * they only read).  The pools must not overlap, and q_out overlaps nothing but q, with q's
- * stride.  The call has no workspace; it is one launch, or two with
+ * they only read).  Neither the pools nor the scale arrays may overlap, and q_out overlaps
+ * nothing but q, with q's stride.  The call has no workspace; it is one launch, or two with
  * cu_seqlens and few tokens a row on average.
  */
 typedef struct sba_paged_append_args {

@@ -621,6 +621,11 @@ int sba_paged_kv_append(const sba_paged_append_args* args, sba_stream_t stream) 
                 "cos and sin must be 16-byte aligned tables of at least one position");
   }
   SBA_SUPPORT((long long)Hkv * 2 + (a.q ? a.Hq : 0) <= 65535, "Hq + 2 Hkv must be <= 65535");
+  if (a.cache.dtype == SBA_E4M3) {  // written by the units of keys and of values at the same time
+    const uintptr_t ks = reinterpret_cast<uintptr_t>(c.ks), vs = reinterpret_cast<uintptr_t>(c.vs);
+    SBA_REQUIRE((ks > vs ? ks - vs : vs - ks) >= sizeof(float) * c.num_pages * (size_t)Hkv,
+                "k_scales and v_scales overlap");
+  }
   return launch_paged_append(c, a.cache.dtype == SBA_E4M3, D, a.k, a.k_stride, a.v, a.v_stride, a.q,
                              a.q_stride, a.q_out, a.q_out_stride, a.Hq, a.cos, a.sin, a.rot_dim,
                              a.max_pos, a.interleaved ? 1 : 0, reinterpret_cast<cudaStream_t>(stream));
