@@ -57,10 +57,10 @@ SBA_API const char* sba_last_error(void);
 /*
  * sba_set_wait_timeout_cycles -- limit, in SM clock cycles, on every internal wait of
  * the warp-specialised kernels (the NSA selection forward on tensor cores, the
- * block-sparse / ragged block attention and the paged attention of many rows).  No counterpart on the pages: it is the
- * library's failure detection.  A wait that runs past the limit records the kernel,
- * role, barrier and work item in the device error word, makes every other wait of its
- * CTA return at once, drains the copies already issued, frees its tensor memory and
+ * block-sparse / ragged block attention and the paged attention of many rows).  No
+ * counterpart on the pages: it is the library's failure detection.  A wait that runs past
+ * the limit records the kernel, role, barrier and work item in the device error word, makes
+ * every other wait of its CTA return at once, drains the copies already issued, frees its tensor memory and
  * returns; sba_check_error() then reports SBA_ERR_TIMEOUT with that location and the
  * outputs of that launch are undefined.  Applies to launches made after the call, from
  * any host thread (process-wide).  cycles == 0 restores the default (4e9 cycles, about
@@ -435,7 +435,9 @@ SBA_API int sba_ragged_flash_attention_fwd(const void* q, const void* k, const v
  * A length outside [0, table_width * page_size], a page number outside [0, num_pages) or a
  * token offset that decreases or leaves [0, N] makes the kernel skip the access and
  * sba_check_error() report SBA_ERR_DEVICE_INPUT; the results of the rows concerned are
- * undefined, nothing is read or written out of range.
+ * undefined, nothing is read or written out of range.  Lengths, offsets and table must not
+ * change while a call runs (its blocks read them more than once, and what the call writes is
+ * then undefined); between calls, and between replays of a captured one, they may.
  * Limits: D in {64, 128}, page_size in {16, 32, 64, 128}, table_width * page_size <= 2^30,
  * B <= 2^24, N <= 2^28.
  */
@@ -517,11 +519,17 @@ SBA_API size_t sba_paged_attention_workspace_size(int B, int N, int Hq, int Hkv,
  * the device: a captured call serves whatever seq_lens holds when it is replayed.
  * Results do not depend on timing.  A key that some query of the row sees takes part with
  * weight 0 in the products of the row's other queries, so its value must be finite.
+ * Softmax sums and accumulators are fp32; the probabilities are rounded to 16 bits before
+ * their products with the values (bf16 over an SBA_BF16 cache, fp16 over an SBA_E4M3 one),
+ * here and in sba_nsa_select_paged_fwd.
  * Internally, on `stream`: the attention kernel and a kernel that merges the items it cut
  * into runs; without cu_seqlens and with tables of few keys, one kernel whose clusters share
  * an item.  Without sinks, calls with many (query, head) rows for each row and KV head (17
  * to 97 on average, by head dimension, dtype and table size) use the kernel with
  * accumulators in tensor memory, whose waits are bounded (sba_set_wait_timeout_cycles).
+ * Both choices go by the width of page_table, which need be no wider than the longest row;
+ * with sinks, or a few long chunks among many decode rows, the keys are read once for each
+ * 16 (query, head) rows.
  */
 typedef struct sba_paged_attention_args {
   sba_paged_cache cache; /* read only */
@@ -551,8 +559,8 @@ SBA_API int sba_paged_attention_fwd(const sba_paged_attention_args* args, sba_st
  * attention of each row's last Q tokens over a paged cache (cu_seqlens must be NULL).
  *
  * Block ids are relative to the row's sequence; causal: the token at position p sees keys
- * <= p.  A token without a visible key (also one left of position 0, when seq_len < Q)
- * gets output 0 and LSE -inf.  One launch, no workspace.
+ * <= p, one left of position 0 (seq_len < Q) none.  A token without a visible key gets
+ * output 0 and LSE -inf.  One launch, no workspace.
  */
 typedef struct sba_nsa_select_paged_args {
   sba_paged_cache cache;         /* read only */

@@ -67,7 +67,10 @@ def library_path() -> str:
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
-    """Load libsba.so (built in-tree by ``_build.build()``); raises if absent."""
+    """Load libsba.so (built in-tree by ``_build.build()``); raises if absent.
+
+    The package's functions run in the in-tree copy.  ``path`` gives the handle of another
+    one, with error words and a wait limit of its own, and changes nothing else."""
     global _lib
     if _lib is not None and path is None:
         return _lib

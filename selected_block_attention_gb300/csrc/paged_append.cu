@@ -22,7 +22,7 @@
 // input is read once and held in registers between the maximum and the store.
 //
 // What bounds it.  Prompts: bytes.  12 rows of up to 2600 tokens, 32 + 2 * 8 heads of 128,
-// e4m3 pages of 64: 340 MB in 65.5 us (5.2 TB/s); the angles of a page's positions are
+// e4m3 pages of 64: 340 MB in 65.2 us (5.2 TB/s); the angles of a page's positions are
 // kept over the heads (79 us when each head reads them again), and the next head's
 // loads are under way (none: 81.7; a second head's as well: 66.4; a ring of cp.async in shared
 // memory instead: 67.3).  One token a row: the chain of length, table,
@@ -552,8 +552,11 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
   const bool few = c.cu == nullptr && c.Qn <= kFew;
   // Token counts only the device knows: pages with few tokens go to the kernel that is made
   // for them when the average row has few.  Rows of n tokens each, e4m3 D = 128 (kFew = 4),
-  // 48 heads, us with one kernel / with two: 256 rows n = 1: 30.2 / 5.3, 4: 29.4 / 10.6,
-  // 8: 30.5 / 34.1, 16: 39.5 / 43.1; 16 rows n = 1: 5.5 / 4.7, 8: 5.6 / 7.2.
+  // 48 heads, us with one kernel / with two, all rows of 150 tokens (a page each, the inputs
+  // of one call over and over): 256 rows n = 1: 30.2 / 5.3, 4: 29.4 / 10.6, 8: 30.5 / 34.1,
+  // 16: 39.5 / 43.1; 16 rows n = 1: 5.5 / 4.7, 8: 5.6 / 7.2.  As chosen, with lengths spread
+  // over the pages and three calls' inputs in turn: 256 rows n = 4: 12.0, 8: 41.5, 16: 49.8,
+  // 32: 67.0 (floors 3.5, 7.0, 13.9, 27.9).
   const bool two = c.cu != nullptr && c.N <= (long long)kFew * c.B;
   if (few || two) {
     // a warp takes as many heads as it has threads for, going by the tokens of the average row
@@ -564,7 +567,7 @@ cudaError_t launch_append(AppendParams p, cudaStream_t st) {
                                            : paged_launch(paged_append_few_kernel<kF8, kD, false>, grid, 128, 0, st, p);
     if (e != cudaSuccess || few || c.N <= kFew) return e;
   }
-  // blocks that are resident together: two of 256 threads on an SM (e4m3, 122 registers),
+  // blocks that are resident together: two of 256 threads on an SM (e4m3, 124 registers),
   // or 1024 threads (bf16)
   const int threads = (kD << c.p_shift) / (16 * append_passes<kF8>);
   const dim3 grid(152 * ((kF8 ? 512 : 1024) / threads));

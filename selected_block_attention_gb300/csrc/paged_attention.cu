@@ -19,12 +19,14 @@
 //
 // What bounds it: the bytes of keys and values, with the work on a tile close behind.  One
 // token for each of 4 rows, 64 heads over 4, D = 128, e4m3, 60000 to 131072 keys: 405 MB in
-// 78.2 us (5.2 TB/s), of which 6 are the launch, the search for a run's place and the merge;
+// 77.3 us (5.2 TB/s), of which 6 are the launch, the search for a run's place and the merge;
 // the schedulers issue in 52 % of the cycles (three warps each) and the time that a warp
-// waits for memory is 8 % of its own, so a warp's chain of conversions, MMAs and softmax
-// steps is what is left.  Tried at this size and left: tiles by TMA, one lane issuing (80.0),
-// six warps a CTA, two CTAs an SM (77.2, but 98.0 against 93.7 for windows and 34.5 against
-// 31.8 for drafts); for D = 64 two groups of 16 rows sharing a warp's tiles (drafts 36.4).
+// waits for memory is an eighth of its own, so a warp's chain of conversions, MMAs and softmax
+// steps is what is left.  64 rows with a window of 4096, cap and sinks: 503 MB in 96.0 us, the
+// same with a tanh in the chain (93.4 without the cap).  Tried and left (against 78.2 then):
+// tiles by TMA, one lane issuing (80.0), six warps a CTA, two CTAs an SM (77.2, but windows
+// 98.0 against 93.7 and drafts 34.5 against 31.8); for D = 64 two groups of 16 rows sharing a
+// warp's tiles (drafts 36.4 against 32.0).
 #include <algorithm>
 #include <string>
 
@@ -41,11 +43,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kCtas = 456;    // three for each of 152 SMs
 constexpr int kMinTiles = 4;  // tiles of a run, at least: one for each warp
 constexpr int kItemCost = 12;  // tiles that an item's fixed cost is worth
-// Tiles of a warp, at most, in paged_small_kernel.  Line and cluster, us, e4m3 D = 128, 8 KV
-// heads, equal lengths: one row of 2000 keys 10.7 / 7.0, of 8000 17.9 / 13.3, of 16000
-// 20.2 / 21.9; 16 rows of 2000 20.1 / 16.7, of 8000 50.5 / 51.8; 48 rows of 300 16.7 / 9.4.
-// Past 8 tiles a warp the two come level, and the cluster's fixed shares lose to the line
-// once the rows' lengths differ.
+// Tiles of a warp, at most, in paged_small_kernel, by the table's width (lengths are the
+// device's).  Line and cluster, us, e4m3 D = 128, 8 KV heads, equal lengths and tables as wide:
+// one row of 2000 keys 10.6 / 6.8, of 8000 17.6 / 12.9, of 16000 19.8 / 21.1; 16 rows of 2000
+// 21.8 / 17.8, of 8000 51.4 / 50.2; 48 rows of 300 16.2 / 9.2.  Past 8 tiles a warp the two
+// come level, and the cluster's fixed shares lose to the line once the rows' lengths differ.
+// So one short row behind a wide table takes the line: 2011 keys, table of 131072: 10.8.
 constexpr int kSmallTiles = 8;
 
 struct PagedAttnParams {
@@ -465,11 +468,11 @@ static bool may_have_many_rows(int B, int N, int Hq, int Hkv) { return (long lon
 
 // Whether it does.  This file's kernel reads the keys once for each 16 rows, the other one
 // once for 256 at a higher price a tile.  32 rows of 7000 to 8000 keys, 8 KV heads, by
-// (query, head) rows (us, here / there): e4m3 D = 128 16: 94 / 214, 32: 170 / 217,
-// 40: 247 / 217; bf16 D = 128 16: 160 / 189, 24: 288 / 189; e4m3 D = 64 48: 154 / 164,
-// 64: 199 / 164; bf16 D = 64 32: 120 / 150, 40: 226 / 150.  Two such rows: e4m3 D = 128
-// 40: 26 / 40, 96: 41 / 40: with few keys this file's finer runs win; the tables bound the
-// keys, and the lines cross near half a million.
+// (query, head) rows (us, here / there; there the rows up to 128 cost alike): e4m3 D = 128
+// 16: 91 / 207, 32: 159 / 207, 40: 236 / 207; bf16 D = 128 16: 159 / 189, 24: 287 / 189; e4m3
+// D = 64 48: 150 / 155, 64: 193 / 155; bf16 D = 64 32: 124 / 144, 40: 225 / 144.  Two such
+// rows: e4m3 D = 128 40: 25 / 39, 96: 39 / 40: with few keys this file's finer runs win; the
+// tables bound the keys, and the lines cross near half a million.
 static bool many_rows(const PagedView& c, int f8, int D, int Hq) {
   const long long rows = (long long)c.N * (Hq / c.Hkv), keys = (long long)c.B * c.Hkv * c.width << c.p_shift;
   const int from = keys < (1 << 19) ? 96 : (f8 ? (D == 128 ? 32 : 48) : (D == 128 ? 16 : 32));
@@ -495,6 +498,9 @@ int launch_paged_attention(const PagedView& c, int f8, int D, const void* q, lon
                            float scale, int window_left, int window_right, float cap,
                            const float* sink_bias, int num_sinks, int sink_per_head, void* out,
                            float* lse, void* workspace, cudaStream_t stream) {
+  // Sinks are this file's alone, whatever the rows: a sinks' tile and its bias are not in the
+  // other kernel's pipeline.  512-token chunks with 4 sinks take 1484 us here, without sinks
+  // 262 there.
   if (num_sinks == 0 && many_rows(c, f8, D, Hq))
     return launch_paged_chunk(c, f8, D, q, q_tok, Hq, scale, window_left, window_right, cap, out, lse, workspace,
                               stream);

@@ -23,12 +23,12 @@
 // Tensor memory: S_w,0 S_w,1 (64 columns each) for w = 0, 1, then O_0, O_1: 512 columns.
 //
 // What bounds it.  4 rows of 512 tokens over 512 to 16384 keys, 32 heads over 8, D = 128,
-// e4m3: 300 GFLOP in 264 us, 1.14 PFLOP/s.  The tensor pipe is busy half of the time: per tile
+// e4m3: 300 GFLOP in 262.5 us, 1.14 PFLOP/s (bf16 250).  The tensor pipe is busy half of the time: per tile
 // and half an S of N = 64 takes 8 x 50 cycles and a PV of N = 128 4 x 64 of about 1030; the
 // rest is the chain of a row's softmax (its 64 scores out of tensor memory, maximum, P back),
 // which the two halves hide for one another only in part, beside the conversion of a tile
 // (2 x 8 loads, 128 conversions and 32 stores a thread).  Four stages of keys and of values
-// keep the loaders ahead of an item's change (three of keys: 273 us where four take 264).
+// keep the loaders ahead of an item's change (three of keys: 273 us where four took 264).
 // Tiles of 128 keys would halve the S instructions' fixed part, but leave one S buffer a
 // half and the softmax on the path of the MMAs: 333 us.
 #include <climits>

@@ -1,7 +1,8 @@
 // One warp's walk over key tiles of a paged cache: 16 query rows, an online softmax.
 //
 // Rows are (query, head) pairs of one KV head, the 16 rows of an m16n8k16 MMA.  A tile is
-// kTileKeys keys, whole 16-key subtiles of one page each, brought into shared memory with 16-byte cp.async through a ring of kStages tiles per warp.
+// kTileKeys keys, whole 16-key subtiles of one page each, brought into shared memory with
+// 16-byte cp.async through a ring of kPagedStages tiles per warp.
 //
 // e4m3 operands.  The tensor instruction takes fp16 pairs.  Codes become fp16 exactly
 // (one conversion per pair); the query row is multiplied by a power of two that puts its
@@ -11,7 +12,9 @@
 // l += p in fp32 and feeds p s 2^(m - u + 8) to the MMA, where u is a running maximum of
 // x + e over the keys, so the product stays below 2^15 whatever the pages' scales are, and
 // what rounds to zero in fp16 lies 2^-33 below the largest contribution.  fp16 keeps 11
-// bits of each probability; a bf16 cache uses bf16 probabilities (8 bits) and u = m.
+// bits of each probability; a bf16 cache uses bf16 probabilities (8 bits) and u = m, as the
+// contiguous kernels do: the MMA takes both operands in one type, and fp16 has not the range
+// of bf16 values.  Sums, maxima and o stay in fp32.
 //
 // Fragments.  The order of the contraction index is free, so the thread that holds
 // elements (2c, 2c+1, 2c+8, 2c+9) of a 16-step takes four neighbouring bytes instead: its
