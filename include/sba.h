@@ -56,8 +56,8 @@ SBA_API const char* sba_last_error(void);
 
 /*
  * sba_set_wait_timeout_cycles -- limit, in SM clock cycles, on every internal wait of
- * the warp-specialised kernels (the NSA selection forward on tensor cores, the
- * block-sparse / ragged block attention and the paged attention of many rows).  No
+ * the warp-specialised kernels (the NSA selection on tensor cores, the block-sparse /
+ * ragged block attention and its gradients, and the paged attention of many rows).  No
  * counterpart on the pages: it is the library's failure detection.  A wait that runs past
  * the limit records the kernel, role, barrier and work item in the device error word, makes
  * every other wait of its CTA return at once, drains the copies already issued, frees its tensor memory and
@@ -292,6 +292,112 @@ SBA_API int sba_blocksparse_attn_fwd(const void* q, const void* k, const void* v
                              int causal, int window_left, int window_right,
                              int padding_segment_id, float softmax_scale,
                              void* out, float* lse, sba_stream_t stream);
+
+/*
+ * sba_blocksparse_attn_bwd_workspace_size -- bytes of device workspace that
+ * sba_blocksparse_attn_bwd needs (two fp32 numbers per query row, and the query blocks that
+ * reach each key tile).  Returns 0 for sizes that it does not support.
+ */
+SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq);
+
+/*
+ * sba_blocksparse_attn_bwd -- gradients of sba_blocksparse_attn_fwd with respect to q, k and v.
+ *
+ * For each row (token, query head) with the keys that the forward gave it, and
+ * P = exp(scale * q.k - lse) on them:
+ *   dV_k += P_k dO,  dS_k = P_k (dO.v_k - dO.O),  dQ = scale * sum_k dS_k k_k,
+ *   dK_k += scale * dS_k q,
+ * dK and dV summed over the query heads of a KV head.  The bounds are those of the forward (query
+ * blocks outside, key blocks inside); the call turns them round by itself, so dK and dV sum
+ * exactly the pairs that the forward used.  The bounds of sba_sparse_mask_dkdv_bounds are not an
+ * input: with a window on one side they are not the forward's read from the key side.
+ *
+ *  q, k, v, q_pos, q_seg, kv_pos, kv_seg, lower, upper, lower_full, upper_full, B, T, Hq, Hkv, D,
+ *  q_block, kv_block, causal, window_left, window_right, padding_segment_id, softmax_scale:
+ *                exactly as passed to the forward that produced `out` and `lse`
+ *  out           [B, T, Hq, D] bf16: the forward's output
+ *  lse           [B, T, Hq] float32: the forward's log-sum-exp (required)
+ *  d_out         [B, T, Hq, D] bf16: gradient of the loss with respect to out
+ *  dq            [B, T, Hq, D] bf16 (written; rows without a key get 0)
+ *  dk, dv        [B, T, Hkv, D] bf16 (written; keys that no row sees get 0)
+ *  workspace     device scratch of at least sba_blocksparse_attn_bwd_workspace_size(B, T, Hq)
+ *                bytes, 256-byte aligned, caller-owned; needs no initialisation.  Calls that may
+ *                overlap on the GPU need one each.
+ * q, k, v, out, d_out, lse, dq, dk and dv must be 16-byte aligned; the outputs overlap neither
+ * an input nor one another (SBA_ERR_INVALID_ARG).  A key that is masked for some rows of a tile
+ * takes part in that tile's products with weight 0, and so does the d_out of a row without keys:
+ * both must be finite.
+ * Supported, as in the forward: q_block == 128, kv_block in {64, 128}, T % 128 == 0, D in
+ * {64, 128}, 1 <= Hq / Hkv, B * T * Hq < 2^31, bf16 (fp32 accumulation; P and dS are rounded to
+ * bf16 before their products).  Results are the same from run to run.
+ * Internally, on `stream`: a kernel that prepares the rows, the dK / dV kernel and the dQ kernel,
+ * which begins while the last blocks of dK / dV run.
+ */
+SBA_API int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                                     const float* lse, const void* d_out, const int32_t* q_pos,
+                                     const int32_t* q_seg, const int32_t* kv_pos, const int32_t* kv_seg,
+                                     const int32_t* lower, const int32_t* upper,
+                                     const int32_t* lower_full, const int32_t* upper_full,
+                                     int B, int T, int Hq, int Hkv, int D, int q_block, int kv_block,
+                                     int causal, int window_left, int window_right,
+                                     int padding_segment_id, float softmax_scale, void* dq, void* dk,
+                                     void* dv, void* workspace, size_t workspace_bytes,
+                                     sba_stream_t stream);
+
+/*
+ * Rotary positions
+ * ----------------
+ * No counterpart on the pages: queries and keys of the attentions above carry their positions as
+ * rotations, which the caller applies before them.  sba_paged_kv_append does it for the tokens of
+ * a paged cache on their way in, from the same tables.
+ *
+ * sba_rotary_tables -- cosines and sines of positions 0 .. length - 1.
+ *
+ * Pair i of rot_dim / 2 turns by f_i = base^(-2 i / rot_dim) radians a position; cos and sin,
+ * [length, rot_dim / 2] float32, get amplitude * cos(p f_i) and amplitude * sin(p f_i).  A context
+ * of more than the length that a model was trained with stretches the low frequencies:
+ *   f_i' = f_i * (keep_i + (1 - keep_i) / factor),
+ *   keep_i = clamp((original_length * f_i / (2 pi) - slow) / (fast - slow), 0, 1),
+ * so pairs that make at least `fast` turns over original_length positions stay, pairs of at most
+ * `slow` turns have their positions divided by factor, and the share between them is linear in the
+ * turns; original_length 0 divides them all.
+ * Angles keep their fraction of a turn to 2^-30 and better for any position; the values are exact
+ * to a few units of the last fp32 place.
+ * length >= 0 (0: nothing is launched), rot_dim a multiple of 16 in [16, 256], base >= 1,
+ * factor >= 1, original_length >= 0, 0 <= slow < fast (read only with original_length > 0), finite
+ * amplitude; cos and sin 16-byte aligned, not overlapping.
+ */
+SBA_API int sba_rotary_tables(int length, int rot_dim, double base, double factor, int original_length,
+                              double slow, double fast, double amplitude, float* cos, float* sin,
+                              sba_stream_t stream);
+
+/*
+ * sba_rotary_embed -- queries and keys rotated by their positions, or turned back.
+ *
+ * The first rot_dim dimensions of each head turn in pairs (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),
+ * computed in fp32: pair i is dimensions (i, i + rot_dim / 2), or with `interleaved` (2 i, 2 i + 1);
+ * the others are copied.  `inverse` negates s: the transpose of the rotation, which takes gradients
+ * of rotated queries and keys to those of the plain ones (and, with tables of amplitude 1, turns
+ * rotated values back).  A token at a negative position passes through as it is; a position >=
+ * max_pos does too, and sba_check_error() reports SBA_ERR_DEVICE_INPUT.
+ * In place (q_out == q, k_out == k) with the same token stride; otherwise no output overlaps an
+ * input or the other output.
+ * dtype SBA_BF16 or SBA_F32; D a multiple of 16 in [16, 256]; rot_dim a multiple of 16 in [16, D];
+ * B * T < 2^31 (0: nothing is launched); tensors 16-byte aligned, token strides multiples of 16
+ * bytes that cover the token's heads.  One launch, no workspace.
+ */
+typedef struct sba_rotary_embed_args {
+  const void* q; /* [B, T, Hq, D], token t of row b at (b * T + t) * q_stride elements (heads dense) */
+  const void* k; /* [B, T, Hkv, D], or NULL (with k_out)                                             */
+  void* q_out;
+  void* k_out;
+  const int32_t* positions; /* [B, T], or NULL: token t of a row sits at t */
+  const float* cos;         /* [max_pos, rot_dim / 2] */
+  const float* sin;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  int B, T, Hq, Hkv, D, dtype, rot_dim, max_pos, interleaved, inverse;
+} sba_rotary_embed_args;
+SBA_API int sba_rotary_embed(const sba_rotary_embed_args* args, sba_stream_t stream);
 
 /*
  * sba_ragged_decode_workspace_size -- bytes of device workspace that

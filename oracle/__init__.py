@@ -21,6 +21,8 @@ source documentation pages named in its docstring:
   per row, the last Q tokens of its range).
 * ``nsa_select_attention_backward`` -- gradients (dq, dk, dv) of the selection
   forward, the softmax backward over the same explicit key sets.
+* ``blocksparse_attention_backward`` -- gradients (dq, dk, dv) of ``blocksparse_attention``.
+* ``rotary_tables``, ``rotary_embed`` -- rotation of queries and keys by position.
 * ``paged_kv_append``, ``paged_attention``, ``nsa_select_paged`` -- the decode operations
   over a paged cache (bf16, or e4m3 with a scale for each page and head).
 
@@ -35,6 +37,8 @@ from .blocksparse import blocksparse_attention
 from .ragged_decode import ragged_decode_attention
 from .ragged_attention import ragged_flash_attention
 from .nsa_backward import nsa_select_attention_backward
+from .blocksparse_backward import blocksparse_attention_backward
+from .rotary import rotary_embed, rotary_frequencies, rotary_tables
 from .paged import nsa_select_paged, paged_attention, paged_kv_append
 
 __all__ = [
@@ -45,6 +49,10 @@ __all__ = [
     "ragged_decode_attention",
     "ragged_flash_attention",
     "nsa_select_attention_backward",
+    "blocksparse_attention_backward",
+    "rotary_embed",
+    "rotary_frequencies",
+    "rotary_tables",
     "nsa_select_paged",
     "paged_attention",
     "paged_kv_append",

@@ -9,6 +9,7 @@ raises.
 
 Entry points (same names as the C ABI without the ``sba_`` prefix):
   nsa_select_fwd, sparse_mask_bounds (forward and dK/dV bounds), blocksparse_attn_fwd,
+  blocksparse_attn_bwd, blocksparse_attn_bwd_workspace_size, rotary_tables, rotary_embed,
   ragged_decode_fwd,
   ragged_decode_fwd_noalloc, ragged_decode_workspace_size, ragged_flash_attention_fwd,
   ragged_flash_attention_workspace_size, paged_kv_append, paged_attention_fwd,
@@ -33,7 +34,8 @@ __all__ = [
     "ragged_flash_attention_workspace_size", "l2_read_probe", "check_error",
     "set_wait_timeout_cycles", "get_wait_timeout_cycles", "nsa_select_bwd",
     "nsa_select_bwd_workspace_size", "paged_kv_append", "paged_attention_fwd",
-    "paged_attention_workspace_size", "nsa_select_paged_fwd", "EXPORTED_SYMBOLS",
+    "paged_attention_workspace_size", "nsa_select_paged_fwd", "blocksparse_attn_bwd",
+    "blocksparse_attn_bwd_workspace_size", "rotary_tables", "rotary_embed", "EXPORTED_SYMBOLS",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -46,7 +48,8 @@ EXPORTED_SYMBOLS = (
     "sba_set_wait_timeout_cycles", "sba_get_wait_timeout_cycles",
     "sba_nsa_select_bwd", "sba_nsa_select_bwd_workspace_size",
     "sba_paged_kv_append", "sba_paged_attention_workspace_size", "sba_paged_attention_fwd",
-    "sba_nsa_select_paged_fwd",
+    "sba_nsa_select_paged_fwd", "sba_blocksparse_attn_bwd_workspace_size",
+    "sba_blocksparse_attn_bwd", "sba_rotary_tables", "sba_rotary_embed",
 )
 
 SBA_BF16, SBA_F32, SBA_E4M3 = 0, 1, 2
@@ -80,7 +83,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                            "selected_block_attention_gb300._build.build()")
     lib = ctypes.CDLL(path)
     vp, i32p, f32p = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
-    ci, cf, csz = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ci, cf, cd, csz = ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
     lib.sba_version.restype = ctypes.c_char_p
     lib.sba_last_error.restype = ctypes.c_char_p
     lib.sba_nsa_select_host_workspace_size.argtypes = [ci] * 10
@@ -101,6 +104,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                              i32p, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, cf,
                                              vp, f32p, vp]
     lib.sba_blocksparse_attn_fwd.restype = ci
+    lib.sba_blocksparse_attn_bwd_workspace_size.argtypes = [ci, ci, ci]
+    lib.sba_blocksparse_attn_bwd_workspace_size.restype = csz
+    lib.sba_blocksparse_attn_bwd.argtypes = [vp, vp, vp, vp, f32p, vp, i32p, i32p, i32p, i32p, i32p, i32p,
+                                             i32p, i32p, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, cf,
+                                             vp, vp, vp, vp, csz, vp]
+    lib.sba_blocksparse_attn_bwd.restype = ci
+    lib.sba_rotary_tables.argtypes = [ci, ci, cd, cd, ci, cd, cd, cd, f32p, f32p, vp]
+    lib.sba_rotary_tables.restype = ci
     lib.sba_ragged_decode_workspace_size.argtypes = [ci, ci, ci, ci, ci]
     lib.sba_ragged_decode_workspace_size.restype = csz
     lib.sba_ragged_decode_fwd.argtypes = [vp, vp, vp, i32p, i32p, ci, ci, ci, ci, ci, cf, ci, ci,
@@ -126,7 +137,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sba_nsa_select_bwd.restype = ci
     lib.sba_paged_attention_workspace_size.argtypes = [ci] * 5
     lib.sba_paged_attention_workspace_size.restype = csz
-    for fn in (lib.sba_paged_kv_append, lib.sba_paged_attention_fwd, lib.sba_nsa_select_paged_fwd):
+    for fn in (lib.sba_paged_kv_append, lib.sba_paged_attention_fwd, lib.sba_nsa_select_paged_fwd,
+               lib.sba_rotary_embed):
         fn.argtypes = [vp, vp]  # the argument struct, the stream
         fn.restype = ci
     lib.sba_set_wait_timeout_cycles.argtypes = [ctypes.c_longlong]
@@ -470,10 +482,12 @@ def ragged_flash_attention_fwd(q, k, v, sequence_start, sequence_end, *, softmax
     return out, lse
 
 
-# ---------------------------------------------------------------- paged caches
-# A decode step makes these calls once per layer on small batches, where the host's time
-# counts, so their checks, allocations and calls are in C++ (csrc/binding.cpp).
-_PAGED_CALLS = ("paged_kv_append", "paged_attention_fwd", "nsa_select_paged_fwd")
+# ---------------------------------------------------------------- calls bound in C++
+# A decode step makes the paged calls once per layer on small batches, and a step on short rows
+# the others: there the host's time counts, so their checks, allocations and calls are in C++
+# (csrc/binding.cpp).
+_PAGED_CALLS = ("paged_kv_append", "paged_attention_fwd", "nsa_select_paged_fwd",
+                "blocksparse_attn_bwd", "rotary_tables", "rotary_embed")
 _paged = None
 
 
@@ -500,12 +514,17 @@ def _first_call(name):
         return getattr(_paged_module(), name)(*args, **kwargs)
 
     call.__name__ = call.__qualname__ = name
-    call.__doc__ = f"{name} of the paged caches (loads the built module on the first call)."
+    call.__doc__ = f"{name} (loads the built module on the first call, which has its description)."
     return call
 
 
 for _name in _PAGED_CALLS:
     globals()[_name] = _first_call(_name)
+
+
+def blocksparse_attn_bwd_workspace_size(B, T, Hq) -> int:
+    """Bytes of the workspace of blocksparse_attn_bwd (0 for sizes that it does not support)."""
+    return int(load_library().sba_blocksparse_attn_bwd_workspace_size(B, T, Hq))
 
 
 def paged_attention_workspace_size(B, N, Hq, Hkv, D) -> int:

@@ -2,7 +2,7 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``selected_block_attention_gb300/_lib/libsba.so``; beside it the Python module of the
-paged-cache calls (``csrc/binding.cpp``, g++ against torch's headers) becomes
+calls bound in C++ (``csrc/binding.cpp``, g++ against torch's headers) becomes
 ``_lib/_paged.so``.  A rebuild is skipped when both are newer than every source and header
 and the module was built for this Python and torch.
 """
@@ -28,7 +28,7 @@ MODULE_PATH = os.path.join(LIB_DIR, "_paged.so")
 MODULE_STAMP = os.path.join(BUILD_DIR, "_paged.for")  # the Python and torch it was built against
 
 SOURCES = ["api.cu", "sparse_mask.cu", "nsa_select.cu", "nsa_backward.cu", "blocksparse_attn.cu",
-           "ragged_decode.cu", "paged_append.cu", "paged_attention.cu", "paged_chunk.cu",
+           "blocksparse_backward.cu", "rotary.cu", "ragged_decode.cu", "paged_append.cu", "paged_attention.cu", "paged_chunk.cu",
            "paged_select.cu", "probe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

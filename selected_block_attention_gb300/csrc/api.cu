@@ -471,6 +471,133 @@ int sba_blocksparse_attn_fwd(const void* q, const void* k, const void* v, const 
                                  reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Whether bytes [a, a + na) and [b, b + nb) have one in common.
+static bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq) {
+  if (B < 1 || T < 1 || T % 128 != 0 || Hq < 1 || (long long)B * T * Hq >= (1LL << 31)) return 0;
+  return blocksparse_bwd_workspace_bytes(B, T, Hq);
+}
+
+int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                             const void* d_out, const int32_t* q_pos, const int32_t* q_seg,
+                             const int32_t* kv_pos, const int32_t* kv_seg, const int32_t* lower,
+                             const int32_t* upper, const int32_t* lower_full, const int32_t* upper_full,
+                             int B, int T, int Hq, int Hkv, int D, int q_block, int kv_block, int causal,
+                             int window_left, int window_right, int padding_segment_id,
+                             float softmax_scale, void* dq, void* dk, void* dv, void* workspace,
+                             size_t workspace_bytes, sba_stream_t stream) {
+  g_last_error.clear();
+  SBA_REQUIRE(q && k && v && out && lse && d_out && q_pos && q_seg && kv_pos && kv_seg && lower && upper &&
+                  lower_full && upper_full && dq && dk && dv,
+              "null pointer");
+  SBA_REQUIRE(B >= 1 && T >= 1 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0, "bad head/size arguments");
+  SBA_REQUIRE(window_left >= -1 && window_right >= -1, "windows must be >= -1");
+  SBA_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out) && aligned16(lse) &&
+                  aligned16(d_out) && aligned16(dq) && aligned16(dk) && aligned16(dv),
+              "q, k, v, out, lse, d_out, dq, dk and dv must be 16-byte aligned");
+  SBA_REQUIRE(std::isfinite(softmax_scale), "softmax_scale must be finite");
+  SBA_SUPPORT(q_block == 128, "q_block must be 128");
+  SBA_SUPPORT(kv_block == 64 || kv_block == 128, "kv_block must be 64 or 128");
+  SBA_SUPPORT(T % 128 == 0, "T must be a multiple of 128");
+  SBA_SUPPORT(D == 64 || D == 128, "D must be 64 or 128");
+  SBA_SUPPORT((long long)B * T * Hq < (1LL << 31), "B * T * Hq must be < 2^31");
+  const size_t rows = static_cast<size_t>(B) * T, nq = rows * Hq * D * 2, nk = rows * Hkv * D * 2;
+  const size_t need = blocksparse_bwd_workspace_bytes(B, T, Hq);
+  SBA_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && workspace_bytes >= need,
+              "workspace missing, not 256-byte aligned or smaller than "
+              "sba_blocksparse_attn_bwd_workspace_size()");
+  const struct { const void* at; size_t n; } in[] = {{q, nq}, {k, nk}, {v, nk}, {out, nq}, {d_out, nq}, {lse, rows * Hq * 4}},
+                                             made[] = {{dq, nq}, {dk, nk}, {dv, nk}, {workspace, need}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& x : in)
+      SBA_REQUIRE(!ranges_meet(made[i].at, made[i].n, x.at, x.n), "dq, dk, dv and the workspace must not overlap an input");
+    for (int j = 0; j < i; ++j)
+      SBA_REQUIRE(!ranges_meet(made[i].at, made[i].n, made[j].at, made[j].n),
+                  "dq, dk, dv and the workspace must not overlap one another");
+  }
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(D));
+  return launch_blocksparse_attn_bwd(q, k, v, out, lse, d_out, q_pos, q_seg, kv_pos, kv_seg, lower, upper,
+                                     lower_full, upper_full, B, T, Hq, Hkv, D, kv_block, causal ? 1 : 0,
+                                     window_left, window_right, padding_segment_id, scale, dq, dk, dv,
+                                     workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int sba_rotary_tables(int length, int rot_dim, double base, double factor, int original_length, double slow,
+                      double fast, double amplitude, float* cos, float* sin, sba_stream_t stream) {
+  g_last_error.clear();
+  SBA_REQUIRE(length >= 0, "length must be >= 0");
+  SBA_REQUIRE(rot_dim >= 16 && rot_dim <= 256 && rot_dim % 16 == 0, "rot_dim must be a multiple of 16 in [16, 256]");
+  SBA_REQUIRE(std::isfinite(base) && base >= 1.0, "base must be finite and >= 1");
+  SBA_REQUIRE(std::isfinite(factor) && factor >= 1.0, "factor must be finite and >= 1");
+  SBA_REQUIRE(original_length >= 0, "original_length must be >= 0");
+  SBA_REQUIRE(original_length == 0 || (std::isfinite(fast) && slow >= 0.0 && slow < fast),
+              "slow and fast must be finite with 0 <= slow < fast");
+  SBA_REQUIRE(std::isfinite(static_cast<float>(amplitude)), "amplitude must be finite");
+  if (length == 0) return SBA_OK;
+  SBA_REQUIRE(cos && sin, "null pointer");
+  SBA_REQUIRE(aligned16(cos) && aligned16(sin), "cos and sin must be 16-byte aligned");
+  const size_t bytes = static_cast<size_t>(length) * (rot_dim / 2) * 4;
+  SBA_REQUIRE(!ranges_meet(cos, bytes, sin, bytes), "cos and sin overlap");
+  return launch_rotary_tables(length, rot_dim, base, factor, original_length, slow, fast, amplitude, cos, sin,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Token rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void* at;
+  long long stride, width;
+};
+// Whether two sets of n rows share a byte; rows of one stride may lie between each other's, as
+// parts of one projection's output do.
+static bool rows_meet(const Rows& a, const Rows& b, long long n) {
+  auto span = [n](const Rows& r) { return static_cast<size_t>((n - 1) * r.stride + r.width); };
+  if (!ranges_meet(a.at, span(a), b.at, span(b))) return false;
+  if (n == 1 || a.stride != b.stride) return true;
+  const long long d = reinterpret_cast<intptr_t>(b.at) - reinterpret_cast<intptr_t>(a.at);
+  const long long m = (d % a.stride + a.stride) % a.stride;  // b's row behind a's
+  return m < a.width || a.stride - m < b.width;
+}
+
+int sba_rotary_embed(const sba_rotary_embed_args* args, sba_stream_t stream) {
+  g_last_error.clear();
+  SBA_REQUIRE(args != nullptr, "null pointer");
+  const sba_rotary_embed_args& a = *args;
+  SBA_REQUIRE(a.B >= 0 && a.T >= 0 && a.Hq >= 1 && (a.k == nullptr || a.Hkv >= 1), "bad head/size arguments");
+  SBA_REQUIRE(a.dtype == SBA_BF16 || a.dtype == SBA_F32, "dtype must be SBA_BF16 or SBA_F32");
+  SBA_REQUIRE(a.rot_dim >= 16 && a.rot_dim <= a.D && a.rot_dim % 16 == 0, "rot_dim must be a multiple of 16 in [16, D]");
+  SBA_SUPPORT(a.D % 16 == 0 && a.D <= 256, "D must be a multiple of 16 up to 256");
+  SBA_SUPPORT((long long)a.B * a.T < (1LL << 31), "B * T must be < 2^31");
+  const long long n = (long long)a.B * a.T;
+  SBA_REQUIRE(!a.k == !a.k_out, "k and k_out go together");
+  if (n == 0) return SBA_OK;
+  SBA_REQUIRE(a.q && a.q_out && a.cos && a.sin, "null pointer");
+  SBA_REQUIRE(a.max_pos >= 1, "cos and sin must have at least one position");
+  SBA_REQUIRE(aligned16(a.q) && aligned16(a.k) && aligned16(a.q_out) && aligned16(a.k_out) && aligned16(a.cos) &&
+                  aligned16(a.sin),
+              "tensors must be 16-byte aligned");
+  const long long size = a.dtype == SBA_F32 ? 4 : 2, wq = size * a.Hq * a.D, wk = size * a.Hkv * a.D;
+  auto strides_ok = [&](long long s, long long width) { return n == 1 || (s * size >= width && s * size % 16 == 0); };
+  SBA_REQUIRE(strides_ok(a.q_stride, wq) && strides_ok(a.q_out_stride, wq) &&
+                  (!a.k || (strides_ok(a.k_stride, wk) && strides_ok(a.k_out_stride, wk))),
+              "token strides must cover the token's heads and be multiples of 16 bytes");
+  const Rows q{a.q, a.q_stride * size, wq}, qo{a.q_out, a.q_out_stride * size, wq};
+  const Rows k{a.k, a.k_stride * size, wk}, ko{a.k_out, a.k_out_stride * size, wk};
+  auto out_of = [&](const Rows& o, const Rows& i) {  // in place, or apart
+    return o.at == i.at ? n == 1 || o.stride == i.stride : !rows_meet(o, i, n);
+  };
+  SBA_REQUIRE(out_of(qo, q), "q_out must be q with its token stride, or apart from it");
+  if (a.k) {
+    SBA_REQUIRE(out_of(ko, k), "k_out must be k with its token stride, or apart from it");
+    SBA_REQUIRE(!rows_meet(qo, k, n) && !rows_meet(ko, q, n) && !rows_meet(qo, ko, n),
+                "q_out and k_out must not overlap, nor q_out k, nor k_out q");
+  }
+  return launch_rotary_embed(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t sba_ragged_decode_workspace_size(int B, int Hq, int S, int D, int window_left) {
   if (B < 1 || Hq < 1 || S < 1 || D < 1) return 0;
   return decode_workspace_bytes(B, Hq, S, D, window_left);
@@ -715,7 +842,8 @@ int sba_check_error(sba_stream_t stream) {
                read_and_clear_error_blocksparse(s, &where) | read_and_clear_error_decode(s, &where) |
                read_and_clear_error_nsa_bwd(s, &where) | read_and_clear_error_append(s, &where) |
                read_and_clear_error_paged(s, &where) | read_and_clear_error_select(s, &where) |
-               read_and_clear_error_chunk(s, &where);
+               read_and_clear_error_chunk(s, &where) | read_and_clear_error_blocksparse_bwd(s, &where) |
+               read_and_clear_error_rotary(s, &where);
   if (w & kDevErrTimeout)
     return set_error(SBA_ERR_TIMEOUT, "a kernel gave up on a bounded internal wait" + where);
   if (w & kDevErrInput)

@@ -1,15 +1,18 @@
-// Python entry points of the paged-cache calls (module _paged): tensors in, argument
-// checks, outputs allocated, one call of the C ABI.
+// Python entry points of the paged-cache calls, the rotary calls and the block-sparse gradients
+// (module _paged): tensors in, argument checks, outputs allocated, one call of the C ABI.
 //
-// A decode step makes these calls once per layer on batches whose kernels take a few
+// A decode step makes the paged calls once per layer on batches whose kernels take a few
 // microseconds, so the host's share counts: reading a dozen tensors' properties, packing
-// and allocating from Python took 17 to 25 us a call, from here 5 to 9.  The other entry points'
+// and allocating from Python took 17 to 25 us a call, from here 5 to 9; likewise the others on
+// short rows.  The other entry points'
 // kernels run long enough for their ctypes binding.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
@@ -103,13 +106,14 @@ int size32(int64_t v, const char* name) {
 }
 
 // Address of a contiguous CUDA tensor on device `index`; null for an absent one.
-void* at_of(const at::Tensor* t, const char* name, int index, at::ScalarType type, at::IntArrayRef shape) {
+void* at_of(const at::Tensor* t, const char* name, int index, at::ScalarType type, at::IntArrayRef shape,
+            const char* whose = "the cache's") {
   if (!t) return nullptr;
   if (t->scalar_type() != type) type_error(std::string(name) + " must be " + c10::toString(type));
   if (!t->is_cuda() || t->get_device() != index || t->sizes() != shape || !t->is_contiguous()) {
     std::string s;
     for (int64_t d : shape) s += (s.empty() ? "" : ", ") + std::to_string(d);
-    value_error(std::string(name) + " must be a contiguous tensor of shape [" + s + "] on the cache's device");
+    value_error(std::string(name) + " must be a contiguous tensor of shape [" + s + "] on " + whose + " device");
   }
   return t->data_ptr();
 }
@@ -187,11 +191,12 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
   return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
-template <class Args>
-void call(int (*fn)(const Args*, sba_stream_t), const Args& a, int index) {
-  // the library launches on the current device and looks up its state there
+// `fn(stream)` with the tensors' device current: the library launches on it and looks up its state
+// there.
+template <class Fn>
+void call_on(int index, Fn fn) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-  const int code = fn(&a, reinterpret_cast<sba_stream_t>(c10::cuda::getCurrentCUDAStream(index).stream()));
+  const int code = fn(reinterpret_cast<sba_stream_t>(c10::cuda::getCurrentCUDAStream(index).stream()));
   if (code == SBA_OK) return;
   PyObject* e = g_error ? PyObject_CallFunction(g_error, "is", code, sba_last_error()) : nullptr;
   if (e) {
@@ -201,6 +206,11 @@ void call(int (*fn)(const Args*, sba_stream_t), const Args& a, int index) {
     PyErr_SetString(PyExc_RuntimeError, sba_last_error());
   }
   throw Raised{};
+}
+
+template <class Args>
+void call(int (*fn)(const Args*, sba_stream_t), const Args& a, int index) {
+  call_on(index, [&](sba_stream_t stream) { return fn(&a, stream); });
 }
 
 template <class Body>
@@ -416,6 +426,238 @@ PyObject* select(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* k
   });
 }
 
+const char kGradDoc[] =
+    "blocksparse_attn_bwd(q, k, v, out, lse, d_out, q_positions, q_segment_ids, kv_positions, "
+    "kv_segment_ids, lower, upper, lower_full, upper_full, q_blocksize, kv_blocksize, *, causal=True, "
+    "window_left=-1, window_right=-1, padding_segment_id=-1, softmax_scale=None, dq=None, dk=None, dv=None, "
+    "workspace=None)\n--\n\n"
+    "Gradients (dq, dk, dv) of blocksparse_attn_fwd (bf16): out and lse are the forward's\n"
+    "results for the same arguments and bounds, d_out the gradient of the loss with respect\n"
+    "to out.";
+PyObject* grad(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  static const Signature sig("blocksparse_attn_bwd", 16, 16,
+                             {"q", "k", "v", "out", "lse", "d_out", "q_positions", "q_segment_ids", "kv_positions",
+                              "kv_segment_ids", "lower", "upper", "lower_full", "upper_full", "q_blocksize",
+                              "kv_blocksize", "causal", "window_left", "window_right", "padding_segment_id",
+                              "softmax_scale", "dq", "dk", "dv", "workspace"});
+  return guarded([&]() -> PyObject* {
+    PyObject* o[32];
+    sig.read(args, nargs, kwnames, o);
+    const at::Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k");
+    if (!q.is_cuda()) value_error("libsba works on CUDA tensors only (no CPU path)");
+    if (q.dim() != 4 || k.dim() != 4) value_error("q must be [B, T, Hq, D], k and v [B, T, Hkv, D]");
+    const int index = static_cast<int>(q.get_device());
+    const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), Hkv = k.size(2), D = q.size(3);
+    const int q_block = whole(o[14], 0), kv_block = whole(o[15], 0);
+    const int64_t qs[4] = {B, T, Hq, D}, ks[4] = {B, T, Hkv, D}, rows[3] = {B, T, Hq}, ts[2] = {B, T};
+    const int64_t bounds[3] = {B, 1, q_block > 0 ? (T + q_block - 1) / q_block : 0};
+    auto at = [&](int i, const char* name, at::ScalarType type, at::IntArrayRef shape) {
+      return at_of(&tensor(o[i], name), name, index, type, shape, "q's");
+    };
+    const void* in[6] = {at(0, "q", at::kBFloat16, qs),     at(1, "k", at::kBFloat16, ks),
+                         at(2, "v", at::kBFloat16, ks),     at(3, "out", at::kBFloat16, qs),
+                         at(4, "lse", at::kFloat, rows),    at(5, "d_out", at::kBFloat16, qs)};
+    static const char* const kInts[8] = {"q_positions", "q_segment_ids", "kv_positions", "kv_segment_ids",
+                                         "lower",       "upper",         "lower_full",   "upper_full"};
+    const int32_t* ints[8];
+    for (int i = 0; i < 8; ++i)
+      ints[i] = static_cast<const int32_t*>(at(6 + i, kInts[i], at::kInt, i < 4 ? at::IntArrayRef(ts) : at::IntArrayRef(bounds)));
+    static const char* const kMade[3] = {"dq", "dk", "dv"};
+    at::Tensor made[3];
+    void* to[3];
+    for (int i = 0; i < 3; ++i) {
+      const at::IntArrayRef shape = i == 0 ? at::IntArrayRef(qs) : at::IntArrayRef(ks);
+      made[i] = o[21 + i] ? tensor(o[21 + i], kMade[i]) : fresh(shape, at::kBFloat16, index);
+      to[i] = at_of(&made[i], kMade[i], index, at::kBFloat16, shape, "q's");
+    }
+    const int b = size32(B, "B"), t = size32(T, "T"), hq = size32(Hq, "Hq");
+    at::Tensor ws;
+    if (o[24]) {
+      ws = tensor(o[24], "workspace");
+      if (!ws.is_cuda() || ws.get_device() != index || !ws.is_contiguous())
+        value_error("workspace must be a contiguous tensor on q's device");
+    } else {
+      const size_t need = sba_blocksparse_attn_bwd_workspace_size(b, t, hq);
+      ws = fresh({static_cast<int64_t>(need ? need : 256)}, at::kByte, index);
+    }
+    const int causal = truth(o[16], true), left = whole(o[17], -1), right = whole(o[18], -1), pad = whole(o[19], -1);
+    const float scale = static_cast<float>(real(o[20], 0.0));
+    call_on(index, [&](sba_stream_t stream) {
+      return sba_blocksparse_attn_bwd(in[0], in[1], in[2], in[3], static_cast<const float*>(in[4]), in[5], ints[0], ints[1],
+                                      ints[2], ints[3], ints[4], ints[5], ints[6], ints[7], b, t, hq, size32(Hkv, "Hkv"),
+                                      size32(D, "D"), q_block, kv_block, causal, left, right, pad, scale, to[0], to[1],
+                                      to[2], ws.data_ptr(), ws.nbytes(), stream);
+    });
+    PyObject* r = PyTuple_New(3);
+    if (!r) throw Raised{};
+    for (int i = 0; i < 3; ++i) {
+      PyObject* x = o[21 + i] ? Py_NewRef(o[21 + i]) : THPVariable_Wrap(made[i]);
+      if (!x) {
+        Py_DECREF(r);
+        throw Raised{};
+      }
+      PyTuple_SET_ITEM(r, i, x);
+    }
+    return r;
+  });
+}
+
+const char kTablesDoc[] =
+    "rotary_tables(length, rot_dim, *, base=10000.0, factor=1.0, original_length=0, slow=1.0, fast=32.0, "
+    "amplitude=1.0, device=None, cos=None, sin=None)\n--\n\n"
+    "Tables (cos, sin), fp32 [length, rot_dim / 2], of positions 0 .. length - 1, as rotary_embed\n"
+    "and paged_kv_append take them.  Pair i turns by base ** (-2 i / rot_dim) radians a position;\n"
+    "factor > 1 stretches them for longer contexts: all of them, or with original_length those that\n"
+    "make fewer than `fast` turns over it (wholly below `slow` turns).  amplitude multiplies both.";
+PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  static const Signature sig("rotary_tables", 2, 2,
+                             {"length", "rot_dim", "base", "factor", "original_length", "slow", "fast", "amplitude",
+                              "device", "cos", "sin"});
+  return guarded([&]() -> PyObject* {
+    PyObject* o[32];
+    sig.read(args, nargs, kwnames, o);
+    const int length = whole(o[0], 0), rot = whole(o[1], 0);
+    const double base = real(o[2], 10000.0), factor = real(o[3], 1.0), slow = real(o[5], 1.0), fast = real(o[6], 32.0);
+    const double amplitude = real(o[7], 1.0);
+    const int original = whole(o[4], 0);
+    if (length < 0 || rot < 0) value_error("length and rot_dim must not be negative");
+    if (!o[9] != !o[10]) value_error("cos and sin go together");
+    const int64_t shape[2] = {length, rot / 2};
+    at::Tensor made[2];
+    void* to[2];
+    int index;
+    if (o[9]) {
+      made[0] = tensor(o[9], "cos");
+      made[1] = tensor(o[10], "sin");
+      if (!made[0].is_cuda()) value_error("libsba works on CUDA tensors only (no CPU path)");
+      index = static_cast<int>(made[0].get_device());
+    } else {
+      c10::Device device(at::kCUDA);
+      if (o[8]) {
+        if (THPDevice_Check(o[8])) {
+          device = reinterpret_cast<THPDevice*>(o[8])->device;
+        } else if (PyUnicode_Check(o[8])) {
+          const char* text = PyUnicode_AsUTF8(o[8]);
+          if (!text) throw Raised{};
+          device = c10::Device(std::string(text));
+        } else {
+          type_error("device must be a torch.device or a text");
+        }
+      }
+      if (!device.is_cuda()) value_error("libsba works on CUDA tensors only (no CPU path)");
+      index = device.has_index() ? device.index() : c10::cuda::current_device();
+      for (at::Tensor& t : made) t = fresh(shape, at::kFloat, index);
+    }
+    to[0] = at_of(&made[0], "cos", index, at::kFloat, shape, "cos's");
+    to[1] = at_of(&made[1], "sin", index, at::kFloat, shape, "cos's");
+    call_on(index, [&](sba_stream_t stream) {
+      return sba_rotary_tables(length, rot, base, factor, original, slow, fast, amplitude, static_cast<float*>(to[0]),
+                               static_cast<float*>(to[1]), stream);
+    });
+    PyObject* a = o[9] ? Py_NewRef(o[9]) : THPVariable_Wrap(made[0]);
+    PyObject* b = a ? (o[10] ? Py_NewRef(o[10]) : THPVariable_Wrap(made[1])) : nullptr;
+    PyObject* r = b ? PyTuple_Pack(2, a, b) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    if (!r) throw Raised{};
+    return r;
+  });
+}
+
+// Token rows [B, T, H, D] or [N, H, D], heads dense inside a token, tokens equally far apart.
+struct Rows {
+  void* at;
+  int64_t B, T, heads, d;
+  long long stride;
+};
+Rows rows_of(const at::Tensor& t, const char* name, const at::Tensor& like) {
+  const int64_t dim = t.dim();
+  if (t.scalar_type() != like.scalar_type()) type_error(std::string(name) + " must have q's dtype");
+  if (dim != like.dim()) value_error(std::string(name) + " must have q's leading dimensions");
+  const auto sz = t.sizes(), st = t.strides();
+  for (int64_t i = 0; i < dim - 2; ++i)
+    if (sz[i] != like.size(i)) value_error(std::string(name) + " must have q's leading dimensions");
+  const int64_t heads = sz[dim - 2], d = sz[dim - 1];
+  if (!t.is_cuda() || t.get_device() != like.get_device() || d != like.size(dim - 1) || (st[dim - 1] != 1 && d > 1) ||
+      (st[dim - 2] != d && heads > 1))
+    value_error(std::string(name) + " must be on q's device, with its head dimension and dense heads");
+  const int64_t B = dim == 4 ? sz[0] : 1, T = sz[dim - 3], n = B * T;
+  const int64_t stride = dim == 4 && T == 1 ? st[0] : st[dim - 3];
+  if (dim == 4 && T > 1 && B > 1 && st[0] != T * stride) value_error(std::string(name) + ": tokens must lie equally far apart");
+  return {t.data_ptr(), B, T, heads, d, n > 1 ? stride : heads * d};
+}
+
+const char kEmbedDoc[] =
+    "rotary_embed(q, k, cos, sin, *, positions=None, interleaved=False, inverse=False, q_out=None, "
+    "k_out=None)\n--\n\n"
+    "Queries and keys rotated by their positions.  q [B, T, Hq, D] and k [B, T, Hkv, D] (or\n"
+    "[N, H, D]; k may be None), bf16 or fp32, may be slices of one projection's output; cos / sin\n"
+    "fp32 [max_pos, rot_dim / 2]; positions int32 [B, T] ([N]), by default those in the row, a\n"
+    "negative one leaves its token as it is.  inverse turns back: the gradient.  Returns\n"
+    "(q_out, k_out), new unless given (may be q and k).";
+PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+  static const Signature sig("rotary_embed", 4, 4,
+                             {"q", "k", "cos", "sin", "positions", "interleaved", "inverse", "q_out", "k_out"});
+  return guarded([&]() -> PyObject* {
+    PyObject* o[32];
+    sig.read(args, nargs, kwnames, o);
+    const at::Tensor& qt = tensor(o[0], "q");
+    if (!qt.is_cuda()) value_error("libsba works on CUDA tensors only (no CPU path)");
+    if (qt.dim() != 3 && qt.dim() != 4) value_error("q must be [B, T, Hq, D] or [N, Hq, D]");
+    const auto type = qt.scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat) type_error("q must be bfloat16 or float32");
+    const int index = static_cast<int>(qt.get_device());
+    const PyObject* none = Py_None;
+    const bool with_k = o[1] != none;
+    if (!with_k && o[8]) value_error("k_out needs k");
+    sba_rotary_embed_args a{};
+    at::Tensor out[2];
+    const Rows q = rows_of(qt, "q", qt);
+    out[0] = o[7] ? tensor(o[7], "q_out") : fresh(qt.sizes(), type, index);
+    const Rows qo = rows_of(out[0], "q_out", qt);
+    if (qo.heads != q.heads) value_error("q_out must have q's shape");
+    a.q = q.at;
+    a.q_out = qo.at;
+    a.q_stride = q.stride;
+    a.q_out_stride = qo.stride;
+    a.Hq = size32(q.heads, "q");
+    if (with_k) {
+      const at::Tensor& kt = tensor(o[1], "k");
+      const Rows k = rows_of(kt, "k", qt);
+      out[1] = o[8] ? tensor(o[8], "k_out") : fresh(kt.sizes(), type, index);
+      const Rows ko = rows_of(out[1], "k_out", qt);
+      if (ko.heads != k.heads) value_error("k_out must have k's shape");
+      a.k = k.at;
+      a.k_out = ko.at;
+      a.k_stride = k.stride;
+      a.k_out_stride = ko.stride;
+      a.Hkv = size32(k.heads, "k");
+    }
+    const at::Tensor &cos = tensor(o[2], "cos"), &sin = tensor(o[3], "sin");
+    if (cos.dim() != 2) value_error("cos and sin must be [max_pos, rot_dim / 2]");
+    a.cos = static_cast<float*>(at_of(&cos, "cos", index, at::kFloat, cos.sizes(), "q's"));
+    a.sin = static_cast<float*>(at_of(&sin, "sin", index, at::kFloat, cos.sizes(), "q's"));
+    a.max_pos = size32(cos.size(0), "cos");
+    a.rot_dim = size32(2 * cos.size(1), "cos");
+    a.positions = static_cast<int32_t*>(at_of(optional(o[4], "positions"), "positions", index, at::kInt,
+                                              qt.sizes().slice(0, qt.dim() - 2), "q's"));
+    a.B = size32(q.B, "q");
+    a.T = size32(q.T, "q");
+    a.D = size32(q.d, "q");
+    a.dtype = type == at::kFloat ? SBA_F32 : SBA_BF16;
+    a.interleaved = truth(o[5], false);
+    a.inverse = truth(o[6], false);
+    call(sba_rotary_embed, a, index);
+    PyObject* x = o[7] ? Py_NewRef(o[7]) : THPVariable_Wrap(out[0]);
+    PyObject* y = x ? (o[8] ? Py_NewRef(o[8]) : with_k ? THPVariable_Wrap(out[1]) : Py_NewRef(Py_None)) : nullptr;
+    PyObject* r = y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    if (!r) throw Raised{};
+    return r;
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_XDECREF(g_error);
   g_error = Py_NewRef(type);
@@ -429,9 +671,15 @@ PyMethodDef kMethods[] = {
      METH_FASTCALL | METH_KEYWORDS, kAttentionDoc},
     {"nsa_select_paged_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(select)),
      METH_FASTCALL | METH_KEYWORDS, kSelectDoc},
+    {"blocksparse_attn_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad)),
+     METH_FASTCALL | METH_KEYWORDS, kGradDoc},
+    {"rotary_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tables)),
+     METH_FASTCALL | METH_KEYWORDS, kTablesDoc},
+    {"rotary_embed", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(embed)),
+     METH_FASTCALL | METH_KEYWORDS, kEmbedDoc},
     {"set_error", set_error, METH_O, "The exception class for the library's error codes: (code, message)."},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Paged-cache calls of libsba.", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Calls of libsba bound in C++: paged caches, rotary positions, block-sparse gradients.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,1265 @@
+// Gradients of attention over SparseMask block bounds, for sm_103a: dQ, dK, dV.
+//
+// The forward (blocksparse_attn.cu) is softmax attention of each row (token, query head) over
+// the keys that the bounds and the token mask leave it.  With P = exp(scale q.k - LSE) on those
+// keys and Delta = rowsum(dO * O):
+//   dV = P^T dO,   dS = P * (dO V^T - Delta),   dQ = scale dS K,   dK = scale dS^T Q.
+// The probabilities are computed again from q, k and the LSE; nothing of size T x T is stored.
+//
+// Three launches, on one stream:
+//   1. prep: Delta and the LSE of every row, negated and laid out [B, Hq, T], so that a tile's
+//      128 values are one run; for each key tile the query blocks whose bounds reach it (the
+//      bounds of the forward, turned round: dK and dV sum exactly the pairs that the forward
+//      used, whatever the positions are).
+//   2. dK / dV: a work item is a tile of 128 keys of one KV head; its steps are the (query
+//      block, query head) pairs that reach it.
+//   3. dQ: a work item is a query block of 128 tokens of one query head; its steps are the
+//      128-key tiles of its bounds.
+// S and dP are computed in both (7 products for the 5 of the formulas).  The other way, one pass
+// with dQ added up in memory, needs B T Hq D fp32 sums cleared, added to by every key tile and
+// rounded at the end, some 2.7 GB beside 1.1 GB of inputs on a batch of 4 x 16384 tokens, and its
+// sums come in an order set by timing.  Here every sum is held in tensor memory by one CTA, in an
+// order that the bounds fix, so results are the same from run to run.
+//
+// Both tensor-core kernels keep one tile of S and one of dP (128 x 128 fp32 each) in tensor memory
+// and are arranged so that the tensor core always has a product to do while the softmax warps work
+// on the other tile.  In steady state, per step:
+//   dK / dV:  dV(i)   S(i+1)   dK(i)   dP(i+1)      softmax warps: dS(i) | P(i+1)
+//   dQ:       S(i+1)  dQ(i)    dP(i+1)              softmax warps: dS(i) | P(i+1)
+// dK / dV works on S^T = K Q^T and dP^T = V dO^T (lanes = keys), whose P^T and dS^T go back over
+// their own columns in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q straight from
+// tensor memory.  dQ holds Q and dO of the item in tensor memory as A operands as well, and dS
+// over dP.
+#include <cuda_bf16.h>
+
+#include <climits>
+#include <cmath>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "sync.cuh"
+
+namespace sba {
+
+static __device__ DevError g_err_bsb = {0u, 0u, 0};
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kM = 128;           // query rows, and keys, of a tile
+constexpr int kHalf = 64;         // columns of a tile that one softmax warpgroup takes
+constexpr int kThreads = 384;     // warp 0 loader, warp 1 MMA issuer, warps 4-11 softmax
+constexpr int kItemSlots = 3;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Role : unsigned { kRoleLoader = 1, kRoleMma = 2, kRoleSoftmax = 3 };
+enum BarId : unsigned {
+  kBarItemFull = 1, kBarItemEmpty, kBarQFull, kBarQEmpty, kBarDoFull, kBarDoEmpty, kBarKFull,
+  kBarKEmpty, kBarVFull, kBarVEmpty, kBarSFull, kBarSEmpty, kBarDpFull, kBarPFull, kBarDsFull,
+  kBarAccFull, kBarAccEmpty, kBarRowFull, kBarRowEmpty
+};
+
+struct Params {
+  const __nv_bfloat16* out;
+  const __nv_bfloat16* dout;
+  const float* lse;
+  const int* q_pos;
+  const int* q_seg;
+  const int* kv_pos;
+  const int* kv_seg;
+  const int* lower;
+  const int* upper;
+  const int* lower_full;
+  const int* upper_full;
+  float* nlse;      // [B, Hq, T]  -LSE in log2 units; -inf for rows without a key
+  float* ndelta;    // [B, Hq, T]  -Delta
+  int4* reach;      // [B, nb]     query blocks [x, y) reach this key tile, z of them
+  int* next;        // next item of dK / dV, of dQ
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int B, T, Hq, Hkv, G, nb, nbkv, tpb, causal, window_left, window_right, pad_id;
+  float scale, scale_log2;
+  int n_items_dq, n_items_kv;
+  long long wait_limit;
+};
+
+// Key range of query block qblk of row b in 64-key tiles: [lo, up) visited, [lof, upf) without a
+// token mask (as the forward reads the bounds).
+struct Range {
+  int lo, up, lof, upf;
+};
+__device__ __forceinline__ Range block_range(const Params& p, int b, int qblk) {
+  const long long row = (long long)b * p.nb + qblk;
+  Range r{0, 0, 0, 0};
+  const int lo = max(p.lower[row], 0), up = min(p.upper[row], p.nbkv);
+  if (up > lo) {
+    r.lo = lo * p.tpb;
+    r.up = up * p.tpb;
+    // full blocks only matter inside [lo, up): clamped so that the products stay in range
+    r.lof = min(max(p.lower_full[row], 0), p.nbkv) * p.tpb;
+    r.upf = min(max(p.upper_full[row], 0), p.nbkv) * p.tpb;
+  }
+  return r;
+}
+
+// ------------------------------------------------------------------ 1. prep
+// Blocks [0, n_delta): 32 tokens x 8 heads each, 16 bytes a thread and row (D / 8 threads a row),
+// transposed through shared memory.  The blocks behind them: a warp for each key tile's reach.
+constexpr int kPrepTok = 32, kPrepHeads = 8;
+template <int D>
+__global__ void __launch_bounds__(256) bsa_bwd_prep_kernel(const Params p, int n_delta, int tok_groups,
+                                                           int head_groups) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0 && tid < 2) p.next[tid] = 0;
+  if (static_cast<int>(blockIdx.x) < n_delta) {
+    __shared__ float sd[kPrepHeads][kPrepTok + 1], sl[kPrepHeads][kPrepTok + 1];
+    const int hg = blockIdx.x % head_groups;
+    const int tg = blockIdx.x / head_groups % tok_groups, b = blockIdx.x / head_groups / tok_groups;
+    const int t0 = tg * kPrepTok, h0 = hg * kPrepHeads;
+    constexpr int kLanes = D / 8;               // threads of a row
+    constexpr int kRows = 256 / kLanes;         // rows of a pass
+    constexpr int kPasses = kPrepTok * kPrepHeads / kRows;
+    const int sub = tid / kLanes, part = tid % kLanes;
+    uint4 ov[kPasses / 2], dv[kPasses / 2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < kPasses / 2; ++i) {
+        const int r = (half * (kPasses / 2) + i) * kRows + sub, h = h0 + r % kPrepHeads;
+        if (h < p.Hq) {
+          const long long o = (((long long)b * p.T + t0 + r / kPrepHeads) * p.Hq + h) * D + part * 8;
+          ov[i] = *reinterpret_cast<const uint4*>(p.out + o);
+          dv[i] = *reinterpret_cast<const uint4*>(p.dout + o);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPasses / 2; ++i) {
+        const int r = (half * (kPasses / 2) + i) * kRows + sub;
+        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov[i]);
+        const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&dv[i]);
+        float acc = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 a = __bfloat1622float2(o2[u]), c = __bfloat1622float2(d2[u]);
+          acc = fmaf(a.x, c.x, fmaf(a.y, c.y, acc));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (part == 0) sd[r % kPrepHeads][r / kPrepHeads] = -acc;
+      }
+    }
+    {
+      const int t = tid / kPrepHeads, h = tid % kPrepHeads;
+      if (h0 + h < p.Hq) sl[h][t] = p.lse[((long long)b * p.T + t0 + t) * p.Hq + h0 + h];
+    }
+    __syncthreads();
+    const int h = tid / kPrepTok, t = tid % kPrepTok;
+    if (h0 + h < p.Hq) {
+      const long long o = ((long long)b * p.Hq + h0 + h) * p.T + t0 + t;
+      const float l = sl[h][t];
+      p.ndelta[o] = sd[h][t];
+      // a row without a key: 2^(s - inf) = 0 for every key
+      p.nlse[o] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+    }
+    return;
+  }
+  const int item = (blockIdx.x - n_delta) * 8 + warp;
+  if (item >= p.B * p.nb) return;
+  const int b = item / p.nb, kt = item % p.nb;
+  int first = INT_MAX, last = -1, n = 0;
+  for (int q0 = 0; q0 < p.nb; q0 += 32) {
+    const int qb = q0 + lane;
+    bool hit = false;
+    if (qb < p.nb) {
+      const Range r = block_range(p, b, qb);
+      hit = r.lo < 2 * kt + 2 && r.up > 2 * kt;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, hit);
+    if (m != 0u) {
+      if (first == INT_MAX) first = q0 + __ffs(m) - 1;
+      last = q0 + 31 - __clz(m);
+      n += __popc(m);
+    }
+  }
+  if (lane == 0) p.reach[item] = make_int4(n ? first : 0, last + 1, n, 0);
+}
+
+// ------------------------------------------------------------------ shared pieces
+// Swizzled tiles start on 1024-byte boundaries, and the budget has no room to move them there; the
+// whole block leaves, and the call is reported as failed, if the shared memory does not begin on one.
+__device__ __forceinline__ bool swizzle_aligned(const void* smem) {
+  if ((smem_u32(smem) & 1023u) == 0u) return true;
+  atomicOr(&g_err_bsb.flags, kDevErrTimeout);
+  return false;
+}
+
+// Byte offset (16-byte units) of K step kk of a K-major 128-byte-swizzled tile of 128 rows.
+constexpr int kPanel = kM * 128;  // 128 rows x 64 elements
+__device__ __forceinline__ uint64_t kmajor(int kk) {
+  return static_cast<uint64_t>(((kk / 4) * kPanel + (kk % 4) * 32) >> 4);
+}
+// ... of a tile read with its 128 rows as the K dimension (16 rows a step).
+__device__ __forceinline__ uint64_t mnmajor(int kk) { return static_cast<uint64_t>((kk * 16 * 128) >> 4); }
+// bf16 columns of K step kk of a 128-column operand that lies in two halves, each over the first
+// 32 of its 64 fp32 columns.
+__device__ __forceinline__ uint32_t half_cols(int kk) { return (kk / 4) * kHalf + (kk % 4) * 8; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h2);
+}
+
+// The other side's positions and segment ids of a warp's 64 columns: columns lane and lane + 32.
+struct Cols {
+  int p0, p1, s0, s1;
+};
+__device__ __forceinline__ Cols load_cols(const int* pos, const int* seg, long long first, int lane) {
+  return Cols{pos[first + lane], pos[first + 32 + lane], seg[first + lane], seg[first + 32 + lane]};
+}
+
+// Columns that a row may pair with, as bits of two words: same segment as the row's and a position
+// in [lo, hi] (none if lo > hi).  Columns at consecutive positions in one segment, or in two runs
+// of one each (a document boundary, the start of padding), give every row one interval; others are
+// tested one by one.
+__device__ __forceinline__ void keep_words(const Cols& c, int lane, long long lo, long long hi, int seg,
+                                           uint32_t& w0, uint32_t& w1) {
+  const unsigned kAll = 0xffffffffu;
+  const int p0 = __shfl_sync(kAll, c.p0, 0), s0 = __shfl_sync(kAll, c.s0, 0), s1 = __shfl_sync(kAll, c.s1, 31);
+  const bool consec = (long long)c.p0 == (long long)p0 + lane && (long long)c.p1 == (long long)p0 + 32 + lane;
+  const unsigned b0 = __ballot_sync(kAll, c.s0 == s0), b1 = __ballot_sync(kAll, c.s1 == s0);
+  const int n0 = __popc(b0) + __popc(b1);  // columns of segment s0, a prefix if they are one run
+  const bool runs = (c.s0 == s0 || c.s0 == s1) && (c.s1 == s0 || c.s1 == s1) &&
+                    b0 == (n0 >= 32 ? kAll : (1u << n0) - 1u) &&
+                    b1 == (n0 <= 32 ? 0u : (n0 >= 64 ? kAll : (1u << (n0 - 32)) - 1u));
+  w0 = w1 = 0u;
+  if (__all_sync(kAll, consec && runs)) {
+    if (lo <= hi && (seg == s0 || seg == s1)) {
+      const bool first = seg == s0;
+      const int jlo = static_cast<int>(min(max(lo - p0, first ? 0LL : (long long)n0), 64LL));
+      const int jhi = static_cast<int>(max(min(hi - p0, first ? n0 - 1LL : 63LL), -1LL));
+      if (jlo <= jhi) {
+        const uint64_t w = (jhi >= 63 ? ~0ull : (2ull << jhi) - 1ull) & (~0ull << jlo);
+        w0 = static_cast<uint32_t>(w);
+        w1 = static_cast<uint32_t>(w >> 32);
+      }
+    }
+  } else {
+    for (int j = 0; j < 32; ++j) {
+      const int pa = __shfl_sync(kAll, c.p0, j), sa = __shfl_sync(kAll, c.s0, j);
+      const int pb = __shfl_sync(kAll, c.p1, j), sb = __shfl_sync(kAll, c.s1, j);
+      w0 |= (sa == seg && pa >= lo && pa <= hi) ? 1u << j : 0u;
+      w1 |= (sb == seg && pb >= lo && pb <= hi) ? 1u << j : 0u;
+    }
+  }
+}
+__device__ __forceinline__ void keep_only(float (&x)[kHalf], uint32_t w0, uint32_t w1) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[j] = (w0 & (1u << j)) ? x[j] : 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[32 + j] = (w1 & (1u << j)) ? x[32 + j] : 0.f;
+}
+
+// 64 fp32 columns of the lane row.
+__device__ __forceinline__ void tmem_ld64(uint32_t a, float (&x)[kHalf]) {
+  tmem_ld_32x32b_x32_nw(a, x);
+  tmem_ld_32x32b_x32_nw(a + 32, x + 32);
+  tmem_wait_ld();
+#pragma unroll
+  for (int j = 0; j < kHalf; ++j) tmem_ld_ready(x[j]);
+}
+
+// N fp32 accumulator columns of the lane row, times f, as bf16 to `to`.
+template <int N>
+__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    float x[32];
+    tmem_ld_32x32b_x32(a + c, x);
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+      *reinterpret_cast<uint4*>(to + c + j) =
+          make_uint4(pack_bf16(x[j] * f, x[j + 1] * f), pack_bf16(x[j + 2] * f, x[j + 3] * f),
+                     pack_bf16(x[j + 4] * f, x[j + 5] * f), pack_bf16(x[j + 6] * f, x[j + 7] * f));
+  }
+}
+
+// ------------------------------------------------------------------ 2. dK / dV
+// What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
+enum StepFlag : int { kFirst = 1, kLast = 2, kEmpty = 4, kEnd = 8 };
+struct alignas(16) StepRow {
+  float nlse[kM];
+  float ndelta[kM];
+  int flags, b, hkv, kt, qblk, item;
+  Range r;
+};
+
+template <int D>
+struct KvCfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = kPanels * kPanel;   // 128 rows of K, V, Q or dO
+  static constexpr int kQStages = 3, kDoStages = 2, kRowSlots = 2;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kTile;
+  static constexpr int kOffQ = 2 * kTile;
+  static constexpr int kOffDo = kOffQ + kQStages * kTile;
+  static constexpr int kOffRows = kOffDo + kDoStages * kTile;
+  static constexpr int kOffBars = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
+  static constexpr int kNumBars = 4 + 2 * kQStages + 2 * kDoStages + 2 * kRowSlots + 7;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;   // tmem address, abort flag, step flags
+  // At least half of an SM's shared memory: one CTA an SM, as each holds all tensor memory.
+  static constexpr int kSmemBytes = (kOffMisc + 8 + 4 * kQStages) > 120 * 1024 ? (kOffMisc + 8 + 4 * kQStages) : 120 * 1024;
+  static constexpr int kSCol = 0, kDpCol = 128, kDvCol = 256, kDkCol = 256 + D;
+  static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
+  static constexpr uint32_t kIdescAcc = make_idesc(128, D, 1u, false, true);
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+// Items: key tiles of windows of kGroupWindow (row, KV head) groups, tile by tile across the
+// window.  Under causal masking early key tiles have the most steps, so a window's longest items
+// go out first; the window bounds the Q and dO that the items running at once read.
+constexpr int kGroupWindow = 8;
+__device__ __forceinline__ void kv_item(const Params& p, int item, int& b, int& hkv, int& kt) {
+  const int per = kGroupWindow * p.nb, win = item / per, rem = item - win * per;
+  const int wsz = min(kGroupWindow, p.B * p.Hkv - win * kGroupWindow);
+  kt = rem / wsz;
+  const int g = win * kGroupWindow + rem % wsz;
+  hkv = g % p.Hkv;
+  b = g / p.Hkv;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const Params p) {
+  using C = KvCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!swizzle_aligned(smem)) return;
+  uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+  uint64_t* k_full = bb;     bb += 1;
+  uint64_t* k_empty = bb;    bb += 1;
+  uint64_t* v_full = bb;     bb += 1;
+  uint64_t* v_empty = bb;    bb += 1;
+  uint64_t* q_full = bb;     bb += C::kQStages;
+  uint64_t* q_empty = bb;    bb += C::kQStages;
+  uint64_t* do_full = bb;    bb += C::kDoStages;
+  uint64_t* do_empty = bb;   bb += C::kDoStages;
+  uint64_t* row_full = bb;   bb += C::kRowSlots;
+  uint64_t* row_empty = bb;  bb += C::kRowSlots;
+  uint64_t* s_full = bb;     bb += 1;
+  uint64_t* p_full = bb;     bb += 1;
+  uint64_t* dp_full = bb;    bb += 1;
+  uint64_t* ds_full = bb;    bb += 1;
+  uint64_t* acc_full = bb;   bb += 1;
+  uint64_t* acc_empty = bb;  bb += 1;
+  uint64_t* mma_done = bb;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* step_flags = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);  // per Q stage
+  const Abort ab{abort_flag, &g_err_bsb, 5u, p.wait_limit};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto row_at = [&](int slot) -> StepRow& {
+    return *reinterpret_cast<StepRow*>(smem + C::kOffRows + slot * sizeof(StepRow));
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(k_full, 1); mbar_init(k_empty, 1); mbar_init(v_full, 1); mbar_init(v_empty, 1);
+    for (int i = 0; i < C::kQStages; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
+    for (int i = 0; i < C::kDoStages; ++i) { mbar_init(&do_full[i], 1); mbar_init(&do_empty[i], 1); }
+    for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], 8); }
+    mbar_init(s_full, 1); mbar_init(p_full, 8); mbar_init(dp_full, 1); mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 8); mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t smem_base = smem_u32(smem);
+  // prep's results (and all that ran before it) are there; the dQ kernel may be set up
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loader
+    int qs = 0, ds = 0, rs = 0;
+    uint32_t qph = 0, dph = 0, rph = 0, kph = 0, vph = 0;
+    // stages loaded and the phase of their last load (bit sets), for the drain
+    uint32_t q_out = 0u, q_last = 0u, d_out = 0u, d_last = 0u, r_out = 0u, r_last = 0u;
+    bool k_out = false, v_out = false;
+    bool ok = true;
+    while (ok) {
+      int item = 0;
+      if (lane == 0) item = atomicAdd(&p.next[0], 1);
+      item = __shfl_sync(0xffffffffu, item, 0);
+      if (item >= p.n_items_kv) {
+        // no more: say so in both rings
+        if (!warp_wait(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) break;
+        if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
+        if (lane == 0) {
+          step_flags[qs] = kEnd;
+          row_at(rs).flags = kEnd;
+          mbar_arrive(&q_full[qs]);
+          mbar_arrive(&row_full[rs]);
+        }
+        __syncwarp();
+        q_out &= ~(1u << qs);  // the last loads there were taken, and their phases are over
+        r_out &= ~(1u << rs);
+        break;
+      }
+      int b, hkv, kt;
+      kv_item(p, item, b, hkv, kt);
+      const int4 reach = p.reach[b * p.nb + kt];
+      const int n_steps = reach.z * p.G;
+      if (n_steps == 0) {
+        if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
+        if (lane == 0) {
+          StepRow& r = row_at(rs);
+          r.flags = kEmpty; r.b = b; r.hkv = hkv; r.kt = kt; r.item = item;
+          mbar_arrive(&row_full[rs]);
+        }
+        __syncwarp();
+        r_out &= ~(1u << rs);
+        if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
+        continue;
+      }
+      int step = 0;
+      const int key0 = b * p.T + kt * kM;
+      for (int q0 = reach.x; q0 < reach.y && ok; q0 += 32) {
+        Range mine{0, 0, 0, 0};
+        if (q0 + lane < reach.y) mine = block_range(p, b, q0 + lane);
+        unsigned hits = __ballot_sync(0xffffffffu, mine.lo < 2 * kt + 2 && mine.up > 2 * kt);
+        while (hits != 0u && ok && step < n_steps) {
+          const int at = __ffs(hits) - 1;
+          hits &= hits - 1u;
+          Range r;
+          r.lo = __shfl_sync(0xffffffffu, mine.lo, at);
+          r.up = __shfl_sync(0xffffffffu, mine.up, at);
+          r.lof = __shfl_sync(0xffffffffu, mine.lof, at);
+          r.upf = __shfl_sync(0xffffffffu, mine.upf, at);
+          const int qblk = q0 + at;
+          for (int g = 0; g < p.G; ++g, ++step) {
+            const int h = hkv * p.G + g, tok0 = b * p.T + qblk * kM;
+            const int flags = (step == 0 ? kFirst : 0) | (step == n_steps - 1 ? kLast : 0);
+            if (step == 0) {
+              if (!warp_wait(k_empty, kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
+              if (lane == 0) {
+                mbar_arrive_expect_tx(k_full, C::kTile);
+#pragma unroll
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                  tma_load_3d(smem + C::kOffK + pn * kPanel, &tm_k, k_full, pn * 64, hkv, key0);
+              }
+              k_out = true; kph ^= 1;
+            }
+            if (!warp_wait(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
+            if (lane == 0) {
+              step_flags[qs] = flags;
+              mbar_arrive_expect_tx(&q_full[qs], C::kTile);
+#pragma unroll
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(smem + C::kOffQ + qs * C::kTile + pn * kPanel, &tm_q, &q_full[qs], pn * 64, h, tok0);
+            }
+            q_out |= 1u << qs; q_last = (q_last & ~(1u << qs)) | (qph << qs);
+            if (++qs == C::kQStages) { qs = 0; qph ^= 1; }
+            if (step == 0) {
+              if (!warp_wait(v_empty, vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
+              if (lane == 0) {
+                mbar_arrive_expect_tx(v_full, C::kTile);
+#pragma unroll
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                  tma_load_3d(smem + C::kOffV + pn * kPanel, &tm_v, v_full, pn * 64, hkv, key0);
+              }
+              v_out = true; vph ^= 1;
+            }
+            if (!warp_wait(&do_empty[ds], dph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&do_full[ds], C::kTile);
+#pragma unroll
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(smem + C::kOffDo + ds * C::kTile + pn * kPanel, &tm_do, &do_full[ds], pn * 64, h, tok0);
+            }
+            d_out |= 1u << ds; d_last = (d_last & ~(1u << ds)) | (dph << ds);
+            if (++ds == C::kDoStages) { ds = 0; dph ^= 1; }
+            if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
+            if (lane == 0) {
+              StepRow& w = row_at(rs);
+              w.flags = flags; w.b = b; w.hkv = hkv; w.kt = kt; w.qblk = qblk; w.item = item; w.r = r;
+              const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
+              mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
+              bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
+              bulk_load(w.ndelta, p.ndelta + o, kM * 4, &row_full[rs]);
+            }
+            __syncwarp();
+            r_out |= 1u << rs; r_last = (r_last & ~(1u << rs)) | (rph << rs);
+            if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
+          }
+        }
+      }
+    }
+    // every copy issued has landed before the CTA may end
+    if (lane == 0) {
+      if (k_out) drain_wait(k_full, kph ^ 1);
+      if (v_out) drain_wait(v_full, vph ^ 1);
+      for (int i = 0; i < C::kQStages; ++i)
+        if ((q_out >> i) & 1u) drain_wait(&q_full[i], (q_last >> i) & 1u);
+      for (int i = 0; i < C::kDoStages; ++i)
+        if ((d_out >> i) & 1u) drain_wait(&do_full[i], (d_last >> i) & 1u);
+      for (int i = 0; i < C::kRowSlots; ++i)
+        if ((r_out >> i) & 1u) drain_wait(&row_full[i], (r_last >> i) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    // Converged warp, one elected lane issues.  Products of one thread run in the order issued,
+    // so S(i + 1) may overwrite the P(i) that dV(i) reads, and dP(i + 1) the dS(i) of dK(i).
+    const uint32_t leader = elect_one();
+    const uint64_t k_desc = make_sdesc(smem_base + C::kOffK, 16, 1024, kLayoutSW128);
+    const uint64_t v_desc = make_sdesc(smem_base + C::kOffV, 16, 1024, kLayoutSW128);
+    const uint64_t q_desc = make_sdesc(smem_base + C::kOffQ, 16, 1024, kLayoutSW128);
+    const uint64_t do_desc = make_sdesc(smem_base + C::kOffDo, 16, 1024, kLayoutSW128);
+    const uint64_t qmn_desc = make_sdesc(smem_base + C::kOffQ, kPanel, 1024, kLayoutSW128);
+    const uint64_t domn_desc = make_sdesc(smem_base + C::kOffDo, kPanel, 1024, kLayoutSW128);
+    auto off = [](int stage) { return static_cast<uint64_t>((stage * C::kTile) >> 4); };
+    int qs = 0, ds = 0;                      // stages of the next S and dP
+    uint32_t qph = 0, dph = 0, kph = 0, vph = 0, pph = 0, dsph = 0, accph = 0;
+    // S of the step in Q stage qs; its flags, or kEnd
+    auto issue_s = [&](int& flags) -> bool {
+      if (!warp_wait(&q_full[qs], qph, ab, kRoleMma, kBarQFull, -1)) return false;
+      flags = step_flags[qs];
+      if (flags & kEnd) return true;
+      if (flags & kFirst) {
+        if (!warp_wait(k_full, kph, ab, kRoleMma, kBarKFull, -1)) return false;
+        kph ^= 1;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_f16_ss_by(leader, tmem + C::kSCol, k_desc + kmajor(kk), q_desc + off(qs) + kmajor(kk), C::kIdescS,
+                      kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, s_full);
+      if (flags & kLast) mma_commit_by(leader, k_empty);
+      if (++qs == C::kQStages) { qs = 0; qph ^= 1; }
+      return true;
+    };
+    auto issue_dp = [&](int flags) -> bool {
+      if (flags & kFirst) {
+        if (!warp_wait(v_full, vph, ab, kRoleMma, kBarVFull, -1)) return false;
+        vph ^= 1;
+      }
+      if (!warp_wait(&do_full[ds], dph, ab, kRoleMma, kBarDoFull, -1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_f16_ss_by(leader, tmem + C::kDpCol, v_desc + kmajor(kk), do_desc + off(ds) + kmajor(kk), C::kIdescS,
+                      kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, dp_full);
+      if (flags & kLast) mma_commit_by(leader, v_empty);
+      if (++ds == C::kDoStages) { ds = 0; dph ^= 1; }
+      return true;
+    };
+    int cur = kEnd, next = kEnd;
+    bool ok = issue_s(cur) && ((cur & kEnd) || issue_dp(cur));
+    int cq = 0, cd = 0;  // stages of the current step's Q and dO
+    while (ok && !(cur & kEnd)) {
+      // dV += P^T dO
+      if (!warp_wait(p_full, pph, ab, kRoleMma, kBarPFull, -1)) break;
+      pph ^= 1;
+      if (cur & kFirst) {
+        if (!warp_wait(acc_empty, accph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
+        accph ^= 1;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kM / 16; ++kk)
+        mma_f16_ts_by(leader, tmem + C::kDvCol, tmem + C::kSCol + half_cols(kk), domn_desc + off(cd) + mnmajor(kk),
+                      C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
+      mma_commit_by(leader, &do_empty[cd]);
+      if (++cd == C::kDoStages) cd = 0;
+      if (!issue_s(next)) break;
+      // dK += dS^T Q
+      if (!warp_wait(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
+      dsph ^= 1;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kM / 16; ++kk)
+        mma_f16_ts_by(leader, tmem + C::kDkCol, tmem + C::kDpCol + half_cols(kk), qmn_desc + off(cq) + mnmajor(kk),
+                      C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
+      mma_commit_by(leader, &q_empty[cq]);
+      if (++cq == C::kQStages) cq = 0;
+      if (cur & kLast) mma_commit_by(leader, acc_full);
+      if (!(next & kEnd) && !issue_dp(next)) break;
+      cur = next;
+    }
+    // every tcgen05 operation of this thread has finished once mma_done fires
+    mma_commit_by(leader, mma_done);
+    drain_wait(mma_done, 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax / epilogue
+    // Lane = key.  Warpgroup w takes the tile's queries 64 w .. 64 w + 63, and of dK and dV the
+    // columns D / 2 w .. in the epilogue.
+    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kHalf, dp_col = tmem + lane_off + C::kDpCol + w * kHalf;
+    int rs = 0;
+    uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
+    long long done_row = -1;       // first element of this thread's key in dk / dv, of a finished item
+    long long lo = 1, hi = 0;      // query positions that may see this key
+    int seg = 0;
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    auto finish = [&](int item) -> bool {
+      if (!warp_wait(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
+      accph ^= 1;
+      tc_fence_after();
+      store_cols<D / 2>(tmem + lane_off + C::kDvCol + w * (D / 2), 1.f, p.dv + done_row + w * (D / 2));
+      store_cols<D / 2>(tmem + lane_off + C::kDkCol + w * (D / 2), p.scale, p.dk + done_row + w * (D / 2));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      done_row = -1;
+      return true;
+    };
+    while (true) {
+      if (!warp_wait(&row_full[rs], rph, ab, kRoleSoftmax, kBarRowFull, -1)) break;
+      const StepRow& st = row_at(rs);
+      const int flags = st.flags, item = st.item;
+      if (flags & kEnd) {
+        if (done_row >= 0) finish(-1);
+        break;
+      }
+      const long long key = (long long)st.b * p.T + st.kt * kM + r;
+      const long long row = (key * p.Hkv + st.hkv) * D;
+      if (flags & kEmpty) {
+        // no query sees these keys
+#pragma unroll
+        for (int j = 0; j < D / 2; j += 8) {
+          *reinterpret_cast<uint4*>(p.dk + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(p.dv + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&row_empty[rs]);
+        if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
+        continue;
+      }
+      if (flags & kFirst) {
+        // key k is seen from position q iff k <= q (causal), q - k <= left, k - q <= right
+        const long long kp = p.kv_pos[key];
+        seg = p.kv_seg[key];
+        lo = LLONG_MIN / 2;
+        hi = LLONG_MAX / 2;
+        if (p.causal) lo = max(lo, kp);
+        if (p.window_right >= 0) lo = max(lo, kp - p.window_right);
+        if (p.window_left >= 0) hi = min(hi, kp + p.window_left);
+        if (seg == p.pad_id) { lo = 1; hi = 0; }
+      }
+      // this warp's 64-key tile among the query block's
+      const int ti = 2 * st.kt + (q4 >> 1);
+      const bool in = ti >= st.r.lo && ti < st.r.up, full = in && ti >= st.r.lof && ti < st.r.upf;
+      Cols cols{};
+      if (in && !full) cols = load_cols(p.q_pos, p.q_seg, (long long)st.b * p.T + st.qblk * kM + w * kHalf, lane);
+      if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) break;
+      sph ^= 1;
+      tc_fence_after();
+      float x[kHalf];
+      tmem_ld64(s_col, x);
+      {
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(st.nlse + w * kHalf);
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 4) {
+          const ulonglong2 l4 = nl[j / 4];
+          float a0, a1, a2, a3;
+          unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, l4.x), a0, a1);
+          unpack_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), scale2, l4.y), a2, a3);
+          x[j] = ex2(a0); x[j + 1] = ex2(a1); x[j + 2] = ex2(a2); x[j + 3] = ex2(a3);
+        }
+      }
+      if (!full) {
+        uint32_t w0 = 0u, w1 = 0u;
+        if (in) keep_words(cols, lane, lo, hi, seg, w0, w1);
+        keep_only(x, w0, w1);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[c * 32 + 2 * j], x[c * 32 + 2 * j + 1]);
+        tmem_st_32x32b_x16_u_nw(s_col + c * 16, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      if (done_row >= 0 && !finish(item)) break;
+      if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) break;
+      dpph ^= 1;
+      tc_fence_after();
+      float y[kHalf];
+      tmem_ld64(dp_col, y);
+      {
+        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(st.ndelta + w * kHalf);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const int i = c * 32 + 2 * j;
+            const ulonglong2 d4 = nd[i / 4];
+            float a0, a1, a2, a3;
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), d4.x), pack_f32x2(x[i], x[i + 1])), a0, a1);
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i + 2], y[i + 3]), d4.y), pack_f32x2(x[i + 2], x[i + 3])), a2, a3);
+            pk[j] = pack_bf16(a0, a1);
+            pk[j + 1] = pack_bf16(a2, a3);
+          }
+          tmem_st_32x32b_x16_u_nw(dp_col + c * 16, pk);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_full);
+        mbar_arrive(&row_empty[rs]);
+      }
+      if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
+      if (flags & kLast) done_row = row;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ 3. dQ
+struct DqItem {
+  int b, hkv, h, qblk, n_steps, item;  // n_steps -1: no more items
+  Range r;
+};
+
+template <int D>
+struct DqCfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = kPanels * kPanel;
+  static constexpr int kKStages = 3, kVStages = 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffDo = kTile;
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kTile;
+  static constexpr int kItemBytes = (static_cast<int>(sizeof(DqItem)) + 15) & ~15;
+  static constexpr int kOffItems = kOffV + kVStages * kTile;
+  static constexpr int kOffBars = kOffItems + kItemSlots * kItemBytes;
+  static constexpr int kNumBars = 2 * kItemSlots + 4 + 2 * kKStages + 2 * kVStages + 7;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
+  static constexpr int kSmemBytes = (kOffMisc + 8) > 120 * 1024 ? (kOffMisc + 8) : 120 * 1024;
+  static constexpr int kSCol = 0, kDpCol = 128, kDqCol = 256, kQCol = 256 + D, kDoCol = kQCol + D / 2;
+  static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
+  static constexpr uint32_t kIdescAcc = make_idesc(128, D, 1u, false, true);
+  static_assert(kDoCol + D / 2 <= 512, "tensor memory budget");
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const Params p) {
+  using C = DqCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!swizzle_aligned(smem)) return;
+  uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+  uint64_t* item_full = bb;  bb += kItemSlots;
+  uint64_t* item_empty = bb; bb += kItemSlots;
+  uint64_t* q_full = bb;     bb += 1;
+  uint64_t* q_empty = bb;    bb += 1;
+  uint64_t* do_full = bb;    bb += 1;
+  uint64_t* do_empty = bb;   bb += 1;
+  uint64_t* k_full = bb;     bb += C::kKStages;
+  uint64_t* k_empty = bb;    bb += C::kKStages;
+  uint64_t* v_full = bb;     bb += C::kVStages;
+  uint64_t* v_empty = bb;    bb += C::kVStages;
+  uint64_t* s_full = bb;     bb += 1;
+  uint64_t* s_empty = bb;    bb += 1;
+  uint64_t* dp_full = bb;    bb += 1;
+  uint64_t* ds_full = bb;    bb += 1;
+  uint64_t* dq_full = bb;    bb += 1;
+  uint64_t* dq_empty = bb;   bb += 1;
+  uint64_t* mma_done = bb;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const Abort ab{abort_flag, &g_err_bsb, 6u, p.wait_limit};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto item_at = [&](int slot) -> DqItem& {
+    return *reinterpret_cast<DqItem*>(smem + C::kOffItems + slot * C::kItemBytes);
+  };
+
+  if (threadIdx.x == 0) {
+    // an item slot is read by the MMA warp and the eight softmax warps
+    for (int i = 0; i < kItemSlots; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); }
+    mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
+    for (int i = 0; i < C::kKStages; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < C::kVStages; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
+    mbar_init(s_full, 1); mbar_init(s_empty, 8); mbar_init(dp_full, 1); mbar_init(ds_full, 8);
+    mbar_init(dq_full, 1); mbar_init(dq_empty, 8); mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t smem_base = smem_u32(smem);
+  // No wait for the dK / dV kernel here: its blocks let this kernel be set up only after their own
+  // wait for prep, and nothing that it writes is read.
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loader
+    int islot = 0, ks = 0, vs = 0;
+    uint32_t iph = 0, qph = 0, kph = 0, vph = 0;
+    uint32_t k_out = 0u, k_last = 0u, v_out = 0u, v_last = 0u;
+    uint32_t q_last = 2u, do_last = 2u;  // phase of the last load, 2: none yet
+    bool ok = true;
+    while (ok) {
+      // from the last query block down: under causal masking later ones have more keys
+      int item = 0;
+      if (lane == 0) item = atomicAdd(&p.next[1], 1);
+      item = __shfl_sync(0xffffffffu, item, 0);
+      if (!warp_wait(&item_empty[islot], iph ^ 1, ab, kRoleLoader, kBarItemEmpty, item)) break;
+      if (item >= p.n_items_dq) {
+        if (lane == 0) {
+          item_at(islot).n_steps = -1;
+          mbar_arrive(&item_full[islot]);
+        }
+        __syncwarp();
+        break;
+      }
+      const int h = item % p.Hq, b = item / p.Hq % p.B, qblk = p.nb - 1 - item / p.Hq / p.B, hkv = h / p.G;
+      const Range r = block_range(p, b, qblk);
+      const int n = (r.up - r.lo + 1) / 2;
+      if (lane == 0) {
+        DqItem& it = item_at(islot);
+        it.b = b; it.hkv = hkv; it.h = h; it.qblk = qblk; it.n_steps = n; it.item = item; it.r = r;
+        mbar_arrive(&item_full[islot]);
+      }
+      __syncwarp();
+      if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
+      if (n == 0) continue;
+      const int tok0 = b * p.T + qblk * kM;
+      for (int t = 0; t < n && ok; ++t) {
+        const int key0 = b * p.T + (r.lo + 2 * t) * kHalf;
+        if (t == 0) {
+          if (!warp_wait(q_empty, qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full, C::kTile);
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_3d(smem + C::kOffQ + pn * kPanel, &tm_q, q_full, pn * 64, h, tok0);
+          }
+          q_last = qph;
+        }
+        if (!warp_wait(&k_empty[ks], kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::kOffK + ks * C::kTile + pn * kPanel, &tm_k, &k_full[ks], pn * 64, hkv, key0);
+        }
+        k_out |= 1u << ks; k_last = (k_last & ~(1u << ks)) | (kph << ks);
+        if (++ks == C::kKStages) { ks = 0; kph ^= 1; }
+        if (t == 0) {
+          if (!warp_wait(do_empty, qph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(do_full, C::kTile);
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_3d(smem + C::kOffDo + pn * kPanel, &tm_do, do_full, pn * 64, h, tok0);
+          }
+          do_last = qph; qph ^= 1;
+        }
+        if (!warp_wait(&v_empty[vs], vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::kOffV + vs * C::kTile + pn * kPanel, &tm_v, &v_full[vs], pn * 64, hkv, key0);
+        }
+        v_out |= 1u << vs; v_last = (v_last & ~(1u << vs)) | (vph << vs);
+        if (++vs == C::kVStages) { vs = 0; vph ^= 1; }
+      }
+    }
+    if (lane == 0) {
+      for (int i = 0; i < C::kKStages; ++i)
+        if ((k_out >> i) & 1u) drain_wait(&k_full[i], (k_last >> i) & 1u);
+      for (int i = 0; i < C::kVStages; ++i)
+        if ((v_out >> i) & 1u) drain_wait(&v_full[i], (v_last >> i) & 1u);
+      if (q_last < 2u) drain_wait(q_full, q_last);
+      if (do_last < 2u) drain_wait(do_full, do_last);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    const uint32_t leader = elect_one();
+    const uint64_t q_desc = make_sdesc(smem_base + C::kOffQ, 16, 1024, kLayoutSW128);
+    const uint64_t do_desc = make_sdesc(smem_base + C::kOffDo, 16, 1024, kLayoutSW128);
+    const uint64_t k_desc = make_sdesc(smem_base + C::kOffK, 16, 1024, kLayoutSW128);
+    const uint64_t kmn_desc = make_sdesc(smem_base + C::kOffK, kPanel, 1024, kLayoutSW128);
+    const uint64_t v_desc = make_sdesc(smem_base + C::kOffV, 16, 1024, kLayoutSW128);
+    auto off = [](int stage) { return static_cast<uint64_t>((stage * C::kTile) >> 4); };
+    int islot = 0, ks = 0, vs = 0, left = 0;   // left: steps of the item not yet taken
+    uint32_t iph = 0, qph = 0, doph = 0, kph = 0, vph = 0, seph = 0, dsph = 0, dqph = 0;
+    // the next step's flags: kFirst, kLast, or kEnd
+    auto next_step = [&](int& flags) -> bool {
+      flags = 0;
+      while (left == 0) {
+        if (!warp_wait(&item_full[islot], iph, ab, kRoleMma, kBarItemFull, -1)) return false;
+        left = item_at(islot).n_steps;
+        __syncwarp();
+        if (left < 0) { flags = kEnd; return true; }
+        if (lane == 0) mbar_arrive(&item_empty[islot]);
+        if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
+        flags = kFirst;
+      }
+      if (--left == 0) flags |= kLast;
+      return true;
+    };
+    // S = Q K^T into its columns, which the softmax warps have read
+    auto issue_s = [&](int flags) -> bool {
+      if (flags & kFirst) {
+        // Q of the item into tensor memory; the previous item's products that read it are done,
+        // as the softmax warps have seen the last of them
+        if (!warp_wait(q_full, qph, ab, kRoleMma, kBarQFull, -1)) return false;
+        qph ^= 1;
+      }
+      if (!warp_wait(&k_full[ks], kph, ab, kRoleMma, kBarKFull, -1) ||
+          !warp_wait(s_empty, seph ^ 1, ab, kRoleMma, kBarSEmpty, -1))
+        return false;
+      seph ^= 1;
+      tc_fence_after();
+      if (flags & kFirst) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) tmem_cp_128x256b_by(leader, tmem + C::kQCol + kk * 8, q_desc + kmajor(kk));
+        mma_commit_by(leader, q_empty);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_f16_ts_by(leader, tmem + C::kSCol, tmem + C::kQCol + kk * 8, k_desc + off(ks) + kmajor(kk), C::kIdescS,
+                      kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, s_full);
+      if (++ks == C::kKStages) { ks = 0; kph ^= 1; }
+      return true;
+    };
+    // dP = dO V^T over the dS that the product before it has read
+    auto issue_dp = [&](int flags) -> bool {
+      if (flags & kFirst) {
+        if (!warp_wait(do_full, doph, ab, kRoleMma, kBarDoFull, -1)) return false;
+        doph ^= 1;
+      }
+      if (!warp_wait(&v_full[vs], vph, ab, kRoleMma, kBarVFull, -1)) return false;
+      tc_fence_after();
+      if (flags & kFirst) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) tmem_cp_128x256b_by(leader, tmem + C::kDoCol + kk * 8, do_desc + kmajor(kk));
+        mma_commit_by(leader, do_empty);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_f16_ts_by(leader, tmem + C::kDpCol, tmem + C::kDoCol + kk * 8, v_desc + off(vs) + kmajor(kk), C::kIdescS,
+                      kk > 0 ? 1u : 0u);
+      mma_commit_by(leader, dp_full);
+      mma_commit_by(leader, &v_empty[vs]);
+      if (++vs == C::kVStages) { vs = 0; vph ^= 1; }
+      return true;
+    };
+    int cur = kEnd, next = kEnd, ck = 0;  // ck: stage of the current step's K
+    bool ok = next_step(cur) && ((cur & kEnd) || (issue_s(cur) && issue_dp(cur)));
+    while (ok && !(cur & kEnd)) {
+      if (!next_step(next)) break;
+      if (!(next & kEnd) && !issue_s(next)) break;
+      // dQ += dS K
+      if (!warp_wait(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
+      dsph ^= 1;
+      if (cur & kFirst) {
+        if (!warp_wait(dq_empty, dqph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
+        dqph ^= 1;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kM / 16; ++kk)
+        mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + half_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
+                      C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
+      mma_commit_by(leader, &k_empty[ck]);
+      if (++ck == C::kKStages) ck = 0;
+      if (cur & kLast) mma_commit_by(leader, dq_full);
+      if (!(next & kEnd) && !issue_dp(next)) break;
+      cur = next;
+    }
+    mma_commit_by(leader, mma_done);
+    drain_wait(mma_done, 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax / epilogue
+    // Lane = query row.  Warpgroup w takes the step's keys 64 w .. 64 w + 63 (one 64-key tile of
+    // the bounds), and of dQ the columns D / 2 w .. in the epilogue.
+    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kHalf, dp_col = tmem + lane_off + C::kDpCol + w * kHalf;
+    int islot = 0;
+    uint32_t iph = 0, sph = 0, dpph = 0, dqph = 0;
+    long long done_row = -1;       // first element of this thread's row in dq, of a finished item
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    auto finish = [&](int item) -> bool {
+      if (!warp_wait(dq_full, dqph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
+      dqph ^= 1;
+      tc_fence_after();
+      store_cols<D / 2>(tmem + lane_off + C::kDqCol + w * (D / 2), p.scale, p.dq + done_row + w * (D / 2));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dq_empty);
+      done_row = -1;
+      return true;
+    };
+    bool ok = true;
+    while (ok) {
+      if (!warp_wait(&item_full[islot], iph, ab, kRoleSoftmax, kBarItemFull, -1)) break;
+      const DqItem& it = item_at(islot);
+      const int n = it.n_steps, item = it.item;
+      if (n < 0) {
+        if (done_row >= 0) finish(-1);
+        break;
+      }
+      const int b = it.b, h = it.h;
+      const Range rg = it.r;
+      const long long tok = (long long)b * p.T + it.qblk * kM + r;
+      const long long o = ((long long)b * p.Hq + h) * p.T + it.qblk * kM + r;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[islot]);
+      if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
+      const long long row = (tok * p.Hq + h) * D;
+      if (n == 0) {
+#pragma unroll
+        for (int j = 0; j < D / 2; j += 8)
+          *reinterpret_cast<uint4*>(p.dq + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      const float nlse = p.nlse[o], ndelta = p.ndelta[o];
+      const int seg = p.q_seg[tok];
+      const long long qp = p.q_pos[tok];
+      long long lo = LLONG_MIN / 2, hi = LLONG_MAX / 2;
+      if (p.causal) hi = min(hi, qp);
+      if (p.window_left >= 0) lo = max(lo, qp - p.window_left);
+      if (p.window_right >= 0) hi = min(hi, qp + p.window_right);
+      if (seg == p.pad_id) { lo = 1; hi = 0; }
+      for (int t = 0; t < n; ++t) {
+        const int ti = rg.lo + 2 * t + w;
+        const bool in = ti < rg.up, full = in && ti >= rg.lof && ti < rg.upf;
+        Cols cols{};
+        if (in && !full) cols = load_cols(p.kv_pos, p.kv_seg, (long long)b * p.T + ti * kHalf, lane);
+        if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) { ok = false; break; }
+        sph ^= 1;
+        tc_fence_after();
+        float x[kHalf];
+        tmem_ld64(s_col, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        {
+          const uint64_t nl2 = pack_f32x2(nlse, nlse);
+#pragma unroll
+          for (int j = 0; j < kHalf; j += 2) {
+            float a0, a1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, nl2), a0, a1);
+            x[j] = ex2(a0);
+            x[j + 1] = ex2(a1);
+          }
+        }
+        if (!full) {
+          uint32_t w0 = 0u, w1 = 0u;
+          if (in) keep_words(cols, lane, lo, hi, seg, w0, w1);
+          keep_only(x, w0, w1);
+        }
+        if (done_row >= 0 && !finish(item)) { ok = false; break; }
+        if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) { ok = false; break; }
+        dpph ^= 1;
+        tc_fence_after();
+        float y[kHalf];
+        tmem_ld64(dp_col, y);
+        {
+          const uint64_t nd2 = pack_f32x2(ndelta, ndelta);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int i = c * 32 + 2 * j;
+              float a0, a1;
+              unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), nd2), pack_f32x2(x[i], x[i + 1])), a0, a1);
+              pk[j] = pack_bf16(a0, a1);
+            }
+            tmem_st_32x32b_x16_u_nw(dp_col + c * 16, pk);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (!ok) break;
+      done_row = row;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // the dK / dV kernel has ended before this one does: what follows on the stream waits for both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ host
+struct Layout {
+  size_t nlse, ndelta, reach, next, total;
+};
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+Layout layout(int B, int T, int Hq) {
+  Layout l{};
+  const size_t rows = static_cast<size_t>(B) * T * Hq * 4;
+  size_t o = 0;
+  l.nlse = o;   o += round256(rows);
+  l.ndelta = o; o += round256(rows);
+  l.reach = o;  o += round256(static_cast<size_t>(B) * (T / kM) * sizeof(int4));
+  l.next = o;   o += 256;
+  l.total = o;
+  return l;
+}
+
+template <class Kernel>
+cudaError_t launch_after(Kernel kernel, int grid, int smem, cudaStream_t st, const CUtensorMap& a, const CUtensorMap& b,
+                         const CUtensorMap& c, const CUtensorMap& d, const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, b, c, d, p);
+}
+
+template <int D>
+int launch_impl(const void* q, const void* k, const void* v, const void* d_out, const Params& p, cudaStream_t stream) {
+  CUtensorMap tq, tdo, tk, tv;
+  auto map = [&](CUtensorMap* m, const void* at, int heads) {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)p.B * p.T};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)kM};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+  };
+  if (!map(&tq, q, p.Hq) || !map(&tdo, d_out, p.Hq) || !map(&tk, k, p.Hkv) || !map(&tv, v, p.Hkv))
+    return set_error(SBA_ERR_CUDA, "blocksparse_attn_bwd: tensor map failed");
+  cudaError_t e = cudaFuncSetAttribute(bsa_bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       KvCfg<D>::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(bsa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes);
+  if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd: set smem attribute");
+  const int tok_groups = p.T / kPrepTok, head_groups = (p.Hq + kPrepHeads - 1) / kPrepHeads;
+  const int n_delta = p.B * tok_groups * head_groups, n_reach = (p.B * p.nb + 7) / 8;
+  bsa_bwd_prep_kernel<D><<<n_delta + n_reach, 256, 0, stream>>>(p, n_delta, tok_groups, head_groups);
+  e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_after(bsa_bwd_dkdv_kernel<D>, std::min(p.n_items_kv, num_sms()), KvCfg<D>::kSmemBytes, stream, tq, tdo,
+                     tk, tv, p);
+  if (e == cudaSuccess)
+    e = launch_after(bsa_bwd_dq_kernel<D>, std::min(p.n_items_dq, num_sms()), DqCfg<D>::kSmemBytes, stream, tq, tdo, tk,
+                     tv, p);
+  if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd launch");
+  return SBA_OK;
+}
+
+}  // namespace
+
+unsigned read_and_clear_error_blocksparse_bwd(cudaStream_t, std::string* where) {
+  DevError w{0u, 0u, 0}, zero{0u, 0u, 0};
+  cudaMemcpyFromSymbol(&w, g_err_bsb, sizeof(w));
+  if (w.flags) {
+    cudaMemcpyToSymbol(g_err_bsb, &zero, sizeof(zero));
+    if (where && w.where) {
+      char buf[96];
+      snprintf(buf, sizeof(buf), " [blocksparse_attn_bwd %s role %u barrier %u item %d]",
+               ((w.where >> 24) & 0xFFu) == 6u ? "dq" : "dkdv", (w.where >> 16) & 0xFFu, w.where & 0xFFFFu, w.item);
+      *where += buf;
+    }
+  }
+  return w.flags;
+}
+
+size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq) { return layout(B, T, Hq).total; }
+
+int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                const void* d_out, const int32_t* q_pos, const int32_t* q_seg, const int32_t* kv_pos,
+                                const int32_t* kv_seg, const int32_t* lower, const int32_t* upper,
+                                const int32_t* lower_full, const int32_t* upper_full, int B, int T, int Hq, int Hkv,
+                                int D, int kv_block, int causal, int window_left, int window_right, int pad_id,
+                                float scale, void* dq, void* dk, void* dv, void* workspace, cudaStream_t stream) {
+  const Layout l = layout(B, T, Hq);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Params p{};
+  p.out = static_cast<const __nv_bfloat16*>(out);
+  p.dout = static_cast<const __nv_bfloat16*>(d_out);
+  p.lse = lse;
+  p.q_pos = q_pos; p.q_seg = q_seg; p.kv_pos = kv_pos; p.kv_seg = kv_seg;
+  p.lower = lower; p.upper = upper; p.lower_full = lower_full; p.upper_full = upper_full;
+  p.nlse = reinterpret_cast<float*>(ws + l.nlse);
+  p.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
+  p.reach = reinterpret_cast<int4*>(ws + l.reach);
+  p.next = reinterpret_cast<int*>(ws + l.next);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.nb = T / kM;
+  p.nbkv = T / kv_block;
+  p.tpb = kv_block / kHalf;
+  p.causal = causal;
+  p.window_left = window_left;
+  p.window_right = window_right;
+  p.pad_id = pad_id;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.n_items_dq = B * Hq * p.nb;
+  p.n_items_kv = B * Hkv * p.nb;
+  p.wait_limit = wait_timeout_cycles();
+  return D == 128 ? launch_impl<128>(q, k, v, d_out, p, stream) : launch_impl<64>(q, k, v, d_out, p, stream);
+}
+
+}  // namespace sba

@@ -35,6 +35,8 @@ int cuda_error(cudaError_t e, const char* what);
 unsigned read_and_clear_error_nsa(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_mask(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_blocksparse(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_blocksparse_bwd(cudaStream_t s, std::string* where);
+unsigned read_and_clear_error_rotary(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_decode(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_nsa_bwd(cudaStream_t s, std::string* where);
 unsigned read_and_clear_error_append(cudaStream_t s, std::string* where);
@@ -62,6 +64,18 @@ int launch_blocksparse_attn(const void* q, const void* k, const void* v, const i
                             int q_block, int kv_block, int causal, int window_left,
                             int window_right, int pad_id, float scale, void* out, float* lse,
                             cudaStream_t stream);
+size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq);
+int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                                const float* lse, const void* d_out, const int32_t* q_pos,
+                                const int32_t* q_seg, const int32_t* kv_pos, const int32_t* kv_seg,
+                                const int32_t* lower, const int32_t* upper, const int32_t* lower_full,
+                                const int32_t* upper_full, int B, int T, int Hq, int Hkv, int D,
+                                int kv_block, int causal, int window_left, int window_right, int pad_id,
+                                float scale, void* dq, void* dk, void* dv, void* workspace,
+                                cudaStream_t stream);
+int launch_rotary_tables(int length, int rot, double base, double factor, int original_length, double slow,
+                         double fast, double amplitude, float* cosp, float* sinp, cudaStream_t stream);
+int launch_rotary_embed(const sba_rotary_embed_args& a, cudaStream_t stream);
 size_t decode_workspace_bytes(int B, int Hq, int S, int D, int window_left);
 int launch_ragged_decode(const void* q, const void* k, const void* v, const int32_t* seq_start,
                          const int32_t* seq_end, int B, int Hq, int Hkv, int S, int D,
