@@ -48,8 +48,10 @@ namespace {
 using namespace ptx;
 
 constexpr int kM = 128;           // query rows, and keys, of a tile
-constexpr int kHalf = 64;         // columns of a tile that one softmax warpgroup takes
-constexpr int kThreads = 384;     // warp 0 loader, warp 1 MMA issuer, warps 4-11 softmax
+constexpr int kSub = 64;          // keys of a tile of the bounds
+constexpr int kCols = 32;         // columns of a tile that one softmax warpgroup takes
+constexpr int kSoftWarps = 16;    // four warpgroups
+constexpr int kThreads = 128 + 32 * kSoftWarps;  // warp 0 loader, warp 1 MMA issuer, warps 4-19 softmax
 constexpr int kItemSlots = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -203,87 +205,56 @@ __device__ __forceinline__ uint64_t kmajor(int kk) {
 }
 // ... of a tile read with its 128 rows as the K dimension (16 rows a step).
 __device__ __forceinline__ uint64_t mnmajor(int kk) { return static_cast<uint64_t>((kk * 16 * 128) >> 4); }
-// bf16 columns of K step kk of a 128-column operand that lies in two halves, each over the first
-// 32 of its 64 fp32 columns.
-__device__ __forceinline__ uint32_t half_cols(int kk) { return (kk / 4) * kHalf + (kk % 4) * 8; }
+// bf16 columns of K step kk of a 128-column operand that lies in four parts, each over the first
+// 16 of a warpgroup's 32 fp32 columns.
+__device__ __forceinline__ uint32_t part_cols(int kk) { return (kk / 2) * kCols + (kk % 2) * 8; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h2);
 }
 
-// The other side's positions and segment ids of a warp's 64 columns: columns lane and lane + 32.
-struct Cols {
-  int p0, p1, s0, s1;
-};
-__device__ __forceinline__ Cols load_cols(const int* pos, const int* seg, long long first, int lane) {
-  return Cols{pos[first + lane], pos[first + 32 + lane], seg[first + lane], seg[first + 32 + lane]};
-}
-
-// Columns that a row may pair with, as bits of two words: same segment as the row's and a position
-// in [lo, hi] (none if lo > hi).  Columns at consecutive positions in one segment, or in two runs
-// of one each (a document boundary, the start of padding), give every row one interval; others are
-// tested one by one.
-__device__ __forceinline__ void keep_words(const Cols& c, int lane, long long lo, long long hi, int seg,
-                                           uint32_t& w0, uint32_t& w1) {
+// Columns of a warp that a row may pair with, as bits: same segment as the row's and a position in
+// [lo, hi] (none if lo > hi).  Lane j holds column j's position and segment.  Columns at consecutive
+// positions in one segment, or in two runs of one each (a document boundary, the start of padding),
+// give every row one interval; others are tested one by one.
+__device__ __forceinline__ uint32_t keep_bits(int cp, int cs, int lane, long long lo, long long hi, int seg) {
   const unsigned kAll = 0xffffffffu;
-  const int p0 = __shfl_sync(kAll, c.p0, 0), s0 = __shfl_sync(kAll, c.s0, 0), s1 = __shfl_sync(kAll, c.s1, 31);
-  const bool consec = (long long)c.p0 == (long long)p0 + lane && (long long)c.p1 == (long long)p0 + 32 + lane;
-  const unsigned b0 = __ballot_sync(kAll, c.s0 == s0), b1 = __ballot_sync(kAll, c.s1 == s0);
-  const int n0 = __popc(b0) + __popc(b1);  // columns of segment s0, a prefix if they are one run
-  const bool runs = (c.s0 == s0 || c.s0 == s1) && (c.s1 == s0 || c.s1 == s1) &&
-                    b0 == (n0 >= 32 ? kAll : (1u << n0) - 1u) &&
-                    b1 == (n0 <= 32 ? 0u : (n0 >= 64 ? kAll : (1u << (n0 - 32)) - 1u));
-  w0 = w1 = 0u;
-  if (__all_sync(kAll, consec && runs)) {
+  const int p0 = __shfl_sync(kAll, cp, 0), s0 = __shfl_sync(kAll, cs, 0), s1 = __shfl_sync(kAll, cs, 31);
+  const unsigned first = __ballot_sync(kAll, cs == s0);
+  const int n0 = __popc(first);  // columns of segment s0, a prefix if they are one run
+  const bool simple = (long long)cp == (long long)p0 + lane && (cs == s0 || cs == s1) &&
+                      first == (n0 >= 32 ? kAll : (1u << n0) - 1u);
+  uint32_t w = 0u;
+  if (__all_sync(kAll, simple)) {
     if (lo <= hi && (seg == s0 || seg == s1)) {
-      const bool first = seg == s0;
-      const int jlo = static_cast<int>(min(max(lo - p0, first ? 0LL : (long long)n0), 64LL));
-      const int jhi = static_cast<int>(max(min(hi - p0, first ? n0 - 1LL : 63LL), -1LL));
-      if (jlo <= jhi) {
-        const uint64_t w = (jhi >= 63 ? ~0ull : (2ull << jhi) - 1ull) & (~0ull << jlo);
-        w0 = static_cast<uint32_t>(w);
-        w1 = static_cast<uint32_t>(w >> 32);
-      }
+      const int jlo = static_cast<int>(min(max(lo - p0, seg == s0 ? 0LL : (long long)n0), 32LL));
+      const int jhi = static_cast<int>(max(min(hi - p0, seg == s0 ? n0 - 1LL : 31LL), -1LL));
+      if (jlo <= jhi) w = (jhi >= 31 ? kAll : (2u << jhi) - 1u) & (kAll << jlo);
     }
   } else {
     for (int j = 0; j < 32; ++j) {
-      const int pa = __shfl_sync(kAll, c.p0, j), sa = __shfl_sync(kAll, c.s0, j);
-      const int pb = __shfl_sync(kAll, c.p1, j), sb = __shfl_sync(kAll, c.s1, j);
-      w0 |= (sa == seg && pa >= lo && pa <= hi) ? 1u << j : 0u;
-      w1 |= (sb == seg && pb >= lo && pb <= hi) ? 1u << j : 0u;
+      const int pj = __shfl_sync(kAll, cp, j), sj = __shfl_sync(kAll, cs, j);
+      w |= (sj == seg && pj >= lo && pj <= hi) ? 1u << j : 0u;
     }
   }
+  return w;
 }
-__device__ __forceinline__ void keep_only(float (&x)[kHalf], uint32_t w0, uint32_t w1) {
+__device__ __forceinline__ void keep_only(float (&x)[kCols], uint32_t w) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) x[j] = (w0 & (1u << j)) ? x[j] : 0.f;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) x[32 + j] = (w1 & (1u << j)) ? x[32 + j] : 0.f;
-}
-
-// 64 fp32 columns of the lane row.
-__device__ __forceinline__ void tmem_ld64(uint32_t a, float (&x)[kHalf]) {
-  tmem_ld_32x32b_x32_nw(a, x);
-  tmem_ld_32x32b_x32_nw(a + 32, x + 32);
-  tmem_wait_ld();
-#pragma unroll
-  for (int j = 0; j < kHalf; ++j) tmem_ld_ready(x[j]);
+  for (int j = 0; j < kCols; ++j) x[j] = (w & (1u << j)) ? x[j] : 0.f;
 }
 
-// N fp32 accumulator columns of the lane row, times f, as bf16 to `to`.
+// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16 to `to`.
 template <int N>
 __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to) {
+  float x[N];
+  if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
 #pragma unroll
-  for (int c = 0; c < N; c += 32) {
-    float x[32];
-    tmem_ld_32x32b_x32(a + c, x);
-#pragma unroll
-    for (int j = 0; j < 32; j += 8)
-      *reinterpret_cast<uint4*>(to + c + j) =
-          make_uint4(pack_bf16(x[j] * f, x[j + 1] * f), pack_bf16(x[j + 2] * f, x[j + 3] * f),
-                     pack_bf16(x[j + 4] * f, x[j + 5] * f), pack_bf16(x[j + 6] * f, x[j + 7] * f));
-  }
+  for (int j = 0; j < N; j += 8)
+    *reinterpret_cast<uint4*>(to + j) =
+        make_uint4(pack_bf16(x[j] * f, x[j + 1] * f), pack_bf16(x[j + 2] * f, x[j + 3] * f),
+                   pack_bf16(x[j + 4] * f, x[j + 5] * f), pack_bf16(x[j + 6] * f, x[j + 7] * f));
 }
 
 // ------------------------------------------------------------------ 2. dK / dV
@@ -369,9 +340,9 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     mbar_init(k_full, 1); mbar_init(k_empty, 1); mbar_init(v_full, 1); mbar_init(v_empty, 1);
     for (int i = 0; i < C::kQStages; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
     for (int i = 0; i < C::kDoStages; ++i) { mbar_init(&do_full[i], 1); mbar_init(&do_empty[i], 1); }
-    for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], 8); }
-    mbar_init(s_full, 1); mbar_init(p_full, 8); mbar_init(dp_full, 1); mbar_init(ds_full, 8);
-    mbar_init(acc_full, 1); mbar_init(acc_empty, 8); mbar_init(mma_done, 1);
+    for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kSoftWarps); }
+    mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps); mbar_init(dp_full, 1); mbar_init(ds_full, kSoftWarps);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, kSoftWarps); mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -583,7 +554,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kM / 16; ++kk)
-        mma_f16_ts_by(leader, tmem + C::kDvCol, tmem + C::kSCol + half_cols(kk), domn_desc + off(cd) + mnmajor(kk),
+        mma_f16_ts_by(leader, tmem + C::kDvCol, tmem + C::kSCol + part_cols(kk), domn_desc + off(cd) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
       mma_commit_by(leader, &do_empty[cd]);
       if (++cd == C::kDoStages) cd = 0;
@@ -594,7 +565,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kM / 16; ++kk)
-        mma_f16_ts_by(leader, tmem + C::kDkCol, tmem + C::kDpCol + half_cols(kk), qmn_desc + off(cq) + mnmajor(kk),
+        mma_f16_ts_by(leader, tmem + C::kDkCol, tmem + C::kDpCol + part_cols(kk), qmn_desc + off(cq) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
       mma_commit_by(leader, &q_empty[cq]);
       if (++cq == C::kQStages) cq = 0;
@@ -608,12 +579,12 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax / epilogue
-    // Lane = key.  Warpgroup w takes the tile's queries 64 w .. 64 w + 63, and of dK and dV the
-    // columns D / 2 w .. in the epilogue.
+    // Lane = key.  Warpgroup w takes the tile's queries 32 w .. 32 w + 31, and of dK and dV the
+    // columns D / 4 w .. in the epilogue.
     const int w = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kHalf, dp_col = tmem + lane_off + C::kDpCol + w * kHalf;
+    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
     int rs = 0;
     uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
     long long done_row = -1;       // first element of this thread's key in dk / dv, of a finished item
@@ -624,8 +595,8 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!warp_wait(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
       accph ^= 1;
       tc_fence_after();
-      store_cols<D / 2>(tmem + lane_off + C::kDvCol + w * (D / 2), 1.f, p.dv + done_row + w * (D / 2));
-      store_cols<D / 2>(tmem + lane_off + C::kDkCol + w * (D / 2), p.scale, p.dk + done_row + w * (D / 2));
+      store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + done_row + w * (D / 4));
+      store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + done_row + w * (D / 4));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
@@ -645,9 +616,9 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (flags & kEmpty) {
         // no query sees these keys
 #pragma unroll
-        for (int j = 0; j < D / 2; j += 8) {
-          *reinterpret_cast<uint4*>(p.dk + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(p.dv + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < D / 4; j += 8) {
+          *reinterpret_cast<uint4*>(p.dk + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(p.dv + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&row_empty[rs]);
@@ -668,17 +639,21 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // this warp's 64-key tile among the query block's
       const int ti = 2 * st.kt + (q4 >> 1);
       const bool in = ti >= st.r.lo && ti < st.r.up, full = in && ti >= st.r.lof && ti < st.r.upf;
-      Cols cols{};
-      if (in && !full) cols = load_cols(p.q_pos, p.q_seg, (long long)st.b * p.T + st.qblk * kM + w * kHalf, lane);
+      int cp = 0, cs = 0;
+      if (in && !full) {
+        const long long col = (long long)st.b * p.T + st.qblk * kM + w * kCols + lane;
+        cp = p.q_pos[col];
+        cs = p.q_seg[col];
+      }
       if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) break;
       sph ^= 1;
       tc_fence_after();
-      float x[kHalf];
-      tmem_ld64(s_col, x);
+      float x[kCols];
+      tmem_ld_32x32b_x32(s_col, x);
       {
-        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(st.nlse + w * kHalf);
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(st.nlse + w * kCols);
 #pragma unroll
-        for (int j = 0; j < kHalf; j += 4) {
+        for (int j = 0; j < kCols; j += 4) {
           const ulonglong2 l4 = nl[j / 4];
           float a0, a1, a2, a3;
           unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, l4.x), a0, a1);
@@ -686,17 +661,12 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           x[j] = ex2(a0); x[j + 1] = ex2(a1); x[j + 2] = ex2(a2); x[j + 3] = ex2(a3);
         }
       }
-      if (!full) {
-        uint32_t w0 = 0u, w1 = 0u;
-        if (in) keep_words(cols, lane, lo, hi, seg, w0, w1);
-        keep_only(x, w0, w1);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      if (!full) keep_only(x, in ? keep_bits(cp, cs, lane, lo, hi, seg) : 0u);
+      {
         uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[c * 32 + 2 * j], x[c * 32 + 2 * j + 1]);
-        tmem_st_32x32b_x16_u_nw(s_col + c * 16, pk);
+        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+        tmem_st_32x32b_x16_u_nw(s_col, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -706,25 +676,22 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) break;
       dpph ^= 1;
       tc_fence_after();
-      float y[kHalf];
-      tmem_ld64(dp_col, y);
+      float y[kCols];
+      tmem_ld_32x32b_x32(dp_col, y);
       {
-        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(st.ndelta + w * kHalf);
+        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(st.ndelta + w * kCols);
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const int i = c * 32 + 2 * j;
-            const ulonglong2 d4 = nd[i / 4];
-            float a0, a1, a2, a3;
-            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), d4.x), pack_f32x2(x[i], x[i + 1])), a0, a1);
-            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i + 2], y[i + 3]), d4.y), pack_f32x2(x[i + 2], x[i + 3])), a2, a3);
-            pk[j] = pack_bf16(a0, a1);
-            pk[j + 1] = pack_bf16(a2, a3);
-          }
-          tmem_st_32x32b_x16_u_nw(dp_col + c * 16, pk);
+        for (int j = 0; j < 16; j += 2) {
+          const int i = 2 * j;
+          const ulonglong2 d4 = nd[i / 4];
+          float a0, a1, a2, a3;
+          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), d4.x), pack_f32x2(x[i], x[i + 1])), a0, a1);
+          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i + 2], y[i + 3]), d4.y), pack_f32x2(x[i + 2], x[i + 3])), a2, a3);
+          pk[j] = pack_bf16(a0, a1);
+          pk[j + 1] = pack_bf16(a2, a3);
         }
+        tmem_st_32x32b_x16_u_nw(dp_col, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -809,13 +776,13 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   };
 
   if (threadIdx.x == 0) {
-    // an item slot is read by the MMA warp and the eight softmax warps
-    for (int i = 0; i < kItemSlots; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 9); }
+    // an item slot is read by the MMA warp and the softmax warps
+    for (int i = 0; i < kItemSlots; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 1 + kSoftWarps); }
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
     for (int i = 0; i < C::kKStages; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < C::kVStages; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
-    mbar_init(s_full, 1); mbar_init(s_empty, 8); mbar_init(dp_full, 1); mbar_init(ds_full, 8);
-    mbar_init(dq_full, 1); mbar_init(dq_empty, 8); mbar_init(mma_done, 1);
+    mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(dp_full, 1); mbar_init(ds_full, kSoftWarps);
+    mbar_init(dq_full, 1); mbar_init(dq_empty, kSoftWarps); mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -869,7 +836,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (n == 0) continue;
       const int tok0 = b * p.T + qblk * kM;
       for (int t = 0; t < n && ok; ++t) {
-        const int key0 = b * p.T + (r.lo + 2 * t) * kHalf;
+        const int key0 = b * p.T + (r.lo + 2 * t) * kSub;
         if (t == 0) {
           if (!warp_wait(q_empty, qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
           if (lane == 0) {
@@ -1008,7 +975,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kM / 16; ++kk)
-        mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + half_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
+        mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
       mma_commit_by(leader, &k_empty[ck]);
       if (++ck == C::kKStages) ck = 0;
@@ -1021,12 +988,12 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax / epilogue
-    // Lane = query row.  Warpgroup w takes the step's keys 64 w .. 64 w + 63 (one 64-key tile of
-    // the bounds), and of dQ the columns D / 2 w .. in the epilogue.
+    // Lane = query row.  Warpgroup w takes the step's keys 32 w .. 32 w + 31 (half of a 64-key tile
+    // of the bounds), and of dQ the columns D / 4 w .. in the epilogue.
     const int w = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kHalf, dp_col = tmem + lane_off + C::kDpCol + w * kHalf;
+    const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
     int islot = 0;
     uint32_t iph = 0, sph = 0, dpph = 0, dqph = 0;
     long long done_row = -1;       // first element of this thread's row in dq, of a finished item
@@ -1035,7 +1002,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (!warp_wait(dq_full, dqph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
       dqph ^= 1;
       tc_fence_after();
-      store_cols<D / 2>(tmem + lane_off + C::kDqCol + w * (D / 2), p.scale, p.dq + done_row + w * (D / 2));
+      store_cols<D / 4>(tmem + lane_off + C::kDqCol + w * (D / 4), p.scale, p.dq + done_row + w * (D / 4));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_empty);
@@ -1061,8 +1028,8 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const long long row = (tok * p.Hq + h) * D;
       if (n == 0) {
 #pragma unroll
-        for (int j = 0; j < D / 2; j += 8)
-          *reinterpret_cast<uint4*>(p.dq + row + w * (D / 2) + j) = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < D / 4; j += 8)
+          *reinterpret_cast<uint4*>(p.dq + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
         continue;
       }
       const float nlse = p.nlse[o], ndelta = p.ndelta[o];
@@ -1074,53 +1041,50 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (p.window_right >= 0) hi = min(hi, qp + p.window_right);
       if (seg == p.pad_id) { lo = 1; hi = 0; }
       for (int t = 0; t < n; ++t) {
-        const int ti = rg.lo + 2 * t + w;
+        const int ti = rg.lo + 2 * t + (w >> 1);
         const bool in = ti < rg.up, full = in && ti >= rg.lof && ti < rg.upf;
-        Cols cols{};
-        if (in && !full) cols = load_cols(p.kv_pos, p.kv_seg, (long long)b * p.T + ti * kHalf, lane);
+        int cp = 0, cs = 0;
+        if (in && !full) {
+          const long long col = (long long)b * p.T + ti * kSub + (w & 1) * kCols + lane;
+          cp = p.kv_pos[col];
+          cs = p.kv_seg[col];
+        }
         if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) { ok = false; break; }
         sph ^= 1;
         tc_fence_after();
-        float x[kHalf];
-        tmem_ld64(s_col, x);
+        float x[kCols];
+        tmem_ld_32x32b_x32(s_col, x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty);
         {
           const uint64_t nl2 = pack_f32x2(nlse, nlse);
 #pragma unroll
-          for (int j = 0; j < kHalf; j += 2) {
+          for (int j = 0; j < kCols; j += 2) {
             float a0, a1;
             unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, nl2), a0, a1);
             x[j] = ex2(a0);
             x[j + 1] = ex2(a1);
           }
         }
-        if (!full) {
-          uint32_t w0 = 0u, w1 = 0u;
-          if (in) keep_words(cols, lane, lo, hi, seg, w0, w1);
-          keep_only(x, w0, w1);
-        }
+        if (!full) keep_only(x, in ? keep_bits(cp, cs, lane, lo, hi, seg) : 0u);
         if (done_row >= 0 && !finish(item)) { ok = false; break; }
         if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) { ok = false; break; }
         dpph ^= 1;
         tc_fence_after();
-        float y[kHalf];
-        tmem_ld64(dp_col, y);
+        float y[kCols];
+        tmem_ld_32x32b_x32(dp_col, y);
         {
           const uint64_t nd2 = pack_f32x2(ndelta, ndelta);
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int i = c * 32 + 2 * j;
-              float a0, a1;
-              unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), nd2), pack_f32x2(x[i], x[i + 1])), a0, a1);
-              pk[j] = pack_bf16(a0, a1);
-            }
-            tmem_st_32x32b_x16_u_nw(dp_col + c * 16, pk);
+          for (int j = 0; j < 16; ++j) {
+            const int i = 2 * j;
+            float a0, a1;
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), nd2), pack_f32x2(x[i], x[i + 1])), a0, a1);
+            pk[j] = pack_bf16(a0, a1);
           }
+          tmem_st_32x32b_x16_u_nw(dp_col, pk);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1249,7 +1213,7 @@ int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, con
   p.B = B; p.T = T; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
   p.nb = T / kM;
   p.nbkv = T / kv_block;
-  p.tpb = kv_block / kHalf;
+  p.tpb = kv_block / kSub;
   p.causal = causal;
   p.window_left = window_left;
   p.window_right = window_right;

@@ -218,6 +218,19 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float* out) {
   for (int i = 0; i < 32; ++i) out[i] = __uint_as_float(r[i]);
 }
 
+// 32 lanes x 16 consecutive 32-bit columns from TMEM, waited for.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float* out) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(out[0]), "=f"(out[1]), "=f"(out[2]), "=f"(out[3]), "=f"(out[4]), "=f"(out[5]),
+        "=f"(out[6]), "=f"(out[7]), "=f"(out[8]), "=f"(out[9]), "=f"(out[10]), "=f"(out[11]),
+        "=f"(out[12]), "=f"(out[13]), "=f"(out[14]), "=f"(out[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns from TMEM without the completion wait: the
 // values may be used only after tmem_wait_ld() and a tmem_ld_ready() on each of them.
 // The destinations are the caller's float registers themselves, so nothing reads them
