@@ -47,6 +47,14 @@ namespace {
 
 using namespace ptx;
 
+// warp_wait behind one probe: most waits here find their phase over, and the step's chain of them is
+// what it takes longest for (8192 tokens: dK / dV 372 -> 350 us, dQ 272 -> 257).
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const Abort& ab, unsigned role,
+                                           unsigned bar_id, int item) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity))) return true;
+  return warp_wait(bar, parity, ab, role, bar_id, item);
+}
+
 constexpr int kM = 128;           // query rows, and keys, of a tile
 constexpr int kSub = 64;          // keys of a tile of the bounds
 constexpr int kCols = 32;         // columns of a tile that one softmax warpgroup takes
@@ -77,6 +85,8 @@ struct Params {
   float* nlse;      // [B, Hq, T]  -LSE in log2 units; -inf for rows without a key
   float* ndelta;    // [B, Hq, T]  -Delta
   int4* reach;      // [B, nb]     query blocks [x, y) reach this key tile, z of them
+  int4* q_cols;     // [B, T / 32] 32 queries' positions and segments (see Cols)
+  int4* kv_cols;    // [B, T / 32] ... and keys'
   int* next;        // next item of dK / dV, of dQ
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
@@ -108,7 +118,8 @@ __device__ __forceinline__ Range block_range(const Params& p, int b, int qblk) {
 
 // ------------------------------------------------------------------ 1. prep
 // Blocks [0, n_delta): 32 tokens x 8 heads each, 16 bytes a thread and row (D / 8 threads a row),
-// transposed through shared memory.  The blocks behind them: a warp for each key tile's reach.
+// transposed through shared memory.  The blocks behind them: a warp for each key tile's reach, and one
+// for each 32 queries and each 32 keys.
 constexpr int kPrepTok = 32, kPrepHeads = 8;
 template <int D>
 __global__ void __launch_bounds__(256) bsa_bwd_prep_kernel(const Params p, int n_delta, int tok_groups,
@@ -168,8 +179,25 @@ __global__ void __launch_bounds__(256) bsa_bwd_prep_kernel(const Params p, int n
     }
     return;
   }
-  const int item = (blockIdx.x - n_delta) * 8 + warp;
-  if (item >= p.B * p.nb) return;
+  int item = (blockIdx.x - n_delta) * 8 + warp;
+  if (item >= p.B * p.nb) {
+    // the warps behind those: 32 tokens' positions and segments, of the queries and of the keys
+    item -= p.B * p.nb;
+    const int groups = p.B * p.nb * (kM / 32);
+    if (item >= 2 * groups) return;
+    const bool keys = item >= groups;
+    if (keys) item -= groups;
+    const int pos = (keys ? p.kv_pos : p.q_pos)[item * 32 + lane], seg = (keys ? p.kv_seg : p.q_seg)[item * 32 + lane];
+    const int p0 = __shfl_sync(0xffffffffu, pos, 0), s0 = __shfl_sync(0xffffffffu, seg, 0);
+    const int s1 = __shfl_sync(0xffffffffu, seg, 31);
+    const unsigned first = __ballot_sync(0xffffffffu, seg == s0);
+    const int n0 = __popc(first);
+    const bool simple = (long long)pos == (long long)p0 + lane && (seg == s0 || seg == s1) &&
+                        first == (n0 >= 32 ? 0xffffffffu : (1u << n0) - 1u);
+    const bool all = __all_sync(0xffffffffu, simple);
+    if (lane == 0) (keys ? p.kv_cols : p.q_cols)[item] = make_int4(p0, s0, s1, all ? n0 : -1);
+    return;
+  }
   const int b = item / p.nb, kt = item % p.nb;
   int first = INT_MAX, last = -1, n = 0;
   for (int q0 = 0; q0 < p.nb; q0 += 32) {
@@ -214,57 +242,87 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h2);
 }
 
+// What prep says of 32 neighbouring tokens: x the first one's position, y and z the first and the
+// last one's segment, w how many have segment y, or -1 if they are not at consecutive positions in
+// one run of segment y and one of z.
+using Cols = int4;
+
 // Columns of a warp that a row may pair with, as bits: same segment as the row's and a position in
-// [lo, hi] (none if lo > hi).  Lane j holds column j's position and segment.  Columns at consecutive
-// positions in one segment, or in two runs of one each (a document boundary, the start of padding),
-// give every row one interval; others are tested one by one.
-__device__ __forceinline__ uint32_t keep_bits(int cp, int cs, int lane, long long lo, long long hi, int seg) {
-  const unsigned kAll = 0xffffffffu;
-  const int p0 = __shfl_sync(kAll, cp, 0), s0 = __shfl_sync(kAll, cs, 0), s1 = __shfl_sync(kAll, cs, 31);
-  const unsigned first = __ballot_sync(kAll, cs == s0);
-  const int n0 = __popc(first);  // columns of segment s0, a prefix if they are one run
-  const bool simple = (long long)cp == (long long)p0 + lane && (cs == s0 || cs == s1) &&
-                      first == (n0 >= 32 ? kAll : (1u << n0) - 1u);
+// [lo, hi] (none if lo > hi).  Consecutive positions in two runs of one segment each (a document
+// boundary, the start of padding) or in one give every row one interval; others are tested one by
+// one.
+__device__ __forceinline__ uint32_t keep_bits(const Cols& c, const int* pos, const int* segs, int lane, int lo, int hi,
+                                              int seg) {
   uint32_t w = 0u;
-  if (__all_sync(kAll, simple)) {
-    if (lo <= hi && (seg == s0 || seg == s1)) {
-      const int jlo = static_cast<int>(min(max(lo - p0, seg == s0 ? 0LL : (long long)n0), 32LL));
-      const int jhi = static_cast<int>(max(min(hi - p0, seg == s0 ? n0 - 1LL : 31LL), -1LL));
-      if (jlo <= jhi) w = (jhi >= 31 ? kAll : (2u << jhi) - 1u) & (kAll << jlo);
+  if (c.w >= 0) {
+    if (lo <= hi && (seg == c.y || seg == c.z)) {
+      const int jlo = static_cast<int>(min(max((long long)lo - c.x, seg == c.y ? 0LL : (long long)c.w), 32LL));
+      const int jhi = static_cast<int>(max(min((long long)hi - c.x, seg == c.y ? c.w - 1LL : 31LL), -1LL));
+      if (jlo <= jhi) w = (jhi >= 31 ? 0xffffffffu : (2u << jhi) - 1u) & (0xffffffffu << jlo);
     }
   } else {
+    const int cp = pos[lane], cs = segs[lane];
     for (int j = 0; j < 32; ++j) {
-      const int pj = __shfl_sync(kAll, cp, j), sj = __shfl_sync(kAll, cs, j);
+      const int pj = __shfl_sync(0xffffffffu, cp, j), sj = __shfl_sync(0xffffffffu, cs, j);
       w |= (sj == seg && pj >= lo && pj <= hi) ? 1u << j : 0u;
     }
   }
   return w;
 }
-__device__ __forceinline__ void keep_only(float (&x)[kCols], uint32_t w) {
-#pragma unroll
-  for (int j = 0; j < kCols; ++j) x[j] = (w & (1u << j)) ? x[j] : 0.f;
+
+// The positions [lo, hi] that a token at `pos` pairs with: as a query `before` positions back and
+// `after` on (-1: all), as a key the other way round.  Positions are 32-bit, so the ends may be
+// clamped to that range.
+__device__ __forceinline__ void in_view(int pos, int before, int after, int& lo, int& hi) {
+  lo = before < 0 ? INT_MIN : static_cast<int>(max((long long)pos - before, (long long)INT_MIN));
+  hi = after < 0 ? INT_MAX : static_cast<int>(min((long long)pos + after, (long long)INT_MAX));
 }
 
-// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16 to `to`.
+// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16.  `to`: this lane's row, the
+// rows of neighbouring lanes `stride` elements apart.  A row's columns are N / 8 chunks of 16 bytes;
+// lanes in groups of as many exchange them, so that each store of the group fills one row's 2 N bytes
+// (a lane storing its own row's chunks writes half a sector to each of 32 lines at a time: with D = 128
+// some 2000 cycles for a tile, of the 25000 of a dQ item).
 template <int N>
-__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to) {
+__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane) {
   float x[N];
   if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
+  constexpr int kChunks = N / 8;
+  uint32_t v[kChunks][4];
 #pragma unroll
-  for (int j = 0; j < N; j += 8)
-    *reinterpret_cast<uint4*>(to + j) =
-        make_uint4(pack_bf16(x[j] * f, x[j + 1] * f), pack_bf16(x[j + 2] * f, x[j + 3] * f),
-                   pack_bf16(x[j + 4] * f, x[j + 5] * f), pack_bf16(x[j + 6] * f, x[j + 7] * f));
+  for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[c][j] = pack_bf16(x[c * 8 + 2 * j] * f, x[c * 8 + 2 * j + 1] * f);
+  // transpose chunks against lanes: afterwards v[i] is this lane's chunk of row i of its group
+#pragma unroll
+  for (int s = 1; s < kChunks; s <<= 1) {
+    const bool odd = (lane & s) != 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      if (c & s) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[c][j] : v[c | s][j], s);
+        if (odd) v[c][j] = got; else v[c | s][j] = got;
+      }
+    }
+  }
+  const int me = lane % kChunks;
+  __nv_bfloat16* row0 = to - me * stride + me * 8;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+    *reinterpret_cast<uint4*>(row0 + i * stride) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
 }
 
 // ------------------------------------------------------------------ 2. dK / dV
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
-enum StepFlag : int { kFirst = 1, kLast = 2, kEmpty = 4, kEnd = 8 };
+// kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
+// token mask (bit numbers).
+enum StepFlag : int { kFirst = 1, kLast = 2, kEmpty = 4, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
 struct alignas(16) StepRow {
   float nlse[kM];
   float ndelta[kM];
-  int flags, b, hkv, kt, qblk, item;
-  Range r;
+  int4 what;  // flags, first query and first key as rows of [B T], KV head
 };
 
 template <int D>
@@ -377,13 +435,16 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       item = __shfl_sync(0xffffffffu, item, 0);
       if (item >= p.n_items_kv) {
         // no more: say so in both rings
-        if (!warp_wait(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) break;
-        if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
+        if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
+        if (lane == 0) {
+          row_at(rs).what.x = kEnd;
+          mbar_arrive(&row_full[rs]);
+        }
+        __syncwarp();
+        if (!wait_phase(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) break;
         if (lane == 0) {
           step_flags[qs] = kEnd;
-          row_at(rs).flags = kEnd;
           mbar_arrive(&q_full[qs]);
-          mbar_arrive(&row_full[rs]);
         }
         __syncwarp();
         q_out &= ~(1u << qs);  // the last loads there were taken, and their phases are over
@@ -395,10 +456,9 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const int4 reach = p.reach[b * p.nb + kt];
       const int n_steps = reach.z * p.G;
       if (n_steps == 0) {
-        if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
+        if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
         if (lane == 0) {
-          StepRow& r = row_at(rs);
-          r.flags = kEmpty; r.b = b; r.hkv = hkv; r.kt = kt; r.item = item;
+          row_at(rs).what = make_int4(kEmpty, 0, b * p.T + kt * kM, hkv);
           mbar_arrive(&row_full[rs]);
         }
         __syncwarp();
@@ -411,21 +471,38 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       for (int q0 = reach.x; q0 < reach.y && ok; q0 += 32) {
         Range mine{0, 0, 0, 0};
         if (q0 + lane < reach.y) mine = block_range(p, b, q0 + lane);
-        unsigned hits = __ballot_sync(0xffffffffu, mine.lo < 2 * kt + 2 && mine.up > 2 * kt);
+        int views = 0;  // of this lane's query block: kIn and kFull bits
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ti = 2 * kt + i;
+          const bool in = ti >= mine.lo && ti < mine.up;
+          views |= (in ? 1 << (kIn + i) : 0) | (in && ti >= mine.lof && ti < mine.upf ? 1 << (kFull + i) : 0);
+        }
+        unsigned hits = __ballot_sync(0xffffffffu, views != 0);
         while (hits != 0u && ok && step < n_steps) {
           const int at = __ffs(hits) - 1;
           hits &= hits - 1u;
-          Range r;
-          r.lo = __shfl_sync(0xffffffffu, mine.lo, at);
-          r.up = __shfl_sync(0xffffffffu, mine.up, at);
-          r.lof = __shfl_sync(0xffffffffu, mine.lof, at);
-          r.upf = __shfl_sync(0xffffffffu, mine.upf, at);
+          const int seen = __shfl_sync(0xffffffffu, views, at);
           const int qblk = q0 + at;
           for (int g = 0; g < p.G; ++g, ++step) {
             const int h = hkv * p.G + g, tok0 = b * p.T + qblk * kM;
             const int flags = (step == 0 ? kFirst : 0) | (step == n_steps - 1 ? kLast : 0);
+            // the step's row goes out first: the softmax warps look it up before they free the tiles that
+            // its other loads wait for
+            if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
+            if (lane == 0) {
+              StepRow& w = row_at(rs);
+              w.what = make_int4(flags | seen | (g > 0 ? kSame : 0), tok0, key0, hkv);
+              const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
+              mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
+              bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
+              bulk_load(w.ndelta, p.ndelta + o, kM * 4, &row_full[rs]);
+            }
+            __syncwarp();
+            r_out |= 1u << rs; r_last = (r_last & ~(1u << rs)) | (rph << rs);
+            if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
             if (step == 0) {
-              if (!warp_wait(k_empty, kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
+              if (!wait_phase(k_empty, kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
               if (lane == 0) {
                 mbar_arrive_expect_tx(k_full, C::kTile);
 #pragma unroll
@@ -434,7 +511,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               k_out = true; kph ^= 1;
             }
-            if (!warp_wait(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
+            if (!wait_phase(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               step_flags[qs] = flags;
               mbar_arrive_expect_tx(&q_full[qs], C::kTile);
@@ -445,7 +522,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             q_out |= 1u << qs; q_last = (q_last & ~(1u << qs)) | (qph << qs);
             if (++qs == C::kQStages) { qs = 0; qph ^= 1; }
             if (step == 0) {
-              if (!warp_wait(v_empty, vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
+              if (!wait_phase(v_empty, vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
               if (lane == 0) {
                 mbar_arrive_expect_tx(v_full, C::kTile);
 #pragma unroll
@@ -454,7 +531,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               v_out = true; vph ^= 1;
             }
-            if (!warp_wait(&do_empty[ds], dph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
+            if (!wait_phase(&do_empty[ds], dph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               mbar_arrive_expect_tx(&do_full[ds], C::kTile);
 #pragma unroll
@@ -463,18 +540,6 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             d_out |= 1u << ds; d_last = (d_last & ~(1u << ds)) | (dph << ds);
             if (++ds == C::kDoStages) { ds = 0; dph ^= 1; }
-            if (!warp_wait(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
-            if (lane == 0) {
-              StepRow& w = row_at(rs);
-              w.flags = flags; w.b = b; w.hkv = hkv; w.kt = kt; w.qblk = qblk; w.item = item; w.r = r;
-              const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
-              mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
-              bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
-              bulk_load(w.ndelta, p.ndelta + o, kM * 4, &row_full[rs]);
-            }
-            __syncwarp();
-            r_out |= 1u << rs; r_last = (r_last & ~(1u << rs)) | (rph << rs);
-            if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
           }
         }
       }
@@ -507,11 +572,11 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint32_t qph = 0, dph = 0, kph = 0, vph = 0, pph = 0, dsph = 0, accph = 0;
     // S of the step in Q stage qs; its flags, or kEnd
     auto issue_s = [&](int& flags) -> bool {
-      if (!warp_wait(&q_full[qs], qph, ab, kRoleMma, kBarQFull, -1)) return false;
+      if (!wait_phase(&q_full[qs], qph, ab, kRoleMma, kBarQFull, -1)) return false;
       flags = step_flags[qs];
       if (flags & kEnd) return true;
       if (flags & kFirst) {
-        if (!warp_wait(k_full, kph, ab, kRoleMma, kBarKFull, -1)) return false;
+        if (!wait_phase(k_full, kph, ab, kRoleMma, kBarKFull, -1)) return false;
         kph ^= 1;
       }
       tc_fence_after();
@@ -526,10 +591,10 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     };
     auto issue_dp = [&](int flags) -> bool {
       if (flags & kFirst) {
-        if (!warp_wait(v_full, vph, ab, kRoleMma, kBarVFull, -1)) return false;
+        if (!wait_phase(v_full, vph, ab, kRoleMma, kBarVFull, -1)) return false;
         vph ^= 1;
       }
-      if (!warp_wait(&do_full[ds], dph, ab, kRoleMma, kBarDoFull, -1)) return false;
+      if (!wait_phase(&do_full[ds], dph, ab, kRoleMma, kBarDoFull, -1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
@@ -545,10 +610,10 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int cq = 0, cd = 0;  // stages of the current step's Q and dO
     while (ok && !(cur & kEnd)) {
       // dV += P^T dO
-      if (!warp_wait(p_full, pph, ab, kRoleMma, kBarPFull, -1)) break;
+      if (!wait_phase(p_full, pph, ab, kRoleMma, kBarPFull, -1)) break;
       pph ^= 1;
       if (cur & kFirst) {
-        if (!warp_wait(acc_empty, accph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
+        if (!wait_phase(acc_empty, accph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
         accph ^= 1;
       }
       tc_fence_after();
@@ -560,7 +625,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (++cd == C::kDoStages) cd = 0;
       if (!issue_s(next)) break;
       // dK += dS^T Q
-      if (!warp_wait(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
+      if (!wait_phase(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
       dsph ^= 1;
       tc_fence_after();
 #pragma unroll
@@ -585,123 +650,137 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
-    int rs = 0;
+    int rs = 0, next_rs = 0;       // row slots of the step and of the one looked up
     uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
-    long long done_row = -1;       // first element of this thread's key in dk / dv, of a finished item
-    long long lo = 1, hi = 0;      // query positions that may see this key
-    int seg = 0;
+    int done_row = -1;             // this thread's key (times heads) of a finished item
+    int lo = 1, hi = 0, seg = 0;   // query positions that may see this key, and its segment
+    // The step to come: its flags, this thread's key, and the columns that pair with it.  Looked up
+    // while the step before waits for dP.
+    int flags = 0, row = 0;
+    uint32_t keep = 0u;
+    auto look_up = [&]() -> bool {
+      if (!wait_phase(&row_full[next_rs], rph, ab, kRoleSoftmax, kBarRowFull, -1)) return false;
+      const int4 st = row_at(next_rs).what;
+      flags = st.x;
+      if (++next_rs == C::kRowSlots) { next_rs = 0; rph ^= 1; }
+      if (flags & kEnd) return true;
+      if (flags & (kFirst | kEmpty)) row = (st.z + r) * p.Hkv + st.w;
+      if (flags & (kEmpty | kSame)) return true;
+      const int mine = flags >> (q4 >> 1);  // this warp's 64 keys
+      const bool in = (mine >> kIn) & 1, full = (mine >> kFull) & 1;
+      Cols cols{};
+      const int col = st.y + w * kCols;
+      if (in && !full) cols = p.q_cols[col / 32];
+      if (flags & kFirst) {
+        // key k is seen from position q iff k <= q (causal), q - k <= left, k - q <= right
+        const int key = st.z + r;
+        in_view(p.kv_pos[key], p.causal ? 0 : p.window_right, p.window_left, lo, hi);
+        seg = p.kv_seg[key];
+        if (seg == p.pad_id) { lo = 1; hi = 0; }
+      }
+      keep = full ? 0xffffffffu : (in ? keep_bits(cols, p.q_pos + col, p.q_seg + col, lane, lo, hi, seg) : 0u);
+      return true;
+    };
+    auto free_row = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&row_empty[rs]);
+      if (++rs == C::kRowSlots) rs = 0;
+    };
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    auto finish = [&](int item) -> bool {
-      if (!warp_wait(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
+    auto finish = [&]() -> bool {
+      if (!wait_phase(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, row)) return false;
       accph ^= 1;
       tc_fence_after();
-      store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + done_row + w * (D / 4));
-      store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + done_row + w * (D / 4));
+      const long long to = (long long)done_row * D + w * (D / 4);
+      store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, (long long)p.Hkv * D, lane);
+      store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, (long long)p.Hkv * D, lane);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
       done_row = -1;
       return true;
     };
+    // P of a step, then the step behind it is looked up, then dS: look_up and finish are each written
+    // once, as the loop's code has to share the instruction caches with the other warps' (two copies of
+    // finish: dK / dV 350 -> 403 us at 8192 tokens).
+    bool work = false;             // a step is in hand (not before the first one, nor for empty items)
     while (true) {
-      if (!warp_wait(&row_full[rs], rph, ab, kRoleSoftmax, kBarRowFull, -1)) break;
-      const StepRow& st = row_at(rs);
-      const int flags = st.flags, item = st.item;
-      if (flags & kEnd) {
-        if (done_row >= 0) finish(-1);
-        break;
+      float x[kCols];
+      const bool last = work && (flags & kLast);
+      const int this_row = row;
+      if (work) {
+        if (!wait_phase(s_full, sph, ab, kRoleSoftmax, kBarSFull, row)) break;
+        sph ^= 1;
+        tc_fence_after();
+        tmem_ld_32x32b_x32(s_col, x);
+        {
+          const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(row_at(rs).nlse + w * kCols);
+#pragma unroll
+          for (int j = 0; j < kCols; j += 4) {
+            const ulonglong2 l4 = nl[j / 4];
+            float a0, a1, a2, a3;
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, l4.x), a0, a1);
+            unpack_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), scale2, l4.y), a2, a3);
+            x[j] = ex2(a0); x[j + 1] = ex2(a1); x[j + 2] = ex2(a2); x[j + 3] = ex2(a3);
+          }
+        }
+        if (__any_sync(0xffffffffu, keep != 0xffffffffu)) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) x[j] = (keep & (1u << j)) ? x[j] : 0.f;
+        }
+        {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+          tmem_st_32x32b_x16_u_nw(s_col, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
       }
-      const long long key = (long long)st.b * p.T + st.kt * kM + r;
-      const long long row = (key * p.Hkv + st.hkv) * D;
+      if (__builtin_expect(done_row >= 0, 0) && !finish()) break;
+      if (flags & kEnd) break;
+      if (!look_up()) break;
+      if (work) {
+        if (!wait_phase(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
+        dpph ^= 1;
+        tc_fence_after();
+        float y[kCols];
+        tmem_ld_32x32b_x32(dp_col, y);
+        {
+          const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(row_at(rs).ndelta + w * kCols);
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const int i = 2 * j;
+            const ulonglong2 d4 = nd[i / 4];
+            float a0, a1, a2, a3;
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), d4.x), pack_f32x2(x[i], x[i + 1])), a0, a1);
+            unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i + 2], y[i + 3]), d4.y), pack_f32x2(x[i + 2], x[i + 3])), a2, a3);
+            pk[j] = pack_bf16(a0, a1);
+            pk[j + 1] = pack_bf16(a2, a3);
+          }
+          tmem_st_32x32b_x16_u_nw(dp_col, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+        free_row();
+      }
+      if (last) done_row = this_row;
       if (flags & kEmpty) {
         // no query sees these keys
+        const long long to = (long long)row * D + w * (D / 4);
 #pragma unroll
         for (int j = 0; j < D / 4; j += 8) {
-          *reinterpret_cast<uint4*>(p.dk + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(p.dv + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(p.dk + to + j) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(p.dv + to + j) = make_uint4(0u, 0u, 0u, 0u);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&row_empty[rs]);
-        if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
-        continue;
+        free_row();
       }
-      if (flags & kFirst) {
-        // key k is seen from position q iff k <= q (causal), q - k <= left, k - q <= right
-        const long long kp = p.kv_pos[key];
-        seg = p.kv_seg[key];
-        lo = LLONG_MIN / 2;
-        hi = LLONG_MAX / 2;
-        if (p.causal) lo = max(lo, kp);
-        if (p.window_right >= 0) lo = max(lo, kp - p.window_right);
-        if (p.window_left >= 0) hi = min(hi, kp + p.window_left);
-        if (seg == p.pad_id) { lo = 1; hi = 0; }
-      }
-      // this warp's 64-key tile among the query block's
-      const int ti = 2 * st.kt + (q4 >> 1);
-      const bool in = ti >= st.r.lo && ti < st.r.up, full = in && ti >= st.r.lof && ti < st.r.upf;
-      int cp = 0, cs = 0;
-      if (in && !full) {
-        const long long col = (long long)st.b * p.T + st.qblk * kM + w * kCols + lane;
-        cp = p.q_pos[col];
-        cs = p.q_seg[col];
-      }
-      if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) break;
-      sph ^= 1;
-      tc_fence_after();
-      float x[kCols];
-      tmem_ld_32x32b_x32(s_col, x);
-      {
-        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(st.nlse + w * kCols);
-#pragma unroll
-        for (int j = 0; j < kCols; j += 4) {
-          const ulonglong2 l4 = nl[j / 4];
-          float a0, a1, a2, a3;
-          unpack_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), scale2, l4.x), a0, a1);
-          unpack_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), scale2, l4.y), a2, a3);
-          x[j] = ex2(a0); x[j + 1] = ex2(a1); x[j + 2] = ex2(a2); x[j + 3] = ex2(a3);
-        }
-      }
-      if (!full) keep_only(x, in ? keep_bits(cp, cs, lane, lo, hi, seg) : 0u);
-      {
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-        tmem_st_32x32b_x16_u_nw(s_col, pk);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-      if (done_row >= 0 && !finish(item)) break;
-      if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) break;
-      dpph ^= 1;
-      tc_fence_after();
-      float y[kCols];
-      tmem_ld_32x32b_x32(dp_col, y);
-      {
-        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(st.ndelta + w * kCols);
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const int i = 2 * j;
-          const ulonglong2 d4 = nd[i / 4];
-          float a0, a1, a2, a3;
-          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i], y[i + 1]), d4.x), pack_f32x2(x[i], x[i + 1])), a0, a1);
-          unpack_f32x2(mul_f32x2(add_f32x2(pack_f32x2(y[i + 2], y[i + 3]), d4.y), pack_f32x2(x[i + 2], x[i + 3])), a2, a3);
-          pk[j] = pack_bf16(a0, a1);
-          pk[j + 1] = pack_bf16(a2, a3);
-        }
-        tmem_st_32x32b_x16_u_nw(dp_col, pk);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_full);
-        mbar_arrive(&row_empty[rs]);
-      }
-      if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
-      if (flags & kLast) done_row = row;
+      work = !(flags & (kEmpty | kEnd));
     }
   }
 
@@ -814,7 +893,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       int item = 0;
       if (lane == 0) item = atomicAdd(&p.next[1], 1);
       item = __shfl_sync(0xffffffffu, item, 0);
-      if (!warp_wait(&item_empty[islot], iph ^ 1, ab, kRoleLoader, kBarItemEmpty, item)) break;
+      if (!wait_phase(&item_empty[islot], iph ^ 1, ab, kRoleLoader, kBarItemEmpty, item)) break;
       if (item >= p.n_items_dq) {
         if (lane == 0) {
           item_at(islot).n_steps = -1;
@@ -838,7 +917,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int t = 0; t < n && ok; ++t) {
         const int key0 = b * p.T + (r.lo + 2 * t) * kSub;
         if (t == 0) {
-          if (!warp_wait(q_empty, qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
+          if (!wait_phase(q_empty, qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
           if (lane == 0) {
             mbar_arrive_expect_tx(q_full, C::kTile);
 #pragma unroll
@@ -847,7 +926,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           q_last = qph;
         }
-        if (!warp_wait(&k_empty[ks], kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
+        if (!wait_phase(&k_empty[ks], kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[ks], C::kTile);
 #pragma unroll
@@ -857,7 +936,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         k_out |= 1u << ks; k_last = (k_last & ~(1u << ks)) | (kph << ks);
         if (++ks == C::kKStages) { ks = 0; kph ^= 1; }
         if (t == 0) {
-          if (!warp_wait(do_empty, qph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
+          if (!wait_phase(do_empty, qph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
           if (lane == 0) {
             mbar_arrive_expect_tx(do_full, C::kTile);
 #pragma unroll
@@ -866,7 +945,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           do_last = qph; qph ^= 1;
         }
-        if (!warp_wait(&v_empty[vs], vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
+        if (!wait_phase(&v_empty[vs], vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&v_full[vs], C::kTile);
 #pragma unroll
@@ -901,7 +980,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto next_step = [&](int& flags) -> bool {
       flags = 0;
       while (left == 0) {
-        if (!warp_wait(&item_full[islot], iph, ab, kRoleMma, kBarItemFull, -1)) return false;
+        if (!wait_phase(&item_full[islot], iph, ab, kRoleMma, kBarItemFull, -1)) return false;
         left = item_at(islot).n_steps;
         __syncwarp();
         if (left < 0) { flags = kEnd; return true; }
@@ -917,11 +996,11 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (flags & kFirst) {
         // Q of the item into tensor memory; the previous item's products that read it are done,
         // as the softmax warps have seen the last of them
-        if (!warp_wait(q_full, qph, ab, kRoleMma, kBarQFull, -1)) return false;
+        if (!wait_phase(q_full, qph, ab, kRoleMma, kBarQFull, -1)) return false;
         qph ^= 1;
       }
-      if (!warp_wait(&k_full[ks], kph, ab, kRoleMma, kBarKFull, -1) ||
-          !warp_wait(s_empty, seph ^ 1, ab, kRoleMma, kBarSEmpty, -1))
+      if (!wait_phase(&k_full[ks], kph, ab, kRoleMma, kBarKFull, -1) ||
+          !wait_phase(s_empty, seph ^ 1, ab, kRoleMma, kBarSEmpty, -1))
         return false;
       seph ^= 1;
       tc_fence_after();
@@ -941,10 +1020,10 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // dP = dO V^T over the dS that the product before it has read
     auto issue_dp = [&](int flags) -> bool {
       if (flags & kFirst) {
-        if (!warp_wait(do_full, doph, ab, kRoleMma, kBarDoFull, -1)) return false;
+        if (!wait_phase(do_full, doph, ab, kRoleMma, kBarDoFull, -1)) return false;
         doph ^= 1;
       }
-      if (!warp_wait(&v_full[vs], vph, ab, kRoleMma, kBarVFull, -1)) return false;
+      if (!wait_phase(&v_full[vs], vph, ab, kRoleMma, kBarVFull, -1)) return false;
       tc_fence_after();
       if (flags & kFirst) {
 #pragma unroll
@@ -966,10 +1045,10 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (!next_step(next)) break;
       if (!(next & kEnd) && !issue_s(next)) break;
       // dQ += dS K
-      if (!warp_wait(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
+      if (!wait_phase(ds_full, dsph, ab, kRoleMma, kBarDsFull, -1)) break;
       dsph ^= 1;
       if (cur & kFirst) {
-        if (!warp_wait(dq_empty, dqph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
+        if (!wait_phase(dq_empty, dqph ^ 1, ab, kRoleMma, kBarAccEmpty, -1)) break;
         dqph ^= 1;
       }
       tc_fence_after();
@@ -996,63 +1075,68 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
     int islot = 0;
     uint32_t iph = 0, sph = 0, dpph = 0, dqph = 0;
-    long long done_row = -1;       // first element of this thread's row in dq, of a finished item
+    int done_row = -1;             // this thread's row (token times heads) of a finished item
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-    auto finish = [&](int item) -> bool {
-      if (!warp_wait(dq_full, dqph, ab, kRoleSoftmax, kBarAccFull, item)) return false;
+    auto finish = [&]() -> bool {
+      if (!wait_phase(dq_full, dqph, ab, kRoleSoftmax, kBarAccFull, done_row)) return false;
       dqph ^= 1;
       tc_fence_after();
-      store_cols<D / 4>(tmem + lane_off + C::kDqCol + w * (D / 4), p.scale, p.dq + done_row + w * (D / 4));
+      store_cols<D / 4>(tmem + lane_off + C::kDqCol + w * (D / 4), p.scale,
+                        p.dq + (long long)done_row * D + w * (D / 4), (long long)p.Hq * D, lane);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_empty);
       done_row = -1;
       return true;
     };
-    bool ok = true;
-    while (ok) {
-      if (!warp_wait(&item_full[islot], iph, ab, kRoleSoftmax, kBarItemFull, -1)) break;
-      const DqItem& it = item_at(islot);
-      const int n = it.n_steps, item = it.item;
-      if (n < 0) {
-        if (done_row >= 0) finish(-1);
-        break;
-      }
-      const int b = it.b, h = it.h;
-      const Range rg = it.r;
-      const long long tok = (long long)b * p.T + it.qblk * kM + r;
-      const long long o = ((long long)b * p.Hq + h) * p.T + it.qblk * kM + r;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[islot]);
-      if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
-      const long long row = (tok * p.Hq + h) * D;
-      if (n == 0) {
+    // The item: steps left, this thread's row, the key positions that it sees and its segment, the
+    // first key of the step's columns and the tiles of the bounds from there on.  The next one is
+    // looked up within the last step, once that needs no more of these than ndelta.
+    int left = 0, row = 0, lo = 0, hi = 0, seg = 0, col = 0;
+    Range rg{};
+    float nlse = 0.f, ndelta = 0.f, ndelta_next = 0.f;
+    auto look_up = [&]() -> bool {
+      while (true) {
+        if (!wait_phase(&item_full[islot], iph, ab, kRoleSoftmax, kBarItemFull, -1)) return false;
+        const DqItem& it = item_at(islot);
+        left = it.n_steps;
+        const int b = it.b, h = it.h, t0 = it.qblk * kM + r;
+        rg = it.r;
+        __syncwarp();
+        if (left < 0) return true;
+        if (lane == 0) mbar_arrive(&item_empty[islot]);
+        if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
+        const int tok = b * p.T + t0;
+        row = tok * p.Hq + h;
+        if (left == 0) {
+          // a query block without keys
 #pragma unroll
-        for (int j = 0; j < D / 4; j += 8)
-          *reinterpret_cast<uint4*>(p.dq + row + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      const float nlse = p.nlse[o], ndelta = p.ndelta[o];
-      const int seg = p.q_seg[tok];
-      const long long qp = p.q_pos[tok];
-      long long lo = LLONG_MIN / 2, hi = LLONG_MAX / 2;
-      if (p.causal) hi = min(hi, qp);
-      if (p.window_left >= 0) lo = max(lo, qp - p.window_left);
-      if (p.window_right >= 0) hi = min(hi, qp + p.window_right);
-      if (seg == p.pad_id) { lo = 1; hi = 0; }
-      for (int t = 0; t < n; ++t) {
-        const int ti = rg.lo + 2 * t + (w >> 1);
-        const bool in = ti < rg.up, full = in && ti >= rg.lof && ti < rg.upf;
-        int cp = 0, cs = 0;
-        if (in && !full) {
-          const long long col = (long long)b * p.T + ti * kSub + (w & 1) * kCols + lane;
-          cp = p.kv_pos[col];
-          cs = p.kv_seg[col];
+          for (int j = 0; j < D / 4; j += 8)
+            *reinterpret_cast<uint4*>(p.dq + (long long)row * D + w * (D / 4) + j) = make_uint4(0u, 0u, 0u, 0u);
+          continue;
         }
-        if (!warp_wait(s_full, sph, ab, kRoleSoftmax, kBarSFull, item)) { ok = false; break; }
+        const int o = (b * p.Hq + h) * p.T + t0;
+        nlse = p.nlse[o];
+        ndelta_next = p.ndelta[o];
+        seg = p.q_seg[tok];
+        in_view(p.q_pos[tok], p.window_left, p.causal ? 0 : p.window_right, lo, hi);
+        if (seg == p.pad_id) { lo = 1; hi = 0; }
+        rg.lo += w >> 1;  // this warp's 64-key tile of the step
+        col = b * p.T + rg.lo * kSub + (w & 1) * kCols;
+        return true;
+      }
+    };
+    // as in dK / dV: P of a step, what comes next, dS
+    bool work = false;
+    while (true) {
+      float x[kCols];
+      if (work) {
+        const bool in = rg.lo < rg.up, full = in && rg.lo >= rg.lof && rg.lo < rg.upf;
+        Cols cols{};
+        if (in && !full) cols = p.kv_cols[col / 32];
+        if (!wait_phase(s_full, sph, ab, kRoleSoftmax, kBarSFull, row)) break;
         sph ^= 1;
         tc_fence_after();
-        float x[kCols];
         tmem_ld_32x32b_x32(s_col, x);
         tc_fence_before();
         __syncwarp();
@@ -1067,9 +1151,25 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             x[j + 1] = ex2(a1);
           }
         }
-        if (!full) keep_only(x, in ? keep_bits(cp, cs, lane, lo, hi, seg) : 0u);
-        if (done_row >= 0 && !finish(item)) { ok = false; break; }
-        if (!warp_wait(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, item)) { ok = false; break; }
+        if (!full) {
+          const uint32_t keep = in ? keep_bits(cols, p.kv_pos + col, p.kv_seg + col, lane, lo, hi, seg) : 0u;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) x[j] = (keep & (1u << j)) ? x[j] : 0.f;
+        }
+      }
+      if (__builtin_expect(done_row >= 0, 0) && !finish()) break;
+      if (left < 0) break;
+      const bool had = work, last = work && --left == 0;
+      if (last) done_row = row;
+      if (last || !work) {
+        if (!look_up()) break;
+        work = left > 0;
+      } else {
+        rg.lo += 2;
+        col += kM;
+      }
+      if (had) {
+        if (!wait_phase(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
         dpph ^= 1;
         tc_fence_after();
         float y[kCols];
@@ -1091,8 +1191,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      if (!ok) break;
-      done_row = row;
+      if (last || !had) ndelta = ndelta_next;
     }
   }
 
@@ -1108,7 +1207,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
 // ------------------------------------------------------------------ host
 struct Layout {
-  size_t nlse, ndelta, reach, next, total;
+  size_t nlse, ndelta, reach, q_cols, kv_cols, next, total;
 };
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 Layout layout(int B, int T, int Hq) {
@@ -1118,6 +1217,9 @@ Layout layout(int B, int T, int Hq) {
   l.nlse = o;   o += round256(rows);
   l.ndelta = o; o += round256(rows);
   l.reach = o;  o += round256(static_cast<size_t>(B) * (T / kM) * sizeof(int4));
+  const size_t cols = static_cast<size_t>(B) * (T / 32) * sizeof(int4);
+  l.q_cols = o; o += round256(cols);
+  l.kv_cols = o; o += round256(cols);
   l.next = o;   o += 256;
   l.total = o;
   return l;
@@ -1157,7 +1259,7 @@ int launch_impl(const void* q, const void* k, const void* v, const void* d_out, 
     e = cudaFuncSetAttribute(bsa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd: set smem attribute");
   const int tok_groups = p.T / kPrepTok, head_groups = (p.Hq + kPrepHeads - 1) / kPrepHeads;
-  const int n_delta = p.B * tok_groups * head_groups, n_reach = (p.B * p.nb + 7) / 8;
+  const int n_delta = p.B * tok_groups * head_groups, n_reach = (9 * p.B * p.nb + 7) / 8;  // 1 + 2 * 128 / 32 warps a block
   bsa_bwd_prep_kernel<D><<<n_delta + n_reach, 256, 0, stream>>>(p, n_delta, tok_groups, head_groups);
   e = cudaGetLastError();
   if (e == cudaSuccess)
@@ -1206,6 +1308,8 @@ int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, con
   p.nlse = reinterpret_cast<float*>(ws + l.nlse);
   p.ndelta = reinterpret_cast<float*>(ws + l.ndelta);
   p.reach = reinterpret_cast<int4*>(ws + l.reach);
+  p.q_cols = reinterpret_cast<int4*>(ws + l.q_cols);
+  p.kv_cols = reinterpret_cast<int4*>(ws + l.kv_cols);
   p.next = reinterpret_cast<int*>(ws + l.next);
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
