@@ -295,8 +295,8 @@ SBA_API int sba_blocksparse_attn_fwd(const void* q, const void* k, const void* v
 
 /*
  * sba_blocksparse_attn_bwd_workspace_size -- bytes of device workspace that
- * sba_blocksparse_attn_bwd needs (24 bytes per query row, and the query blocks that
- * reach each key tile).  Returns 0 for sizes that it does not support.
+ * sba_blocksparse_attn_bwd needs (8 bytes per query row, and a few per token).
+ * Returns 0 for sizes that it does not support.
  */
 SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq);
 

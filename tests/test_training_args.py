@@ -62,7 +62,7 @@ def test_gradients(sba, kw, code, says):
 def test_gradient_workspace(sba):
     size = sba.blocksparse_attn_bwd_workspace_size
     up = lambda n: -(-n // 256) * 256  # noqa: E731
-    assert size(2, 1024, 6) == 2 * up(2 * 1024 * 6 * 4) + up(2 * 1024 * 6 * 16) + up(2 * 8 * 16) + 2 * up(2 * 32 * 16) + 256
+    assert size(2, 1024, 6) == 2 * up(2 * 1024 * 6 * 4) + up(2 * 8 * 16) + 2 * up(2 * 32 * 16) + 256
     assert size(1, 200, 4) == size(0, 128, 4) == size(1, 128, 0) == size(1, 1 << 20, 2048) == 0
 
 
