@@ -318,7 +318,7 @@ __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* t
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
 // kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
 // token mask (bit numbers).
-enum StepFlag : int { kFirst = 1, kLast = 2, kEmpty = 4, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
+enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
 struct alignas(16) StepRow {
   float nlse[kM];
   float ndelta[kM];
@@ -357,6 +357,18 @@ __device__ __forceinline__ void kv_item(const Params& p, int item, int& b, int& 
   const int g = win * kGroupWindow + rem % wsz;
   hkv = g % p.Hkv;
   b = g / p.Hkv;
+}
+
+// dK and dV of a tile of keys set to zero by one warp.
+template <int D>
+__device__ __forceinline__ void zero_rows(const Params& p, int key0, int hkv, int lane) {
+  constexpr int kChunks = D / 8;  // of 16 bytes a row
+#pragma unroll 1
+  for (int i = lane; i < kM * kChunks; i += 32) {
+    const long long at = ((long long)(key0 + i / kChunks) * p.Hkv + hkv) * D + i % kChunks * 8;
+    *reinterpret_cast<uint4*>(p.dk + at) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(p.dv + at) = make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
 template <int D>
@@ -455,19 +467,15 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       kv_item(p, item, b, hkv, kt);
       const int4 reach = p.reach[b * p.nb + kt];
       const int n_steps = reach.z * p.G;
+      const int key0 = b * p.T + kt * kM;
       if (n_steps == 0) {
-        if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) break;
-        if (lane == 0) {
-          row_at(rs).what = make_int4(kEmpty, 0, b * p.T + kt * kM, hkv);
-          mbar_arrive(&row_full[rs]);
-        }
-        __syncwarp();
-        r_out &= ~(1u << rs);
-        if (++rs == C::kRowSlots) { rs = 0; rph ^= 1; }
+        // No query sees these keys.  The zeros are written from here, as many such tiles may follow one
+        // another: in the row ring they would wait for the softmax warps, these in finish() for the last
+        // item's sums, the MMA warp before those for the next item's Q, and that for this warp.
+        zero_rows<D>(p, key0, hkv, lane);
         continue;
       }
       int step = 0;
-      const int key0 = b * p.T + kt * kM;
       for (int q0 = reach.x; q0 < reach.y && ok; q0 += 32) {
         Range mine{0, 0, 0, 0};
         if (q0 + lane < reach.y) mine = block_range(p, b, q0 + lane);
@@ -664,8 +672,8 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       flags = st.x;
       if (++next_rs == C::kRowSlots) { next_rs = 0; rph ^= 1; }
       if (flags & kEnd) return true;
-      if (flags & (kFirst | kEmpty)) row = (st.z + r) * p.Hkv + st.w;
-      if (flags & (kEmpty | kSame)) return true;
+      if (flags & kFirst) row = (st.z + r) * p.Hkv + st.w;
+      if (flags & kSame) return true;
       const int mine = flags >> (q4 >> 1);  // this warp's 64 keys
       const bool in = (mine >> kIn) & 1, full = (mine >> kFull) & 1;
       Cols cols{};
@@ -703,7 +711,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     // P of a step, then the step behind it is looked up, then dS: look_up and finish are each written
     // once, as the loop's code has to share the instruction caches with the other warps' (two copies of
     // finish: dK / dV 350 -> 403 us at 8192 tokens).
-    bool work = false;             // a step is in hand (not before the first one, nor for empty items)
+    bool work = false;             // a step is in hand
     while (true) {
       float x[kCols];
       const bool last = work && (flags & kLast);
@@ -770,17 +778,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         free_row();
       }
       if (last) done_row = this_row;
-      if (flags & kEmpty) {
-        // no query sees these keys
-        const long long to = (long long)row * D + w * (D / 4);
-#pragma unroll
-        for (int j = 0; j < D / 4; j += 8) {
-          *reinterpret_cast<uint4*>(p.dk + to + j) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(p.dv + to + j) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        free_row();
-      }
-      work = !(flags & (kEmpty | kEnd));
+      work = !(flags & kEnd);
     }
   }
 

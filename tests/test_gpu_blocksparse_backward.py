@@ -285,6 +285,17 @@ def test_many_items_a_block(sba):
     check_all(sba, Case(B=B, T=T, Hq=8, Hkv=4, D=64, kb=64, seg=seg, seed=130).forward())
 
 
+@pytest.mark.parametrize("D,seen", [(64, 512), (128, 128), (128, 256)])
+def test_runs_of_unseen_key_tiles(sba, D, seen):
+    """More key tiles than blocks on the GPU, and after every few that queries see many that none does:
+    a block takes several of those behind one with sums still to store."""
+    B, T, Hq = 2, 4096, 8
+    seg = np.full((B, T), -1, np.int64)
+    for t in range(0, T, 1024):
+        seg[:, t:t + seen] = t
+    check_all(sba, Case(B=B, T=T, Hq=Hq, Hkv=Hq, D=D, seg=seg, seed=140).forward())
+
+
 def test_full_size_sampled(sba):
     """4 x 16384 tokens, 32 heads over 8, window (1024, 0): the forward's own out and lse, dq on sampled
     tokens, dk and dv of whole key tiles from all rows that see them."""
