@@ -295,10 +295,11 @@ SBA_API int sba_blocksparse_attn_fwd(const void* q, const void* k, const void* v
 
 /*
  * sba_blocksparse_attn_bwd_workspace_size -- bytes of device workspace that
- * sba_blocksparse_attn_bwd needs (8 bytes per query row, and a few per token).
- * Returns 0 for sizes that it does not support.
+ * sba_blocksparse_attn_bwd needs (8 bytes per query row, a few per token, and with
+ * fewer key tiles and KV heads than SMs fp32 sums of dK and dV for parts of the query heads, 80 MB at
+ * most).  Returns 0 for sizes that it does not support.
  */
-SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq);
+SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq, int Hkv, int D);
 
 /*
  * sba_blocksparse_attn_bwd -- gradients of sba_blocksparse_attn_fwd with respect to q, k and v.
@@ -320,8 +321,8 @@ SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq);
  *  d_out         [B, T, Hq, D] bf16: gradient of the loss with respect to out
  *  dq            [B, T, Hq, D] bf16 (written; rows without a key get 0)
  *  dk, dv        [B, T, Hkv, D] bf16 (written; keys that no row sees get 0)
- *  workspace     device scratch of at least sba_blocksparse_attn_bwd_workspace_size(B, T, Hq)
- *                bytes, 256-byte aligned, caller-owned; needs no initialisation.  Calls that may
+ *  workspace     device scratch of at least sba_blocksparse_attn_bwd_workspace_size(B, T, Hq,
+ *                Hkv, D) bytes, 256-byte aligned, caller-owned; needs no initialisation.  Calls that may
  *                overlap on the GPU need one each.
  * q, k, v, out, d_out, lse, dq, dk and dv must be 16-byte aligned; the outputs overlap neither
  * an input nor one another (SBA_ERR_INVALID_ARG).  A key that is masked for some rows of a tile
@@ -330,8 +331,8 @@ SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq);
  * Supported, as in the forward: q_block == 128, kv_block in {64, 128}, T % 128 == 0, D in
  * {64, 128}, 1 <= Hq / Hkv, B * T * Hq < 2^31, bf16 (fp32 accumulation; P and dS are rounded to
  * bf16 before their products).  Results are the same from run to run.
- * Internally, on `stream`: a kernel that prepares the rows, the dK / dV kernel and the dQ kernel,
- * which begins while the last blocks of dK / dV run.
+ * Internally, on `stream`: a kernel that prepares the rows, the dK / dV kernel, the dQ kernel,
+ * which begins while the last blocks of dK / dV run, and a merge of dK and dV where they are in parts.
  */
 SBA_API int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                                      const float* lse, const void* d_out, const int32_t* q_pos,

@@ -104,7 +104,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                              i32p, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, cf,
                                              vp, f32p, vp]
     lib.sba_blocksparse_attn_fwd.restype = ci
-    lib.sba_blocksparse_attn_bwd_workspace_size.argtypes = [ci, ci, ci]
+    lib.sba_blocksparse_attn_bwd_workspace_size.argtypes = [ci] * 5
     lib.sba_blocksparse_attn_bwd_workspace_size.restype = csz
     lib.sba_blocksparse_attn_bwd.argtypes = [vp, vp, vp, vp, f32p, vp, i32p, i32p, i32p, i32p, i32p, i32p,
                                              i32p, i32p, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, ci, cf,
@@ -522,9 +522,9 @@ for _name in _PAGED_CALLS:
     globals()[_name] = _first_call(_name)
 
 
-def blocksparse_attn_bwd_workspace_size(B, T, Hq) -> int:
+def blocksparse_attn_bwd_workspace_size(B, T, Hq, Hkv, D) -> int:
     """Bytes of the workspace of blocksparse_attn_bwd (0 for sizes that it does not support)."""
-    return int(load_library().sba_blocksparse_attn_bwd_workspace_size(B, T, Hq))
+    return int(load_library().sba_blocksparse_attn_bwd_workspace_size(B, T, Hq, Hkv, D))
 
 
 def paged_attention_workspace_size(B, N, Hq, Hkv, D) -> int:

@@ -477,9 +477,11 @@ static bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq) {
-  if (B < 1 || T < 1 || T % 128 != 0 || Hq < 1 || (long long)B * T * Hq >= (1LL << 31)) return 0;
-  return blocksparse_bwd_workspace_bytes(B, T, Hq);
+size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq, int Hkv, int D) {
+  if (B < 1 || T < 1 || T % 128 != 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128) ||
+      (long long)B * T * Hq >= (1LL << 31))
+    return 0;
+  return blocksparse_bwd_workspace_bytes(B, T, Hq, Hkv, D);
 }
 
 int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -506,7 +508,7 @@ int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const 
   SBA_SUPPORT(D == 64 || D == 128, "D must be 64 or 128");
   SBA_SUPPORT((long long)B * T * Hq < (1LL << 31), "B * T * Hq must be < 2^31");
   const size_t rows = static_cast<size_t>(B) * T, nq = rows * Hq * D * 2, nk = rows * Hkv * D * 2;
-  const size_t need = blocksparse_bwd_workspace_bytes(B, T, Hq);
+  const size_t need = blocksparse_bwd_workspace_bytes(B, T, Hq, Hkv, D);
   SBA_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && workspace_bytes >= need,
               "workspace missing, not 256-byte aligned or smaller than "
               "sba_blocksparse_attn_bwd_workspace_size()");

@@ -477,7 +477,7 @@ PyObject* grad(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwn
       if (!ws.is_cuda() || ws.get_device() != index || !ws.is_contiguous())
         value_error("workspace must be a contiguous tensor on q's device");
     } else {
-      const size_t need = sba_blocksparse_attn_bwd_workspace_size(b, t, hq);
+      const size_t need = sba_blocksparse_attn_bwd_workspace_size(b, t, hq, size32(Hkv, "Hkv"), size32(D, "D"));
       ws = fresh({static_cast<int64_t>(need ? need : 256)}, at::kByte, index);
     }
     const int causal = truth(o[16], true), left = whole(o[17], -1), right = whole(o[18], -1), pad = whole(o[19], -1);

@@ -6,15 +6,16 @@
 //   dV = P^T dO,   dS = P * (dO V^T - Delta),   dQ = scale dS K,   dK = scale dS^T Q.
 // The probabilities are computed again from q, k and the LSE; nothing of size T x T is stored.
 //
-// Three launches, on one stream:
+// Three or four launches, on one stream:
 //   1. prep: Delta and the LSE of every row, negated and laid out [B, Hq, T], so that a tile's
 //      128 values are one run; for each key tile the query blocks whose bounds reach it (the
 //      bounds of the forward, turned round: dK and dV sum exactly the pairs that the forward
 //      used, whatever the positions are).
 //   2. dK / dV: a work item is a tile of 128 keys of one KV head; its steps are the (query
-//      block, query head) pairs that reach it.
+//      block, query head) pairs that reach it.  With few such tiles, those of a part of the heads.
 //   3. dQ: a work item is a query block of 128 tokens of one query head; its steps are the
 //      128-key tiles of its bounds.
+//   4. merge, if the heads are in parts: their dK and dV added up.
 // S and dP are computed in both (7 products for the 5 of the formulas).  The other way, one pass
 // with dQ added up in memory, needs B T Hq D fp32 sums cleared, added to by every key tile and
 // rounded at the end, some 2.7 GB beside 1.1 GB of inputs on a batch of 4 x 16384 tokens, and its
@@ -26,6 +27,10 @@
 // on the other tile.  In steady state, per step:
 //   dK / dV:  dV(i)   S(i+1)   dK(i)   dP(i+1)      softmax warps: dS(i) | P(i+1)
 //   dQ:       S(i+1)  dQ(i)    dP(i+1)              softmax warps: dS(i) | P(i+1)
+// What bounds them is the chain of the warp that issues the products: with its waits for the softmax
+// warps taken out, one row of 8192 still takes 82 % of its time, with the exponentials taken out 98 %,
+// with an eighth of the products 84 %.  Four products of 128 x 128 x 128 take the tensor core 2048 cycles
+// a step; the kernels run at 60 to 70 % of that.
 // dK / dV works on S^T = K Q^T and dP^T = V dO^T (lanes = keys), whose P^T and dS^T go back over
 // their own columns in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q straight from
 // tensor memory.  dQ holds Q and dO of the item in tensor memory as A operands as well, and dS
@@ -91,6 +96,8 @@ struct Params {
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  float* parts;     // [n_split, dK and dV, B T, Hkv, D] sums of a part of the query heads, or null
+  int n_split;      // parts of a KV head's query heads, each an item's
   int B, T, Hq, Hkv, G, nb, nbkv, tpb, causal, window_left, window_right, pad_id;
   float scale, scale_log2;
   int n_items_dq, n_items_kv;
@@ -278,22 +285,12 @@ __device__ __forceinline__ void in_view(int pos, int before, int after, int& lo,
   hi = after < 0 ? INT_MAX : static_cast<int>(min((long long)pos + after, (long long)INT_MAX));
 }
 
-// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16.  `to`: this lane's row, the
-// rows of neighbouring lanes `stride` elements apart.  A row's columns are N / 8 chunks of 16 bytes;
-// lanes in groups of as many exchange them, so that each store of the group fills one row's 2 N bytes
-// (a lane storing its own row's chunks writes half a sector to each of 32 lines at a time: with D = 128
-// some 2000 cycles for a tile, of the 25000 of a dQ item).
-template <int N>
-__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane) {
-  float x[N];
-  if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
-  constexpr int kChunks = N / 8;
-  uint32_t v[kChunks][4];
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[c][j] = pack_bf16(x[c * 8 + 2 * j] * f, x[c * 8 + 2 * j + 1] * f);
-  // transpose chunks against lanes: afterwards v[i] is this lane's chunk of row i of its group
+// A row's columns are kChunks chunks of 16 bytes, a lane holds a row: transposes chunks against lanes in
+// groups of kChunks, so that afterwards v[i] is this lane's chunk of row i of its group and a store of
+// the group fills one row (a lane storing its own row's chunks writes half a sector to each of 32 lines
+// at a time: with D = 128 some 2000 cycles for a tile of dQ, of the 25000 of its item).
+template <int kChunks>
+__device__ __forceinline__ void swap_chunks(uint32_t (&v)[kChunks][4], int lane) {
 #pragma unroll
   for (int s = 1; s < kChunks; s <<= 1) {
     const bool odd = (lane & s) != 0;
@@ -307,6 +304,21 @@ __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* t
       }
     }
   }
+}
+
+// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16.  `to`: this lane's row, the
+// rows of neighbouring lanes `stride` elements apart.
+template <int N>
+__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane) {
+  float x[N];
+  if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
+  constexpr int kChunks = N / 8;
+  uint32_t v[kChunks][4];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[c][j] = pack_bf16(x[c * 8 + 2 * j] * f, x[c * 8 + 2 * j + 1] * f);
+  swap_chunks(v, lane);
   const int me = lane % kChunks;
   __nv_bfloat16* row0 = to - me * stride + me * 8;
 #pragma unroll
@@ -314,10 +326,31 @@ __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* t
     *reinterpret_cast<uint4*>(row0 + i * stride) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
 }
 
+// The same columns in fp32, for the merge; 16 at a time, as the caller holds P meanwhile (all 32 at once
+// spilled: 8192 tokens of 16 heads in two parts 600 -> 840 us).
+template <int N>
+__device__ __forceinline__ void store_part(uint32_t a, float* to, long long stride, int lane) {
+  const int me = lane % 4;
+  float* row0 = to - me * stride + me * 4;
+#pragma unroll 1
+  for (int c = 0; c < N; c += 16) {
+    float x[16];
+    tmem_ld_32x32b_x16(a + c, x);
+    uint32_t v[4][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j / 4][j % 4] = __float_as_uint(x[j]);
+    swap_chunks(v, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(row0 + i * stride + c) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+  }
+}
+
 // ------------------------------------------------------------------ 2. dK / dV
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
 // kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
 // token mask (bit numbers).
+// kSame: the query block of the step before.  From bit 16 on: the item's part.
 enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
 struct alignas(16) StepRow {
   float nlse[kM];
@@ -346,32 +379,42 @@ struct KvCfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// Items: key tiles of windows of kGroupWindow (row, KV head) groups, tile by tile across the
-// window.  Under causal masking early key tiles have the most steps, so a window's longest items
-// go out first; the window bounds the Q and dO that the items running at once read.
+// Items: key tiles of windows of kGroupWindow (row, KV head, part of its query heads) groups, tile by
+// tile across the window.  Under causal masking early key tiles have the most steps, so a window's
+// longest items go out first; the window bounds the Q and dO that the items running at once read.
 constexpr int kGroupWindow = 8;
-__device__ __forceinline__ void kv_item(const Params& p, int item, int& b, int& hkv, int& kt) {
+__device__ __forceinline__ void kv_item(const Params& p, int item, int& b, int& hkv, int& part, int& kt) {
   const int per = kGroupWindow * p.nb, win = item / per, rem = item - win * per;
-  const int wsz = min(kGroupWindow, p.B * p.Hkv - win * kGroupWindow);
+  const int wsz = min(kGroupWindow, p.B * p.Hkv * p.n_split - win * kGroupWindow);
   kt = rem / wsz;
-  const int g = win * kGroupWindow + rem % wsz;
+  int g = win * kGroupWindow + rem % wsz;
+  part = g % p.n_split;
+  g /= p.n_split;
   hkv = g % p.Hkv;
   b = g / p.Hkv;
 }
 
 // dK and dV of a tile of keys set to zero by one warp.
-template <int D>
-__device__ __forceinline__ void zero_rows(const Params& p, int key0, int hkv, int lane) {
-  constexpr int kChunks = D / 8;  // of 16 bytes a row
+template <int D, bool kSplit>
+__device__ __forceinline__ void zero_rows(const Params& p, int part, int key0, int hkv, int lane) {
+  constexpr int kChunks = D / (kSplit ? 4 : 8);  // of 16 bytes a row
 #pragma unroll 1
   for (int i = lane; i < kM * kChunks; i += 32) {
-    const long long at = ((long long)(key0 + i / kChunks) * p.Hkv + hkv) * D + i % kChunks * 8;
-    *reinterpret_cast<uint4*>(p.dk + at) = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(p.dv + at) = make_uint4(0u, 0u, 0u, 0u);
+    const long long row = (long long)(key0 + i / kChunks) * p.Hkv + hkv;
+    const int c = i % kChunks;
+    if constexpr (kSplit) {
+      const long long rows = (long long)p.B * p.T * p.Hkv;
+      reinterpret_cast<uint4*>(p.parts + (part * 2 * rows + row) * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4*>(p.parts + ((part * 2 + 1) * rows + row) * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      reinterpret_cast<uint4*>(p.dk + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4*>(p.dv + row * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 
-template <int D>
+// kSplit: the item's sums are a part's, and leave in fp32 for the merge kernel.
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -463,16 +506,16 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         r_out &= ~(1u << rs);
         break;
       }
-      int b, hkv, kt;
-      kv_item(p, item, b, hkv, kt);
+      int b, hkv, part, kt;
+      kv_item(p, item, b, hkv, part, kt);
       const int4 reach = p.reach[b * p.nb + kt];
-      const int n_steps = reach.z * p.G;
+      const int heads = p.G / p.n_split, n_steps = reach.z * heads;
       const int key0 = b * p.T + kt * kM;
       if (n_steps == 0) {
         // No query sees these keys.  The zeros are written from here, as many such tiles may follow one
         // another: in the row ring they would wait for the softmax warps, these in finish() for the last
         // item's sums, the MMA warp before those for the next item's Q, and that for this warp.
-        zero_rows<D>(p, key0, hkv, lane);
+        zero_rows<D, kSplit>(p, part, key0, hkv, lane);
         continue;
       }
       int step = 0;
@@ -492,15 +535,15 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           hits &= hits - 1u;
           const int seen = __shfl_sync(0xffffffffu, views, at);
           const int qblk = q0 + at;
-          for (int g = 0; g < p.G; ++g, ++step) {
-            const int h = hkv * p.G + g, tok0 = b * p.T + qblk * kM;
+          for (int g = 0; g < heads; ++g, ++step) {
+            const int h = hkv * p.G + part * heads + g, tok0 = b * p.T + qblk * kM;
             const int flags = (step == 0 ? kFirst : 0) | (step == n_steps - 1 ? kLast : 0);
             // the step's row goes out first: the softmax warps look it up before they free the tiles that
             // its other loads wait for
             if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               StepRow& w = row_at(rs);
-              w.what = make_int4(flags | seen | (g > 0 ? kSame : 0), tok0, key0, hkv);
+              w.what = make_int4(flags | seen | (g > 0 ? kSame : 0) | part << 16, tok0, key0, hkv);
               const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
               mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
               bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
@@ -665,6 +708,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     // The step to come: its flags, this thread's key, and the columns that pair with it.  Looked up
     // while the step before waits for dP.
     int flags = 0, row = 0;
+    const int rows = p.B * p.T * p.Hkv;
     uint32_t keep = 0u;
     auto look_up = [&]() -> bool {
       if (!wait_phase(&row_full[next_rs], rph, ab, kRoleSoftmax, kBarRowFull, -1)) return false;
@@ -672,7 +716,10 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       flags = st.x;
       if (++next_rs == C::kRowSlots) { next_rs = 0; rph ^= 1; }
       if (flags & kEnd) return true;
-      if (flags & kFirst) row = (st.z + r) * p.Hkv + st.w;
+      if (flags & kFirst) {
+        row = (st.z + r) * p.Hkv + st.w;
+        if (kSplit) row += (flags >> 16) * 2 * rows;  // below 4 x 152 x 2 x 128
+      }
       if (flags & kSame) return true;
       const int mine = flags >> (q4 >> 1);  // this warp's 64 keys
       const bool in = (mine >> kIn) & 1, full = (mine >> kFull) & 1;
@@ -699,9 +746,14 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!wait_phase(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, row)) return false;
       accph ^= 1;
       tc_fence_after();
-      const long long to = (long long)done_row * D + w * (D / 4);
-      store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, (long long)p.Hkv * D, lane);
-      store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, (long long)p.Hkv * D, lane);
+      const long long to = (long long)done_row * D + w * (D / 4), stride = (long long)p.Hkv * D;
+      if constexpr (kSplit) {
+        store_part<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), p.parts + (long long)rows * D + to, stride, lane);
+        store_part<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.parts + to, stride, lane);
+      } else {
+        store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, stride, lane);
+        store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, stride, lane);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
@@ -1203,12 +1255,44 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ------------------------------------------------------------------ 4. merge
+// dK and dV of the parts added up in order: four elements a thread, each part read once.
+__global__ void __launch_bounds__(256) bsa_bwd_merge_kernel(const float4* __restrict__ parts, int n_split, long long n4,
+                                                            float scale, uint2* __restrict__ dk, uint2* __restrict__ dv) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * n4; i += gridDim.x * 256LL) {
+    float4 s = parts[i];
+    for (int k = 1; k < n_split; ++k) {
+      const float4 t = parts[2 * n4 * k + i];
+      s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+    }
+    const bool keys = i < n4;
+    const float f = keys ? scale : 1.f;
+    (keys ? dk + i : dv + (i - n4))[0] = make_uint2(pack_bf16(s.x * f, s.y * f), pack_bf16(s.z * f, s.w * f));
+  }
+}
+
 // ------------------------------------------------------------------ host
+// Parts of a KV head's query heads.  An item is a key tile with all steps of its query heads; fewer
+// items than SMs leave SMs without one while the longest run, so heads are divided until there are
+// enough (one row of 8192, 16 heads over 1: 1461 -> 617 us; of 2048: 343 -> 69), at most into as many
+// as four times the SMs, which bounds the sums' memory.  256 items divided in two as well only pay for
+// the merge (16 heads over 4 at 8192: 606 -> 630 us), and so do items of at most 16 steps, which end
+// soon (2 rows of 1024, 4 heads over 2: 22.5 -> 23.5; with 32 steps it pays: 53 -> 29).
+int split_of(int B, int T, int Hq, int Hkv) {
+  const int G = Hq / Hkv, nb = T / kM;
+  const long long items = (long long)B * Hkv * nb;
+  if ((long long)nb * G <= 16) return 1;
+  int n = 1;
+  for (int d = 2; d <= G && items * n < 152 && items * d <= 4 * 152; ++d)
+    if (G % d == 0) n = d;
+  return n;
+}
 struct Layout {
-  size_t nlse, ndelta, reach, q_cols, kv_cols, next, total;
+  size_t nlse, ndelta, reach, q_cols, kv_cols, next, parts, total;
+  int n_split;
 };
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-Layout layout(int B, int T, int Hq) {
+Layout layout(int B, int T, int Hq, int Hkv, int D) {
   Layout l{};
   const size_t rows = static_cast<size_t>(B) * T * Hq * 4;
   size_t o = 0;
@@ -1219,6 +1303,9 @@ Layout layout(int B, int T, int Hq) {
   l.q_cols = o; o += round256(cols);
   l.kv_cols = o; o += round256(cols);
   l.next = o;   o += 256;
+  l.n_split = split_of(B, T, Hq, Hkv);
+  l.parts = o;
+  if (l.n_split > 1) o += round256(static_cast<size_t>(l.n_split) * 2 * B * T * Hkv * D * 4);
   l.total = o;
   return l;
 }
@@ -1251,8 +1338,8 @@ int launch_impl(const void* q, const void* k, const void* v, const void* d_out, 
   };
   if (!map(&tq, q, p.Hq) || !map(&tdo, d_out, p.Hq) || !map(&tk, k, p.Hkv) || !map(&tv, v, p.Hkv))
     return set_error(SBA_ERR_CUDA, "blocksparse_attn_bwd: tensor map failed");
-  cudaError_t e = cudaFuncSetAttribute(bsa_bwd_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       KvCfg<D>::kSmemBytes);
+  const auto dkdv = p.n_split > 1 ? bsa_bwd_dkdv_kernel<D, true> : bsa_bwd_dkdv_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, KvCfg<D>::kSmemBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(bsa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd: set smem attribute");
@@ -1261,11 +1348,18 @@ int launch_impl(const void* q, const void* k, const void* v, const void* d_out, 
   bsa_bwd_prep_kernel<D><<<n_delta + n_reach, 256, 0, stream>>>(p, n_delta, tok_groups, head_groups);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_after(bsa_bwd_dkdv_kernel<D>, std::min(p.n_items_kv, num_sms()), KvCfg<D>::kSmemBytes, stream, tq, tdo,
+    e = launch_after(dkdv, std::min(p.n_items_kv, num_sms()), KvCfg<D>::kSmemBytes, stream, tq, tdo,
                      tk, tv, p);
   if (e == cudaSuccess)
     e = launch_after(bsa_bwd_dq_kernel<D>, std::min(p.n_items_dq, num_sms()), DqCfg<D>::kSmemBytes, stream, tq, tdo, tk,
                      tv, p);
+  if (e == cudaSuccess && p.n_split > 1) {
+    const long long n4 = (long long)p.B * p.T * p.Hkv * D / 4;
+    const int grid = static_cast<int>(std::min<long long>((2 * n4 + 255) / 256, 8LL * num_sms()));
+    bsa_bwd_merge_kernel<<<grid, 256, 0, stream>>>(reinterpret_cast<const float4*>(p.parts), p.n_split, n4, p.scale,
+                                                   reinterpret_cast<uint2*>(p.dk), reinterpret_cast<uint2*>(p.dv));
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd launch");
   return SBA_OK;
 }
@@ -1287,7 +1381,7 @@ unsigned read_and_clear_error_blocksparse_bwd(cudaStream_t, std::string* where) 
   return w.flags;
 }
 
-size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq) { return layout(B, T, Hq).total; }
+size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D) { return layout(B, T, Hq, Hkv, D).total; }
 
 int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
                                 const void* d_out, const int32_t* q_pos, const int32_t* q_seg, const int32_t* kv_pos,
@@ -1295,7 +1389,7 @@ int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, con
                                 const int32_t* lower_full, const int32_t* upper_full, int B, int T, int Hq, int Hkv,
                                 int D, int kv_block, int causal, int window_left, int window_right, int pad_id,
                                 float scale, void* dq, void* dk, void* dv, void* workspace, cudaStream_t stream) {
-  const Layout l = layout(B, T, Hq);
+  const Layout l = layout(B, T, Hq, Hkv, D);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Params p{};
   p.out = static_cast<const __nv_bfloat16*>(out);
@@ -1309,6 +1403,8 @@ int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, con
   p.q_cols = reinterpret_cast<int4*>(ws + l.q_cols);
   p.kv_cols = reinterpret_cast<int4*>(ws + l.kv_cols);
   p.next = reinterpret_cast<int*>(ws + l.next);
+  p.parts = l.n_split > 1 ? reinterpret_cast<float*>(ws + l.parts) : nullptr;
+  p.n_split = l.n_split;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
@@ -1323,7 +1419,7 @@ int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, con
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.n_items_dq = B * Hq * p.nb;
-  p.n_items_kv = B * Hkv * p.nb;
+  p.n_items_kv = B * Hkv * p.nb * p.n_split;
   p.wait_limit = wait_timeout_cycles();
   return D == 128 ? launch_impl<128>(q, k, v, d_out, p, stream) : launch_impl<64>(q, k, v, d_out, p, stream);
 }

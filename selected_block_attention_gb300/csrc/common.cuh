@@ -64,7 +64,7 @@ int launch_blocksparse_attn(const void* q, const void* k, const void* v, const i
                             int q_block, int kv_block, int causal, int window_left,
                             int window_right, int pad_id, float scale, void* out, float* lse,
                             cudaStream_t stream);
-size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq);
+size_t blocksparse_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 int launch_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                                 const float* lse, const void* d_out, const int32_t* q_pos,
                                 const int32_t* q_seg, const int32_t* kv_pos, const int32_t* kv_seg,

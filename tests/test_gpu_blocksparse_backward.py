@@ -226,7 +226,7 @@ def test_given_outputs_and_workspace(sba):
     c = Case(T=256, seed=110).forward()
     want = c.call(sba)
     made = [torch.full_like(x, float("nan")) for x in want]
-    need = sba.blocksparse_attn_bwd_workspace_size(1, 256, 4)
+    need = sba.blocksparse_attn_bwd_workspace_size(1, 256, 4, 2, 128)
     ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
     got = c.call(sba, dq=made[0], dk=made[1], dv=made[2], workspace=ws)
     sba.check_error()
@@ -294,6 +294,17 @@ def test_runs_of_unseen_key_tiles(sba, D, seen):
     for t in range(0, T, 1024):
         seg[:, t:t + seen] = t
     check_all(sba, Case(B=B, T=T, Hq=Hq, Hkv=Hq, D=D, seg=seg, seed=140).forward())
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D", [(1, 1024, 8, 1, 128), (1, 1536, 12, 2, 64), (2, 1024, 5, 1, 64)])
+def test_heads_in_parts(sba, B, T, Hq, Hkv, D):
+    """Few key tiles and KV heads: a KV head's query heads are divided among items and their sums merged
+    (also for key tiles that no query sees)."""
+    assert sba.blocksparse_attn_bwd_workspace_size(B, T, Hq, Hkv, D) > 8 * B * T * Hkv * D
+    seg = np.zeros((B, T), np.int64)
+    seg[:, 500:800] = -1
+    seg[:, 800:] = 1
+    check_all(sba, Case(B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, seg=seg, seed=135).forward())
 
 
 def test_full_size_sampled(sba):

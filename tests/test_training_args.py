@@ -35,7 +35,7 @@ def _grad(sba, **kw):
     lib = sba.load_library()
     a = {n: _at((i + 1) << 32) for i, n in enumerate(GRAD)}
     a.update(B=1, T=256, Hq=4, Hkv=2, D=128, q_block=128, kv_block=64, causal=1, left=-1, right=-1, pad=-1, scale=0.0,
-             bytes=lib.sba_blocksparse_attn_bwd_workspace_size(1, 256, 4), stream=None)
+             bytes=lib.sba_blocksparse_attn_bwd_workspace_size(1, 256, 4, 2, 128), stream=None)
     a.update(kw)
     return lib.sba_blocksparse_attn_bwd(*[a[n] for n in GRAD]), lib.sba_last_error().decode()
 
@@ -62,8 +62,12 @@ def test_gradients(sba, kw, code, says):
 def test_gradient_workspace(sba):
     size = sba.blocksparse_attn_bwd_workspace_size
     up = lambda n: -(-n // 256) * 256  # noqa: E731
-    assert size(2, 1024, 6) == 2 * up(2 * 1024 * 6 * 4) + up(2 * 8 * 16) + 2 * up(2 * 32 * 16) + 256
-    assert size(1, 200, 4) == size(0, 128, 4) == size(1, 128, 0) == size(1, 1 << 20, 2048) == 0
+    rows = lambda B, T, Hq: 2 * up(B * T * Hq * 4) + up(B * T // 128 * 16) + 2 * up(B * T // 32 * 16) + 256  # noqa: E731
+    assert size(2, 1024, 6, 3, 128) == rows(2, 1024, 6)
+    # 32 key tiles of one KV head: its 8 query heads in parts of 1, so that there are 152 items
+    assert size(1, 4096, 8, 1, 64) == rows(1, 4096, 8) + 8 * 2 * 4096 * 64 * 4
+    assert size(1, 200, 4, 2, 128) == size(0, 128, 4, 2, 128) == size(1, 128, 0, 1, 128) == size(1, 1 << 20, 2048, 1, 64) == 0
+    assert size(1, 128, 4, 3, 128) == size(1, 128, 4, 2, 96) == 0
 
 
 def _tables(sba, length=8, rot=32, base=1e4, factor=1.0, original=0, slow=1.0, fast=32.0, amplitude=1.0,
