@@ -27,10 +27,13 @@
 // on the other tile.  In steady state, per step:
 //   dK / dV:  dV(i)   S(i+1)   dK(i)   dP(i+1)      softmax warps: dS(i) | P(i+1)
 //   dQ:       S(i+1)  dQ(i)    dP(i+1)              softmax warps: dS(i) | P(i+1)
-// What bounds them is the chain of the warp that issues the products: with its waits for the softmax
-// warps taken out, one row of 8192 still takes 82 % of its time, with the exponentials taken out 98 %,
-// with an eighth of the products 84 %.  Four products of 128 x 128 x 128 take the tensor core 2048 cycles
-// a step; the kernels run at 60 to 70 % of that.
+// What bounds them is the tensor core: the seven products over whole tiles of one row of 8192 (16 heads
+// over 4) take 519 us at the rate of a large library product in a burst and 577 at its sustained one, the
+// kernels 575 to 620 with prep, by the GPU's clocks; of a batch of 4 x 16384 behind a window of 1024, 1855
+// and 2066, the kernels 2390 to 2570, 160 of it prep's.  Heads of 64 have half the products and the same
+// softmax: there the chain of waits through the issuing warp is as long (2 x 4096, 12 heads over 4, 500
+// and 300 tokens in view: 42 us at that rate, 109 taken).  Exponentials left out, or a second tile of S
+// for heads of 64, change nothing.
 // dK / dV works on S^T = K Q^T and dP^T = V dO^T (lanes = keys), whose P^T and dS^T go back over
 // their own columns in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q straight from
 // tensor memory.  dQ holds Q and dO of the item in tensor memory as A operands as well, and dS
@@ -369,7 +372,7 @@ struct KvCfg {
   static constexpr int kOffDo = kOffQ + kQStages * kTile;
   static constexpr int kOffRows = kOffDo + kDoStages * kTile;
   static constexpr int kOffBars = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
-  static constexpr int kNumBars = 4 + 2 * kQStages + 2 * kDoStages + 2 * kRowSlots + 7;
+  static constexpr int kNumBars = 4 + kQStages + kDoStages + 2 * kRowSlots + 7;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;   // tmem address, abort flag, step flags
   // At least half of an SM's shared memory: one CTA an SM, as each holds all tensor memory.
   static constexpr int kSmemBytes = (kOffMisc + 8 + 4 * kQStages) > 120 * 1024 ? (kOffMisc + 8 + 4 * kQStages) : 120 * 1024;
@@ -428,9 +431,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   uint64_t* v_full = bb;     bb += 1;
   uint64_t* v_empty = bb;    bb += 1;
   uint64_t* q_full = bb;     bb += C::kQStages;
-  uint64_t* q_empty = bb;    bb += C::kQStages;
   uint64_t* do_full = bb;    bb += C::kDoStages;
-  uint64_t* do_empty = bb;   bb += C::kDoStages;
   uint64_t* row_full = bb;   bb += C::kRowSlots;
   uint64_t* row_empty = bb;  bb += C::kRowSlots;
   uint64_t* s_full = bb;     bb += 1;
@@ -451,8 +452,8 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1); mbar_init(k_empty, 1); mbar_init(v_full, 1); mbar_init(v_empty, 1);
-    for (int i = 0; i < C::kQStages; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
-    for (int i = 0; i < C::kDoStages; ++i) { mbar_init(&do_full[i], 1); mbar_init(&do_empty[i], 1); }
+    for (int i = 0; i < C::kQStages; ++i) mbar_init(&q_full[i], 1);
+    for (int i = 0; i < C::kDoStages; ++i) mbar_init(&do_full[i], 1);
     for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kSoftWarps); }
     mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps); mbar_init(dp_full, 1); mbar_init(ds_full, kSoftWarps);
     mbar_init(acc_full, 1); mbar_init(acc_empty, kSoftWarps); mbar_init(mma_done, 1);
@@ -478,7 +479,11 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loader
-    int qs = 0, ds = 0, rs = 0;
+    // dP(n - 1) follows dV(n - 2) and dK(n - 2), so once it is there the stages of dO(n - 2) and Q(n - 2) are
+    // free: dO(n) waits for that, and Q(n) has nothing left to wait for, as dO(n - 1) did.  dP(n) does
+    // not come before dO(n), so the phase waited for is always the last one.
+    static_assert(C::kDoStages == 2 && C::kQStages == 3, "the order above");
+    int qs = 0, ds = 0, rs = 0, n_loaded = 0;
     uint32_t qph = 0, dph = 0, rph = 0, kph = 0, vph = 0;
     // stages loaded and the phase of their last load (bit sets), for the drain
     uint32_t q_out = 0u, q_last = 0u, d_out = 0u, d_last = 0u, r_out = 0u, r_last = 0u;
@@ -496,7 +501,6 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           mbar_arrive(&row_full[rs]);
         }
         __syncwarp();
-        if (!wait_phase(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) break;
         if (lane == 0) {
           step_flags[qs] = kEnd;
           mbar_arrive(&q_full[qs]);
@@ -562,7 +566,6 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               k_out = true; kph ^= 1;
             }
-            if (!wait_phase(&q_empty[qs], qph ^ 1, ab, kRoleLoader, kBarQEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               step_flags[qs] = flags;
               mbar_arrive_expect_tx(&q_full[qs], C::kTile);
@@ -582,7 +585,11 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               v_out = true; vph ^= 1;
             }
-            if (!wait_phase(&do_empty[ds], dph ^ 1, ab, kRoleLoader, kBarDoEmpty, item)) { ok = false; break; }
+            if (n_loaded >= 2 && !wait_phase(dp_full, (n_loaded - 1) & 1, ab, kRoleLoader, kBarDoEmpty, item)) {
+              ok = false;
+              break;
+            }
+            ++n_loaded;
             if (lane == 0) {
               mbar_arrive_expect_tx(&do_full[ds], C::kTile);
 #pragma unroll
@@ -672,7 +679,6 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       for (int kk = 0; kk < kM / 16; ++kk)
         mma_f16_ts_by(leader, tmem + C::kDvCol, tmem + C::kSCol + part_cols(kk), domn_desc + off(cd) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
-      mma_commit_by(leader, &do_empty[cd]);
       if (++cd == C::kDoStages) cd = 0;
       if (!issue_s(next)) break;
       // dK += dS^T Q
@@ -683,7 +689,6 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       for (int kk = 0; kk < kM / 16; ++kk)
         mma_f16_ts_by(leader, tmem + C::kDkCol, tmem + C::kDpCol + part_cols(kk), qmn_desc + off(cq) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
-      mma_commit_by(leader, &q_empty[cq]);
       if (++cq == C::kQStages) cq = 0;
       if (cur & kLast) mma_commit_by(leader, acc_full);
       if (!(next & kEnd) && !issue_dp(next)) break;
@@ -860,7 +865,7 @@ struct DqCfg {
   static constexpr int kItemBytes = (static_cast<int>(sizeof(DqItem)) + 15) & ~15;
   static constexpr int kOffItems = kOffV + kVStages * kTile;
   static constexpr int kOffBars = kOffItems + kItemSlots * kItemBytes;
-  static constexpr int kNumBars = 2 * kItemSlots + 4 + 2 * kKStages + 2 * kVStages + 7;
+  static constexpr int kNumBars = 2 * kItemSlots + 4 + kKStages + kVStages + 8;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;
   static constexpr int kSmemBytes = (kOffMisc + 8) > 120 * 1024 ? (kOffMisc + 8) : 120 * 1024;
   static constexpr int kSCol = 0, kDpCol = 128, kDqCol = 256, kQCol = 256 + D, kDoCol = kQCol + D / 2;
@@ -886,12 +891,10 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint64_t* do_full = bb;    bb += 1;
   uint64_t* do_empty = bb;   bb += 1;
   uint64_t* k_full = bb;     bb += C::kKStages;
-  uint64_t* k_empty = bb;    bb += C::kKStages;
   uint64_t* v_full = bb;     bb += C::kVStages;
-  uint64_t* v_empty = bb;    bb += C::kVStages;
   uint64_t* s_full = bb;     bb += 1;
   uint64_t* s_empty = bb;    bb += 1;
-  uint64_t* dp_full = bb;    bb += 1;
+  uint64_t* dp_full = bb;    bb += 2;  // by turns
   uint64_t* ds_full = bb;    bb += 1;
   uint64_t* dq_full = bb;    bb += 1;
   uint64_t* dq_empty = bb;   bb += 1;
@@ -908,9 +911,9 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     // an item slot is read by the MMA warp and the softmax warps
     for (int i = 0; i < kItemSlots; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 1 + kSoftWarps); }
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
-    for (int i = 0; i < C::kKStages; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
-    for (int i = 0; i < C::kVStages; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
-    mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(dp_full, 1); mbar_init(ds_full, kSoftWarps);
+    for (int i = 0; i < C::kKStages; ++i) mbar_init(&k_full[i], 1);
+    for (int i = 0; i < C::kVStages; ++i) mbar_init(&v_full[i], 1);
+    mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(&dp_full[0], 1); mbar_init(&dp_full[1], 1); mbar_init(ds_full, kSoftWarps);
     mbar_init(dq_full, 1); mbar_init(dq_empty, kSoftWarps); mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -933,7 +936,10 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loader
-    int islot = 0, ks = 0, vs = 0;
+    // dP(n - 2) read V(n - 2) and follows dQ(n - 3), which read K(n - 3): once it is there both stages
+    // of step n are free.  dP(n), whose phase comes next on the same barrier, waits for V(n).
+    static_assert(C::kVStages == 2 && C::kKStages == 3, "the order above");
+    int islot = 0, ks = 0, vs = 0, n_loaded = 0;
     uint32_t iph = 0, qph = 0, kph = 0, vph = 0;
     uint32_t k_out = 0u, k_last = 0u, v_out = 0u, v_last = 0u;
     uint32_t q_last = 2u, do_last = 2u;  // phase of the last load, 2: none yet
@@ -976,7 +982,12 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           q_last = qph;
         }
-        if (!wait_phase(&k_empty[ks], kph ^ 1, ab, kRoleLoader, kBarKEmpty, item)) { ok = false; break; }
+        if (n_loaded >= 2 &&
+            !wait_phase(&dp_full[n_loaded & 1], ((n_loaded >> 1) - 1) & 1, ab, kRoleLoader, kBarKEmpty, item)) {
+          ok = false;
+          break;
+        }
+        ++n_loaded;
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[ks], C::kTile);
 #pragma unroll
@@ -995,7 +1006,6 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           do_last = qph; qph ^= 1;
         }
-        if (!wait_phase(&v_empty[vs], vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
         if (lane == 0) {
           mbar_arrive_expect_tx(&v_full[vs], C::kTile);
 #pragma unroll
@@ -1084,8 +1094,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int kk = 0; kk < D / 16; ++kk)
         mma_f16_ts_by(leader, tmem + C::kDpCol, tmem + C::kDoCol + kk * 8, v_desc + off(vs) + kmajor(kk), C::kIdescS,
                       kk > 0 ? 1u : 0u);
-      mma_commit_by(leader, dp_full);
-      mma_commit_by(leader, &v_empty[vs]);
+      mma_commit_by(leader, &dp_full[vs]);
       if (++vs == C::kVStages) { vs = 0; vph ^= 1; }
       return true;
     };
@@ -1106,7 +1115,6 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int kk = 0; kk < kM / 16; ++kk)
         mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
                       C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
-      mma_commit_by(leader, &k_empty[ck]);
       if (++ck == C::kKStages) ck = 0;
       if (cur & kLast) mma_commit_by(leader, dq_full);
       if (!(next & kEnd) && !issue_dp(next)) break;
@@ -1124,7 +1132,7 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
     int islot = 0;
-    uint32_t iph = 0, sph = 0, dpph = 0, dqph = 0;
+    uint32_t iph = 0, sph = 0, dpph = 0, dpt = 0, dqph = 0;
     int done_row = -1;             // this thread's row (token times heads) of a finished item
     const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     auto finish = [&]() -> bool {
@@ -1219,8 +1227,9 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         col += kM;
       }
       if (had) {
-        if (!wait_phase(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
-        dpph ^= 1;
+        if (!wait_phase(&dp_full[dpt], dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
+        dpph ^= dpt;
+        dpt ^= 1;
         tc_fence_after();
         float y[kCols];
         tmem_ld_32x32b_x32(dp_col, y);
