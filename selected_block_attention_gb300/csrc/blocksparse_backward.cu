@@ -32,7 +32,7 @@
 // kernels 575 to 620 with prep, by the GPU's clocks; of a batch of 4 x 16384 behind a window of 1024, 1855
 // and 2066, the kernels 2390 to 2570, 160 of it prep's.  Heads of 64 have half the products and the same
 // softmax: there the chain of waits through the issuing warp is as long (2 x 4096, 12 heads over 4, 500
-// and 300 tokens in view: 42 us at that rate, 109 taken).  Exponentials left out, or a second tile of S
+// and 300 tokens in view: 42 us at that rate, 103 taken).  Exponentials left out, or a second tile of S
 // for heads of 64, change nothing.
 // dK / dV works on S^T = K Q^T and dP^T = V dO^T (lanes = keys), whose P^T and dS^T go back over
 // their own columns in bf16 and are the A operands of dV += P^T dO and dK += dS^T Q straight from
@@ -365,14 +365,17 @@ template <int D>
 struct KvCfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = kPanels * kPanel;   // 128 rows of K, V, Q or dO
-  static constexpr int kQStages = 3, kDoStages = 2, kRowSlots = 2;
+  // Heads of 64 leave room to load further ahead, above all the rows, which a step's exponentials begin
+  // with (2 x 4096 tokens, 12 heads over 4: 107.5 -> 102.8 us; four stages and six rows no more).
+  static constexpr int kQStages = 3, kDoStages = D == 64 ? 3 : 2, kRowSlots = D == 64 ? 4 : 2;
+  static constexpr int kDpBars = 2;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kTile;
   static constexpr int kOffQ = 2 * kTile;
   static constexpr int kOffDo = kOffQ + kQStages * kTile;
   static constexpr int kOffRows = kOffDo + kDoStages * kTile;
   static constexpr int kOffBars = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
-  static constexpr int kNumBars = 4 + kQStages + kDoStages + 2 * kRowSlots + 7;
+  static constexpr int kNumBars = 4 + kQStages + kDoStages + 2 * kRowSlots + kDpBars + 6;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;   // tmem address, abort flag, step flags
   // At least half of an SM's shared memory: one CTA an SM, as each holds all tensor memory.
   static constexpr int kSmemBytes = (kOffMisc + 8 + 4 * kQStages) > 120 * 1024 ? (kOffMisc + 8 + 4 * kQStages) : 120 * 1024;
@@ -436,7 +439,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   uint64_t* row_empty = bb;  bb += C::kRowSlots;
   uint64_t* s_full = bb;     bb += 1;
   uint64_t* p_full = bb;     bb += 1;
-  uint64_t* dp_full = bb;    bb += 1;
+  uint64_t* dp_full = bb;    bb += C::kDpBars;  // by turns
   uint64_t* ds_full = bb;    bb += 1;
   uint64_t* acc_full = bb;   bb += 1;
   uint64_t* acc_empty = bb;  bb += 1;
@@ -455,7 +458,9 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     for (int i = 0; i < C::kQStages; ++i) mbar_init(&q_full[i], 1);
     for (int i = 0; i < C::kDoStages; ++i) mbar_init(&do_full[i], 1);
     for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kSoftWarps); }
-    mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps); mbar_init(dp_full, 1); mbar_init(ds_full, kSoftWarps);
+    mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps); 
+    for (int i = 0; i < C::kDpBars; ++i) mbar_init(&dp_full[i], 1);
+    mbar_init(ds_full, kSoftWarps);
     mbar_init(acc_full, 1); mbar_init(acc_empty, kSoftWarps); mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -479,10 +484,17 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loader
-    // dP(n - 1) follows dV(n - 2) and dK(n - 2), so once it is there the stages of dO(n - 2) and Q(n - 2) are
-    // free: dO(n) waits for that, and Q(n) has nothing left to wait for, as dO(n - 1) did.  dP(n) does
-    // not come before dO(n), so the phase waited for is always the last one.
-    static_assert(C::kDoStages == 2 && C::kQStages == 3, "the order above");
+    // Steps are counted through all items.  The issuing warp's order is dV(n), S(n + 1), dK(n), dP(n + 1):
+    // once dP(n) is there, the stages of Q and dO that steps before n read are free.  Step n's loads wait
+    // for dP(n + 1 - stages), Q's of heads of 128, with a stage more than dO, for nothing, as dO(n - 1) did.
+    // dP takes barriers by turns, so that a wait cannot take one phase for another: on the barrier waited
+    // for, the next phase needs a dO that is not loaded yet, and the one before was over when the loads of
+    // the step before began.
+    auto dp_there = [&](int n, int item) {
+      return n < 0 || wait_phase(&dp_full[n % C::kDpBars], (n / C::kDpBars) & 1, ab, kRoleLoader, kBarDoEmpty, item);
+    };
+    constexpr bool kTogether = C::kQStages == C::kDoStages;
+    static_assert(C::kDpBars >= C::kDoStages - 1 && C::kQStages - C::kDoStages <= 1, "the order above");
     int qs = 0, ds = 0, rs = 0, n_loaded = 0;
     uint32_t qph = 0, dph = 0, rph = 0, kph = 0, vph = 0;
     // stages loaded and the phase of their last load (bit sets), for the drain
@@ -566,6 +578,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               k_out = true; kph ^= 1;
             }
+            if (kTogether && !dp_there(n_loaded + 1 - C::kDoStages, item)) { ok = false; break; }
             if (lane == 0) {
               step_flags[qs] = flags;
               mbar_arrive_expect_tx(&q_full[qs], C::kTile);
@@ -585,10 +598,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               }
               v_out = true; vph ^= 1;
             }
-            if (n_loaded >= 2 && !wait_phase(dp_full, (n_loaded - 1) & 1, ab, kRoleLoader, kBarDoEmpty, item)) {
-              ok = false;
-              break;
-            }
+            if (!kTogether && n_loaded >= 2 && !dp_there(n_loaded - 1, item)) { ok = false; break; }
             ++n_loaded;
             if (lane == 0) {
               mbar_arrive_expect_tx(&do_full[ds], C::kTile);
@@ -626,7 +636,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint64_t qmn_desc = make_sdesc(smem_base + C::kOffQ, kPanel, 1024, kLayoutSW128);
     const uint64_t domn_desc = make_sdesc(smem_base + C::kOffDo, kPanel, 1024, kLayoutSW128);
     auto off = [](int stage) { return static_cast<uint64_t>((stage * C::kTile) >> 4); };
-    int qs = 0, ds = 0;                      // stages of the next S and dP
+    int qs = 0, ds = 0, dpt = 0;             // stages of the next S and dP, barrier of dP
     uint32_t qph = 0, dph = 0, kph = 0, vph = 0, pph = 0, dsph = 0, accph = 0;
     // S of the step in Q stage qs; its flags, or kEnd
     auto issue_s = [&](int& flags) -> bool {
@@ -658,7 +668,8 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       for (int kk = 0; kk < D / 16; ++kk)
         mma_f16_ss_by(leader, tmem + C::kDpCol, v_desc + kmajor(kk), do_desc + off(ds) + kmajor(kk), C::kIdescS,
                       kk > 0 ? 1u : 0u);
-      mma_commit_by(leader, dp_full);
+      mma_commit_by(leader, &dp_full[dpt]);
+      if (++dpt == C::kDpBars) dpt = 0;
       if (flags & kLast) mma_commit_by(leader, v_empty);
       if (++ds == C::kDoStages) { ds = 0; dph ^= 1; }
       return true;
@@ -708,6 +719,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint32_t s_col = tmem + lane_off + C::kSCol + w * kCols, dp_col = tmem + lane_off + C::kDpCol + w * kCols;
     int rs = 0, next_rs = 0;       // row slots of the step and of the one looked up
     uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
+    int dpt = 0;                   // barrier of the next dP
     int done_row = -1;             // this thread's key (times heads) of a finished item
     int lo = 1, hi = 0, seg = 0;   // query positions that may see this key, and its segment
     // The step to come: its flags, this thread's key, and the columns that pair with it.  Looked up
@@ -808,8 +820,8 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (flags & kEnd) break;
       if (!look_up()) break;
       if (work) {
-        if (!wait_phase(dp_full, dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
-        dpph ^= 1;
+        if (!wait_phase(&dp_full[dpt], dpph, ab, kRoleSoftmax, kBarDpFull, row)) break;
+        if (++dpt == C::kDpBars) { dpt = 0; dpph ^= 1; }
         tc_fence_after();
         float y[kCols];
         tmem_ld_32x32b_x32(dp_col, y);
