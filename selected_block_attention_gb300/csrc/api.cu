@@ -507,12 +507,14 @@ int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const 
   SBA_SUPPORT(T % 128 == 0, "T must be a multiple of 128");
   SBA_SUPPORT(D == 64 || D == 128, "D must be 64 or 128");
   SBA_SUPPORT((long long)B * T * Hq < (1LL << 31), "B * T * Hq must be < 2^31");
-  const size_t rows = static_cast<size_t>(B) * T, nq = rows * Hq * D * 2, nk = rows * Hkv * D * 2;
+  const size_t rows = static_cast<size_t>(B) * T, nq = rows * Hq * D * 2, nk = rows * Hkv * D * 2, nb = rows / 128 * 4;
   const size_t need = blocksparse_bwd_workspace_bytes(B, T, Hq, Hkv, D);
   SBA_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && workspace_bytes >= need,
               "workspace missing, not 256-byte aligned or smaller than "
               "sba_blocksparse_attn_bwd_workspace_size()");
-  const struct { const void* at; size_t n; } in[] = {{q, nq}, {k, nk}, {v, nk}, {out, nq}, {d_out, nq}, {lse, rows * Hq * 4}},
+  const struct { const void* at; size_t n; } in[] = {{q, nq}, {k, nk}, {v, nk}, {out, nq}, {d_out, nq}, {lse, rows * Hq * 4},
+                                                 {q_pos, rows * 4}, {q_seg, rows * 4}, {kv_pos, rows * 4}, {kv_seg, rows * 4},
+                                                 {lower, nb}, {upper, nb}, {lower_full, nb}, {upper_full, nb}},
                                              made[] = {{dq, nq}, {dk, nk}, {dv, nk}, {workspace, need}};
   for (int i = 0; i < 4; ++i) {
     for (const auto& x : in)
@@ -596,6 +598,13 @@ int sba_rotary_embed(const sba_rotary_embed_args* args, sba_stream_t stream) {
     SBA_REQUIRE(out_of(ko, k), "k_out must be k with its token stride, or apart from it");
     SBA_REQUIRE(!rows_meet(qo, k, n) && !rows_meet(ko, q, n) && !rows_meet(qo, ko, n),
                 "q_out and k_out must not overlap, nor q_out k, nor k_out q");
+  }
+  const size_t angles = static_cast<size_t>(a.max_pos) * (a.rot_dim / 2) * 4;
+  for (const Rows* o : {&qo, &ko}) {
+    const size_t span = o->at ? static_cast<size_t>((n - 1) * o->stride + o->width) : 0;
+    SBA_REQUIRE(!ranges_meet(o->at, span, a.cos, angles) && !ranges_meet(o->at, span, a.sin, angles) &&
+                    !(a.positions && ranges_meet(o->at, span, a.positions, n * 4)),
+                "q_out and k_out must not overlap cos, sin or positions");
   }
   return launch_rotary_embed(a, reinterpret_cast<cudaStream_t>(stream));
 }

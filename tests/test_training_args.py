@@ -53,6 +53,8 @@ def _grad(sba, **kw):
     (dict(dk=_at((2 << 32) + 16)), INVALID, "overlap"),               # inside k
     (dict(dk=_at(0x900000000000), dv=_at(0x900000000100)), INVALID, "overlap"),
     (dict(workspace=_at(6 << 32)), INVALID, "overlap"),               # on d_out
+    (dict(dv=_at((8 << 32) - 16)), INVALID, "overlap"),               # into q_seg
+    (dict(dq=_at((14 << 32) - 0x1fff0)), INVALID, "overlap"),         # into upper_full
 ])
 def test_gradients(sba, kw, code, says):
     got, text = _grad(sba, **kw)
@@ -122,6 +124,8 @@ def _embed(sba, **kw):
     (dict(q_out=1 << 32, q_out_stride=512), INVALID, "q_out"), (dict(q_out=(1 << 32) + 16), INVALID, "q_out"),
     (dict(k_out=(2 << 32) + 16), INVALID, "k_out"), (dict(q_out=2 << 32), INVALID, "overlap"),
     (dict(k_out=(1 << 32) + 1024), INVALID, "overlap"), (dict(k_out=(3 << 32) + 1024), INVALID, "overlap"),
+    (dict(cos=(3 << 32) + 1024), INVALID, "overlap"), (dict(sin=4 << 32), INVALID, "overlap"),
+    (dict(positions=(4 << 32) + 64), INVALID, "overlap"),
     # parts of one projection's output: q_out would reach into k
     (dict(k=(1 << 32) + 256, q_stride=512, k_stride=512, q_out=(1 << 32), q_out_stride=512), INVALID, "overlap")])
 def test_rotation(sba, kw, code, says):
