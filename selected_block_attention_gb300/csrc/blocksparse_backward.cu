@@ -925,7 +925,8 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
     for (int i = 0; i < C::kKStages; ++i) mbar_init(&k_full[i], 1);
     for (int i = 0; i < C::kVStages; ++i) mbar_init(&v_full[i], 1);
-    mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(&dp_full[0], 1); mbar_init(&dp_full[1], 1); mbar_init(ds_full, kSoftWarps);
+    mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(&dp_full[0], 1); mbar_init(&dp_full[1], 1);
+    mbar_init(ds_full, kSoftWarps);
     mbar_init(dq_full, 1); mbar_init(dq_empty, kSoftWarps); mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();

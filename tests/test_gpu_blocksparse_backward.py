@@ -307,6 +307,29 @@ def test_heads_in_parts(sba, B, T, Hq, Hkv, D):
     check_all(sba, Case(B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, seg=seg, seed=135).forward())
 
 
+def test_heads_in_parts_captured_and_at_once(sba):
+    """The form with a merge, the same results eager, from a graph, and on two streams at once."""
+    c = Case(T=1024, Hq=8, Hkv=1, D=64, seed=136).forward()
+    want = [x.clone() for x in c.call(sba)]
+    for _ in range(2):
+        c.call(sba)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.call(sba)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    made = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                made.append(c.call(sba))
+        g.replay()
+    torch.cuda.synchronize()
+    for got in (out, *made):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    sba.check_error()
+
+
 def test_full_size_sampled(sba):
     """4 x 16384 tokens, 32 heads over 8, window (1024, 0): the forward's own out and lse, dq on sampled
     tokens, dk and dv of whole key tiles from all rows that see them."""
