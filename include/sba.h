@@ -325,9 +325,11 @@ SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq, int
  *                Hkv, D) bytes, 256-byte aligned, caller-owned; needs no initialisation.  Calls that may
  *                overlap on the GPU need one each.
  * q, k, v, out, d_out, lse, dq, dk and dv must be 16-byte aligned; the outputs overlap neither
- * an input nor one another (SBA_ERR_INVALID_ARG).  A key that is masked for some rows of a tile
- * takes part in that tile's products with weight 0, and so does the d_out of a row without keys:
- * both must be finite.
+ * an input nor one another (SBA_ERR_INVALID_ARG).  Pairs that the mask leaves out inside the bounds
+ * take part in their tile's products with weight 0, and so do the rows of a query block in dK and dV of
+ * all 128 keys of a tile that its bounds reach.  So all rows of a query block with bounds that are not
+ * empty need finite q, out and d_out, padding too, and the keys inside its bounds finite k and v.  Keys
+ * in no bounds and the rows of query blocks with empty ones may hold anything: nothing of them is taken.
  * Supported, as in the forward: q_block == 128, kv_block in {64, 128}, T % 128 == 0, D in
  * {64, 128}, 1 <= Hq / Hkv, B * T * Hq < 2^31, bf16 (fp32 accumulation; P and dS are rounded to
  * bf16 before their products).  Results are the same from run to run.

@@ -92,7 +92,7 @@ struct Params {
   const int* upper_full;
   float* nlse;      // [B, Hq, T]  -LSE in log2 units; -inf for rows without a key
   float* ndelta;    // [B, Hq, T]  -Delta
-  int4* reach;      // [B, nb]     query blocks [x, y) reach this key tile, z of them
+  int4* reach;      // [B, nb]     query blocks [x, y) reach this key tile, z of them; w: which halves (bits)
   int4* q_cols;     // [B, T / 32] 32 queries' positions and segments (see Cols)
   int4* kv_cols;    // [B, T / 32] ... and keys'
   int* next;        // next item of dK / dV, of dQ
@@ -209,13 +209,14 @@ __global__ void __launch_bounds__(256) bsa_bwd_prep_kernel(const Params p, int n
     return;
   }
   const int b = item / p.nb, kt = item % p.nb;
-  int first = INT_MAX, last = -1, n = 0;
+  int first = INT_MAX, last = -1, n = 0, halves = 0;
   for (int q0 = 0; q0 < p.nb; q0 += 32) {
     const int qb = q0 + lane;
     bool hit = false;
     if (qb < p.nb) {
       const Range r = block_range(p, b, qb);
       hit = r.lo < 2 * kt + 2 && r.up > 2 * kt;
+      halves |= (r.lo <= 2 * kt && r.up > 2 * kt ? 1 : 0) | (r.lo <= 2 * kt + 1 && r.up > 2 * kt + 1 ? 2 : 0);
     }
     const unsigned m = __ballot_sync(0xffffffffu, hit);
     if (m != 0u) {
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(256) bsa_bwd_prep_kernel(const Params p, int n
       n += __popc(m);
     }
   }
-  if (lane == 0) p.reach[item] = make_int4(n ? first : 0, last + 1, n, 0);
+  halves = __reduce_or_sync(0xffffffffu, halves);
+  if (lane == 0) p.reach[item] = make_int4(n ? first : 0, last + 1, n, halves);
 }
 
 // ------------------------------------------------------------------ shared pieces
@@ -309,12 +311,17 @@ __device__ __forceinline__ void swap_chunks(uint32_t (&v)[kChunks][4], int lane)
   }
 }
 
-// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16.  `to`: this lane's row, the
-// rows of neighbouring lanes `stride` elements apart.
+// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16, or zeros.  `to`: this lane's row,
+// the rows of neighbouring lanes `stride` elements apart.
 template <int N>
-__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane) {
+__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane,
+                                           bool zeros = false) {
   float x[N];
   if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
+  if (zeros) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = 0.f;
+  }
   constexpr int kChunks = N / 8;
   uint32_t v[kChunks][4];
 #pragma unroll
@@ -332,7 +339,7 @@ __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* t
 // The same columns in fp32, for the merge; 16 at a time, as the caller holds P meanwhile (all 32 at once
 // spilled: 8192 tokens of 16 heads in two parts 600 -> 840 us).
 template <int N>
-__device__ __forceinline__ void store_part(uint32_t a, float* to, long long stride, int lane) {
+__device__ __forceinline__ void store_part(uint32_t a, float* to, long long stride, int lane, bool zeros) {
   const int me = lane % 4;
   float* row0 = to - me * stride + me * 4;
 #pragma unroll 1
@@ -341,7 +348,7 @@ __device__ __forceinline__ void store_part(uint32_t a, float* to, long long stri
     tmem_ld_32x32b_x16(a + c, x);
     uint32_t v[4][4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j / 4][j % 4] = __float_as_uint(x[j]);
+    for (int j = 0; j < 16; ++j) v[j / 4][j % 4] = zeros ? 0u : __float_as_uint(x[j]);
     swap_chunks(v, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -353,8 +360,10 @@ __device__ __forceinline__ void store_part(uint32_t a, float* to, long long stri
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
 // kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
 // token mask (bit numbers).
-// kSame: the query block of the step before.  From bit 16 on: the item's part.
-enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
+// kSame: the query block of the step before.  kUnseen, kUnseen + 1 (bit numbers): no bounds take in the
+// tile's first, second 64 keys.  kHalf (dQ): the bounds end within the step's tile.  From bit 16 on: the
+// item's part.
+enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256, kUnseen = 9, kHalf = 2048 };
 struct alignas(16) StepRow {
   float nlse[kM];
   float ndelta[kM];
@@ -526,7 +535,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       kv_item(p, item, b, hkv, part, kt);
       const int4 reach = p.reach[b * p.nb + kt];
       const int heads = p.G / p.n_split, n_steps = reach.z * heads;
-      const int key0 = b * p.T + kt * kM;
+      const int key0 = b * p.T + kt * kM, unseen = (~reach.w & 3) << kUnseen;
       if (n_steps == 0) {
         // No query sees these keys.  The zeros are written from here, as many such tiles may follow one
         // another: in the row ring they would wait for the softmax warps, these in finish() for the last
@@ -559,7 +568,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               StepRow& w = row_at(rs);
-              w.what = make_int4(flags | seen | (g > 0 ? kSame : 0) | part << 16, tok0, key0, hkv);
+              w.what = make_int4(flags | seen | unseen | (g > 0 ? kSame : 0) | part << 16, tok0, key0, hkv);
               const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
               mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
               bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
@@ -720,7 +729,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     int rs = 0, next_rs = 0;       // row slots of the step and of the one looked up
     uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
     int dpt = 0;                   // barrier of the next dP
-    int done_row = -1;             // this thread's key (times heads) of a finished item
+    int done_row = -1;             // this thread's key (times heads) of a finished item, -2 - key if unseen
     int lo = 1, hi = 0, seg = 0;   // query positions that may see this key, and its segment
     // The step to come: its flags, this thread's key, and the columns that pair with it.  Looked up
     // while the step before waits for dP.
@@ -763,13 +772,15 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!wait_phase(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, row)) return false;
       accph ^= 1;
       tc_fence_after();
-      const long long to = (long long)done_row * D + w * (D / 4), stride = (long long)p.Hkv * D;
+      // Keys in no bounds get zeros, whatever their values left in the sums (0 times NaN is NaN).
+      const bool none = done_row < 0;
+      const long long to = (long long)(none ? -2 - done_row : done_row) * D + w * (D / 4), stride = (long long)p.Hkv * D;
       if constexpr (kSplit) {
-        store_part<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), p.parts + (long long)rows * D + to, stride, lane);
-        store_part<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.parts + to, stride, lane);
+        store_part<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), p.parts + (long long)rows * D + to, stride, lane, none);
+        store_part<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.parts + to, stride, lane, none);
       } else {
-        store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, stride, lane);
-        store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, stride, lane);
+        store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, stride, lane, none);
+        store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, stride, lane, none);
       }
       tc_fence_before();
       __syncwarp();
@@ -784,7 +795,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     while (true) {
       float x[kCols];
       const bool last = work && (flags & kLast);
-      const int this_row = row;
+      const int this_row = (flags >> (kUnseen + (q4 >> 1))) & 1 ? -2 - row : row;
       if (work) {
         if (!wait_phase(s_full, sph, ab, kRoleSoftmax, kBarSFull, row)) break;
         sph ^= 1;
@@ -816,7 +827,7 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      if (__builtin_expect(done_row >= 0, 0) && !finish()) break;
+      if (__builtin_expect(done_row != -1, 0) && !finish()) break;
       if (flags & kEnd) break;
       if (!look_up()) break;
       if (work) {
@@ -1049,19 +1060,21 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     auto off = [](int stage) { return static_cast<uint64_t>((stage * C::kTile) >> 4); };
     int islot = 0, ks = 0, vs = 0, left = 0;   // left: steps of the item not yet taken
     uint32_t iph = 0, qph = 0, doph = 0, kph = 0, vph = 0, seph = 0, dsph = 0, dqph = 0;
-    // the next step's flags: kFirst, kLast, or kEnd
+    int odd = 0;                               // kHalf if the item has an odd number of 64-key tiles
+    // the next step's flags: kFirst, kLast, kHalf, or kEnd
     auto next_step = [&](int& flags) -> bool {
       flags = 0;
       while (left == 0) {
         if (!wait_phase(&item_full[islot], iph, ab, kRoleMma, kBarItemFull, -1)) return false;
         left = item_at(islot).n_steps;
+        odd = ((item_at(islot).r.up - item_at(islot).r.lo) & 1) != 0 ? kHalf : 0;
         __syncwarp();
         if (left < 0) { flags = kEnd; return true; }
         if (lane == 0) mbar_arrive(&item_empty[islot]);
         if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
         flags = kFirst;
       }
-      if (--left == 0) flags |= kLast;
+      if (--left == 0) flags |= kLast | odd;
       return true;
     };
     // S = Q K^T into its columns, which the softmax warps have read
@@ -1124,10 +1137,13 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         dqph ^= 1;
       }
       tc_fence_after();
+      // K behind the end of the bounds takes no part: those rows are keys that the item does not see or,
+      // behind a row's last tile, another sequence's, and 0 times what they hold need not be 0.
+      const uint32_t second = (cur & kHalf) ? 0u : leader;
 #pragma unroll
       for (int kk = 0; kk < kM / 16; ++kk)
-        mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
-                      C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
+        mma_f16_ts_by(kk < kM / 32 ? leader : second, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk),
+                      kmn_desc + off(ck) + mnmajor(kk), C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
       if (++ck == C::kKStages) ck = 0;
       if (cur & kLast) mma_commit_by(leader, dq_full);
       if (!(next & kEnd) && !issue_dp(next)) break;
