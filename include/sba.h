@@ -333,8 +333,8 @@ SBA_API size_t sba_blocksparse_attn_bwd_workspace_size(int B, int T, int Hq, int
  * Supported, as in the forward: q_block == 128, kv_block in {64, 128}, T % 128 == 0, D in
  * {64, 128}, 1 <= Hq / Hkv, B * T * Hq < 2^31, bf16 (fp32 accumulation; P and dS are rounded to
  * bf16 before their products).  Results are the same from run to run.
- * Internally, on `stream`: a kernel that prepares the rows, the dK / dV kernel, the dQ kernel,
- * which begins while the last blocks of dK / dV run, and a merge of dK and dV where they are in parts.
+ * Internally, on `stream`: a kernel that prepares the rows, one for dK, dV and dQ, and a merge of dK and
+ * dV where they are in parts.
  */
 SBA_API int sba_blocksparse_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                                      const float* lse, const void* d_out, const int32_t* q_pos,

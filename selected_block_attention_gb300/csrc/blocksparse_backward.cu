@@ -6,23 +6,24 @@
 //   dV = P^T dO,   dS = P * (dO V^T - Delta),   dQ = scale dS K,   dK = scale dS^T Q.
 // The probabilities are computed again from q, k and the LSE; nothing of size T x T is stored.
 //
-// Three or four launches, on one stream:
+// Two or three launches, on one stream:
 //   1. prep: Delta and the LSE of every row, negated and laid out [B, Hq, T], so that a tile's
 //      128 values are one run; for each key tile the query blocks whose bounds reach it (the
 //      bounds of the forward, turned round: dK and dV sum exactly the pairs that the forward
 //      used, whatever the positions are).
-//   2. dK / dV: a work item is a tile of 128 keys of one KV head; its steps are the (query
-//      block, query head) pairs that reach it.  With few such tiles, those of a part of the heads.
-//   3. dQ: a work item is a query block of 128 tokens of one query head; its steps are the
-//      128-key tiles of its bounds.
-//   4. merge, if the heads are in parts: their dK and dV added up.
+//   2. the products.  dK / dV: a work item is a tile of 128 keys of one KV head; its steps are the
+//      (query block, query head) pairs that reach it.  With few such tiles, those of a part of the
+//      heads.  dQ: a work item is a query block of 128 tokens of one query head; its steps are the
+//      128-key tiles of its bounds.  A block takes items of dK / dV until there are none left, then
+//      items of dQ; blocks that find none of the first kind begin with dQ at once.
+//   3. merge, if the heads are in parts: their dK and dV added up.
 // S and dP are computed in both (7 products for the 5 of the formulas).  The other way, one pass
 // with dQ added up in memory, needs B T Hq D fp32 sums cleared, added to by every key tile and
 // rounded at the end, some 2.7 GB beside 1.1 GB of inputs on a batch of 4 x 16384 tokens, and its
 // sums come in an order set by timing.  Here every sum is held in tensor memory by one CTA, in an
 // order that the bounds fix, so results are the same from run to run.
 //
-// Both tensor-core kernels keep one tile of S and one of dP (128 x 128 fp32 each) in tensor memory
+// Both halves of the kernel keep one tile of S and one of dP (128 x 128 fp32 each) in tensor memory
 // and are arranged so that the tensor core always has a product to do while the softmax warps work
 // on the other tile.  In steady state, per step:
 //   dK / dV:  dV(i)   S(i+1)   dK(i)   dP(i+1)      softmax warps: dS(i) | P(i+1)
@@ -356,7 +357,7 @@ __device__ __forceinline__ void store_part(uint32_t a, float* to, long long stri
   }
 }
 
-// ------------------------------------------------------------------ 2. dK / dV
+// ------------------------------------------------------------------ 2. the products: dK / dV
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
 // kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
 // token mask (bit numbers).
@@ -383,15 +384,11 @@ struct KvCfg {
   static constexpr int kOffQ = 2 * kTile;
   static constexpr int kOffDo = kOffQ + kQStages * kTile;
   static constexpr int kOffRows = kOffDo + kDoStages * kTile;
-  static constexpr int kOffBars = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
+  static constexpr int kEnd = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
   static constexpr int kNumBars = 4 + kQStages + kDoStages + 2 * kRowSlots + kDpBars + 6;
-  static constexpr int kOffMisc = kOffBars + kNumBars * 8;   // tmem address, abort flag, step flags
-  // At least half of an SM's shared memory: one CTA an SM, as each holds all tensor memory.
-  static constexpr int kSmemBytes = (kOffMisc + 8 + 4 * kQStages) > 120 * 1024 ? (kOffMisc + 8 + 4 * kQStages) : 120 * 1024;
   static constexpr int kSCol = 0, kDpCol = 128, kDvCol = 256, kDkCol = 256 + D;
   static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
   static constexpr uint32_t kIdescAcc = make_idesc(128, D, 1u, false, true);
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 // Items: key tiles of windows of kGroupWindow (row, KV head, part of its query heads) groups, tile by
@@ -428,68 +425,69 @@ __device__ __forceinline__ void zero_rows(const Params& p, int part, int key0, i
   }
 }
 
-// kSplit: the item's sums are a part's, and leave in fp32 for the merge kernel.
-template <int D, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
-bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const Params p) {
-  using C = KvCfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  if (!swizzle_aligned(smem)) return;
-  uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
-  uint64_t* k_full = bb;     bb += 1;
-  uint64_t* k_empty = bb;    bb += 1;
-  uint64_t* v_full = bb;     bb += 1;
-  uint64_t* v_empty = bb;    bb += 1;
-  uint64_t* q_full = bb;     bb += C::kQStages;
-  uint64_t* do_full = bb;    bb += C::kDoStages;
-  uint64_t* row_full = bb;   bb += C::kRowSlots;
-  uint64_t* row_empty = bb;  bb += C::kRowSlots;
-  uint64_t* s_full = bb;     bb += 1;
-  uint64_t* p_full = bb;     bb += 1;
-  uint64_t* dp_full = bb;    bb += C::kDpBars;  // by turns
-  uint64_t* ds_full = bb;    bb += 1;
-  uint64_t* acc_full = bb;   bb += 1;
-  uint64_t* acc_empty = bb;  bb += 1;
-  uint64_t* mma_done = bb;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* step_flags = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);  // per Q stage
-  const Abort ab{abort_flag, &g_err_bsb, 5u, p.wait_limit};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto row_at = [&](int slot) -> StepRow& {
-    return *reinterpret_cast<StepRow*>(smem + C::kOffRows + slot * sizeof(StepRow));
-  };
-
-  if (threadIdx.x == 0) {
+template <int D>
+struct KvBars {
+  uint64_t *k_full, *k_empty, *v_full, *v_empty, *q_full, *do_full, *row_full, *row_empty, *s_full, *p_full;
+  uint64_t *dp_full, *ds_full, *acc_full, *acc_empty, *mma_done;  // dp_full by turns
+  __device__ __forceinline__ explicit KvBars(uint64_t* bb) {
+    using C = KvCfg<D>;
+    k_full = bb;     bb += 1;
+    k_empty = bb;    bb += 1;
+    v_full = bb;     bb += 1;
+    v_empty = bb;    bb += 1;
+    q_full = bb;     bb += C::kQStages;
+    do_full = bb;    bb += C::kDoStages;
+    row_full = bb;   bb += C::kRowSlots;
+    row_empty = bb;  bb += C::kRowSlots;
+    s_full = bb;     bb += 1;
+    p_full = bb;     bb += 1;
+    dp_full = bb;    bb += C::kDpBars;
+    ds_full = bb;    bb += 1;
+    acc_full = bb;   bb += 1;
+    acc_empty = bb;  bb += 1;
+    mma_done = bb;
+  }
+  __device__ __forceinline__ void init() const {
+    using C = KvCfg<D>;
     mbar_init(k_full, 1); mbar_init(k_empty, 1); mbar_init(v_full, 1); mbar_init(v_empty, 1);
     for (int i = 0; i < C::kQStages; ++i) mbar_init(&q_full[i], 1);
     for (int i = 0; i < C::kDoStages; ++i) mbar_init(&do_full[i], 1);
     for (int i = 0; i < C::kRowSlots; ++i) { mbar_init(&row_full[i], 1); mbar_init(&row_empty[i], kSoftWarps); }
-    mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps); 
+    mbar_init(s_full, 1); mbar_init(p_full, kSoftWarps);
     for (int i = 0; i < C::kDpBars; ++i) mbar_init(&dp_full[i], 1);
     mbar_init(ds_full, kSoftWarps);
     mbar_init(acc_full, 1); mbar_init(acc_empty, kSoftWarps); mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_do);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const uint32_t smem_base = smem_u32(smem);
-  // prep's results (and all that ran before it) are there; the dQ kernel may be set up
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+};
+
+// What a block's warps share besides the barriers.
+struct Block {
+  uint8_t* smem;
+  uint32_t tmem;
+  volatile int* abort_flag;
+  volatile int* step_flags;  // dK / dV: per Q stage
+};
+
+// Items of dK / dV until there are none left.  kSplit: an item's sums are a part's, and leave in fp32 for
+// the merge kernel.
+template <int D, bool kSplit>
+__device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                           const CUtensorMap& tm_v, const Params& p, const Block& block,
+                                           const KvBars<D>& bars) {
+  using C = KvCfg<D>;
+  uint64_t *const k_full = bars.k_full, *const k_empty = bars.k_empty, *const v_full = bars.v_full,
+           *const v_empty = bars.v_empty, *const q_full = bars.q_full, *const do_full = bars.do_full,
+           *const row_full = bars.row_full, *const row_empty = bars.row_empty, *const s_full = bars.s_full,
+           *const p_full = bars.p_full, *const dp_full = bars.dp_full, *const ds_full = bars.ds_full,
+           *const acc_full = bars.acc_full, *const acc_empty = bars.acc_empty, *const mma_done = bars.mma_done;
+  uint8_t* const smem = block.smem;
+  volatile int* const step_flags = block.step_flags;
+  const uint32_t tmem = block.tmem, smem_base = smem_u32(smem);
+  const Abort ab{block.abort_flag, &g_err_bsb, 5u, p.wait_limit};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto row_at = [&](int slot) -> StepRow& {
+    return *reinterpret_cast<StepRow*>(smem + C::kOffRows + slot * sizeof(StepRow));
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loader
@@ -861,16 +859,9 @@ bsa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       work = !(flags & kEnd);
     }
   }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
 }
 
-// ------------------------------------------------------------------ 3. dQ
+// ------------------------------------------------------------------ dQ
 struct DqItem {
   int b, hkv, h, qblk, n_steps, item;  // n_steps -1: no more items
   Range r;
@@ -887,50 +878,38 @@ struct DqCfg {
   static constexpr int kOffV = kOffK + kKStages * kTile;
   static constexpr int kItemBytes = (static_cast<int>(sizeof(DqItem)) + 15) & ~15;
   static constexpr int kOffItems = kOffV + kVStages * kTile;
-  static constexpr int kOffBars = kOffItems + kItemSlots * kItemBytes;
+  static constexpr int kEnd = kOffItems + kItemSlots * kItemBytes;
   static constexpr int kNumBars = 2 * kItemSlots + 4 + kKStages + kVStages + 8;
-  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
-  static constexpr int kSmemBytes = (kOffMisc + 8) > 120 * 1024 ? (kOffMisc + 8) : 120 * 1024;
   static constexpr int kSCol = 0, kDpCol = 128, kDqCol = 256, kQCol = 256 + D, kDoCol = kQCol + D / 2;
   static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
   static constexpr uint32_t kIdescAcc = make_idesc(128, D, 1u, false, true);
   static_assert(kDoCol + D / 2 <= 512, "tensor memory budget");
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const Params p) {
-  using C = DqCfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  if (!swizzle_aligned(smem)) return;
-  uint64_t* bb = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
-  uint64_t* item_full = bb;  bb += kItemSlots;
-  uint64_t* item_empty = bb; bb += kItemSlots;
-  uint64_t* q_full = bb;     bb += 1;
-  uint64_t* q_empty = bb;    bb += 1;
-  uint64_t* do_full = bb;    bb += 1;
-  uint64_t* do_empty = bb;   bb += 1;
-  uint64_t* k_full = bb;     bb += C::kKStages;
-  uint64_t* v_full = bb;     bb += C::kVStages;
-  uint64_t* s_full = bb;     bb += 1;
-  uint64_t* s_empty = bb;    bb += 1;
-  uint64_t* dp_full = bb;    bb += 2;  // by turns
-  uint64_t* ds_full = bb;    bb += 1;
-  uint64_t* dq_full = bb;    bb += 1;
-  uint64_t* dq_empty = bb;   bb += 1;
-  uint64_t* mma_done = bb;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  const Abort ab{abort_flag, &g_err_bsb, 6u, p.wait_limit};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto item_at = [&](int slot) -> DqItem& {
-    return *reinterpret_cast<DqItem*>(smem + C::kOffItems + slot * C::kItemBytes);
-  };
-
-  if (threadIdx.x == 0) {
+struct DqBars {
+  uint64_t *item_full, *item_empty, *q_full, *q_empty, *do_full, *do_empty, *k_full, *v_full, *s_full, *s_empty;
+  uint64_t *dp_full, *ds_full, *dq_full, *dq_empty, *mma_done;  // dp_full by turns
+  __device__ __forceinline__ explicit DqBars(uint64_t* bb) {
+    using C = DqCfg<D>;
+    item_full = bb;  bb += kItemSlots;
+    item_empty = bb; bb += kItemSlots;
+    q_full = bb;     bb += 1;
+    q_empty = bb;    bb += 1;
+    do_full = bb;    bb += 1;
+    do_empty = bb;   bb += 1;
+    k_full = bb;     bb += C::kKStages;
+    v_full = bb;     bb += C::kVStages;
+    s_full = bb;     bb += 1;
+    s_empty = bb;    bb += 1;
+    dp_full = bb;    bb += 2;
+    ds_full = bb;    bb += 1;
+    dq_full = bb;    bb += 1;
+    dq_empty = bb;   bb += 1;
+    mma_done = bb;
+  }
+  __device__ __forceinline__ void init() const {
+    using C = DqCfg<D>;
     // an item slot is read by the MMA warp and the softmax warps
     for (int i = 0; i < kItemSlots; ++i) { mbar_init(&item_full[i], 1); mbar_init(&item_empty[i], 1 + kSoftWarps); }
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
@@ -939,24 +918,27 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(s_full, 1); mbar_init(s_empty, kSoftWarps); mbar_init(&dp_full[0], 1); mbar_init(&dp_full[1], 1);
     mbar_init(ds_full, kSoftWarps);
     mbar_init(dq_full, 1); mbar_init(dq_empty, kSoftWarps); mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_do);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
-  const uint32_t smem_base = smem_u32(smem);
-  // No wait for the dK / dV kernel here: its blocks let this kernel be set up only after their own
-  // wait for prep, and nothing that it writes is read.
+};
+
+// Items of dQ until there are none left.
+template <int D>
+__device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const Params& p, const Block& block,
+                                         const DqBars<D>& bars) {
+  using C = DqCfg<D>;
+  uint64_t *const item_full = bars.item_full, *const item_empty = bars.item_empty, *const q_full = bars.q_full,
+           *const q_empty = bars.q_empty, *const do_full = bars.do_full, *const do_empty = bars.do_empty,
+           *const k_full = bars.k_full, *const v_full = bars.v_full, *const s_full = bars.s_full,
+           *const s_empty = bars.s_empty, *const dp_full = bars.dp_full, *const ds_full = bars.ds_full,
+           *const dq_full = bars.dq_full, *const dq_empty = bars.dq_empty, *const mma_done = bars.mma_done;
+  uint8_t* const smem = block.smem;
+  const uint32_t tmem = block.tmem, smem_base = smem_u32(smem);
+  const Abort ab{block.abort_flag, &g_err_bsb, 6u, p.wait_limit};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto item_at = [&](int slot) -> DqItem& {
+    return *reinterpret_cast<DqItem*>(smem + C::kOffItems + slot * C::kItemBytes);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loader
@@ -1282,18 +1264,75 @@ bsa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (last || !had) ndelta = ndelta_next;
     }
   }
+}
 
+// ------------------------------------------------------------------ both
+template <int D>
+struct Cfg {
+  using Kv = KvCfg<D>;
+  using Dq = DqCfg<D>;
+  static constexpr int kOffKvBars = Kv::kEnd > Dq::kEnd ? Kv::kEnd : Dq::kEnd;
+  static constexpr int kOffDqBars = kOffKvBars + Kv::kNumBars * 8;
+  static constexpr int kOffMisc = kOffDqBars + Dq::kNumBars * 8;  // tmem address, abort flag, step flags
+  static constexpr int kUsed = kOffMisc + 8 + 4 * Kv::kQStages;
+  // At least half of an SM's shared memory: one CTA an SM, as each holds all tensor memory.
+  static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  // dK / dV's rows are read by the warps; copies of dQ do not go there, so that no proxy fence is due
+  static_assert(Kv::kOffRows >= Dq::kOffItems, "rows behind the tiles of dQ");
+};
+
+// dK / dV and dQ are one kernel, set up while prep runs, so that every block waits for prep itself before
+// it reads what prep left.  As two kernels, the second of them started ahead of the first one's end to fill
+// its idle SMs, the second has no such wait that would not also be one for the end of the first.
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+bsa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!swizzle_aligned(smem)) return;
+  const KvBars<D> kv_bars(reinterpret_cast<uint64_t*>(smem + C::kOffKvBars));
+  const DqBars<D> dq_bars(reinterpret_cast<uint64_t*>(smem + C::kOffDqBars));
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    kv_bars.init();
+    dq_bars.init();
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Block block{smem, *tmem_holder, abort_flag, reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8)};
+  // prep's results (and all that ran before it) are there
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dkdv_items<D, kSplit>(tm_q, tm_do, tm_k, tm_v, p, block, kv_bars);
+  // All copies have landed, all products are done and read: shared and tensor memory are dQ's, unless a
+  // wait has run out.
+  tc_fence_before();
+  const int stop = __syncthreads_or(*abort_flag);
+  tc_fence_after();
+  if (stop == 0) dq_items<D>(tm_q, tm_do, tm_k, tm_v, p, block, dq_bars);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(block.tmem, 512);
   }
-  // the dK / dV kernel has ended before this one does: what follows on the stream waits for both
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// ------------------------------------------------------------------ 4. merge
+// ------------------------------------------------------------------ 3. merge
 // dK and dV of the parts added up in order: four elements a thread, each part read once.
 __global__ void __launch_bounds__(256) bsa_bwd_merge_kernel(const float4* __restrict__ parts, int n_split, long long n4,
                                                             float scale, uint2* __restrict__ dk, uint2* __restrict__ dv) {
@@ -1348,22 +1387,6 @@ Layout layout(int B, int T, int Hq, int Hkv, int D) {
   return l;
 }
 
-template <class Kernel>
-cudaError_t launch_after(Kernel kernel, int grid, int smem, cudaStream_t st, const CUtensorMap& a, const CUtensorMap& b,
-                         const CUtensorMap& c, const CUtensorMap& d, const Params& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, b, c, d, p);
-}
-
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const void* d_out, const Params& p, cudaStream_t stream) {
   CUtensorMap tq, tdo, tk, tv;
@@ -1376,21 +1399,26 @@ int launch_impl(const void* q, const void* k, const void* v, const void* d_out, 
   };
   if (!map(&tq, q, p.Hq) || !map(&tdo, d_out, p.Hq) || !map(&tk, k, p.Hkv) || !map(&tv, v, p.Hkv))
     return set_error(SBA_ERR_CUDA, "blocksparse_attn_bwd: tensor map failed");
-  const auto dkdv = p.n_split > 1 ? bsa_bwd_dkdv_kernel<D, true> : bsa_bwd_dkdv_kernel<D, false>;
-  cudaError_t e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, KvCfg<D>::kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(bsa_bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes);
+  const auto kernel = p.n_split > 1 ? bsa_bwd_kernel<D, true> : bsa_bwd_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
   if (e != cudaSuccess) return cuda_error(e, "blocksparse_attn_bwd: set smem attribute");
   const int tok_groups = p.T / kPrepTok, head_groups = (p.Hq + kPrepHeads - 1) / kPrepHeads;
   const int n_delta = p.B * tok_groups * head_groups, n_reach = (9 * p.B * p.nb + 7) / 8;  // 1 + 2 * 128 / 32 warps a block
   bsa_bwd_prep_kernel<D><<<n_delta + n_reach, 256, 0, stream>>>(p, n_delta, tok_groups, head_groups);
   e = cudaGetLastError();
-  if (e == cudaSuccess)
-    e = launch_after(dkdv, std::min(p.n_items_kv, num_sms()), KvCfg<D>::kSmemBytes, stream, tq, tdo,
-                     tk, tv, p);
-  if (e == cudaSuccess)
-    e = launch_after(bsa_bwd_dq_kernel<D>, std::min(p.n_items_dq, num_sms()), DqCfg<D>::kSmemBytes, stream, tq, tdo, tk,
-                     tv, p);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(p.n_items_kv + p.n_items_dq, num_sms()));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tq, tdo, tk, tv, p);
+  }
   if (e == cudaSuccess && p.n_split > 1) {
     const long long n4 = (long long)p.B * p.T * p.Hkv * D / 4;
     const int grid = static_cast<int>(std::min<long long>((2 * n4 + 255) / 256, 8LL * num_sms()));
