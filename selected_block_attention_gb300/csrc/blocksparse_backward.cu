@@ -312,17 +312,12 @@ __device__ __forceinline__ void swap_chunks(uint32_t (&v)[kChunks][4], int lane)
   }
 }
 
-// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16, or zeros.  `to`: this lane's row,
-// the rows of neighbouring lanes `stride` elements apart.
+// N = 32 or 16 fp32 accumulator columns of the lane row, times f, as bf16.  `to`: this lane's row, the
+// rows of neighbouring lanes `stride` elements apart.
 template <int N>
-__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane,
-                                           bool zeros = false) {
+__device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* to, long long stride, int lane) {
   float x[N];
   if constexpr (N == 32) tmem_ld_32x32b_x32(a, x); else tmem_ld_32x32b_x16(a, x);
-  if (zeros) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = 0.f;
-  }
   constexpr int kChunks = N / 8;
   uint32_t v[kChunks][4];
 #pragma unroll
@@ -340,7 +335,7 @@ __device__ __forceinline__ void store_cols(uint32_t a, float f, __nv_bfloat16* t
 // The same columns in fp32, for the merge; 16 at a time, as the caller holds P meanwhile (all 32 at once
 // spilled: 8192 tokens of 16 heads in two parts 600 -> 840 us).
 template <int N>
-__device__ __forceinline__ void store_part(uint32_t a, float* to, long long stride, int lane, bool zeros) {
+__device__ __forceinline__ void store_part(uint32_t a, float* to, long long stride, int lane) {
   const int me = lane % 4;
   float* row0 = to - me * stride + me * 4;
 #pragma unroll 1
@@ -349,7 +344,7 @@ __device__ __forceinline__ void store_part(uint32_t a, float* to, long long stri
     tmem_ld_32x32b_x16(a + c, x);
     uint32_t v[4][4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j / 4][j % 4] = zeros ? 0u : __float_as_uint(x[j]);
+    for (int j = 0; j < 16; ++j) v[j / 4][j % 4] = __float_as_uint(x[j]);
     swap_chunks(v, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -361,10 +356,8 @@ __device__ __forceinline__ void store_part(uint32_t a, float* to, long long stri
 // What the loader says of a step, in the row ring's slot; flags also beside the Q ring's stage.
 // kIn, kIn + 1: the bounds take in the tile's first and second 64 keys; kFull, kFull + 1: without a
 // token mask (bit numbers).
-// kSame: the query block of the step before.  kUnseen, kUnseen + 1 (bit numbers): no bounds take in the
-// tile's first, second 64 keys.  kHalf (dQ): the bounds end within the step's tile.  From bit 16 on: the
-// item's part.
-enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256, kUnseen = 9, kHalf = 2048 };
+// kSame: the query block of the step before.  From bit 16 on: the item's part.
+enum StepFlag : int { kFirst = 1, kLast = 2, kEnd = 8, kIn = 4, kFull = 6, kSame = 256 };
 struct alignas(16) StepRow {
   float nlse[kM];
   float ndelta[kM];
@@ -384,7 +377,7 @@ struct KvCfg {
   static constexpr int kOffQ = 2 * kTile;
   static constexpr int kOffDo = kOffQ + kQStages * kTile;
   static constexpr int kOffRows = kOffDo + kDoStages * kTile;
-  static constexpr int kEnd = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
+  static constexpr int kDataEnd = kOffRows + kRowSlots * static_cast<int>(sizeof(StepRow));
   static constexpr int kNumBars = 4 + kQStages + kDoStages + 2 * kRowSlots + kDpBars + 6;
   static constexpr int kSCol = 0, kDpCol = 128, kDvCol = 256, kDkCol = 256 + D;
   static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
@@ -460,6 +453,26 @@ struct KvBars {
   }
 };
 
+// Boxes of 128 tokens of a head and 64 columns, of K and V also of 64 tokens.
+struct Maps {
+  CUtensorMap q, d_out, k, k_half, v_half;
+};
+
+// 64 tokens from token0 on of a head to the first half of a tile, those from token1 on to the second.  A half
+// outside the bounds is read as zeros, by a box that begins behind the last token: its keys take part in the
+// products with weight 0, and 0 times what they hold, which behind a row's last tile is another sequence's,
+// need not be 0.
+template <int kPanels>
+__device__ __forceinline__ void load_halves(uint8_t* to, const CUtensorMap& map, uint64_t* bar, int head, int token0,
+                                            int token1) {
+  mbar_arrive_expect_tx(bar, kPanels * kPanel);
+#pragma unroll
+  for (int pn = 0; pn < kPanels; ++pn) {
+    tma_load_3d(to + pn * kPanel, &map, bar, pn * 64, head, token0);
+    tma_load_3d(to + pn * kPanel + kPanel / 2, &map, bar, pn * 64, head, token1);
+  }
+}
+
 // What a block's warps share besides the barriers.
 struct Block {
   uint8_t* smem;
@@ -471,9 +484,7 @@ struct Block {
 // Items of dK / dV until there are none left.  kSplit: an item's sums are a part's, and leave in fp32 for
 // the merge kernel.
 template <int D, bool kSplit>
-__device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
-                                           const CUtensorMap& tm_v, const Params& p, const Block& block,
-                                           const KvBars<D>& bars) {
+__device__ __forceinline__ void dkdv_items(const Maps& maps, const Params& p, const Block& block, const KvBars<D>& bars) {
   using C = KvCfg<D>;
   uint64_t *const k_full = bars.k_full, *const k_empty = bars.k_empty, *const v_full = bars.v_full,
            *const v_empty = bars.v_empty, *const q_full = bars.q_full, *const do_full = bars.do_full,
@@ -533,7 +544,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
       kv_item(p, item, b, hkv, part, kt);
       const int4 reach = p.reach[b * p.nb + kt];
       const int heads = p.G / p.n_split, n_steps = reach.z * heads;
-      const int key0 = b * p.T + kt * kM, unseen = (~reach.w & 3) << kUnseen;
+      const int key0 = b * p.T + kt * kM;
       if (n_steps == 0) {
         // No query sees these keys.  The zeros are written from here, as many such tiles may follow one
         // another: in the row ring they would wait for the softmax warps, these in finish() for the last
@@ -566,7 +577,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
             if (!wait_phase(&row_empty[rs], rph ^ 1, ab, kRoleLoader, kBarRowEmpty, item)) { ok = false; break; }
             if (lane == 0) {
               StepRow& w = row_at(rs);
-              w.what = make_int4(flags | seen | unseen | (g > 0 ? kSame : 0) | part << 16, tok0, key0, hkv);
+              w.what = make_int4(flags | seen | (g > 0 ? kSame : 0) | part << 16, tok0, key0, hkv);
               const long long o = ((long long)b * p.Hq + h) * p.T + qblk * kM;
               mbar_arrive_expect_tx(&row_full[rs], 2 * kM * 4);
               bulk_load(w.nlse, p.nlse + o, kM * 4, &row_full[rs]);
@@ -581,7 +592,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
                 mbar_arrive_expect_tx(k_full, C::kTile);
 #pragma unroll
                 for (int pn = 0; pn < C::kPanels; ++pn)
-                  tma_load_3d(smem + C::kOffK + pn * kPanel, &tm_k, k_full, pn * 64, hkv, key0);
+                  tma_load_3d(smem + C::kOffK + pn * kPanel, &maps.k, k_full, pn * 64, hkv, key0);
               }
               k_out = true; kph ^= 1;
             }
@@ -591,18 +602,15 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
               mbar_arrive_expect_tx(&q_full[qs], C::kTile);
 #pragma unroll
               for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(smem + C::kOffQ + qs * C::kTile + pn * kPanel, &tm_q, &q_full[qs], pn * 64, h, tok0);
+                tma_load_3d(smem + C::kOffQ + qs * C::kTile + pn * kPanel, &maps.q, &q_full[qs], pn * 64, h, tok0);
             }
             q_out |= 1u << qs; q_last = (q_last & ~(1u << qs)) | (qph << qs);
             if (++qs == C::kQStages) { qs = 0; qph ^= 1; }
             if (step == 0) {
               if (!wait_phase(v_empty, vph ^ 1, ab, kRoleLoader, kBarVEmpty, item)) { ok = false; break; }
-              if (lane == 0) {
-                mbar_arrive_expect_tx(v_full, C::kTile);
-#pragma unroll
-                for (int pn = 0; pn < C::kPanels; ++pn)
-                  tma_load_3d(smem + C::kOffV + pn * kPanel, &tm_v, v_full, pn * 64, hkv, key0);
-              }
+              if (lane == 0)
+                load_halves<C::kPanels>(smem + C::kOffV, maps.v_half, v_full, hkv, (reach.w & 1) ? key0 : p.B * p.T,
+                                        (reach.w & 2) ? key0 + kSub : p.B * p.T);
               v_out = true; vph ^= 1;
             }
             if (!kTogether && n_loaded >= 2 && !dp_there(n_loaded - 1, item)) { ok = false; break; }
@@ -611,7 +619,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
               mbar_arrive_expect_tx(&do_full[ds], C::kTile);
 #pragma unroll
               for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(smem + C::kOffDo + ds * C::kTile + pn * kPanel, &tm_do, &do_full[ds], pn * 64, h, tok0);
+                tma_load_3d(smem + C::kOffDo + ds * C::kTile + pn * kPanel, &maps.d_out, &do_full[ds], pn * 64, h, tok0);
             }
             d_out |= 1u << ds; d_last = (d_last & ~(1u << ds)) | (dph << ds);
             if (++ds == C::kDoStages) { ds = 0; dph ^= 1; }
@@ -727,7 +735,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
     int rs = 0, next_rs = 0;       // row slots of the step and of the one looked up
     uint32_t rph = 0, sph = 0, dpph = 0, accph = 0;
     int dpt = 0;                   // barrier of the next dP
-    int done_row = -1;             // this thread's key (times heads) of a finished item, -2 - key if unseen
+    int done_row = -1;             // this thread's key (times heads) of a finished item
     int lo = 1, hi = 0, seg = 0;   // query positions that may see this key, and its segment
     // The step to come: its flags, this thread's key, and the columns that pair with it.  Looked up
     // while the step before waits for dP.
@@ -770,15 +778,13 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
       if (!wait_phase(acc_full, accph, ab, kRoleSoftmax, kBarAccFull, row)) return false;
       accph ^= 1;
       tc_fence_after();
-      // Keys in no bounds get zeros, whatever their values left in the sums (0 times NaN is NaN).
-      const bool none = done_row < 0;
-      const long long to = (long long)(none ? -2 - done_row : done_row) * D + w * (D / 4), stride = (long long)p.Hkv * D;
+      const long long to = (long long)done_row * D + w * (D / 4), stride = (long long)p.Hkv * D;
       if constexpr (kSplit) {
-        store_part<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), p.parts + (long long)rows * D + to, stride, lane, none);
-        store_part<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.parts + to, stride, lane, none);
+        store_part<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), p.parts + (long long)rows * D + to, stride, lane);
+        store_part<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.parts + to, stride, lane);
       } else {
-        store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, stride, lane, none);
-        store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, stride, lane, none);
+        store_cols<D / 4>(tmem + lane_off + C::kDvCol + w * (D / 4), 1.f, p.dv + to, stride, lane);
+        store_cols<D / 4>(tmem + lane_off + C::kDkCol + w * (D / 4), p.scale, p.dk + to, stride, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -793,7 +799,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
     while (true) {
       float x[kCols];
       const bool last = work && (flags & kLast);
-      const int this_row = (flags >> (kUnseen + (q4 >> 1))) & 1 ? -2 - row : row;
+      const int this_row = row;
       if (work) {
         if (!wait_phase(s_full, sph, ab, kRoleSoftmax, kBarSFull, row)) break;
         sph ^= 1;
@@ -825,7 +831,7 @@ __device__ __forceinline__ void dkdv_items(const CUtensorMap& tm_q, const CUtens
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      if (__builtin_expect(done_row != -1, 0) && !finish()) break;
+      if (__builtin_expect(done_row >= 0, 0) && !finish()) break;
       if (flags & kEnd) break;
       if (!look_up()) break;
       if (work) {
@@ -878,7 +884,7 @@ struct DqCfg {
   static constexpr int kOffV = kOffK + kKStages * kTile;
   static constexpr int kItemBytes = (static_cast<int>(sizeof(DqItem)) + 15) & ~15;
   static constexpr int kOffItems = kOffV + kVStages * kTile;
-  static constexpr int kEnd = kOffItems + kItemSlots * kItemBytes;
+  static constexpr int kDataEnd = kOffItems + kItemSlots * kItemBytes;
   static constexpr int kNumBars = 2 * kItemSlots + 4 + kKStages + kVStages + 8;
   static constexpr int kSCol = 0, kDpCol = 128, kDqCol = 256, kQCol = 256 + D, kDoCol = kQCol + D / 2;
   static constexpr uint32_t kIdescS = make_idesc(128, kM, 1u, false, false);
@@ -923,9 +929,7 @@ struct DqBars {
 
 // Items of dQ until there are none left.
 template <int D>
-__device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
-                                         const CUtensorMap& tm_v, const Params& p, const Block& block,
-                                         const DqBars<D>& bars) {
+__device__ __forceinline__ void dq_items(const Maps& maps, const Params& p, const Block& block, const DqBars<D>& bars) {
   using C = DqCfg<D>;
   uint64_t *const item_full = bars.item_full, *const item_empty = bars.item_empty, *const q_full = bars.q_full,
            *const q_empty = bars.q_empty, *const do_full = bars.do_full, *const do_empty = bars.do_empty,
@@ -984,7 +988,7 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensor
             mbar_arrive_expect_tx(q_full, C::kTile);
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_3d(smem + C::kOffQ + pn * kPanel, &tm_q, q_full, pn * 64, h, tok0);
+              tma_load_3d(smem + C::kOffQ + pn * kPanel, &maps.q, q_full, pn * 64, h, tok0);
           }
           q_last = qph;
         }
@@ -994,12 +998,8 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensor
           break;
         }
         ++n_loaded;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[ks], C::kTile);
-#pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(smem + C::kOffK + ks * C::kTile + pn * kPanel, &tm_k, &k_full[ks], pn * 64, hkv, key0);
-        }
+        const int key1 = r.lo + 2 * t + 1 < r.up ? key0 + kSub : p.B * p.T;
+        if (lane == 0) load_halves<C::kPanels>(smem + C::kOffK + ks * C::kTile, maps.k_half, &k_full[ks], hkv, key0, key1);
         k_out |= 1u << ks; k_last = (k_last & ~(1u << ks)) | (kph << ks);
         if (++ks == C::kKStages) { ks = 0; kph ^= 1; }
         if (t == 0) {
@@ -1008,16 +1008,11 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensor
             mbar_arrive_expect_tx(do_full, C::kTile);
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_3d(smem + C::kOffDo + pn * kPanel, &tm_do, do_full, pn * 64, h, tok0);
+              tma_load_3d(smem + C::kOffDo + pn * kPanel, &maps.d_out, do_full, pn * 64, h, tok0);
           }
           do_last = qph; qph ^= 1;
         }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&v_full[vs], C::kTile);
-#pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(smem + C::kOffV + vs * C::kTile + pn * kPanel, &tm_v, &v_full[vs], pn * 64, hkv, key0);
-        }
+        if (lane == 0) load_halves<C::kPanels>(smem + C::kOffV + vs * C::kTile, maps.v_half, &v_full[vs], hkv, key0, key1);
         v_out |= 1u << vs; v_last = (v_last & ~(1u << vs)) | (vph << vs);
         if (++vs == C::kVStages) { vs = 0; vph ^= 1; }
       }
@@ -1042,21 +1037,19 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensor
     auto off = [](int stage) { return static_cast<uint64_t>((stage * C::kTile) >> 4); };
     int islot = 0, ks = 0, vs = 0, left = 0;   // left: steps of the item not yet taken
     uint32_t iph = 0, qph = 0, doph = 0, kph = 0, vph = 0, seph = 0, dsph = 0, dqph = 0;
-    int odd = 0;                               // kHalf if the item has an odd number of 64-key tiles
-    // the next step's flags: kFirst, kLast, kHalf, or kEnd
+    // the next step's flags: kFirst, kLast, or kEnd
     auto next_step = [&](int& flags) -> bool {
       flags = 0;
       while (left == 0) {
         if (!wait_phase(&item_full[islot], iph, ab, kRoleMma, kBarItemFull, -1)) return false;
         left = item_at(islot).n_steps;
-        odd = ((item_at(islot).r.up - item_at(islot).r.lo) & 1) != 0 ? kHalf : 0;
         __syncwarp();
         if (left < 0) { flags = kEnd; return true; }
         if (lane == 0) mbar_arrive(&item_empty[islot]);
         if (++islot == kItemSlots) { islot = 0; iph ^= 1; }
         flags = kFirst;
       }
-      if (--left == 0) flags |= kLast | odd;
+      if (--left == 0) flags |= kLast;
       return true;
     };
     // S = Q K^T into its columns, which the softmax warps have read
@@ -1119,13 +1112,10 @@ __device__ __forceinline__ void dq_items(const CUtensorMap& tm_q, const CUtensor
         dqph ^= 1;
       }
       tc_fence_after();
-      // K behind the end of the bounds takes no part: those rows are keys that the item does not see or,
-      // behind a row's last tile, another sequence's, and 0 times what they hold need not be 0.
-      const uint32_t second = (cur & kHalf) ? 0u : leader;
 #pragma unroll
       for (int kk = 0; kk < kM / 16; ++kk)
-        mma_f16_ts_by(kk < kM / 32 ? leader : second, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk),
-                      kmn_desc + off(ck) + mnmajor(kk), C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
+        mma_f16_ts_by(leader, tmem + C::kDqCol, tmem + C::kDpCol + part_cols(kk), kmn_desc + off(ck) + mnmajor(kk),
+                      C::kIdescAcc, ((cur & kFirst) && kk == 0) ? 0u : 1u);
       if (++ck == C::kKStages) ck = 0;
       if (cur & kLast) mma_commit_by(leader, dq_full);
       if (!(next & kEnd) && !issue_dp(next)) break;
@@ -1271,7 +1261,7 @@ template <int D>
 struct Cfg {
   using Kv = KvCfg<D>;
   using Dq = DqCfg<D>;
-  static constexpr int kOffKvBars = Kv::kEnd > Dq::kEnd ? Kv::kEnd : Dq::kEnd;
+  static constexpr int kOffKvBars = Kv::kDataEnd > Dq::kDataEnd ? Kv::kDataEnd : Dq::kDataEnd;
   static constexpr int kOffDqBars = kOffKvBars + Kv::kNumBars * 8;
   static constexpr int kOffMisc = kOffDqBars + Dq::kNumBars * 8;  // tmem address, abort flag, step flags
   static constexpr int kUsed = kOffMisc + 8 + 4 * Kv::kQStages;
@@ -1287,8 +1277,7 @@ struct Cfg {
 // its idle SMs, the second has no such wait that would not also be one for the end of the first.
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
-bsa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+bsa_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!swizzle_aligned(smem)) return;
@@ -1302,10 +1291,11 @@ bsa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     dq_bars.init();
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_do);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.d_out);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.k_half);
+    tma_prefetch_desc(&maps.v_half);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -1317,13 +1307,13 @@ bsa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const Block block{smem, *tmem_holder, abort_flag, reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8)};
   // prep's results (and all that ran before it) are there
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  dkdv_items<D, kSplit>(tm_q, tm_do, tm_k, tm_v, p, block, kv_bars);
+  dkdv_items<D, kSplit>(maps, p, block, kv_bars);
   // All copies have landed, all products are done and read: shared and tensor memory are dQ's, unless a
   // wait has run out.
   tc_fence_before();
   const int stop = __syncthreads_or(*abort_flag);
   tc_fence_after();
-  if (stop == 0) dq_items<D>(tm_q, tm_do, tm_k, tm_v, p, block, dq_bars);
+  if (stop == 0) dq_items<D>(maps, p, block, dq_bars);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1389,15 +1379,16 @@ Layout layout(int B, int T, int Hq, int Hkv, int D) {
 
 template <int D>
 int launch_impl(const void* q, const void* k, const void* v, const void* d_out, const Params& p, cudaStream_t stream) {
-  CUtensorMap tq, tdo, tk, tv;
-  auto map = [&](CUtensorMap* m, const void* at, int heads) {
+  Maps maps;
+  auto map = [&](CUtensorMap* m, const void* at, int heads, int rows) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)p.B * p.T};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-    cuuint32_t box[3] = {64, 1, (cuuint32_t)kM};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
     return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dims, strides, box,
                              CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
   };
-  if (!map(&tq, q, p.Hq) || !map(&tdo, d_out, p.Hq) || !map(&tk, k, p.Hkv) || !map(&tv, v, p.Hkv))
+  if (!map(&maps.q, q, p.Hq, kM) || !map(&maps.d_out, d_out, p.Hq, kM) || !map(&maps.k, k, p.Hkv, kM) ||
+      !map(&maps.k_half, k, p.Hkv, kSub) || !map(&maps.v_half, v, p.Hkv, kSub))
     return set_error(SBA_ERR_CUDA, "blocksparse_attn_bwd: tensor map failed");
   const auto kernel = p.n_split > 1 ? bsa_bwd_kernel<D, true> : bsa_bwd_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
@@ -1417,7 +1408,7 @@ int launch_impl(const void* q, const void* k, const void* v, const void* d_out, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, tq, tdo, tk, tv, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, maps, p);
   }
   if (e == cudaSuccess && p.n_split > 1) {
     const long long n4 = (long long)p.B * p.T * p.Hkv * D / 4;
