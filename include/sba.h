@@ -382,7 +382,8 @@ SBA_API int sba_rotary_tables(int length, int rot_dim, double base, double facto
  * the others are copied.  `inverse` negates s: the transpose of the rotation, which takes gradients
  * of rotated queries and keys to those of the plain ones (and, with tables of amplitude 1, turns
  * rotated values back).  A token at a negative position passes through as it is; a position >=
- * max_pos does too, and sba_check_error() reports SBA_ERR_DEVICE_INPUT.
+ * max_pos does too, and sba_check_error() reports SBA_ERR_DEVICE_INPUT.  Without positions T > max_pos is
+ * refused (SBA_ERR_INVALID_ARG).
  * In place (q_out == q, k_out == k) with the same token stride; otherwise no output overlaps an
  * input or the other output.
  * dtype SBA_BF16 or SBA_F32; D a multiple of 16 in [16, 256]; rot_dim a multiple of 16 in [16, D];

@@ -580,6 +580,7 @@ int sba_rotary_embed(const sba_rotary_embed_args* args, sba_stream_t stream) {
   if (n == 0) return SBA_OK;
   SBA_REQUIRE(a.q && a.q_out && a.cos && a.sin, "null pointer");
   SBA_REQUIRE(a.max_pos >= 1, "cos and sin must have at least one position");
+  SBA_REQUIRE(a.positions || a.T <= a.max_pos, "without positions T must be at most max_pos, the tables' length");
   SBA_REQUIRE(aligned16(a.q) && aligned16(a.k) && aligned16(a.q_out) && aligned16(a.k_out) && aligned16(a.cos) &&
                   aligned16(a.sin),
               "tensors must be 16-byte aligned");

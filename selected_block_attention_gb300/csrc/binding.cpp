@@ -592,8 +592,8 @@ const char kEmbedDoc[] =
     "k_out=None)\n--\n\n"
     "Queries and keys rotated by their positions.  q [B, T, Hq, D] and k [B, T, Hkv, D] (or\n"
     "[N, H, D]; k may be None), bf16 or fp32, may be slices of one projection's output; cos / sin\n"
-    "fp32 [max_pos, rot_dim / 2]; positions int32 [B, T] ([N]), by default those in the row, a\n"
-    "negative one leaves its token as it is.  inverse turns back: the gradient.  Returns\n"
+    "fp32 [max_pos, rot_dim / 2]; positions int32 [B, T] ([N]), by default those in the row (at most\n"
+    "max_pos of them), a negative one leaves its token as it is.  inverse turns back: the gradient.  Returns\n"
     "(q_out, k_out), new unless given (may be q and k).";
 PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
   static const Signature sig("rotary_embed", 4, 4,
