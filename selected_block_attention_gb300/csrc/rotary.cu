@@ -11,6 +11,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "rotary_turns.h"
 
 namespace sba {
 
@@ -21,9 +22,8 @@ namespace {
 // ------------------------------------------------------------------ tables
 // The angle of a far position loses its fraction of a turn in 32 bits.  Here a pair's frequency
 // is a 64-bit fixed-point number of turns a position (2^-64 steps), so position * frequency
-// modulo 2^64 is the fraction of a turn itself, off by at most position * 2^-64 turns beside the
-// 2^-53 of the frequency's own rounding.  Its quarter turns are the two bits above the rest, which becomes
-// a float, relative precision kept: r in [-1, 1) eighths of a turn.  There sin(pi/4 r) = r S(r^2) and
+// modulo 2^64 is the fraction of a turn itself, off by at most position * 2^-64 turns.  Its quarter turns
+// are the two bits above the rest, which becomes a float, relative precision kept: r in [-1, 1) eighths of a turn.  There sin(pi/4 r) = r S(r^2) and
 // cos(pi/4 r) = 1 + r^2 C(r^2) with cubic S and C, fitted here by exchange for the least maximal error on
 // [0, 1]: 2.4e-9 and 1.9e-10, below a tenth of fp32's rounding.  Amplitude is in the coefficients.
 // What bounds the kernel is instruction issue beside the writes: 131072 positions of 64 pairs take 15.0 us
@@ -243,13 +243,7 @@ unsigned read_and_clear_error_rotary(cudaStream_t, std::string* where) {
 int launch_rotary_tables(int length, int rot, double base, double factor, int original_length, double slow, double fast,
                          double amplitude, float* cosp, float* sinp, cudaStream_t stream) {
   TableParams p{};
-  const double turn = 6.283185307179586476925286766559;
-  for (int i = 0; i < rot / 2; ++i) {
-    const double f = std::pow(base, -2.0 * i / rot) / turn;  // turns a position
-    double keep = 0.0;
-    if (original_length > 0) keep = std::fmin(1.0, std::fmax(0.0, (original_length * f - slow) / (fast - slow)));
-    p.turn[i] = static_cast<unsigned long long>(std::ldexp(f * (keep + (1.0 - keep) / factor), 64));
-  }
+  rotary_turns(rot, base, factor, original_length, slow, fast, p.turn);
   p.cosp = cosp;
   p.sinp = sinp;
   p.length = length;
