@@ -3,8 +3,8 @@
 //
 // Pair i of a head's first rot_dim dimensions turns by position * f_i:
 //   (x0, x1) -> (x0 c - x1 s, x1 c + x0 s),
-// with s negated for the transpose (the gradient of the rotation).  Both kernels only move bytes:
-// the tables are written once, every element of q and k is read and written once.
+// with s negated for the transpose (the gradient of the rotation).  The rotation only moves bytes, every
+// element of q and k read and written once; the tables are written once and computed on the way.
 #include <cuda_bf16.h>
 
 #include <cmath>
