@@ -191,6 +191,13 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
   return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
+// A given tensor has new values: autograd must not use the old ones that it may have saved.
+void written(PyObject* given) {
+  if (!given) return;
+  const at::Tensor& t = THPVariable_Unpack(given);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // `fn(stream)` with the tensors' device current: the library launches on it and looks up its state
 // there.
 template <class Fn>
@@ -433,7 +440,7 @@ const char kGradDoc[] =
     "workspace=None)\n--\n\n"
     "Gradients (dq, dk, dv) of blocksparse_attn_fwd (bf16): out and lse are the forward's\n"
     "results for the same arguments and bounds, d_out the gradient of the loss with respect\n"
-    "to out.";
+    "to out.  No autograd graph is built; given outputs count as changed for graphs that saved them.";
 PyObject* grad(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
   static const Signature sig("blocksparse_attn_bwd", 16, 16,
                              {"q", "k", "v", "out", "lse", "d_out", "q_positions", "q_segment_ids", "kv_positions",
@@ -488,6 +495,7 @@ PyObject* grad(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwn
                                       size32(D, "D"), q_block, kv_block, causal, left, right, pad, scale, to[0], to[1],
                                       to[2], ws.data_ptr(), ws.nbytes(), stream);
     });
+    for (int i = 0; i < 3; ++i) written(o[21 + i]);
     PyObject* r = PyTuple_New(3);
     if (!r) throw Raised{};
     for (int i = 0; i < 3; ++i) {
@@ -554,6 +562,8 @@ PyObject* tables(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* k
       return sba_rotary_tables(length, rot, base, factor, original, slow, fast, amplitude, static_cast<float*>(to[0]),
                                static_cast<float*>(to[1]), stream);
     });
+    written(o[9]);
+    written(o[10]);
     PyObject* a = o[9] ? Py_NewRef(o[9]) : THPVariable_Wrap(made[0]);
     PyObject* b = a ? (o[10] ? Py_NewRef(o[10]) : THPVariable_Wrap(made[1])) : nullptr;
     PyObject* r = b ? PyTuple_Pack(2, a, b) : nullptr;
@@ -594,7 +604,8 @@ const char kEmbedDoc[] =
     "[N, H, D]; k may be None), bf16 or fp32, may be slices of one projection's output; cos / sin\n"
     "fp32 [max_pos, rot_dim / 2]; positions int32 [B, T] ([N]), by default those in the row (at most\n"
     "max_pos of them), a negative one leaves its token as it is.  inverse turns back: the gradient.  Returns\n"
-    "(q_out, k_out), new unless given (may be q and k).";
+    "(q_out, k_out), new unless given (may be q and k).  No autograd graph is built: the gradient is\n"
+    "the call with inverse; given outputs count as changed for graphs that saved them.";
 PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
   static const Signature sig("rotary_embed", 4, 4,
                              {"q", "k", "cos", "sin", "positions", "interleaved", "inverse", "q_out", "k_out"});
@@ -648,6 +659,8 @@ PyObject* embed(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw
     a.interleaved = truth(o[5], false);
     a.inverse = truth(o[6], false);
     call(sba_rotary_embed, a, index);
+    written(o[7]);
+    written(o[8]);
     PyObject* x = o[7] ? Py_NewRef(o[7]) : THPVariable_Wrap(out[0]);
     PyObject* y = x ? (o[8] ? Py_NewRef(o[8]) : with_k ? THPVariable_Wrap(out[1]) : Py_NewRef(Py_None)) : nullptr;
     PyObject* r = y ? PyTuple_Pack(2, x, y) : nullptr;
