@@ -869,7 +869,7 @@ __device__ __forceinline__ void dkdv_items(const Maps& maps, const Params& p, co
 
 // ------------------------------------------------------------------ dQ
 struct DqItem {
-  int b, hkv, h, qblk, n_steps, item;  // n_steps -1: no more items
+  int b, h, qblk, n_steps;  // n_steps -1: no more items
   Range r;
 };
 
@@ -973,7 +973,7 @@ __device__ __forceinline__ void dq_items(const Maps& maps, const Params& p, cons
       const int n = (r.up - r.lo + 1) / 2;
       if (lane == 0) {
         DqItem& it = item_at(islot);
-        it.b = b; it.hkv = hkv; it.h = h; it.qblk = qblk; it.n_steps = n; it.item = item; it.r = r;
+        it.b = b; it.h = h; it.qblk = qblk; it.n_steps = n; it.r = r;
         mbar_arrive(&item_full[islot]);
       }
       __syncwarp();
