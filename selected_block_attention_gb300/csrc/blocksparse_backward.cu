@@ -19,9 +19,9 @@
 //   3. merge, if the heads are in parts: their dK and dV added up.
 // S and dP are computed in both (7 products for the 5 of the formulas).  The other way, one pass
 // with dQ added up in memory, needs B T Hq D fp32 sums cleared, added to by every key tile and
-// rounded at the end, some 2.7 GB beside 1.1 GB of inputs on a batch of 4 x 16384 tokens, and its
-// sums come in an order set by timing.  Here every sum is held in tensor memory by one CTA, in an
-// order that the bounds fix, so results are the same from run to run.
+// rounded at the end, some 2.7 GB beside 1.9 GB of inputs on a batch of 4 x 16384 tokens (32 heads over 8
+// of 128), and its sums come in an order set by timing.  Here every sum is held in tensor memory by one CTA,
+// in an order that the bounds fix, so results are the same from run to run.
 //
 // Both halves of the kernel keep one tile of S and one of dP (128 x 128 fp32 each) in tensor memory
 // and are arranged so that the tensor core always has a product to do while the softmax warps work
@@ -30,8 +30,8 @@
 //   dQ:       S(i+1)  dQ(i)    dP(i+1)              softmax warps: dS(i) | P(i+1)
 // What bounds them is the tensor core: the seven products over whole tiles of one row of 8192 (16 heads
 // over 4) take 519 us at the rate of a large library product in a burst and 577 at its sustained one, the
-// kernels 575 to 620 with prep, by the GPU's clocks; of a batch of 4 x 16384 behind a window of 1024, 1855
-// and 2066, the kernels 2390 to 2570, 160 of it prep's.  Heads of 64 have half the products and the same
+// kernels 570 to 630 with prep, by the GPU's clocks; of a batch of 4 x 16384 behind a window of 1024, 1855
+// and 2066, the kernels 2430 to 2600, 160 of it prep's.  Heads of 64 have half the products and the same
 // softmax: there the chain of waits through the issuing warp is as long (2 x 4096, 12 heads over 4, 500
 // and 300 tokens in view: 42 us at that rate, 103 taken).  Exponentials left out, or a second tile of S
 // for heads of 64, change nothing.
@@ -461,7 +461,7 @@ struct Maps {
 // 64 tokens from token0 on of a head to the first half of a tile, those from token1 on to the second.  A half
 // outside the bounds is read as zeros, by a box that begins behind the last token: its keys take part in the
 // products with weight 0, and 0 times what they hold, which behind a row's last tile is another sequence's,
-// need not be 0.
+// need not be 0.  Two boxes for whole tiles too: they cost nothing beside one of 128.
 template <int kPanels>
 __device__ __forceinline__ void load_halves(uint8_t* to, const CUtensorMap& map, uint64_t* bar, int head, int token0,
                                             int token1) {
@@ -1341,7 +1341,7 @@ __global__ void __launch_bounds__(256) bsa_bwd_merge_kernel(const float4* __rest
 // ------------------------------------------------------------------ host
 // Parts of a KV head's query heads.  An item is a key tile with all steps of its query heads; fewer
 // items than SMs leave SMs without one while the longest run, so heads are divided until there are
-// enough (one row of 8192, 16 heads over 1: 1461 -> 617 us; of 2048: 343 -> 69), at most into as many
+// enough (one row of 8192, 16 heads over 1: 1454 -> 613 us; of 2048: 341 -> 68), at most into as many
 // as four times the SMs, which bounds the sums' memory.  256 items divided in two as well only pay for
 // the merge (16 heads over 4 at 8192: 606 -> 630 us), and so do items of at most 16 steps, which end
 // soon (2 rows of 1024, 4 heads over 2: 22.5 -> 23.5; with 32 steps it pays: 53 -> 29).
