@@ -303,7 +303,9 @@ def run(st):
         if c["op"] == "rotate":
             q, k = sba.rotary_embed(st["q"], st["k"], st["cos"], st["sin"], positions=st["pos"], interleaved=c["pairs"], inverse=c["inverse"])
             return dict(q=q, k=k)
-        dq, dk, dv = sba.blocksparse_attn_bwd(st["q"], st["k"], st["v"], st["out"], st["lse"], st["do"], st["pos"], st["seg"], st["pos"], st["seg"],
+        # as the forward leaves it: for rows of one query block the state's may be a view in another order
+        out = st["out"].contiguous()
+        dq, dk, dv = sba.blocksparse_attn_bwd(st["q"], st["k"], st["v"], out, st["lse"], st["do"], st["pos"], st["seg"], st["pos"], st["seg"],
                                               *st["bounds"], QB, c["kb"], causal=c["causal"], window_left=c["left"], window_right=c["right"])
         return dict(dq=dq, dk=dk, dv=dv)
     return {"tables": _tables_plain, "rotate": _rotate_plain, "grad": _grad_plain}[c["op"]](st)
